@@ -99,6 +99,7 @@ def lib():
                   "da_probe_packed",
                   "dce_finalize_shard", "dce_backward_shard", "da_rowmax_cached", "da_accumulate_finalize_cached"):
             getattr(L, f).restype = C.c_int
+        train.declare(L)
         _lib = L
     return _lib
 
@@ -739,3 +740,8 @@ def probe_int_mac_rate(iters=4096, nblocks=None):
     b.synchronize()
     macs = iters * nblocks * 512 * int(L.da_probe_int_mac_per_thread_iter())
     return macs / (a.elapsed_time(b) * 1e-3)
+
+
+from . import train  # noqa: E402  (needs the helpers above)
+from .train import (AdamW, adamw_state_len, adamw_step, attention, attention_backward,  # noqa: E402,F401
+                    attention_forward, layer_norm, layer_norm_backward, layer_norm_forward)

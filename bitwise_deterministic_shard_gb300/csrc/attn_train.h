@@ -1,0 +1,64 @@
+// Internal interface of the training attention (capped, distance-biased and masked scores):
+// forward, its join of key ranges, and the backward passes.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace detattn {
+
+constexpr int TA_TILE = 128;          // queries, and keys, of a tile
+
+// smallest and largest document id of a 128-key tile (negative ids left out) and whether it has
+// negative ones (or ends past the last key)
+struct TaBounds {
+  int lo, hi, neg;
+};
+
+struct TaArgs {
+  // rank-5 maps {D, heads of the box's group, S, groups, B}, boxes of 64 columns
+  CUtensorMap q, k, v, o, go, dq, dk, dv;
+  const float* slopes;                // [Hq] or null
+  const int* docs;                    // [B, Skv] or null
+  const TaBounds* bounds;             // [B, key tiles] with docs
+  const TaBounds* qbounds;            // backward: [B, query tiles] with docs
+  const int* prefix;                  // [B] or null
+  float* lse;                         // [B, Hq, Sq], natural logarithm
+  float2* rows;                       // backward: [B, Hq, query tiles x 128] (lse log2 e, delta); +inf, 0 for a
+                                      // row that sees nothing and past the last query
+  float* part;                        // split forward: sums [2 splits][B Hkv][128][DP], then (max, total) pairs
+  void* out;                          // join of the split forward: strides of b, h, s
+  int64_t os[3];
+  int* status;
+  int B, Hq, Hkv, Sq, Skv, D;
+  int group;                          // query heads of a key head
+  int pack;                           // query heads in one tile: group when Sq * group <= 128, else 1
+  int qrows;                          // queries of a tile
+  int qtiles;                         // query tiles (of a head, or of a group of heads when packed)
+  int ktiles;
+  int causal;
+  int splits;                         // > 0: key ranges, each CTA's two softmax groups on every other tile
+  float scale;                        // of the products
+  float softcap;
+};
+
+template <int DP, bool BF>
+cudaError_t ta_forward(const TaArgs& a, cudaStream_t st);
+template <int DP, bool BF>
+cudaError_t ta_dkv(const TaArgs& a, cudaStream_t st);
+template <int DP, bool BF>
+cudaError_t ta_dq(const TaArgs& a, cudaStream_t st);
+// tiles of the last S tokens of each row of docs [B, Skv]
+cudaError_t ta_bounds(const int* docs, int B, int Skv, int S, TaBounds* out, cudaStream_t st);
+// the rows array: delta = sum over d of out * grad; strides of b, h, s in elements
+struct TaRowsArgs {
+  const void* out;
+  const void* grad;
+  const float* lse;
+  float2* rows;
+  int64_t os[3], gs[3];
+  int B, Hq, Sq, D, qtiles, bf;
+};
+cudaError_t ta_rows(const TaRowsArgs& a, cudaStream_t st);
+
+}  // namespace detattn

@@ -69,6 +69,7 @@ typedef struct CUstream_st* da_stream_t; /* a cudaStream_t */
 /* element types */
 #define DA_F32 0
 #define DA_BF16 1
+#define DA_F16 2   /* training operators (dta_*, dln_*, dow_*) only */
 
 #define DA_NUM_NDIG 15
 #define DA_DEN_NDIG 6
@@ -319,6 +320,84 @@ int da_probe_packed(int which, uint32_t lo_bits, int64_t count, int64_t* mismatc
  * ORs DA_STATUS_TIMEOUT into *dev_status (device int32, required): the caller reads the
  * status, and the context stays usable.  Exercises the timeout path without a fault. */
 int da_probe_bounded_wait(int32_t* dev_status, da_stream_t stream);
+
+/* ---- Training operators ------------------------------------------------------------------
+ * Attention with capped, distance-biased and masked scores and its gradient, layer norm and its
+ * gradient, and AdamW.  Unlike the exact reductions above they compute in binary32 (16-bit
+ * operands of the tensor cores where said) in a FIXED ORDER that depends on the sizes and types
+ * alone: no atomics add values, so equal calls give equal bytes on every run.  The conventions above
+ * (caller-owned memory, checks before any launch, the device status word) hold. */
+
+/* One attention problem.  q: [B, Hq, Sq, D]; k, v: [B, Hkv, Skv, D]; all bf16 or all f16;
+ * Sq <= Skv (query i stands at position i + Skv - Sq), D a multiple of 8 up to 128,
+ * Hq % Hkv == 0.  Pointers are 16-byte aligned and the strides of b, h and s multiples of 8
+ * elements (where the dimension is longer than 1), not zero.
+ *   t = scale q.k;  u = softcap > 0 ? softcap tanh(t / softcap) : t;  s = u - slopes[h] |pos_i - j|
+ * Query i sees key j when (not causal, or j <= pos_i, or j < prefix[b]) and, with docs,
+ * docs[b][j] == docs[b][pos_i] >= 0.  A query that sees nothing gets a zero output, an lse of -inf and
+ * zero gradients.  Tokens with a negative id may hold any bits, NaN among them; other inputs must
+ * be finite (a row whose sum is not sets DA_STATUS_NONFINITE). */
+typedef struct {
+  da_tensor q, k, v;
+  int32_t causal;
+  float scale;            /* NaN selects 1/sqrt(D) */
+  float softcap;          /* 0: scores are not capped; else positive and finite */
+  const float* slopes;    /* optional device f32 [Hq]: the score falls by slopes[h] per position of distance */
+  const int32_t* docs;    /* optional device int32 [B, Skv]: document of each token, negative: padding */
+  const int32_t* prefix;  /* optional device int32 [B], needs causal: keys below it are seen by all queries */
+  int32_t* dev_status;    /* optional device int32, OR-ed with DA_STATUS_* bits */
+} dta_desc;
+
+/* Bytes of device workspace (256-byte aligned) of dta_forward (backward = 0) and dta_backward
+ * (backward = 1); 0 for a descriptor that they refuse. */
+size_t dta_workspace_bytes(const dta_desc* desc, int backward);
+
+/* out: [B, Hq, Sq, D] of q's type, strides as above; lse: optional device f32 [B, Hq, Sq], the
+ * natural logarithm of each row's sum of exponentials, which the backward pass takes. */
+int dta_forward(const dta_desc* desc, const da_tensor* out, float* lse, void* ws, size_t ws_bytes, da_stream_t stream);
+
+/* Gradients of sum(out * grad).  out, lse: the forward's; grad: [B, Hq, Sq, D] of q's type;
+ * dq, dk, dv: shaped and typed as q, k, v (a key head's gradient is the sum over its query heads). */
+int dta_backward(const dta_desc* desc, const da_tensor* out, const float* lse, const da_tensor* grad,
+                 const da_tensor* dq, const da_tensor* dk, const da_tensor* dv, void* ws, size_t ws_bytes,
+                 da_stream_t stream);
+
+/* Layer norm over the columns of x: y = (x - mean) rstd w + b, rstd = 1 / sqrt(var + eps).
+ * x, y: [rows, cols] of one type (f32, bf16, f16); w, b: optional device [cols], contiguous, of type
+ * wdtype (x's or f32); mean, rstd: device f32 [rows], written. */
+int dln_forward(const da_matrix* x, const void* w, const void* b, int wdtype, float eps, const da_matrix* y, float* mean,
+                float* rstd, da_stream_t stream);
+
+/* dx from dy and the forward's x, mean and rstd; dw, db: optional device [cols] of type wdtype, each
+ * a sum over the rows in binary32 and a fixed order, rounded once.  ws: at least
+ * dln_workspace_bytes(rows, cols) when dw or db is wanted. */
+size_t dln_workspace_bytes(int64_t rows, int64_t cols);
+int dln_backward(const da_matrix* dy, const da_matrix* x, const void* w, int wdtype, const float* mean, const float* rstd,
+                 const da_matrix* dx, void* dw, void* db, void* ws, size_t ws_bytes, da_stream_t stream);
+
+/* One tensor of an AdamW step: numel elements at param and grad, contiguous; its states are the elements
+ * [state, state + numel) of the state arrays, state a multiple of 256. */
+typedef struct {
+  void* param;
+  const void* grad;
+  int64_t numel;
+  int64_t state;
+} dow_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;           /* 1 on the first step */
+} dow_hyper;
+
+/* AdamW, in place, over n tensors of one type (f32, bf16, f16).  Per element, every operation
+ * rounded once to binary32, scalars formed in binary64 and rounded:
+ *   g = grad (times *grad_scale when given);  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) (g g)
+ *   p = p (1 - lr wd) - lr / (1 - b1^step) * (m / (sqrt(v) / sqrt(1 - b2^step) + eps))
+ * state_bits 32: m, v are device f32 [state_len].  state_bits 8: m, v are device e4m3 [state_len] with
+ * a f32 scale for each 256 elements (m_scale, v_scale: [state_len / 256], scale = largest magnitude
+ * / 448); v holds the square root, in which a value above zero never becomes zero; elements of a
+ * tensor's last block past its end become zero.  state_len is a multiple of 256. */
+int dow_adamw(const dow_tensor* tensors, int n, int dtype, int state_bits, void* m, void* v, float* m_scale,
+              float* v_scale, int64_t state_len, const dow_hyper* hyper, const float* grad_scale, da_stream_t stream);
 
 #ifdef __cplusplus
 }
