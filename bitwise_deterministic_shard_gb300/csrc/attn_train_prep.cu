@@ -43,9 +43,11 @@ __global__ void __launch_bounds__(256) ta_rows_kernel(const TaRowsArgs a) {
     for (int k = 0; k < 2; k++) {
       const int d = (u + 8 * k) * 8;
       if (d < a.D) {
-        const Pack<T, 8> x = *reinterpret_cast<const Pack<T, 8>*>(o + d), y = *reinterpret_cast<const Pack<T, 8>*>(g + d);
+        Run<T, 8> x, y;
+        x.load(o + d);
+        y.load(g + d);
 #pragma unroll
-        for (int e = 0; e < 8; e++) s = __fmaf_rn(Elem<T>::get(x.e[e]), Elem<T>::get(y.e[e]), s);
+        for (int e = 0; e < 8; e++) s = __fmaf_rn(x.get(e), y.get(e), s);
       }
     }
   }

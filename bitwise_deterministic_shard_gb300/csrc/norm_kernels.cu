@@ -4,15 +4,24 @@
 //   y = h w + b;   a = dy w;   dx = rstd (a - mean(a) - h mean(a h))
 //   dw = sum over rows of dy h;   db = sum over rows of dy
 //
-// What bounds it: HBM (x and y once forward, x, dy and dx once backward).  A row is read once
-// and stays in the registers of its group of threads (a warp up to 128 16-byte vectors, else a
-// CTA of up to 1024 threads with two vectors each); both statistics come from those
-// registers, so the variance is the centred sum, not a difference of sums.  Wider rows are read
-// again from L2 by a looping variant.  Rows that do not start on 16 bytes are read element by
-// element with the threads of a warp on neighbouring elements (a warp's access is still one run).
-// In the backward pass a group keeps its columns over a run of rows, so dw and db are sums in
-// its registers; each run writes one row of partial sums and a second kernel adds these in a fixed
-// order.  The runs depend on the sizes alone.  All sums are binary32.
+// What bounds it: HBM (x and y once forward, x, dy and dx once backward).  A row is read once: it stays in the
+// registers, or the shared memory, of its warp or CTA, and both statistics come from there, so the
+// variance is the centred sum, not a difference of sums.  Variants, by the 16-byte vectors of a row:
+//   aligned, 129 to 1024 vectors, many rows: streaming CTAs (below) that copy the next rows while they work
+//     on the present ones and keep the weights in registers;
+//   otherwise, up to 128 vectors: a warp a row; up to 2048: a CTA a row (forward) or a run of rows (backward),
+//     rows that do not start and end on 16 bytes element by element, the threads of a warp on
+//     neighbouring elements (a warp's access is still one run);
+//   wider rows are read again from L2 by looping variants.
+// In the backward pass a group of threads keeps its columns over a run of rows, so dw and db are sums in
+// its registers; each run writes one row of partial sums and a second kernel adds these in a fixed order.
+// The runs depend on the sizes alone.  All sums are binary32; pairs of elements go through the packed
+// multiplier and adder.
+// 8192 x 4096 bf16, f32 weights: forward 30 us (0.65 of the measured copy bandwidth; 46 with a CTA a row that
+// reads the weights again for each, 49 with a warp a row), backward 48 us with the sum of the partial rows
+// (0.62; 79 + 5 and 59 so).  3001 x 5003 f32, unaligned: 27 and 59 us (0.66, 0.45).
+#include <algorithm>
+
 #include "../../include/detattn.h"
 #include "train_kernels.h"
 #include "train_math.cuh"
@@ -20,82 +29,103 @@
 namespace detattn {
 namespace {
 
+using f2::u64;
+
 constexpr int WARP_ROWS = 4;      // rows (warps) of a CTA of the warp-per-row variants
 
 // element e of vector k of thread t of G: 16-byte vectors, or runs of single elements
 template <int G, int VEC, bool AL>
-__device__ __forceinline__ int64_t col(int k, int e, int t) {
-  return AL ? ((int64_t)k * G + t) * VEC + e : ((int64_t)k * VEC + e) * G + t;
+__device__ __forceinline__ int col(int k, int e, int t) {   // rows of the register variants have under 2^15 columns
+  return AL ? (k * G + t) * VEC + e : (k * VEC + e) * G + t;
 }
 
-// the row's elements of this thread, as packed registers; zero past the end
+// the row's elements of this thread, as 32-bit words; zero past the end
 template <typename T, int G, int NV, bool AL>
 struct Row {
   static constexpr int VEC = Elem<T>::VEC;
-  Pack<T, VEC> r[NV];
-  __device__ __forceinline__ void load(const T* row, int64_t cols, int t) {
+  Run<T, VEC> r[NV];
+  __device__ __forceinline__ void load(const T* row, int cols, int t) {
 #pragma unroll
     for (int k = 0; k < NV; k++) {
-      if (AL && col<G, VEC, AL>(k, VEC, t) <= cols) {
-        r[k] = *reinterpret_cast<const Pack<T, VEC>*>(row + col<G, VEC, AL>(k, 0, t));
+      r[k].zero();
+      if constexpr (AL) {
+        if (col<G, VEC, AL>(k, 0, t) < cols) r[k].load(row + col<G, VEC, AL>(k, 0, t));
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; e++) {
-          const int64_t c = col<G, VEC, AL>(k, e, t);
-          r[k].e[e] = c < cols ? row[c] : Elem<T>::put(0.f);
+          const int c = col<G, VEC, AL>(k, e, t);
+          if (c < cols) r[k].put_bits(e, row[c]);
         }
       }
     }
   }
-  __device__ __forceinline__ float get(int k, int e) const { return Elem<T>::get(r[k].e[e]); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < NV; k++) r[k].zero();
+  }
+  __device__ __forceinline__ void keep() {
+#pragma unroll
+    for (int k = 0; k < NV; k++) r[k].keep();
+  }
+  __device__ __forceinline__ u64 get2(int k, int i) const { return r[k].get2(i); }
 };
 
-template <typename T, int G, int NV, bool AL>
-__device__ __forceinline__ void store_vec(T* row, int64_t cols, int t, int k, const float* v) {
+template <typename T, int G, bool AL>
+__device__ __forceinline__ void store_vec(T* row, int cols, int t, int k, const Run<T, Elem<T>::VEC>& r) {
   constexpr int VEC = Elem<T>::VEC;
-  if (AL && col<G, VEC, AL>(k, VEC, t) <= cols) {
-    Pack<T, VEC> r;
-#pragma unroll
-    for (int e = 0; e < VEC; e++) r.e[e] = Elem<T>::put(v[e]);
-    *reinterpret_cast<Pack<T, VEC>*>(row + col<G, VEC, AL>(k, 0, t)) = r;
+  if constexpr (AL) {
+    if (col<G, VEC, AL>(k, 0, t) < cols) r.store(row + col<G, VEC, AL>(k, 0, t));
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; e++) {
-      const int64_t c = col<G, VEC, AL>(k, e, t);
-      if (c < cols) row[c] = Elem<T>::put(v[e]);
+      const int c = col<G, VEC, AL>(k, e, t);
+      if (c < cols) row[c] = r.bits(e);
     }
   }
 }
 
 // weights of the thread's vector k: f32 or the rows' type, ones (or zeros) without a tensor
 template <typename T, int G, bool AL>
-__device__ __forceinline__ void load_w(const void* w, bool f32, float none, int64_t cols, int t, int k, float* v) {
+__device__ __forceinline__ void load_w(const void* w, bool f32, float none, int cols, int t, int k, u64 (&v)[Elem<T>::VEC / 2]) {
   constexpr int VEC = Elem<T>::VEC;
   if (!w) {
 #pragma unroll
-    for (int e = 0; e < VEC; e++) v[e] = none;
+    for (int i = 0; i < VEC / 2; i++) v[i] = f2::splat(none);
     return;
   }
-  const int64_t c0 = col<G, VEC, AL>(k, 0, t);
-  if (AL && col<G, VEC, AL>(k, VEC, t) <= cols) {
-    if (f32) {
+  const int c0 = col<G, VEC, AL>(k, 0, t);
+  if constexpr (AL) {
+    if (c0 >= cols) {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; i++) v[i] = 0;
+    } else if (f32) {
 #pragma unroll
       for (int q = 0; q < VEC / 4; q++) {
         const float4 f = *reinterpret_cast<const float4*>((const float*)w + c0 + 4 * q);
-        v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
+        v[2 * q] = f2::pack(f.x, f.y);
+        v[2 * q + 1] = f2::pack(f.z, f.w);
       }
     } else {
-      const Pack<T, VEC> r = *reinterpret_cast<const Pack<T, VEC>*>((const T*)w + c0);
+      Run<T, VEC> r;
+      r.load((const T*)w + c0);
 #pragma unroll
-      for (int e = 0; e < VEC; e++) v[e] = Elem<T>::get(r.e[e]);
+      for (int i = 0; i < VEC / 2; i++) v[i] = r.get2(i);
     }
-    return;
-  }
+  } else {
+    float f[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; e++) {
-    const int64_t c = col<G, VEC, AL>(k, e, t);
-    v[e] = c >= cols ? 0.f : f32 ? ((const float*)w)[c] : Elem<T>::get(((const T*)w)[c]);
+    for (int e = 0; e < VEC; e++) {
+      const int c = col<G, VEC, AL>(k, e, t);
+      f[e] = c >= cols ? 0.f : f32 ? ((const float*)w)[c] : Elem<T>::get(((const T*)w)[c]);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC / 2; i++) v[i] = f2::pack(f[2 * i], f[2 * i + 1]);
   }
+}
+__device__ __forceinline__ float both(u64 v) {
+  float a, b;
+  f2::unpack(v, a, b);
+  return __fadd_rn(a, b);
 }
 
 // sum over the group of G threads, the same bits in each
@@ -129,40 +159,57 @@ __device__ __forceinline__ void group_sum2(float& x, float& y, float* sh) {
   }
 }
 
+// CTAs of an SM that the registers have to allow: enough loads in flight, but the row stays in registers
+constexpr int fwd_ctas(int g) { return g == 32 ? 8 : g == 128 ? 10 : 4; }
+constexpr int bwd_ctas(int g, int nv) { return g == 32 ? nv == 1 ? 8 : 4 : g == 128 ? 4 : g == 256 ? 2 : 1; }
+
 template <typename T, int G, int NV, bool AL>
-__global__ void __launch_bounds__(G == 32 ? 32 * WARP_ROWS : G) norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(G == 32 ? 32 * WARP_ROWS : G, fwd_ctas(G)) norm_fwd_kernel(const NormArgs a) {
   constexpr int VEC = Elem<T>::VEC;
   __shared__ float sh[64];
+  const int cols = (int)a.cols;
   const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int64_t row = G == 32 ? (int64_t)blockIdx.x * WARP_ROWS + (threadIdx.x >> 5) : blockIdx.x;
   if (G == 32 && row >= a.rows) return;
   Row<T, G, NV, AL> x;
-  x.load((const T*)a.x + row * a.xs, a.cols, t);
-  float s = 0.f;
+  x.load((const T*)a.x + row * a.xs, cols, t);
+  u64 s = 0;
 #pragma unroll
   for (int k = 0; k < NV; k++)
 #pragma unroll
-    for (int e = 0; e < VEC; e++) s = __fadd_rn(s, x.get(k, e));
+    for (int i = 0; i < VEC / 2; i++) s = f2::add(s, x.get2(k, i));
   const float n = (float)a.cols;
-  const float mean = __fdiv_rn(group_sum<G>(s, sh), n);
-  s = 0.f;
+  const float mean = __fdiv_rn(group_sum<G>(both(s), sh), n);
+  x.keep();
+  s = 0;
+  const u64 off = f2::splat(-mean);
 #pragma unroll
   for (int k = 0; k < NV; k++)
 #pragma unroll
-    for (int e = 0; e < VEC; e++) {
-      const float d = col<G, VEC, AL>(k, e, t) < a.cols ? x.get(k, e) - mean : 0.f;
-      s = __fmaf_rn(d, d, s);
+    for (int i = 0; i < VEC / 2; i++) {
+      u64 d = f2::add(x.get2(k, i), off);
+      if (AL) {
+        if (col<G, VEC, AL>(k, 0, t) >= cols) d = 0;
+      } else {
+        float p, q;
+        f2::unpack(d, p, q);
+        d = f2::pack(col<G, VEC, AL>(k, 2 * i, t) < cols ? p : 0.f, col<G, VEC, AL>(k, 2 * i + 1, t) < cols ? q : 0.f);
+      }
+      s = f2::fma(d, d, s);
     }
-  const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(group_sum<G>(s, sh), n) + a.eps));
+  const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(group_sum<G>(both(s), sh), n) + a.eps));
+  const u64 rstd2 = f2::splat(rstd);
   const bool wf = a.wdtype == DA_F32;
+  x.keep();
 #pragma unroll
   for (int k = 0; k < NV; k++) {
-    float w[VEC], b[VEC], y[VEC];
-    load_w<T, G, AL>(a.w, wf, 1.f, a.cols, t, k, w);
-    load_w<T, G, AL>(a.b, wf, 0.f, a.cols, t, k, b);
+    u64 w[VEC / 2], b[VEC / 2];
+    load_w<T, G, AL>(a.w, wf, 1.f, cols, t, k, w);
+    load_w<T, G, AL>(a.b, wf, 0.f, cols, t, k, b);
+    Run<T, VEC> y;
 #pragma unroll
-    for (int e = 0; e < VEC; e++) y[e] = __fmaf_rn((x.get(k, e) - mean) * rstd, w[e], b[e]);
-    store_vec<T, G, NV, AL>((T*)a.y + row * a.ys, a.cols, t, k, y);
+    for (int i = 0; i < VEC / 2; i++) y.set2(i, f2::fma(f2::mul(f2::add(x.get2(k, i), off), rstd2), w[i], b[i]));
+    store_vec<T, G, AL>((T*)a.y + row * a.ys, cols, t, k, y);
   }
   if (t == 0) {
     a.mean[row] = mean;
@@ -199,87 +246,145 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormArgs a) {
   }
 }
 
-// One CTA takes the rows [part * per, ...); in the warp variants its warps take every fourth.
-template <typename T, int G, int NV, bool AL>
-__global__ void __launch_bounds__(G == 32 ? 32 * WARP_ROWS : G) norm_bwd_kernel(const NormArgs a, int64_t per) {
-  constexpr int VEC = Elem<T>::VEC;
-  constexpr int STEP = G == 32 ? WARP_ROWS : 1;
-  __shared__ float sh[G == 32 ? 32 * NV * VEC * 2 : 64];
-  const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x;
+// One CTA takes the rows [part * per, ...), R at a time; in the warp variants each warp takes every
+// fourth group of R.
+template <typename T, int G, int NV, int R, bool AL>
+__global__ void __launch_bounds__(G == 32 ? 32 * WARP_ROWS : G, bwd_ctas(G, NV)) norm_bwd_kernel(const NormArgs a, int64_t per) {
+  constexpr int VEC = Elem<T>::VEC, W = G / 32;
+  const int cols = (int)a.cols;
+  constexpr int STEP = G == 32 ? WARP_ROWS * R : R;
+  __shared__ __align__(8) float sh[G == 32 ? 32 * NV * VEC * 2 : 4 * R * W];
+  const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t r0 = (int64_t)blockIdx.x * per, r1 = min(r0 + per, a.rows);
   const float inv_n = __fdiv_rn(1.f, (float)a.cols);
   const bool wf = a.wdtype == DA_F32;
-  float gw[NV][VEC], gb[NV][VEC];
+  u64 gw[NV][VEC / 2], gb[NV][VEC / 2];
 #pragma unroll
   for (int k = 0; k < NV; k++)
 #pragma unroll
-    for (int e = 0; e < VEC; e++) gw[k][e] = gb[k][e] = 0.f;
-  for (int64_t row = r0 + (G == 32 ? threadIdx.x >> 5 : 0); row < r1; row += STEP) {
-    Row<T, G, NV, AL> x, dy;
-    x.load((const T*)a.x + row * a.xs, a.cols, t);
-    dy.load((const T*)a.dy + row * a.dys, a.cols, t);
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float s1 = 0.f, s2 = 0.f;
+    for (int i = 0; i < VEC / 2; i++) gw[k][i] = gb[k][i] = 0;
+  Row<T, G, NV, AL> x[R], dy[R];
+  float mean[R], rstd[R];
+  const auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int k = 0; k < NV; k++) {
-      float w[VEC];
-      load_w<T, G, AL>(a.w, wf, 1.f, a.cols, t, k, w);
-#pragma unroll
-      for (int e = 0; e < VEC; e++) {
-        const float d = dy.get(k, e), h = (x.get(k, e) - mean) * rstd, ad = d * w[e];
-        gw[k][e] = __fmaf_rn(d, h, gw[k][e]);   // past the row's end d is zero
-        gb[k][e] = __fadd_rn(gb[k][e], d);
-        s1 = __fadd_rn(s1, ad);
-        s2 = __fmaf_rn(ad, h, s2);
+    for (int r = 0; r < R; r++) {
+      if (row + r < r1) {
+        x[r].load((const T*)a.x + (row + r) * a.xs, cols, t);
+        dy[r].load((const T*)a.dy + (row + r) * a.dys, cols, t);
+        mean[r] = a.mean[row + r];
+        rstd[r] = a.rstd[row + r];
+      } else {                       // no row: adds nothing
+        x[r].zero();
+        dy[r].zero();
+        mean[r] = rstd[r] = 0.f;
       }
     }
-    group_sum2<G>(s1, s2, sh);
-    s1 *= inv_n;
-    s2 *= inv_n;
+  };
+  int turn = 0;
+  for (int64_t row = r0 + (G == 32 ? warp * R : 0); row < r1; row += STEP, turn ^= 1) {
+    fetch(row);
+    u64 t1[R], t2[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) t1[r] = t2[r] = 0;
 #pragma unroll
     for (int k = 0; k < NV; k++) {
-      float w[VEC], dx[VEC];
-      load_w<T, G, AL>(a.w, wf, 1.f, a.cols, t, k, w);
+      u64 w[VEC / 2];
+      load_w<T, G, AL>(a.w, wf, 1.f, cols, t, k, w);
 #pragma unroll
-      for (int e = 0; e < VEC; e++) {
-        const float h = (x.get(k, e) - mean) * rstd;
-        dx[e] = __fmaf_rn(-h, s2, __fmaf_rn(dy.get(k, e), w[e], -s1)) * rstd;
+      for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int i = 0; i < VEC / 2; i++) {
+          const u64 d = dy[r].get2(k, i), h = f2::mul(f2::add(x[r].get2(k, i), f2::splat(-mean[r])), f2::splat(rstd[r]));
+          const u64 ad = f2::mul(d, w[i]);
+          gw[k][i] = f2::fma(d, h, gw[k][i]);   // past the row's end d is zero
+          gb[k][i] = f2::add(gb[k][i], d);
+          t1[r] = f2::add(t1[r], ad);
+          t2[r] = f2::fma(ad, h, t2[r]);
+        }
+    }
+    float s1[R], s2[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      s1[r] = warp_sum(both(t1[r]));
+      s2[r] = warp_sum(both(t2[r]));
+    }
+    if constexpr (G > 32) {          // two sets of words by turns: one barrier a step
+      float* at = sh + turn * (2 * R * W);
+      if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+          at[(2 * r) * W + warp] = s1[r];
+          at[(2 * r + 1) * W + warp] = s2[r];
+        }
       }
-      store_vec<T, G, NV, AL>((T*)a.y + row * a.ys, a.cols, t, k, dx);
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        s1[r] = warp_sum(lane < W ? at[(2 * r) * W + lane] : 0.f);
+        s2[r] = warp_sum(lane < W ? at[(2 * r + 1) * W + lane] : 0.f);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      x[r].keep();
+      dy[r].keep();
+    }
+#pragma unroll
+    for (int k = 0; k < NV; k++) {
+      u64 w[VEC / 2];
+      load_w<T, G, AL>(a.w, wf, 1.f, cols, t, k, w);
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        const u64 m1 = f2::splat(-s1[r] * inv_n), m2 = f2::splat(-s2[r] * inv_n), rr = f2::splat(rstd[r]);
+        Run<T, VEC> dx;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; i++) {
+          const u64 h = f2::mul(f2::add(x[r].get2(k, i), f2::splat(-mean[r])), rr);
+          dx.set2(i, f2::mul(f2::fma(h, m2, f2::fma(dy[r].get2(k, i), w[i], m1)), rr));
+        }
+        if (row + r < r1) store_vec<T, G, AL>((T*)a.y + (row + r) * a.ys, cols, t, k, dx);
+      }
     }
   }
   if (!a.part) return;
   if constexpr (G == 32) {   // the warps' sums in the order of the warps
-    const int w = threadIdx.x >> 5;
+    u64* at = reinterpret_cast<u64*>(sh) + t;
     for (int turn = 0; turn < WARP_ROWS; turn++) {
-      if (w == turn) {
+      if (warp == turn) {
 #pragma unroll
         for (int k = 0; k < NV; k++)
 #pragma unroll
-          for (int e = 0; e < VEC; e++) {
-            float* at = sh + (k * VEC + e) * 64 + t;
+          for (int i = 0; i < VEC / 2; i++) {
+            const int o = (k * VEC / 2 + i) * 64;
             if (turn) {
-              gw[k][e] = __fadd_rn(at[0], gw[k][e]);
-              gb[k][e] = __fadd_rn(at[32], gb[k][e]);
+              gw[k][i] = f2::add(at[o], gw[k][i]);
+              gb[k][i] = f2::add(at[o + 32], gb[k][i]);
             }
-            at[0] = gw[k][e];
-            at[32] = gb[k][e];
+            at[o] = gw[k][i];
+            at[o + 32] = gb[k][i];
           }
       }
       __syncthreads();
     }
-    if (w != WARP_ROWS - 1) return;
+    if (warp != WARP_ROWS - 1) return;
   }
   float* pw = a.part + (int64_t)blockIdx.x * a.cols;
   float* pb = pw + (int64_t)gridDim.x * a.cols;
 #pragma unroll
   for (int k = 0; k < NV; k++)
 #pragma unroll
-    for (int e = 0; e < VEC; e++) {
-      const int64_t c = col<G, VEC, AL>(k, e, t);
-      if (c < a.cols) {
-        pw[c] = gw[k][e];
-        pb[c] = gb[k][e];
+    for (int i = 0; i < VEC / 2; i++) {
+      float w0, w1, b0, b1;
+      f2::unpack(gw[k][i], w0, w1);
+      f2::unpack(gb[k][i], b0, b1);
+      const int c0 = col<G, VEC, AL>(k, 2 * i, t), c1 = col<G, VEC, AL>(k, 2 * i + 1, t);
+      if (c0 < cols) {
+        pw[c0] = w0;
+        pb[c0] = b0;
+      }
+      if (c1 < cols) {
+        pw[c1] = w1;
+        pb[c1] = b1;
       }
     }
 }
@@ -319,6 +424,254 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const NormArgs a, i
   }
 }
 
+// ---- streaming variants: aligned rows of more than 128 vectors ----
+//
+// A CTA stays for a run of rows (backward) or every gridDim-th group of rows (forward).  Each thread owns
+// NV 16-byte vectors of the columns, keeps their weights in registers, and copies its own parts of the
+// next rows into its own slots of shared memory (cp.async: no register holds a load in flight, and no
+// barrier is needed for data that only the copying thread reads).  R rows share the barriers of a step.
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {   // zeros where there is no row or column
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T>
+__device__ __forceinline__ Run<T, Elem<T>::VEC> slot(uint32_t at) {
+  Run<T, Elem<T>::VEC> r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(at));
+  return r;
+}
+
+// N sums at once over the CTA of G threads, by turns in two sets of words: one barrier
+template <int G, int N>
+__device__ __forceinline__ void cta_sums(float (&v)[N], float* sh, int turn) {
+  constexpr int W = G / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* at = sh + turn * (N * W);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    v[i] = warp_sum(v[i]);
+    if (lane == 0) at[i * W + warp] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    float x = lane < W ? at[i * W + lane] : 0.f;
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
+    v[i] = __shfl_sync(0xffffffffu, x, 0);
+  }
+}
+
+template <typename T, int G, int NV, int R, int ST>
+__global__ void __launch_bounds__(G, 512 / G) norm_fwd_stream_kernel(const NormArgs a) {
+  constexpr int VEC = Elem<T>::VEC, W = G / 32;
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float sh[2 * R * W];
+  const int cols = (int)a.cols, t = threadIdx.x;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
+  const bool wf = a.wdtype == DA_F32;
+  u64 w[NV][VEC / 2], b[NV][VEC / 2];
+#pragma unroll
+  for (int k = 0; k < NV; k++) {
+    load_w<T, G, true>(a.w, wf, 1.f, cols, t, k, w[k]);
+    load_w<T, G, true>(a.b, wf, 0.f, cols, t, k, b[k]);
+  }
+  const auto fetch = [&](int64_t row, int st) {
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+      for (int k = 0; k < NV; k++) {
+        const int c = col<G, VEC, true>(k, 0, t);
+        const bool real = row + r < a.rows && c < cols;
+        copy16(mine + ((st * R + r) * NV + k) * (G * 16), (const T*)a.x + (real ? (row + r) * a.xs + c : 0), real);
+      }
+    copy_commit();
+  };
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t row = (int64_t)blockIdx.x * R;
+#pragma unroll
+  for (int s = 0; s < ST - 1; s++) fetch(row + s * step, s);
+  const float n = (float)a.cols;
+  int st = 0, turn = 0;
+  for (; row < a.rows; row += step) {
+    fetch(row + (ST - 1) * step, st == 0 ? ST - 1 : st - 1);
+    copy_wait<ST - 1>();
+    const uint32_t at = mine + st * R * NV * (G * 16);
+    float v[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      u64 s = 0;
+#pragma unroll
+      for (int k = 0; k < NV; k++) {
+        const auto x = slot<T>(at + (r * NV + k) * (G * 16));
+#pragma unroll
+        for (int i = 0; i < VEC / 2; i++) s = f2::add(s, x.get2(i));
+      }
+      v[r] = both(s);
+    }
+    cta_sums<G, R>(v, sh, turn);
+    turn ^= 1;
+    float mean[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      mean[r] = __fdiv_rn(v[r], n);
+      u64 s = 0;
+#pragma unroll
+      for (int k = 0; k < NV; k++) {
+        const auto x = slot<T>(at + (r * NV + k) * (G * 16));
+        if (col<G, VEC, true>(k, 0, t) < cols) {
+#pragma unroll
+          for (int i = 0; i < VEC / 2; i++) {
+            const u64 d = f2::add(x.get2(i), f2::splat(-mean[r]));
+            s = f2::fma(d, d, s);
+          }
+        }
+      }
+      v[r] = both(s);
+    }
+    cta_sums<G, R>(v, sh, turn);
+    turn ^= 1;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(v[r], n) + a.eps));
+      if (row + r < a.rows) {
+#pragma unroll
+        for (int k = 0; k < NV; k++) {
+          const auto x = slot<T>(at + (r * NV + k) * (G * 16));
+          Run<T, VEC> y;
+#pragma unroll
+          for (int i = 0; i < VEC / 2; i++)
+            y.set2(i, f2::fma(f2::mul(f2::add(x.get2(i), f2::splat(-mean[r])), f2::splat(rstd)), w[k][i], b[k][i]));
+          store_vec<T, G, true>((T*)a.y + (row + r) * a.ys, cols, t, k, y);
+        }
+        if (t == 0) {
+          a.mean[row + r] = mean[r];
+          a.rstd[row + r] = rstd;
+        }
+      }
+    }
+    st = st == ST - 1 ? 0 : st + 1;
+  }
+}
+
+template <typename T, int G, int NV, int R, int ST>
+__global__ void __launch_bounds__(G, 512 / G) norm_bwd_stream_kernel(const NormArgs a, int64_t per) {
+  constexpr int VEC = Elem<T>::VEC, W = G / 32;
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float sh[4 * R * W];
+  const int cols = (int)a.cols, t = threadIdx.x;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + t * 16;
+  const bool wf = a.wdtype == DA_F32;
+  const int64_t r0 = (int64_t)blockIdx.x * per, r1 = min(r0 + per, a.rows);
+  const float inv_n = __fdiv_rn(1.f, (float)a.cols);
+  u64 w[NV][VEC / 2], gw[NV][VEC / 2], gb[NV][VEC / 2];
+#pragma unroll
+  for (int k = 0; k < NV; k++) {
+    load_w<T, G, true>(a.w, wf, 1.f, cols, t, k, w[k]);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; i++) gw[k][i] = gb[k][i] = 0;
+  }
+  const auto fetch = [&](int64_t row, int st) {
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+      for (int k = 0; k < NV; k++) {
+        const int c = col<G, VEC, true>(k, 0, t);
+        const bool real = row + r < r1 && c < cols;
+        const uint32_t at = mine + ((st * R + r) * NV + k) * (G * 32);
+        copy16(at, (const T*)a.x + (real ? (row + r) * a.xs + c : 0), real);
+        copy16(at + G * 16, (const T*)a.dy + (real ? (row + r) * a.dys + c : 0), real);
+      }
+    copy_commit();
+  };
+  float mean[R], rstd[R], nmean[R], nrstd[R];
+  const auto stats = [&](int64_t row) {
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      nmean[r] = row + r < r1 ? a.mean[row + r] : 0.f;
+      nrstd[r] = row + r < r1 ? a.rstd[row + r] : 0.f;
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < ST - 1; s++) fetch(r0 + s * R, s);
+  stats(r0);
+  int st = 0, turn = 0;
+  for (int64_t row = r0; row < r1; row += R) {
+    fetch(row + (ST - 1) * R, st == 0 ? ST - 1 : st - 1);
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      mean[r] = nmean[r];
+      rstd[r] = nrstd[r];
+    }
+    stats(row + R);
+    copy_wait<ST - 1>();
+    const uint32_t at = mine + st * R * NV * (G * 32);
+    float s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      u64 t1 = 0, t2 = 0;
+#pragma unroll
+      for (int k = 0; k < NV; k++) {
+        const auto x = slot<T>(at + (r * NV + k) * (G * 32)), dy = slot<T>(at + (r * NV + k) * (G * 32) + G * 16);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; i++) {
+          const u64 d = dy.get2(i), h = f2::mul(f2::add(x.get2(i), f2::splat(-mean[r])), f2::splat(rstd[r]));
+          const u64 ad = f2::mul(d, w[k][i]);
+          gw[k][i] = f2::fma(d, h, gw[k][i]);
+          gb[k][i] = f2::add(gb[k][i], d);
+          t1 = f2::add(t1, ad);
+          t2 = f2::fma(ad, h, t2);
+        }
+      }
+      s[2 * r] = both(t1);
+      s[2 * r + 1] = both(t2);
+    }
+    cta_sums<G, 2 * R>(s, sh, turn);
+    turn ^= 1;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const u64 m1 = f2::splat(-s[2 * r] * inv_n), m2 = f2::splat(-s[2 * r + 1] * inv_n), rr = f2::splat(rstd[r]);
+      if (row + r < r1) {
+#pragma unroll
+        for (int k = 0; k < NV; k++) {
+          const auto x = slot<T>(at + (r * NV + k) * (G * 32)), dy = slot<T>(at + (r * NV + k) * (G * 32) + G * 16);
+          Run<T, VEC> dx;
+#pragma unroll
+          for (int i = 0; i < VEC / 2; i++) {
+            const u64 h = f2::mul(f2::add(x.get2(i), f2::splat(-mean[r])), rr);
+            dx.set2(i, f2::mul(f2::fma(h, m2, f2::fma(dy.get2(i), w[k][i], m1)), rr));
+          }
+          store_vec<T, G, true>((T*)a.y + (row + r) * a.ys, cols, t, k, dx);
+        }
+      }
+    }
+    st = st == ST - 1 ? 0 : st + 1;
+  }
+  if (!a.part) return;
+  float* pw = a.part + (int64_t)blockIdx.x * a.cols;
+  float* pb = pw + (int64_t)gridDim.x * a.cols;
+#pragma unroll
+  for (int k = 0; k < NV; k++) {
+    const int c = col<G, VEC, true>(k, 0, t);
+    if (c < cols) {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; i++) {
+        float p, q;
+        f2::unpack(gw[k][i], p, q);
+        pw[c + 2 * i] = p;
+        pw[c + 2 * i + 1] = q;
+        f2::unpack(gb[k][i], p, q);
+        pb[c + 2 * i] = p;
+        pb[c + 2 * i + 1] = q;
+      }
+    }
+  }
+}
+
 // dw and db from the partial rows: 32 columns a CTA, 32 warps over the rows, then the warps' sums
 // in their order.  blockIdx.y: 0 dw, 1 db.
 template <typename W>
@@ -350,47 +703,78 @@ void fwd_go(const NormArgs& a, bool al, cudaStream_t st) {
   if (al) norm_fwd_kernel<T, G, NV, true><<<grid, threads, 0, st>>>(a);
   else norm_fwd_kernel<T, G, NV, false><<<grid, threads, 0, st>>>(a);
 }
-template <typename T, int G, int NV>
+template <typename T, int G, int NV, int R>
 void bwd_go(const NormArgs& a, bool al, unsigned grid, int64_t per, cudaStream_t st) {
   const int threads = G == 32 ? 32 * WARP_ROWS : G;
-  if (al) norm_bwd_kernel<T, G, NV, true><<<grid, threads, 0, st>>>(a, per);
-  else norm_bwd_kernel<T, G, NV, false><<<grid, threads, 0, st>>>(a, per);
+  if (al) norm_bwd_kernel<T, G, NV, R, true><<<grid, threads, 0, st>>>(a, per);
+  else norm_bwd_kernel<T, G, NV, R, false><<<grid, threads, 0, st>>>(a, per);
+}
+
+template <typename T, int G, int R, int ST>
+cudaError_t fwd_stream(const NormArgs& a, cudaStream_t st) {
+  constexpr int bytes = ST * R * 2 * G * 16;
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(norm_fwd_stream_kernel<T, G, 2, R, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (ready != cudaSuccess) return ready;
+  norm_fwd_stream_kernel<T, G, 2, R, ST><<<(unsigned)std::min<int64_t>(152 * 512 / G, (a.rows + R - 1) / R), G, bytes, st>>>(a);
+  return cudaSuccess;
+}
+template <typename T, int G, int R, int ST>
+cudaError_t bwd_stream(const NormArgs& a, unsigned grid, int64_t per, cudaStream_t st) {
+  constexpr int bytes = ST * R * 2 * G * 32;
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(norm_bwd_stream_kernel<T, G, 2, R, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (ready != cudaSuccess) return ready;
+  norm_bwd_stream_kernel<T, G, 2, R, ST><<<grid, G, bytes, st>>>(a, per);
+  return cudaSuccess;
 }
 
 template <typename T>
 void fwd(const NormArgs& a, cudaStream_t st) {
   constexpr int VEC = Elem<T>::VEC;
-  const bool al = al16(a.x) && al16(a.y) && a.xs % VEC == 0 && a.ys % VEC == 0 && al16(a.w) && al16(a.b);
+  const bool al = a.cols % VEC == 0 && al16(a.x) && al16(a.y) && a.xs % VEC == 0 && a.ys % VEC == 0 && al16(a.w) && al16(a.b);
   const int64_t nv = (a.cols + VEC - 1) / VEC;
+  if (al && nv > 128 && nv <= 1024 && a.rows >= 1216) {
+    if (nv <= 256) fwd_stream<T, 128, 2, 2>(a, st);
+    else if (nv <= 512) fwd_stream<T, 256, 2, 2>(a, st);
+    else fwd_stream<T, 512, 2, 2>(a, st);
+    return;
+  }
   if (nv <= 32) fwd_go<T, 32, 1>(a, al, st);
   else if (nv <= 128) fwd_go<T, 32, 4>(a, al, st);
   else if (nv <= 256) fwd_go<T, 128, 2>(a, al, st);
-  else if (nv <= 512) fwd_go<T, 256, 2>(a, al, st);
-  else if (nv <= 1024) fwd_go<T, 512, 2>(a, al, st);
-  else if (nv <= 2048) fwd_go<T, 1024, 2>(a, al, st);
+  else if (nv <= 512) fwd_go<T, 128, 4>(a, al, st);
+  else if (nv <= 1024) fwd_go<T, 256, 4>(a, al, st);
+  else if (nv <= 1536) fwd_go<T, 256, 6>(a, al, st);
+  else if (nv <= 2048) fwd_go<T, 256, 8>(a, al, st);
   else norm_fwd_wide_kernel<T><<<(unsigned)a.rows, 1024, 0, st>>>(a);
 }
 template <typename T>
 void bwd(const NormArgs& a, unsigned grid, int64_t per, cudaStream_t st) {
   constexpr int VEC = Elem<T>::VEC;
-  const bool al = al16(a.x) && al16(a.y) && al16(a.dy) && a.xs % VEC == 0 && a.ys % VEC == 0 && a.dys % VEC == 0 && al16(a.w);
+  const bool al = a.cols % VEC == 0 && al16(a.x) && al16(a.y) && al16(a.dy) && a.xs % VEC == 0 && a.ys % VEC == 0 && a.dys % VEC == 0 && al16(a.w);
   const int64_t nv = (a.cols + VEC - 1) / VEC;
-  if (nv <= 32) bwd_go<T, 32, 1>(a, al, grid, per, st);
-  else if (nv <= 128) bwd_go<T, 32, 4>(a, al, grid, per, st);
-  else if (nv <= 256) bwd_go<T, 128, 2>(a, al, grid, per, st);
-  else if (nv <= 512) bwd_go<T, 256, 2>(a, al, grid, per, st);
-  else if (nv <= 1024) bwd_go<T, 512, 2>(a, al, grid, per, st);
-  else if (nv <= 2048) bwd_go<T, 1024, 2>(a, al, grid, per, st);
+  if (al && nv > 128 && nv <= 1024) {
+    if (nv <= 256) bwd_stream<T, 128, 2, 2>(a, grid, per, st);
+    else if (nv <= 512) bwd_stream<T, 256, 2, 2>(a, grid, per, st);
+    else bwd_stream<T, 512, 2, 2>(a, grid, per, st);
+    return;
+  }
+  if (nv <= 32) bwd_go<T, 32, 1, 2>(a, al, grid, per, st);
+  else if (nv <= 128) bwd_go<T, 32, 4, 1>(a, al, grid, per, st);
+  else if (nv <= 256) bwd_go<T, 128, 2, 2>(a, al, grid, per, st);
+  else if (nv <= 512) bwd_go<T, 256, 2, 2>(a, al, grid, per, st);
+  else if (nv <= 1024) bwd_go<T, 512, 2, 1>(a, al, grid, per, st);
+  else if (nv <= 1536) bwd_go<T, 512, 3, 1>(a, al, grid, per, st);
+  else if (nv <= 2048) bwd_go<T, 512, 4, 1>(a, al, grid, per, st);
   else norm_bwd_wide_kernel<T><<<grid, 1024, 0, st>>>(a, per);
 }
 
 int64_t rows_per(int64_t rows, int64_t cols) {
-  // about two resident CTAs (eight of the warp variants) on each of 152 SMs; a run has at least
-  // as many rows as the CTA has warps that share them
-  const bool narrow = cols <= 1024;
-  const int64_t want = narrow ? 152 * 8 : 152 * 2;
-  const int64_t per = (rows + want - 1) / want;
-  return narrow ? (per + WARP_ROWS - 1) / WARP_ROWS * WARP_ROWS : per < 1 ? 1 : per;
+  // about two resident CTAs (eight of the warp variants) on each of 152 SMs; a run has a multiple
+  // of the rows that a CTA takes at a time
+  const int64_t want = cols <= 1024 ? 152 * 8 : 152 * 2, by = cols <= 1024 ? 8 : 2;
+  return ((rows + want - 1) / want + by - 1) / by * by;
 }
 
 }  // namespace

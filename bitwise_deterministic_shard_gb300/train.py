@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+import struct
 
 import torch
 
@@ -35,20 +36,24 @@ class _Hyper(C.Structure):
                 ("weight_decay", C.c_double), ("step", C.c_int64)]
 
 
+# The same structures as bytes: one pack is several times cheaper than filling a ctypes structure, and
+# the smallest calls here take no longer on the GPU than their arguments on the host.
+_TENSOR, _DESC, _MATRIX, _HYPER = (struct.Struct(f) for f in ("Pi8q", "Pi8q" * 3 + "iffPPPP", "Pi3q", "5dq"))
+
+
 _NAMES = ("dta_forward", "dta_backward", "dln_forward", "dln_backward", "dow_adamw")
 
 
 def declare(L):
     """Argument types of the training entry points of a loaded library."""
-    P, T, M, I = C.c_void_p, C.POINTER(_Tensor), C.POINTER(_Matrix), C.c_int
-    D = C.POINTER(_Train)
-    L.dta_workspace_bytes.argtypes, L.dta_workspace_bytes.restype = [D, I], C.c_size_t
-    L.dta_forward.argtypes = [D, T, P, P, C.c_size_t, P]
-    L.dta_backward.argtypes = [D, T, P, T, T, T, T, P, C.c_size_t, P]
-    L.dln_forward.argtypes = [M, P, P, I, C.c_float, M, P, P, P]
-    L.dln_workspace_bytes.argtypes, L.dln_workspace_bytes.restype = [C.c_int64, C.c_int64], C.c_size_t
-    L.dln_backward.argtypes = [M, M, P, I, P, P, M, P, P, P, C.c_size_t, P]
-    L.dow_adamw.argtypes = [C.POINTER(_Param), I, I, I, P, P, P, P, C.c_int64, C.POINTER(_Hyper), P, P]
+    P, I, N = C.c_void_p, C.c_int, C.c_size_t
+    L.dta_workspace_bytes.argtypes, L.dta_workspace_bytes.restype = [P, I], N
+    L.dta_forward.argtypes = [P, P, P, P, N, P]
+    L.dta_backward.argtypes = [P, P, P, P, P, P, P, P, N, P]
+    L.dln_forward.argtypes = [P, P, P, I, C.c_float, P, P, P, P]
+    L.dln_workspace_bytes.argtypes, L.dln_workspace_bytes.restype = [C.c_int64, C.c_int64], N
+    L.dln_backward.argtypes = [P, P, P, I, P, P, P, P, P, P, N, P]
+    L.dow_adamw.argtypes = [P, I, I, I, P, P, P, P, C.c_int64, P, P, P]
     for f in _NAMES:
         getattr(L, f).restype = C.c_int
 
@@ -60,12 +65,25 @@ def _code(t, name, allowed=_CODES):
     return c
 
 
-def _same_device(device, **ts):
-    for name, t in ts.items():
-        if t is not None:
-            _da._cuda(t, name)
-            if t.device != device:
-                raise DetAttnError(f"{name} is on {t.device}, expected {device}")
+def _on(index, name, t):
+    """t on the device of that index (as torch.Tensor.get_device gives it)."""
+    _da._cuda(t, name)
+    if t.get_device() != index:
+        raise DetAttnError(f"{name} is on another device")
+
+
+def _stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _room(need, ws, device):
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    return ws
 
 
 # ---------------------------------------------------------------- attention
@@ -73,86 +91,79 @@ def _same_device(device, **ts):
 _HALF = {torch.bfloat16: 1, torch.float16: 2}
 
 
+def _fits(t):
+    """Whether the kernels' tensor maps can describe t: its last dimension contiguous, its start on 16 bytes, its
+    other strides multiples of 8 and not zero (where the dimension is longer than 1)."""
+    s0, s1, s2, s3 = t.stride()
+    if t.data_ptr() & 15 or s3 != 1:
+        return False
+    if s0 > 0 and s1 > 0 and s2 > 0 and not (s0 | s1 | s2) & 7:
+        return True
+    return all(n <= 1 or (x > 0 and x % 8 == 0) for n, x in zip(t.shape, (s0, s1, s2)))
+
+
 def _ready(t):
-    """t in a layout that the kernels' tensor maps can describe: itself, or a contiguous copy (a
-    last dimension that is not contiguous, broadcast dimensions, strides or starts off 16 bytes)."""
-    st, sh = t.stride(), t.shape
-    if (st[3] == 1 and t.data_ptr() % 16 == 0
-            and all(n <= 1 or (x > 0 and x % 8 == 0) for n, x in zip(sh[:3], st[:3]))):
-        return t
-    return t.clone(memory_format=torch.contiguous_format)
+    """t itself where it fits, else a contiguous copy."""
+    return t if _fits(t) else t.detach().clone(memory_format=torch.contiguous_format)
 
 
-def _view4(t, name, code) -> _Tensor:
-    x = _Tensor()
-    x.ptr, x.dtype = t.data_ptr(), code
-    x.B, x.H, x.S, x.D = t.shape
-    x.stride[:] = t.stride()
-    return x
+def _view(t, code):
+    return _TENSOR.pack(t.data_ptr(), code, *t.shape, *t.stride())
+
+
+def _option(t, name, dtype, shape, index):
+    if t is None:
+        return None
+    _on(index, name, t)
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise DetAttnError(f"{name} must be {dtype} {list(shape)}")
+    return t if t.is_contiguous() else t.contiguous()
 
 
 class _Attention:
     """Checked arguments of one attention call; keeps the tensors alive while it lives."""
+    __slots__ = ("desc", "keep", "code", "index", "device", "lse_shape")
 
     def __init__(self, Q, K, V, causal, scale, softcap, slopes, docs, prefix, status):
-        for t, name in ((Q, "Q"), (K, "K"), (V, "V")):
-            _da._cuda(t, name)
-            if t.dim() != 4:
-                raise DetAttnError(f"{name} must be [B, H, S, D]")
-        code = _code(Q, "Q", _HALF)
+        _da._cuda(Q, "Q")
+        index = self.index = Q.get_device()
+        _on(index, "K", K)
+        _on(index, "V", V)
+        if Q.dim() != 4 or K.dim() != 4 or V.dim() != 4:
+            raise DetAttnError("Q, K and V must be [B, H, S, D]")
+        code = self.code = _code(Q, "Q", _HALF)
         if K.dtype != Q.dtype or V.dtype != Q.dtype:
             raise DetAttnError("Q, K and V must share one dtype (bf16 or f16)")
-        self.device, dev = Q.device, Q.device
-        _same_device(dev, K=K, V=V, slopes=slopes, docs=docs, prefix=prefix, status=status)
-        self.B, self.Hq, self.Sq, self.D = Q.shape
-        _, self.Hkv, self.Skv, _ = K.shape
-        if slopes is not None and (slopes.dtype != torch.float32 or tuple(slopes.shape) != (self.Hq,)):
-            raise DetAttnError(f"slopes must be f32 [{self.Hq}]")
+        self.device = Q.device
+        B, Hq, Sq, _ = Q.shape
+        self.lse_shape = (B, Hq, Sq)
         if slopes is not None and slopes.requires_grad:
             raise DetAttnError("slopes have no gradient: pass them detached")
-        if docs is not None and (docs.dtype != torch.int32 or tuple(docs.shape) != (self.B, self.Skv)):
-            raise DetAttnError(f"docs must be int32 [{self.B}, {self.Skv}]")
-        if prefix is not None and (prefix.dtype != torch.int32 or tuple(prefix.shape) != (self.B,)):
-            raise DetAttnError(f"prefix must be int32 [{self.B}]")
-        slopes, docs, prefix = (None if t is None else t.contiguous() for t in (slopes, docs, prefix))
-        q, k, v = (_ready(t.detach()) for t in (Q, K, V))
-        self.keep = [q, k, v, slopes, docs, prefix]
-        self.code = code
-        d = self.desc = _Train()
-        d.q, d.k, d.v = _view4(q, "Q", code), _view4(k, "K", code), _view4(v, "V", code)
-        d.causal = 1 if causal else 0
-        d.scale = math.nan if scale is None else float(scale)
-        d.softcap = float(softcap)
-        d.slopes, d.docs, d.prefix = _addr(slopes), _addr(docs), _addr(prefix)
-        d.dev_status = None if status is None else _da._sptr(status).value
-
-    def workspace(self, backward, ws):
-        need = int(_da.lib().dta_workspace_bytes(C.byref(self.desc), backward))
-        if ws is None or ws.numel() * ws.element_size() < need:
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        return ws, need
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+        slopes = _option(slopes, "slopes", torch.float32, (Hq,), index)
+        docs = _option(docs, "docs", torch.int32, (B, K.shape[2]), index)
+        prefix = _option(prefix, "prefix", torch.int32, (B,), index)
+        q, k, v = _ready(Q), _ready(K), _ready(V)
+        self.keep = (q, k, v, slopes, docs, prefix)
+        if status is not None:
+            _on(index, "status", status)
+            status = _da._sptr(status).value
+        self.desc = _DESC.pack(q.data_ptr(), code, *q.shape, *q.stride(), k.data_ptr(), code, *k.shape, *k.stride(),
+                               v.data_ptr(), code, *v.shape, *v.stride(), 1 if causal else 0,
+                               math.nan if scale is None else scale, softcap, _addr(slopes) or 0, _addr(docs) or 0,
+                               _addr(prefix) or 0, status or 0)
 
 
 def _like(t):
     """An uninitialised tensor of t's layout where that is dense and fit for the kernels, else contiguous."""
-    o = torch.empty_like(t)
-    return o if _ready_layout(o) else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
-def _ready_layout(t):
-    return t.stride(3) == 1 and all(n <= 1 or (x > 0 and x % 8 == 0) for n, x in zip(t.shape[:3], t.stride()[:3]))
+    o = torch.empty_like(t, requires_grad=False)
+    return o if _fits(o) else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _given(out, like, name):
     if out is None:
         return _like(like)
     _da._cuda(out, name)
-    if (out.dtype != like.dtype or out.shape != like.shape or out.device != like.device or not _ready_layout(out)
-            or out.data_ptr() % 16):
+    if out.dtype != like.dtype or out.shape != like.shape or out.device != like.device or not _fits(out):
         raise DetAttnError(f"{name} must be {like.dtype} {tuple(like.shape)} on {like.device}, 16-byte aligned, "
                            "its last dimension contiguous and its other strides multiples of 8")
     return out
@@ -169,14 +180,15 @@ def attention_forward(Q, K, V, causal=False, scale=None, softcap=0.0, slopes=Non
     A query sees key j when not causal, or j <= its position, or j < prefix[b] (int32 [B], with causal
     only), and, with docs (int32 [B, Skv]), when both tokens have the same id >= 0.  A query that
     sees nothing gets zeros and lse = -inf.  Few queries (Sq * Hq / Hkv <= 128) read the keys once per
-    key head, split over the GPU.  out takes Q's layout."""
+    key head, split over the GPU.  out takes Q's layout.  Tensors that the kernels cannot address (a last
+    dimension that is not contiguous, strides or starts off 16 bytes, broadcast dimensions) are copied."""
     A = _Attention(Q, K, V, causal, scale, softcap, slopes, docs, prefix, status)
-    out = _given(out, Q.detach(), "out")
-    lse = torch.empty((A.B, A.Hq, A.Sq), dtype=torch.float32, device=A.device) if need_lse else None
-    ws, need = A.workspace(0, workspace)
-    o = _view4(out, "out", A.code)
-    _da._check(_da.lib().dta_forward(C.byref(A.desc), C.byref(o), _addr(lse), _addr(ws), need, _da._stream()),
-               "attention_forward")
+    out = _given(out, Q, "out")
+    lse = torch.empty(A.lse_shape, dtype=torch.float32, device=A.device) if need_lse else None
+    L = _da.lib()
+    need = L.dta_workspace_bytes(A.desc, 0)
+    ws = _room(need, workspace, A.device)
+    _da._check(L.dta_forward(A.desc, _view(out, A.code), _addr(lse), _addr(ws), need, _stream(A.index)), "attention_forward")
     return out, lse
 
 
@@ -186,18 +198,19 @@ def attention_backward(Q, K, V, out, lse, grad, causal=False, scale=None, softca
     The gradient of a shared key head is the sum over its query heads, formed in binary32."""
     A = _Attention(Q, K, V, causal, scale, softcap, slopes, docs, prefix, status)
     for t, name in ((out, "out"), (grad, "grad")):
-        _da._cuda(t, name)
-        if t.dtype != Q.dtype or t.shape != Q.shape or t.device != Q.device:
-            raise DetAttnError(f"{name} must be {Q.dtype} {tuple(Q.shape)} on {Q.device}")
-    _da._cuda(lse, "lse")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (A.B, A.Hq, A.Sq) or lse.device != A.device:
-        raise DetAttnError(f"lse must be f32 {(A.B, A.Hq, A.Sq)} on {A.device}")
-    out, grad, lse = _ready(out.detach()), _ready(grad.detach()), lse.contiguous()
-    dq, dk, dv = (_like(t.detach()) for t in (Q, K, V))
-    ws, need = A.workspace(1, workspace)
-    v = [_view4(t, "", A.code) for t in (out, grad, dq, dk, dv)]
-    _da._check(_da.lib().dta_backward(C.byref(A.desc), C.byref(v[0]), _addr(lse), C.byref(v[1]), C.byref(v[2]), C.byref(v[3]),
-                                      C.byref(v[4]), _addr(ws), need, _da._stream()), "attention_backward")
+        _on(A.index, name, t)
+        if t.dtype != Q.dtype or t.shape != Q.shape:
+            raise DetAttnError(f"{name} must be {Q.dtype} {tuple(Q.shape)}")
+    _on(A.index, "lse", lse)
+    if lse.dtype != torch.float32 or lse.shape != A.lse_shape:
+        raise DetAttnError(f"lse must be f32 {A.lse_shape}")
+    out, grad, lse = _ready(out), _ready(grad), lse.contiguous()
+    dq, dk, dv = _like(Q), _like(K), _like(V)
+    L, c = _da.lib(), A.code
+    need = L.dta_workspace_bytes(A.desc, 1)
+    ws = _room(need, workspace, A.device)
+    _da._check(L.dta_backward(A.desc, _view(out, c), lse.data_ptr(), _view(grad, c), _view(dq, c), _view(dk, c), _view(dv, c),
+                              _addr(ws), need, _stream(A.index)), "attention_backward")
     return dq, dk, dv
 
 
@@ -227,97 +240,93 @@ def attention(Q, K, V, causal=False, scale=None, softcap=0.0, slopes=None, docs=
 
 # ---------------------------------------------------------------- layer norm
 
-def _rows(t, name, code):
-    """t [..., cols] as a matrix of rows: itself where one row stride describes it, else a contiguous copy."""
-    cols = t.shape[-1]
+def _rows(t, code, cols):
+    """t [..., cols] as the bytes of a matrix of rows, and t: itself where one row stride describes it, else a
+    contiguous copy."""
+    n = t.numel() // cols
     if t.is_contiguous():
-        n = t.numel() // cols if cols else 0
-        stride = cols
-    else:
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < cols):
-            t = t.contiguous() if t.dim() == 1 or t.stride(-1) != 1 or not _even(t) else t
-        n = t.numel() // cols if cols else 0
-        stride = t.stride(-2) if t.dim() > 1 and n > 1 and t.shape[-2] > 1 else cols
-        if t.is_contiguous():
-            stride = cols
-    m = _Matrix()
-    m.ptr, m.dtype, m.rows, m.cols, m.row_stride = t.data_ptr(), code, n, cols, stride
-    return m, t
-
-
-def _even(t):
-    """Whether the leading dimensions of t are one run of rows at the stride of its last but one."""
-    want = t.stride(-2)
-    if want < t.shape[-1]:
-        return False
-    for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] > 1 and t.stride(i) != want:
-            return False
-        want *= t.shape[i]
-    return True
+        return _MATRIX.pack(t.data_ptr(), code, n, cols, cols), t
+    if t.dim() > 1 and (cols == 1 or t.stride(-1) == 1):
+        # the leading dimensions as one run of rows: strides of those longer than 1, from the last on
+        run = want = None
+        for i in range(t.dim() - 2, -1, -1):
+            if t.shape[i] > 1:
+                if run is None:
+                    run = want = t.stride(i)
+                if t.stride(i) != want:
+                    run = -1
+                    break
+                want *= t.shape[i]
+        if run is None or run >= cols:
+            return _MATRIX.pack(t.data_ptr(), code, n, cols, cols if run is None else run), t
+    t = t.detach().contiguous()
+    return _MATRIX.pack(t.data_ptr(), code, n, cols, cols), t
 
 
 def _weights(x, weight, bias):
+    _da._cuda(x, "x")
     cols = x.shape[-1] if x.dim() else 0
     if cols < 1:
         raise DetAttnError("x must be [..., cols] with at least one column")
-    code = _code(x, "x")
+    code, index = _code(x, "x"), x.get_device()
     wt = None
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is None:
             continue
-        if tuple(t.shape) != (cols,) or t.dtype not in (x.dtype, torch.float32):
+        _on(index, name, t)
+        if t.dim() != 1 or t.shape[0] != cols or (t.dtype != x.dtype and t.dtype != torch.float32):
             raise DetAttnError(f"{name} must be [{cols}] of x's dtype or f32")
         if wt is not None and t.dtype != wt:
             raise DetAttnError("weight and bias must share one dtype")
         wt = t.dtype
-    _same_device(x.device, weight=weight, bias=bias)
-    return cols, code, wt or x.dtype
+    return cols, code, wt or x.dtype, index
+
+
+def _packed(t):
+    return t if t is None or t.is_contiguous() else t.detach().contiguous()
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps=1e-5):
     """Layer norm over the last dimension: (y like x, mean f32, rstd f32, one per row).
     x [..., cols] f32, bf16 or f16; weight and bias [cols] of x's dtype or f32, or None."""
-    _da._cuda(x, "x")
-    cols, code, wt = _weights(x, weight, bias)
-    X, x = _rows(x.detach(), "x", code)
-    weight, bias = (None if t is None else t.detach().contiguous() for t in (weight, bias))
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    Y, _ = _rows(y, "y", code)
-    mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device).unbind(0)
-    _da._check(_da.lib().dln_forward(C.byref(X), _addr(weight), _addr(bias), _CODES[wt], eps, C.byref(Y), _addr(mean),
-                                     _addr(rstd), _da._stream()), "layer_norm_forward")
+    cols, code, wt, index = _weights(x, weight, bias)
+    X, x = _rows(x, code, cols)
+    weight, bias = _packed(weight), _packed(bias)
+    shape, dev = x.shape, x.device
+    y = torch.empty(shape, dtype=x.dtype, device=dev)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    Y = _MATRIX.pack(y.data_ptr(), code, mean.numel(), cols, cols)
+    _da._check(_da.lib().dln_forward(X, _addr(weight), _addr(bias), _CODES[wt], eps, Y, mean.data_ptr(), rstd.data_ptr(),
+                                     _stream(index)), "layer_norm_forward")
     return y, mean, rstd
 
 
 def layer_norm_backward(grad, x, weight, mean, rstd, need_weight=True, need_bias=True, workspace=None):
     """(dx, dweight, dbias) from the upstream gradient and layer_norm_forward's mean and rstd; the
     weight gradients are None where not needed, and of weight's dtype (x's without a weight)."""
-    _da._cuda(grad, "grad")
-    _da._cuda(x, "x")
-    cols, code, wt = _weights(x, weight, None)
+    cols, code, wt, index = _weights(x, weight, None)
+    _on(index, "grad", grad)
     if grad.shape != x.shape or grad.dtype != x.dtype:
         raise DetAttnError("grad must have x's shape and dtype")
     rows = x.numel() // cols
     for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _da._cuda(t, name)
+        _on(index, name, t)
         if t.dtype != torch.float32 or t.numel() != rows or not t.is_contiguous():
             raise DetAttnError(f"{name} must be contiguous f32 with one entry per row")
-    _same_device(x.device, grad=grad, mean=mean, rstd=rstd)
-    X, x = _rows(x.detach(), "x", code)
-    G, grad = _rows(grad.detach(), "grad", code)
-    weight = None if weight is None else weight.detach().contiguous()
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    DX, _ = _rows(dx, "dx", code)
-    dw = torch.empty(cols, dtype=wt, device=x.device) if need_weight else None
-    db = torch.empty(cols, dtype=wt, device=x.device) if need_bias else None
+    X, x = _rows(x, code, cols)
+    G, grad = _rows(grad, code, cols)
+    weight = _packed(weight)
+    dev = x.device
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    DX = _MATRIX.pack(dx.data_ptr(), code, rows, cols, cols)
+    dw = torch.empty(cols, dtype=wt, device=dev) if need_weight else None
+    db = torch.empty(cols, dtype=wt, device=dev) if need_bias else None
     L = _da.lib()
-    need = int(L.dln_workspace_bytes(rows, cols)) if need_weight or need_bias else 0
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _da._check(L.dln_backward(C.byref(G), C.byref(X), _addr(weight), _CODES[wt], _addr(mean), _addr(rstd), C.byref(DX),
-                              _addr(dw), _addr(db), _addr(workspace) if need else None, need, _da._stream()),
-               "layer_norm_backward")
+    need = L.dln_workspace_bytes(rows, cols) if need_weight or need_bias else 0
+    ws = _room(need, workspace, dev)
+    _da._check(L.dln_backward(G, X, _addr(weight), _CODES[wt], mean.data_ptr(), rstd.data_ptr(), DX, _addr(dw), _addr(db),
+                              _addr(ws), need, _stream(index)), "layer_norm_backward")
     return dx, dw, db
 
 
@@ -370,39 +379,38 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
         raise DetAttnError("params and grads must have the same length")
     if not params:
         return
-    dt, dev = params[0].dtype, params[0].device
+    dt, index = params[0].dtype, params[0].get_device()
     code = _code(params[0], "params")
-    n = len(params)
-    table = (_Param * n)()
-    at = k = 0
+    _da._cuda(params[0], "params")
+    table, at = [], 0
     for p, g in zip(params, grads):
-        if p.dtype != dt or p.device != dev or not p.is_contiguous():
+        if p.dtype != dt or p.get_device() != index or not p.is_contiguous():
             raise DetAttnError("params must be contiguous tensors of one dtype on one device")
         m = p.numel()
         if g is not None:
-            if g.dtype != dt or g.device != dev or g.numel() != m or not g.is_contiguous():
+            if g.dtype != dt or g.numel() != m or g.get_device() != index or not g.is_contiguous():
                 raise DetAttnError("grads must be contiguous, of their params' dtype, device and size")
-            e = table[k]
-            e.param, e.grad, e.numel, e.state = p.data_ptr(), g.data_ptr(), m, at
-            k += 1
-        at += -(-m // STATE_BLOCK) * STATE_BLOCK
-    _da._cuda(params[0], "params")
+            table += (p.data_ptr(), g.data_ptr(), m, at)
+        at += (m + STATE_BLOCK - 1) // STATE_BLOCK * STATE_BLOCK
     bits = 8 if exp_avg.dtype == torch.float8_e4m3fn else 32
     st = torch.float8_e4m3fn if bits == 8 else torch.float32
     for t, name, want, length in ((exp_avg, "exp_avg", st, at), (exp_avg_sq, "exp_avg_sq", st, at),
                                   (exp_avg_scale, "exp_avg_scale", torch.float32, at // STATE_BLOCK),
                                   (exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, at // STATE_BLOCK)):
-        if name.endswith("scale") and bits == 32:
+        if bits == 32 and name.endswith("scale"):
             if t is not None:
                 raise DetAttnError("scales go with 8-bit states")
             continue
-        if t is None or t.dtype != want or t.numel() != length or not t.is_contiguous() or t.device != dev:
-            raise DetAttnError(f"{name} must be contiguous {want} [{length}] on {dev}")
-    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.device != dev):
-        raise DetAttnError(f"grad_scale must be one f32 element on {dev}")
-    h = _Hyper(lr, betas[0], betas[1], eps, weight_decay, int(step))
-    _da._check(_da.lib().dow_adamw(table, k, code, bits, _addr(exp_avg), _addr(exp_avg_sq), _addr(exp_avg_scale),
-                                   _addr(exp_avg_sq_scale), at, C.byref(h), _addr(grad_scale), _da._stream()), "adamw_step")
+        if t is None or t.dtype != want or t.numel() != length or not t.is_contiguous() or t.get_device() != index:
+            raise DetAttnError(f"{name} must be contiguous {want} [{length}] on the params' device")
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
+                                   or grad_scale.get_device() != index):
+        raise DetAttnError("grad_scale must be one f32 element on the params' device")
+    k = len(table) // 4
+    _da._check(_da.lib().dow_adamw(struct.pack(f"{4 * k}Q", *table), k, code, bits, exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
+                                   _addr(exp_avg_scale), _addr(exp_avg_sq_scale), at,
+                                   _HYPER.pack(lr, betas[0], betas[1], eps, weight_decay, int(step)), _addr(grad_scale),
+                                   _stream(index)), "adamw_step")
 
 
 class AdamW:
