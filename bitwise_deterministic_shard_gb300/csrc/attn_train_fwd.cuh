@@ -24,6 +24,7 @@
 #pragma once
 #include "../../include/detattn.h"
 #include "attn_train.h"
+#include "pack2.cuh"
 #include "tc5_tile.cuh"
 
 namespace detattn {
@@ -32,8 +33,53 @@ namespace ta {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float tanh_any(float x) {   // 1 - 2 / (1 + e^2x): error 2^-22 absolute
+using f2::u64;
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// tanh.  Any argument: 1 - 2 / (1 + e^2x), two operations of the special function unit, 2^-22 absolute.  On
+// [-1, 1], where the scores of a capped model nearly always are: x P(x^2), P of degree 5 fitted for the least
+// greatest error (least squares with weights moved toward the largest errors), 3.1e-7 absolute with
+// binary32 steps, on the packed multiplier.  The special function unit would otherwise bound the kernel:
+// three of its operations a score instead of one (forward 169 -> see above).
+__device__ __forceinline__ float tanh_any(float x) {
   return __fmaf_rn(-2.f, tc5::rcp(1.f + tc5::ex2(x * (2.f * LOG2E))), 1.f);
+}
+__device__ __forceinline__ u64 tanh_small2(u64 x) {
+  const u64 z = f2::mul(x, x);
+  u64 p = f2::fma(f2::splat(-0x1.742c6ap-9f), z, f2::splat(0x1.0803b2p-6f));
+  p = f2::fma(p, z, f2::splat(-0x1.a191cep-5f));
+  p = f2::fma(p, z, f2::splat(0x1.0f6ea4p-3f));
+  p = f2::fma(p, z, f2::splat(-0x1.553ce0p-2f));
+  p = f2::fma(p, z, f2::splat(0x1.ffff96p-1f));
+  return f2::mul(x, p);
+}
+// v <- tanh(k v) for N scores of each lane; the warp decides which form it takes
+template <int N>
+__device__ __forceinline__ void tanh_row(float* v, float k) {
+  float m[2] = {0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < N; c += 4) {
+    m[0] = max3_abs(m[0], v[c], v[c + 1]);
+    m[1] = max3_abs(m[1], v[c + 2], v[c + 3]);
+  }
+  if (__any_sync(0xffffffffu, !(fmaxf(m[0], m[1]) * fabsf(k) <= 1.f))) {
+#pragma unroll
+    for (int c = 0; c < N; c++) v[c] = tanh_any(v[c] * k);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 2)
+      f2::unpack(tanh_small2(f2::mul(f2::pack(v[c], v[c + 1]), f2::splat(k))), v[c], v[c + 1]);
+  }
 }
 
 // Which key tiles a tile of queries needs.  A whole warp calls it.
@@ -61,6 +107,11 @@ __device__ __forceinline__ int2 key_range(const TaArgs& a, int b, int first_pos,
 
 }  // namespace ta
 
+// Two softmax groups and a control group (copies, products, two idle warps).  setmaxnreg moves the control group's
+// registers to the softmax threads, which hold a row's 128 scores: 384 x 168 at launch = 128 x 56 + 256 x 224.  The
+// control group never takes its registers back: an idle warp's request would be met before the softmax groups'.
+constexpr int TA_FWD_THREADS = 384;
+
 template <int DP>
 struct TaFwdSmem {
   static constexpr int TILE = DP / 64 * tc5::PANEL;
@@ -70,7 +121,7 @@ struct TaFwdSmem {
 };
 
 template <int DP, bool BF>
-__global__ void __launch_bounds__(320, 1) ta_fwd_kernel(const __grid_constant__ TaArgs a) {
+__global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_constant__ TaArgs a) {
   using namespace tc5;
   using namespace ta;
   using L = TaFwdSmem<DP>;
@@ -172,6 +223,8 @@ __global__ void __launch_bounds__(320, 1) ta_fwd_kernel(const __grid_constant__ 
   }
   const int ntile = hi - lo;
 
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
   if (warp == 8) {
     // ---- copies: queries once, then keys and values in the order in which the products take them ----
     if (lane == 0 && ntile > 0) {
@@ -289,8 +342,10 @@ __global__ void __launch_bounds__(320, 1) ta_fwd_kernel(const __grid_constant__ 
         mbar_drain(&gone, 0);
       }
     }
+  }
   } else {
     // ---- softmax ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
     const int i = wg;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;      // TMEM lane 32 (w % 4) in bits 16 and up
     const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * DP;
@@ -327,7 +382,7 @@ __global__ void __launch_bounds__(320, 1) ta_fwd_kernel(const __grid_constant__ 
       }
       if (cap) {
 #pragma unroll
-        for (int c = 0; c < 128; c++) v[c] = tanh_any(v[c] * capx);
+        for (int c = 0; c < 4; c++) tanh_row<32>(v + 32 * c, capx);
       }
       if (biased) {
         const float d0 = (float)(pos - j0);
@@ -349,11 +404,11 @@ __global__ void __launch_bounds__(320, 1) ta_fwd_kernel(const __grid_constant__ 
             if (j0 + c >= lim) v[c] = -INFINITY;
         }
       }
-      float top[4];
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; c++) top[c] = v[c];
+      for (int c = 0; c < 128; c += 8)
 #pragma unroll
-      for (int c = 4; c < 128; c++) top[c & 3] = fmaxf(top[c & 3], v[c]);
+        for (int e = 0; e < 4; e++) top[e] = max3(top[e], v[c + 2 * e], v[c + 2 * e + 1]);
       const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       const bool grow = cnt == 0 || mx > m + lazy;
       if (__any_sync(0xffffffffu, grow)) {
@@ -374,20 +429,27 @@ __global__ void __launch_bounds__(320, 1) ta_fwd_kernel(const __grid_constant__ 
         }
       }
       const float mf = m == -INFINITY ? 0.f : m * f;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      u64 sum[2] = {0, 0};
+      const u64 ff = f2::splat(f), shift = f2::splat(-mf);
 #pragma unroll
       for (int c = 0; c < 4; c++) {
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float x = ex2(__fmaf_rn(v[32 * c + e], f, -mf)), y = ex2(__fmaf_rn(v[32 * c + e + 1], f, -mf));
-          sum[e & 2] += x;
-          sum[(e & 2) + 1] += y;
+          float x, y;
+          f2::unpack(f2::fma(f2::pack(v[32 * c + e], v[32 * c + e + 1]), ff, shift), x, y);
+          x = ex2(x);
+          y = ex2(y);
+          sum[(e >> 1) & 1] = f2::add(sum[(e >> 1) & 1], f2::pack(x, y));
           p[e >> 1] = pack16<BF>(x, y);
         }
         st_x16(ts + 16 * c, p);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      {
+        float x, y;
+        f2::unpack(f2::add(sum[0], sum[1]), x, y);
+        l += x + y;
+      }
       if (padded) {   // padding may hold NaN, and 0 NaN is NaN: its value rows become zeros
         const int d = n - lo, k = alt ? min(ntile, d + 2) + d : 1 + 2 * d;   // this value tile in the order of the copies
         mbar_wait(&kv_full[k % NST], (k / NST) & 1, abort);
@@ -459,6 +521,7 @@ __global__ void __launch_bounds__(320, 1) ta_fwd_kernel(const __grid_constant__ 
         }
       }
     }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");   // as the control group, for what follows
   }
   fence_before();
   __syncthreads();
@@ -516,7 +579,7 @@ cudaError_t ta_forward(const TaArgs& a, cudaStream_t st) {
   if (ready != cudaSuccess) return ready;
   const int HB = a.B * (a.Hq / a.pack);
   const unsigned grid = (unsigned)HB * (a.splits > 0 ? a.splits : (a.qtiles + 1) / 2);
-  ta_fwd_kernel<DP, BF><<<grid, 320, L::BYTES, st>>>(a);
+  ta_fwd_kernel<DP, BF><<<grid, TA_FWD_THREADS, L::BYTES, st>>>(a);
   if (a.splits > 0) {
     const int64_t rows = (int64_t)HB * a.pack * a.Sq;
     ta_join_kernel<DP, BF><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);
