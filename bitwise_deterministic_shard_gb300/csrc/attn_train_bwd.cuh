@@ -50,39 +50,6 @@ __device__ __forceinline__ int2 query_range(const TaArgs& a, int b, int n) {
   return make_int2(q0, max(q0, q1));
 }
 
-// COLS columns of a TMEM accumulator (plus more times a second one, where more is not 0), times k, to
-// 16 bits in a tile's row r (swizzled units)
-template <bool BF, int COLS>
-__device__ __forceinline__ void row_out(uint32_t tile, uint32_t taddr, uint32_t taddr2, int r, int c0, float k, float more,
-                                        bool some) {
-  using namespace tc5;
-#pragma unroll
-  for (int c = c0; c < c0 + COLS; c += 32) {
-    float o[32];
-    if (some) {
-      ld_x32(taddr + c, o);
-      ld_wait();
-      if (taddr2 != taddr) {
-        float x[32];
-        ld_x32(taddr2 + c, x);
-        ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; e++) o[e] = __fmaf_rn(more, x[e], o[e]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 32; e++) o[e] = some ? o[e] * k : 0.f;
-#pragma unroll
-    for (int u = 0; u < 4; u++) {
-      const int unit = ((c & 63) >> 3) + u;
-      const uint32_t at = tile + (c >> 6) * PANEL + r * 128 + ((unit ^ (r & 7)) << 4);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack16<BF>(o[8 * u], o[8 * u + 1])),
-                   "r"(pack16<BF>(o[8 * u + 2], o[8 * u + 3])), "r"(pack16<BF>(o[8 * u + 4], o[8 * u + 5])),
-                   "r"(pack16<BF>(o[8 * u + 6], o[8 * u + 7]))
-                   : "memory");
-    }
-  }
-}
 }  // namespace ta
 
 template <int DP>

@@ -4,9 +4,11 @@
 //   o = sum exp(s - m) v / sum exp(s - m);  lse = m + log sum exp(s - m)
 //
 // One CTA holds two tiles of 128 queries and runs over the key tiles once.  Per query tile a group of
-// four warps owns one query row a thread: it reads its scores from TMEM, keeps the row's running
-// maximum and sum in registers, and writes exp2 of the scores back to TMEM as 16-bit weights,
-// over the scores they came from, where the second product takes them as its A operand.  The two
+// eight warps owns a query row with two threads, each with 64 of the tile's 128 keys: a thread reads its scores
+// from TMEM, keeps the row's maximum and its part of the sum in registers, and writes exp2 of the scores
+// back to TMEM as 16-bit weights, over the scores they came from, where the second product takes them
+// as its A operand.  (Two threads a row: four warps a scheduler hide each other's latencies; with one thread a
+// row two warps issued in 39 % of the cycles.)  The two
 // groups alternate on the tensor cores: while one computes weights, the other's products run.  One
 // warp copies tiles (tensor maps, a ring of key and value tiles), one issues all products:
 //   S_i = Q_i K_n^T (128 x 128 x D),  O_i += P_i V_n (128 x D x 128).
@@ -46,41 +48,58 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   return d;
 }
 
-// tanh.  Any argument: 1 - 2 / (1 + e^2x), two operations of the special function unit, 2^-22 absolute.  On
+// Scores of a row in log2 units: f tanh(k t) with a cap (k = scale / cap, f = cap log2 e), else f t (f = scale log2 e).
+//
+// tanh of any argument: 1 - 2 / (1 + e^2x), two operations of the special function unit, 2^-22 absolute.  On
 // [-1, 1], where the scores of a capped model nearly always are: x P(x^2), P of degree 5 fitted for the least
 // greatest error (least squares with weights moved toward the largest errors), 3.1e-7 absolute with
-// binary32 steps, on the packed multiplier.  The special function unit would otherwise bound the kernel:
-// three of its operations a score instead of one (forward 169 -> see above).
+// binary32 steps, on the packed multiplier; k and f are folded into the coefficients.  The special
+// function unit would otherwise bound the kernel: three of its operations a score instead of one.
 __device__ __forceinline__ float tanh_any(float x) {
   return __fmaf_rn(-2.f, tc5::rcp(1.f + tc5::ex2(x * (2.f * LOG2E))), 1.f);
 }
-__device__ __forceinline__ u64 tanh_small2(u64 x) {
-  const u64 z = f2::mul(x, x);
-  u64 p = f2::fma(f2::splat(-0x1.742c6ap-9f), z, f2::splat(0x1.0803b2p-6f));
-  p = f2::fma(p, z, f2::splat(-0x1.a191cep-5f));
-  p = f2::fma(p, z, f2::splat(0x1.0f6ea4p-3f));
-  p = f2::fma(p, z, f2::splat(-0x1.553ce0p-2f));
-  p = f2::fma(p, z, f2::splat(0x1.ffff96p-1f));
-  return f2::mul(x, p);
-}
-// v <- tanh(k v) for N scores of each lane; the warp decides which form it takes
-template <int N>
-__device__ __forceinline__ void tanh_row(float* v, float k) {
-  float m[2] = {0.f, 0.f};
+struct Cap {
+  float c[6], k, f, most;   // most: the largest |t| that the polynomial takes, 0 where its coefficients would over- or underflow
+  __device__ __forceinline__ Cap(float scale, float cap) {
+    k = scale / cap;
+    f = cap * LOG2E;
+    const float a = fabsf(k);
+    most = a >= 0x1p-12f && a <= 0x1p10f ? 1.f / a : 0.f;
+    constexpr float p[6] = {0x1.ffff96p-1f, -0x1.553ce0p-2f, 0x1.0f6ea4p-3f, -0x1.a191cep-5f, 0x1.0803b2p-6f, -0x1.742c6ap-9f};
+    float power = k;
 #pragma unroll
-  for (int c = 0; c < N; c += 4) {
-    m[0] = max3_abs(m[0], v[c], v[c + 1]);
-    m[1] = max3_abs(m[1], v[c + 2], v[c + 3]);
+    for (int i = 0; i < 6; i++) {
+      c[i] = p[i] * power * f;
+      power *= k * k;
+    }
   }
-  if (__any_sync(0xffffffffu, !(fmaxf(m[0], m[1]) * fabsf(k) <= 1.f))) {
-#pragma unroll
-    for (int c = 0; c < N; c++) v[c] = tanh_any(v[c] * k);
-  } else {
-#pragma unroll
-    for (int c = 0; c < N; c += 2)
-      f2::unpack(tanh_small2(f2::mul(f2::pack(v[c], v[c + 1]), f2::splat(k))), v[c], v[c + 1]);
+  __device__ __forceinline__ u64 small2(u64 t) const {
+    const u64 z = f2::mul(t, t);
+    u64 p = f2::fma(f2::splat(c[5]), z, f2::splat(c[4]));
+    p = f2::fma(p, z, f2::splat(c[3]));
+    p = f2::fma(p, z, f2::splat(c[2]));
+    p = f2::fma(p, z, f2::splat(c[1]));
+    p = f2::fma(p, z, f2::splat(c[0]));
+    return f2::mul(t, p);
   }
-}
+  // v <- f tanh(k v) for N scores of each lane; the warp decides which form it takes
+  template <int N>
+  __device__ __forceinline__ void apply(float* v) const {
+    float m[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      m[0] = max3_abs(m[0], v[i], v[i + 1]);
+      m[1] = max3_abs(m[1], v[i + 2], v[i + 3]);
+    }
+    if (__any_sync(0xffffffffu, !(fmaxf(m[0], m[1]) <= most))) {
+#pragma unroll
+      for (int i = 0; i < N; i++) v[i] = f * tanh_any(v[i] * k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) f2::unpack(small2(f2::pack(v[i], v[i + 1])), v[i], v[i + 1]);
+    }
+  }
+};
 
 // Which key tiles a tile of queries needs.  A whole warp calls it.
 __device__ __forceinline__ int2 key_range(const TaArgs& a, int b, int first_pos, int last_pos, int dlo, int dhi) {
@@ -105,19 +124,53 @@ __device__ __forceinline__ int2 key_range(const TaArgs& a, int b, int first_pos,
   return make_int2(n0, n1);
 }
 
+// COLS columns of a TMEM accumulator (plus more times a second one, where more is not 0), times k, to
+// 16 bits in a tile's row r (swizzled units); zeros without `some`, which is the same in all lanes (the loads are the
+// whole warp's)
+template <bool BF, int COLS>
+__device__ __forceinline__ void row_out(uint32_t tile, uint32_t taddr, uint32_t taddr2, int r, int c0, float k, float more,
+                                        bool some) {
+  using namespace tc5;
+#pragma unroll
+  for (int c = c0; c < c0 + COLS; c += 32) {
+    float o[32];
+    if (some) {
+      ld_x32(taddr + c, o);
+      ld_wait();
+      if (taddr2 != taddr) {
+        float x[32];
+        ld_x32(taddr2 + c, x);
+        ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; e++) o[e] = __fmaf_rn(more, x[e], o[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e++) o[e] = some ? o[e] * k : 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int unit = ((c & 63) >> 3) + u;
+      const uint32_t at = tile + (c >> 6) * PANEL + r * 128 + ((unit ^ (r & 7)) << 4);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack16<BF>(o[8 * u], o[8 * u + 1])),
+                   "r"(pack16<BF>(o[8 * u + 2], o[8 * u + 3])), "r"(pack16<BF>(o[8 * u + 4], o[8 * u + 5])),
+                   "r"(pack16<BF>(o[8 * u + 6], o[8 * u + 7]))
+                   : "memory");
+    }
+  }
+}
 }  // namespace ta
 
-// Two softmax groups and a control group (copies, products, two idle warps).  setmaxnreg moves the control group's
-// registers to the softmax threads, which hold a row's 128 scores: 384 x 168 at launch = 128 x 56 + 256 x 224.  The
-// control group never takes its registers back: an idle warp's request would be met before the softmax groups'.
-constexpr int TA_FWD_THREADS = 384;
+// Two groups of eight softmax warps and a control group (copies, products, two idle warps).  setmaxnreg moves
+// the control group's registers to the softmax threads: 640 x 96 at launch = 128 x 32 + 512 x 112.  The control
+// group never takes its registers back: an idle warp's request would be met before the softmax groups'.
+constexpr int TA_FWD_THREADS = 640;
 
 template <int DP>
 struct TaFwdSmem {
   static constexpr int TILE = DP / 64 * tc5::PANEL;
-  static constexpr int NST = DP == 128 ? 5 : 8;
-  static constexpr int Q = 0, KV = 2 * TILE, END = KV + NST * TILE;
-  static constexpr int BYTES = END + 1024;
+  // two query tiles and a ring of key and value tiles; the split form has one query tile and a stage more
+  static constexpr int NST = DP == 128 ? 4 : 8, MOST = NST + 1;
+  static constexpr int Q = 0, BYTES = (2 + NST) * TILE + 1024;
 };
 
 template <int DP, bool BF>
@@ -125,11 +178,12 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   using namespace tc5;
   using namespace ta;
   using L = TaFwdSmem<DP>;
-  constexpr int NST = L::NST, TILE = L::TILE;
+  constexpr int TILE = L::TILE;
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t q_full, kv_full[NST], kv_empty[NST], s_full[2], p_full[2], o_full[2], gone;
+  __shared__ uint64_t q_full, kv_full[L::MOST], kv_empty[L::MOST], s_full[2], p_full[2], o_full[2], gone;
   __shared__ uint32_t tmem_at;
-  __shared__ int dead, wdoc[8][2], range[2][2], qdoc[2][3];
+  __shared__ int dead, wdoc[16][2], range[2][2], qdoc[2][3];
+  __shared__ float exchange[2][2][2][128];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &dead;
@@ -140,9 +194,11 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   const bool alt = a.splits > 0;
   const int t = alt ? 0 : (int)(gridDim.x / HB) - 1 - blockIdx.x / HB;   // the last queries first: with causal masking the longest
   const int z = alt ? blockIdx.x / HB : 0;
+  const int nst = alt ? L::MOST : L::NST;
+  const uint32_t kv0 = base + (alt ? TILE : 2 * TILE);
 
   // this thread's query row (softmax groups)
-  const int wg = warp >> 2, r = threadIdx.x & 127;
+  const int wg = warp >> 3, half = (warp >> 2) & 1, r = threadIdx.x & 127;
   const int qt = alt ? 0 : 2 * t + wg;
   int qi, head;
   if (a.pack > 1) {
@@ -161,18 +217,18 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     dead = 0;
     mbar_init(&q_full, 1);
     mbar_init(&gone, 1);
-    for (int s = 0; s < NST; s++) {
+    for (int s = 0; s < L::MOST; s++) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 256);
       mbar_init(&o_full[i], 1);
     }
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(&tmem_at, 512);
+  if (warp == 17) tmem_alloc(&tmem_at, 512);
   if (wg < 2) {
     const int dl = __reduce_min_sync(0xffffffffu, doc < 0 ? 0x7fffffff : doc), dh = __reduce_max_sync(0xffffffffu, doc);
     const int neg = __any_sync(0xffffffffu, valid && doc < 0);
@@ -184,7 +240,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   fence_before();
   __syncthreads();
   fence_after();
-  if (wg < 2 && (warp & 3) == 0) {
+  if (wg < 2 && (warp & 7) == 0) {
     int dl = 0x7fffffff, dh = -1, neg = 0;
     for (int w = warp; w < warp + 4; w++) {
       int x = wdoc[w][1];
@@ -196,7 +252,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       dh = max(dh, x);
     }
     const int q0 = (a.pack > 1 ? 0 : qt * TA_TILE) + off;
-    const int q1 = (a.pack > 1 ? a.Sq : min(qt * TA_TILE + TA_TILE, a.Sq)) - 1 + off;
+    const int q1 = (qt >= a.qtiles ? 0 : a.pack > 1 ? a.Sq : min(qt * TA_TILE + TA_TILE, a.Sq)) - 1 + off;   // none: below q0
     const int2 nr = key_range(a, b, q0, q1, dl, dh);
     if (lane == 0) {
       range[wg][0] = nr.x;
@@ -223,9 +279,9 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   }
   const int ntile = hi - lo;
 
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
-  if (warp == 8) {
+  if (warp >= 16) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");
+  if (warp == 16) {
     // ---- copies: queries once, then keys and values in the order in which the products take them ----
     if (lane == 0 && ntile > 0) {
       const int nq = alt ? 1 : 2;
@@ -234,16 +290,16 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       for (int i = 0; i < nq; i++)
         for (int p = 0; p < DP / 64; p++) {
           const int at = base + L::Q + i * TILE + p * PANEL;
-          if (a.pack > 1) tma_load(at, &a.q, p * 64, 0, 0, h, b, &q_full);
+          if (a.pack > 1) tma_load(at, &a.q, p * 64, 0, 0, h, b, &q_full);   // an empty second tile too
           else tma_load(at, &a.q, p * 64, 0, min(2 * t + i, a.qtiles - 1) * TA_TILE, h, b, &q_full);
         }
       int it = 0;
       auto fetch = [&](const CUtensorMap* map, int n) -> bool {
-        const int s = it % NST;
-        if (it >= NST && !mbar_wait(&kv_empty[s], ((it / NST) - 1) & 1, abort)) return false;
+        const int s = it % nst;
+        if (it >= nst && !mbar_wait(&kv_empty[s], ((it / nst) - 1) & 1, abort)) return false;
         mbar_expect_tx(&kv_full[s], TILE);
         for (int p = 0; p < DP / 64; p++)
-          tma_load(base + L::KV + s * TILE + p * PANEL, map, p * 64, 0, n * TA_TILE, kh, b, &kv_full[s]);
+          tma_load(kv0 + s * TILE + p * PANEL, map, p * 64, 0, n * TA_TILE, kh, b, &kv_full[s]);
         it++;
         return true;
       };
@@ -255,18 +311,18 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         if (ok && n + ahead < hi) ok = fetch(&a.k, n + ahead);
       }
       // nothing may be in flight when the CTA ends
-      for (int k = max(0, it - NST); k < it; k++) mbar_drain(&kv_full[k % NST], (k / NST) & 1);
+      for (int k = max(0, it - nst); k < it; k++) mbar_drain(&kv_full[k % nst], (k / nst) & 1);
       mbar_drain(&q_full, 0);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---- products ----
     if (lane == 0 && ntile > 0) {
       const uint32_t id_s = idesc<BF>(128, 128, false), id_o = idesc<BF>(128, DP, true);
       int it = 0;
       auto wait_kv = [&](uint32_t& at) -> bool {
-        const int s = it % NST;
-        at = base + L::KV + s * TILE;
-        return mbar_wait(&kv_full[s], (it / NST) & 1, abort);
+        const int s = it % nst;
+        at = kv0 + s * TILE;
+        return mbar_wait(&kv_full[s], (it / nst) & 1, abort);
       };
       auto scores = [&](int i, uint32_t ktile) {
         const uint32_t q = base + L::Q + (alt ? 0 : i * TILE);
@@ -286,13 +342,13 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         if (ok) {
           if (lo < hi0) scores(0, kt);
           if (lo < hi1) scores(1, kt);
-          commit(&kv_empty[it % NST]);
+          commit(&kv_empty[it % nst]);
           it++;
         }
         for (int n = lo; n < hi && ok; n++) {
           ok = wait_kv(vt);
           if (!ok) break;
-          const int vs = it++ % NST;
+          const int vs = it++ % nst;
           bool have_k = false;
           for (int i = 0; i < 2 && ok; i++) {
             const int end = i ? hi1 : hi0;
@@ -312,14 +368,14 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
           }
           if (!ok) break;
           commit(&kv_empty[vs]);
-          if (have_k) commit(&kv_empty[it++ % NST]);
+          if (have_k) commit(&kv_empty[it++ % nst]);
         }
       } else {
         for (int i = 0; i < 2 && ok && lo + i < hi; i++) {
           if (i) ok = wait_kv(kt);
           if (!ok) break;
           scores(i, kt);
-          commit(&kv_empty[it++ % NST]);
+          commit(&kv_empty[it++ % nst]);
         }
         for (int n = lo; n < hi && ok; n++) {
           const int i = (n - lo) & 1;
@@ -328,12 +384,12 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
           fence_after();
           values(i, vt, n - lo < 2);
           if (n + 2 >= hi) commit(&o_full[i]);
-          commit(&kv_empty[it++ % NST]);
+          commit(&kv_empty[it++ % nst]);
           if (n + 2 < hi) {
             ok = wait_kv(kt);
             if (!ok) break;
             scores(i, kt);
-            commit(&kv_empty[it++ % NST]);
+            commit(&kv_empty[it++ % nst]);
           }
         }
       }
@@ -345,17 +401,17 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   }
   } else {
     // ---- softmax ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
-    const int i = wg;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;" ::: "memory");
+    const int i = wg, pair = 1 + i * 4 + (warp & 3);         // named barrier of the two warps with this warp's rows
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;      // TMEM lane 32 (w % 4) in bits 16 and up
-    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * DP;
-    const bool cap = a.softcap > 0.f;
-    const float capx = cap ? a.scale / a.softcap : 0.f;
-    const float f0 = (cap ? a.softcap : a.scale) * LOG2E;    // scores' units -> log2 units
+    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * DP + half * (DP / 2);
+    const bool capped = a.softcap > 0.f;
+    const Cap cap(a.scale, capped ? a.softcap : 1.f);
+    const float f0 = a.scale * LOG2E;
     const float slope = a.slopes && valid ? a.slopes[head] * LOG2E : 0.f;
-    const bool biased = a.slopes != nullptr || !(f0 > 0.f);  // applied before the maximum
-    const float f = biased ? 1.f : f0;
-    const float lazy = 8.f / f;
+    // without cap and bias the scores stay products (of a positive scale) until the exponential
+    const bool units = capped || a.slopes != nullptr || !(f0 > 0.f);
+    const float f = units ? 1.f : f0, lazy = 8.f / f;
     int lim = a.Skv;
     if (a.causal) lim = min(lim, max(pos + 1, a.prefix ? a.prefix[b] : 0));
     const int first_pos = (a.pack > 1 ? 0 : qt * TA_TILE) + off;
@@ -364,67 +420,76 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     float m = -INFINITY, l = 0.f;
     const int step = alt ? 2 : 1, end = i ? hi1 : hi0;
     int cnt = 0;
-    bool ok = true;
+    // a wait that gives up (dead is set) only spoils values: every barrier below is still passed
     for (int n = lo + (alt ? i : 0); n < end; n += step, cnt++) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], cnt & 1, abort));
-      if (!ok) break;
+      mbar_wait(&s_full[i], cnt & 1, abort);
+      __syncwarp();
       fence_after();
-      float v[128];
-#pragma unroll
-      for (int c = 0; c < 4; c++) ld_x32(ts + 32 * c, v + 32 * c);
+      float v[64];
+      ld_x32(ts + half * 64, v);
+      ld_x32(ts + half * 64 + 32, v + 32);
       ld_wait();
-      const int j0 = n * TA_TILE;
-      bool masked = j0 + TA_TILE > full, padded = false;
+      const int j0 = n * TA_TILE + half * 64;
+      bool masked = (n + 1) * TA_TILE > full, padded = false;
       if (a.docs) {
         const TaBounds bd = a.bounds[(int64_t)b * a.ktiles + n];
         padded = bd.neg;
         masked |= bd.neg || bd.lo != bd.hi || bd.lo != qdoc[i][0] || bd.lo != qdoc[i][1] || qdoc[i][2];
       }
-      if (cap) {
+      if (capped) {
+        cap.apply<32>(v);
+        cap.apply<32>(v + 32);
+      } else if (units) {
 #pragma unroll
-        for (int c = 0; c < 4; c++) tanh_row<32>(v + 32 * c, capx);
+        for (int c = 0; c < 64; c++) v[c] *= f0;
       }
-      if (biased) {
+      if (a.slopes) {
         const float d0 = (float)(pos - j0);
 #pragma unroll
-        for (int c = 0; c < 128; c++) v[c] = __fmaf_rn(v[c], f0, -slope * fabsf(d0 - (float)c));
+        for (int c = 0; c < 64; c++) v[c] = __fmaf_rn(-slope, fabsf(d0 - (float)c), v[c]);
       }
       if (masked) {
         if (a.docs) {
           const int* dj = a.docs + (int64_t)b * a.Skv + j0;
           const int left = a.Skv - j0;
 #pragma unroll
-          for (int c = 0; c < 128; c++) {
+          for (int c = 0; c < 64; c++) {
             const int d = c < left ? dj[c] : -1;
             if (j0 + c >= lim || d != doc || doc < 0) v[c] = -INFINITY;
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 128; c++)
+          for (int c = 0; c < 64; c++)
             if (j0 + c >= lim) v[c] = -INFINITY;
         }
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 128; c += 8)
+      for (int c = 0; c < 64; c += 8)
 #pragma unroll
         for (int e = 0; e < 4; e++) top[e] = max3(top[e], v[c + 2 * e], v[c + 2 * e + 1]);
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      // The row's maximum over both threads; the two sets of words by turns, so one barrier does.  It also lets the
+      // weights overwrite scores that the other thread has read.
+      exchange[cnt & 1][i][half][r] = mx;
+      bar_sync(pair, 64);
+      mx = fmaxf(mx, exchange[cnt & 1][i][half ^ 1][r]);
       const bool grow = cnt == 0 || mx > m + lazy;
-      if (__any_sync(0xffffffffu, grow)) {
+      if (__any_sync(0xffffffffu, grow)) {   // the same in both warps of these rows
         const float mn = grow ? fmaxf(m, mx) : m;
         const float k = mn == m ? 1.f : ex2((m - mn) * f);
         l *= k;
         m = mn;
         if (cnt > 0) {
 #pragma unroll
-          for (int c = 0; c < DP / 32; c++) {
-            float o[32];
-            ld_x32(to + 32 * c, o);
+          for (int c = 0; c < DP / 2; c += 16) {   // 16 at a time: the scores are live
+            float o[16];
+            uint32_t w[16];
+            ld_x16(to + c, o);
             ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; e++) o[e] *= k;
-            st_x32(to + 32 * c, o);
+            for (int e = 0; e < 16; e++) w[e] = __float_as_uint(o[e] * k);
+            st_x16(to + c, w);
           }
         }
       }
@@ -432,7 +497,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       u64 sum[2] = {0, 0};
       const u64 ff = f2::splat(f), shift = f2::splat(-mf);
 #pragma unroll
-      for (int c = 0; c < 4; c++) {
+      for (int c = 0; c < 2; c++) {
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -443,7 +508,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
           sum[(e >> 1) & 1] = f2::add(sum[(e >> 1) & 1], f2::pack(x, y));
           p[e >> 1] = pack16<BF>(x, y);
         }
-        st_x16(ts + 16 * c, p);
+        st_x16(ts + half * 32 + 16 * c, p);
       }
       {
         float x, y;
@@ -452,43 +517,31 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       }
       if (padded) {   // padding may hold NaN, and 0 NaN is NaN: its value rows become zeros
         const int d = n - lo, k = alt ? min(ntile, d + 2) + d : 1 + 2 * d;   // this value tile in the order of the copies
-        mbar_wait(&kv_full[k % NST], (k / NST) & 1, abort);
-        if (j0 + r < a.Skv && a.docs[(int64_t)b * a.Skv + j0 + r] < 0) zero_row<DP>(base + L::KV + (k % NST) * TILE, r);
+        const int j = n * TA_TILE + r;
+        mbar_wait(&kv_full[k % nst], (k / nst) & 1, abort);
+        if (half == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(kv0 + (k % nst) * TILE, r);
         __syncwarp();
       }
       st_wait();
       fence_before();
       mbar_arrive(&p_full[i]);
     }
-    if (cnt > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], 0, abort));
+    if (cnt > 0) mbar_wait(&o_full[i], 0, abort);
     if (ntile > 0) mbar_wait(&q_full, 0, abort);   // a group without key tiles still reuses its query tile below
+    __syncwarp();
     fence_after();
-    if (valid && !isfinite(l) && a.status) atomicOr(a.status, DA_STATUS_NONFINITE);
+    exchange[cnt & 1][i][half][r] = l;
+    bar_sync(pair, 64);
+    l = half ? exchange[cnt & 1][i][0][r] + l : l + exchange[cnt & 1][i][1][r];
+    if (valid && !isfinite(l) && half == 0 && a.status) atomicOr(a.status, DA_STATUS_NONFINITE);
+    __syncwarp();
     if (!alt) {
-      const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
       const uint32_t tile = base + L::Q + i * TILE;
-#pragma unroll
-      for (int c = 0; c < DP / 32; c++) {
-        float o[32];
-        if (cnt > 0) {
-          ld_x32(to + 32 * c, o);
-          ld_wait();
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e++) o[e] = cnt > 0 && l != 0.f ? o[e] * inv : 0.f;
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const int unit = (c & 1) * 4 + u;
-          const uint32_t at = tile + (c >> 1) * PANEL + r * 128 + ((unit ^ (r & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack16<BF>(o[8 * u], o[8 * u + 1])),
-                       "r"(pack16<BF>(o[8 * u + 2], o[8 * u + 3])), "r"(pack16<BF>(o[8 * u + 4], o[8 * u + 5])),
-                       "r"(pack16<BF>(o[8 * u + 6], o[8 * u + 7]))
-                       : "memory");
-        }
-      }
+      row_out<BF, DP / 2>(tile, tmem + lanes + 256 + i * DP, tmem + lanes + 256 + i * DP, r, half * (DP / 2),
+                          l > 0.f ? 1.f / l : l, 0.f, cnt > 0);   // a row that sees nothing: zeros times zero
       fence_async_smem();
-      bar_sync(1 + i, 128);
-      if (r == 0 && qt < a.qtiles && ok) {
+      bar_sync(9 + i, 256);
+      if (r == 0 && half == 0 && qt < a.qtiles && !dead) {
         for (int p = 0; p < DP / 64; p++)
           if (p * 64 < a.D) {
             if (a.pack > 1) {
@@ -500,34 +553,34 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         tma_store_commit();
         tma_store_wait();
       }
-      if (a.lse && valid && qt < a.qtiles)
+      if (a.lse && half == 0 && valid && qt < a.qtiles)
         a.lse[((int64_t)b * a.Hq + head) * a.Sq + qi] = l > 0.f ? (m * f + log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
     } else {
       const int64_t row = ((int64_t)(2 * z + i) * HB + hb) * TA_TILE + r;
-      float* o = a.part + row * DP;
+      float* o = a.part + row * DP + half * (DP / 2);
       float2* ml = reinterpret_cast<float2*>(a.part + (int64_t)2 * a.splits * HB * TA_TILE * DP) + row;
-      if (valid) *ml = make_float2(m * f, l);
+      if (valid && half == 0) *ml = make_float2(m * f, l);
 #pragma unroll
-      for (int c = 0; c < DP / 32; c++) {
+      for (int c = 0; c < DP / 2; c += 32) {
         float x[32];
         if (cnt > 0) {
-          ld_x32(to + 32 * c, x);
+          ld_x32(to + c, x);
           ld_wait();
         }
         if (valid && cnt > 0) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(o + 32 * c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            *reinterpret_cast<float4*>(o + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         }
       }
     }
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");   // as the control group, for what follows
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");   // as the control group, for what follows
   }
   fence_before();
   __syncthreads();
   fence_after();
   if (threadIdx.x == 0 && dead && a.status) atomicOr(a.status, DA_STATUS_TIMEOUT);
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // Joins the key ranges of the split forward: one warp a query row, the ranges in their order.
