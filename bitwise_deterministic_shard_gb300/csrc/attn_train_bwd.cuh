@@ -135,49 +135,51 @@ __global__ void __launch_bounds__(320, 1) ta_dkv_kernel(const __grid_constant__ 
       mbar_drain(&kv_full, 0);
     }
   } else if (warp == 9) {
-    if (lane == 0 && total > 0) {
+    const int steps = same(total);
+    if (steps > 0) {
+      const uint32_t one = elect(), tm = same(tmem);
       const uint32_t id_s = idesc<BF>(128, 128, false), id_o = idesc<BF>(128, DP, true);
-      const uint32_t ts = tmem, tp = tmem + 128, tv = tmem + 256, tk = tmem + 256 + DP;
+      const uint32_t ts = tm, tp = tm + 128, tv = tm + 256, tk = tm + 256 + DP;
       const uint32_t ktile = base + L::KEEP, vtile = ktile + TILE;
       auto stage = [&](int it) { return base + L::ST + (it % NST) * L::STAGE; };
       auto scores = [&](int it) {
 #pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_bf16(ts, desc_k(ktile, s), desc_k(stage(it), s), id_s, s > 0);
-        commit(&s_full);
+        for (int s = 0; s < DP / 16; s++) mma_ss(ts, desc_k(ktile, s), desc_k(stage(it), s), id_s, s > 0, one);
+        commit_one(&s_full, one);
       };
       auto grads = [&](int it) {
 #pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_bf16(tp, desc_k(vtile, s), desc_k(stage(it) + TILE, s), id_s, s > 0);
-        commit(&dp_full);
+        for (int s = 0; s < DP / 16; s++) mma_ss(tp, desc_k(vtile, s), desc_k(stage(it) + TILE, s), id_s, s > 0, one);
+        commit_one(&dp_full, one);
       };
-      bool ok = mbar_wait(&kv_full, 0, abort) && mbar_wait(&q_full[0], 0, abort);
+      bool ok = all_of(mbar_wait(&kv_full, 0, abort) && mbar_wait(&q_full[0], 0, abort));
       if (ok) {
         fence_after();
         scores(0);
         grads(0);
       }
-      for (int it = 0; it < total && ok; it++) {
-        ok = mbar_wait(&p_full, it & 1, abort);
+      for (int it = 0; it < steps && ok; it++) {
+        ok = all_of(mbar_wait(&p_full, it & 1, abort));
         if (!ok) break;
         fence_after();
 #pragma unroll
-        for (int s = 0; s < 8; s++) mma_ts(tv, ts + 8 * s, desc_mn(stage(it) + TILE, s), id_o, s > 0 || it > 0);
-        if (it + 1 < total) {
-          ok = mbar_wait(&q_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort);
+        for (int s = 0; s < 8; s++) mma_ts(tv, ts + 8 * s, desc_mn(stage(it) + TILE, s), id_o, s > 0 || it > 0, one);
+        if (it + 1 < steps) {
+          ok = all_of(mbar_wait(&q_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
           if (!ok) break;
           scores(it + 1);
         }
-        ok = mbar_wait(&ds_full, it & 1, abort);
+        ok = all_of(mbar_wait(&ds_full, it & 1, abort));
         if (!ok) break;
         fence_after();
 #pragma unroll
-        for (int s = 0; s < 8; s++) mma_ts(tk, tp + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0);
-        commit(&q_empty[it % NST]);
-        if (it + 1 < total) grads(it + 1);
+        for (int s = 0; s < 8; s++) mma_ts(tk, tp + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0, one);
+        commit_one(&q_empty[it % NST], one);
+        if (it + 1 < steps) grads(it + 1);
       }
-      commit(&done);
+      commit_one(&done, one);
       if (!ok) {
-        commit(&gone);
+        commit_one(&gone, one);
         mbar_drain(&gone, 0);
       }
     }
@@ -386,49 +388,51 @@ __global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ T
       mbar_drain(&q_full, 0);
     }
   } else if (warp == 9) {
-    if (lane == 0 && total > 0) {
+    const int steps = same(total);
+    if (steps > 0) {
+      const uint32_t one = elect(), tm = same(tmem);
       const uint32_t id_s = idesc<BF>(128, 128, false), id_o = idesc<BF>(128, DP, true);
-      const uint32_t ts = tmem, tp = tmem + 128, tq = tmem + 256, te = tmem + 256 + DP;
+      const uint32_t ts = tm, tp = tm + 128, tq = tm + 256, te = tm + 256 + DP;
       const uint32_t qtile = base + L::KEEP, gtile = qtile + TILE;
       auto stage = [&](int it) { return base + L::ST + (it % NST) * L::STAGE; };
       auto scores = [&](int it) {
 #pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_bf16(ts, desc_k(qtile, s), desc_k(stage(it), s), id_s, s > 0);
-        commit(&s_full);
+        for (int s = 0; s < DP / 16; s++) mma_ss(ts, desc_k(qtile, s), desc_k(stage(it), s), id_s, s > 0, one);
+        commit_one(&s_full, one);
       };
       auto grads = [&](int it) {
 #pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_bf16(tp, desc_k(gtile, s), desc_k(stage(it) + TILE, s), id_s, s > 0);
-        commit(&dp_full);
+        for (int s = 0; s < DP / 16; s++) mma_ss(tp, desc_k(gtile, s), desc_k(stage(it) + TILE, s), id_s, s > 0, one);
+        commit_one(&dp_full, one);
       };
-      bool ok = mbar_wait(&q_full, 0, abort) && mbar_wait(&kv_full[0], 0, abort);
+      bool ok = all_of(mbar_wait(&q_full, 0, abort) && mbar_wait(&kv_full[0], 0, abort));
       if (ok) {
         fence_after();
         scores(0);
         grads(0);
       }
-      for (int it = 0; it < total && ok; it++) {
-        ok = mbar_wait(&p_full, it & 1, abort);
+      for (int it = 0; it < steps && ok; it++) {
+        ok = all_of(mbar_wait(&p_full, it & 1, abort));
         if (!ok) break;
         fence_after();
 #pragma unroll
-        for (int s = 0; s < 8; s++) mma_ts(te, ts + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0);
-        if (it + 1 < total) {
-          ok = mbar_wait(&kv_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort);
+        for (int s = 0; s < 8; s++) mma_ts(te, ts + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0, one);
+        if (it + 1 < steps) {
+          ok = all_of(mbar_wait(&kv_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
           if (!ok) break;
           scores(it + 1);
         }
-        ok = mbar_wait(&ds_full, it & 1, abort);
+        ok = all_of(mbar_wait(&ds_full, it & 1, abort));
         if (!ok) break;
         fence_after();
 #pragma unroll
-        for (int s = 0; s < 8; s++) mma_ts(tq, tp + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0);
-        commit(&kv_empty[it % NST]);
-        if (it + 1 < total) grads(it + 1);
+        for (int s = 0; s < 8; s++) mma_ts(tq, tp + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0, one);
+        commit_one(&kv_empty[it % NST], one);
+        if (it + 1 < steps) grads(it + 1);
       }
-      commit(&done);
+      commit_one(&done, one);
       if (!ok) {
-        commit(&gone);
+        commit_one(&gone, one);
         mbar_drain(&gone, 0);
       }
     }

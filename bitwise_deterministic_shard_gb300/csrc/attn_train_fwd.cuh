@@ -5,19 +5,25 @@
 //
 // One CTA holds two tiles of 128 queries and runs over the key tiles once.  Per query tile a group of
 // eight warps owns a query row with two threads, each with 64 of the tile's 128 keys: a thread reads its scores
-// from TMEM, keeps the row's maximum and its part of the sum in registers, and writes exp2 of the scores
-// back to TMEM as 16-bit weights, over the scores they came from, where the second product takes them
-// as its A operand.  (Two threads a row: four warps a scheduler hide each other's latencies; with one thread a
-// row two warps issued in 39 % of the cycles.)  The two
-// groups alternate on the tensor cores: while one computes weights, the other's products run.  One
-// warp copies tiles (tensor maps, a ring of key and value tiles), one issues all products:
+// from TMEM, keeps the row's maximum and its part of the sum in registers, and writes exp2 of the scores as
+// 16-bit weights to shared memory, where the second product takes them as its A operand.  One warp
+// copies tiles (tensor maps, a ring of key and value tiles), one issues all products as they become possible:
 //   S_i = Q_i K_n^T (128 x 128 x D),  O_i += P_i V_n (128 x D x 128).
-// TMEM: two score tiles and two output tiles, 2 x 128 + 2 x D columns.
+// TMEM: two score tiles and two output tiles, 2 x 128 + 2 x D columns, 512 for D = 128.  That is why the weights go
+// to shared memory: over the scores in TMEM they would hold up the next scores until the second product
+// had read them (a group then waited 2450 of the 6300 cycles of a step for its scores).  So the next scores
+// are computed while the present ones are worked on.
+//
+// What bounds it: the softmax's arithmetic (per score 9 cycles of the FP32 pipe with a cap, 2 without, 4 of the
+// special function unit, against 8 of the tensor cores for two products of D = 128) and the latencies
+// that four softmax warps a scheduler leave open.
 //
 // The weights are rounded to the inputs' 16-bit type (the tensor cores take both operands in one
 // type); the sum of the weights and the output are binary32.  The maximum is moved only when
 // it grows by more than 2^8: until then weights are at most 2^8 too large, which the division by
-// their sum undoes exactly, and the output needs no rescaling.
+// their sum undoes exactly, and the output needs no rescaling.  Capped bf16 scores without a bias need no
+// maximum: they lie within +-cap, so with a cap of at most 44 (2^+-64) nothing over- or underflows in
+// binary32's range, which bf16 shares, with the constant 0 in the maximum's place.
 //
 // Few queries (Sq * group <= 128): the heads that share a key head are the rows of one tile, so
 // a cache is read once; both groups take the same queries and every other key tile, and the key range
@@ -124,6 +130,41 @@ __device__ __forceinline__ int2 key_range(const TaArgs& a, int b, int first_pos,
   return make_int2(n0, n1);
 }
 
+// The first n of N columns as bits, 32 to a word.
+template <int N>
+__device__ __forceinline__ void first_bits(uint32_t (&w)[N / 32], int n) {
+#pragma unroll
+  for (int i = 0; i < N / 32; i++) {
+    const int k = n - 32 * i;
+    w[i] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+  }
+}
+// Keeps of each lane's bits those of columns whose document is its own: other[0, N) are the columns' ids (left of
+// them exist), doc the lane's.  A warp's rows hold few documents, so the columns' ids are compared once for
+// each of these, a lane a column.  A whole warp calls it.
+template <int N>
+__device__ __forceinline__ void same_doc(uint32_t (&w)[N / 32], const int* other, int left, int doc) {
+  const int lane = threadIdx.x & 31;
+  int id[N / 32];
+#pragma unroll
+  for (int i = 0; i < N / 32; i++) id[i] = 32 * i + lane < left ? other[32 * i + lane] : -1;
+  uint32_t todo = __ballot_sync(0xffffffffu, doc >= 0);
+  if (doc < 0) {
+#pragma unroll
+    for (int i = 0; i < N / 32; i++) w[i] = 0;
+  }
+  while (todo) {
+    const int d = __shfl_sync(0xffffffffu, doc, __ffs(todo) - 1);
+    const bool mine = doc == d;
+#pragma unroll
+    for (int i = 0; i < N / 32; i++) {
+      const uint32_t same = __ballot_sync(0xffffffffu, id[i] == d);
+      if (mine) w[i] &= same;
+    }
+    todo &= ~__ballot_sync(0xffffffffu, mine);
+  }
+}
+
 // COLS columns of a TMEM accumulator (plus more times a second one, where more is not 0), times k, to
 // 16 bits in a tile's row r (swizzled units); zeros without `some`, which is the same in all lanes (the loads are the
 // whole warp's)
@@ -167,10 +208,11 @@ constexpr int TA_FWD_THREADS = 640;
 
 template <int DP>
 struct TaFwdSmem {
-  static constexpr int TILE = DP / 64 * tc5::PANEL;
-  // two query tiles and a ring of key and value tiles; the split form has one query tile and a stage more
-  static constexpr int NST = DP == 128 ? 4 : 8, MOST = NST + 1;
-  static constexpr int Q = 0, BYTES = (2 + NST) * TILE + 1024;
+  static constexpr int TILE = DP / 64 * tc5::PANEL, PTILE = 2 * tc5::PANEL;
+  // two query tiles, two tiles of weights and a ring of key and value tiles (the split form has one query tile and
+  // a stage more), then the rows' maxima
+  static constexpr int NST = DP == 128 ? 3 : 7, MOST = NST + 1;
+  static constexpr int Q = 0, P = 2 * TILE, KV = P + 2 * PTILE, MAX = KV + NST * TILE, END = MAX + 2048;
 };
 
 template <int DP, bool BF>
@@ -180,11 +222,12 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   using L = TaFwdSmem<DP>;
   constexpr int TILE = L::TILE;
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t q_full, kv_full[L::MOST], kv_empty[L::MOST], s_full[2], p_full[2], o_full[2], gone;
+  __shared__ uint64_t q_full, kv_full[L::MOST], kv_empty[L::MOST], s_full[2], s_read[2], p_full[2], pv_done[2], gone;
   __shared__ uint32_t tmem_at;
   __shared__ int dead, wdoc[16][2], range[2][2], qdoc[2][3];
-  __shared__ float exchange[2][2][2][128];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  // the rows' maxima in the two halves of the keys, as bf16 rounded up (any value near the maximum does): [turn][tile][half][row]
+  uint16_t* const exchange = reinterpret_cast<uint16_t*>(raw + (base - smem_addr(raw)) + L::MAX);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &dead;
 
@@ -195,7 +238,8 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   const int t = alt ? 0 : (int)(gridDim.x / HB) - 1 - blockIdx.x / HB;   // the last queries first: with causal masking the longest
   const int z = alt ? blockIdx.x / HB : 0;
   const int nst = alt ? L::MOST : L::NST;
-  const uint32_t kv0 = base + (alt ? TILE : 2 * TILE);
+  // the ring's stages: the split form's last one lies in the second query tile
+  const auto stage_at = [&](int s) { return base + (s < L::NST ? L::KV + s * TILE : TILE); };
 
   // this thread's query row (softmax groups)
   const int wg = warp >> 3, half = (warp >> 2) & 1, r = threadIdx.x & 127;
@@ -223,8 +267,9 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_read[i], 256);
       mbar_init(&p_full[i], 256);
-      mbar_init(&o_full[i], 1);
+      mbar_init(&pv_done[i], 1);
     }
     mbar_fence_init();
   }
@@ -299,102 +344,81 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         if (it >= nst && !mbar_wait(&kv_empty[s], ((it / nst) - 1) & 1, abort)) return false;
         mbar_expect_tx(&kv_full[s], TILE);
         for (int p = 0; p < DP / 64; p++)
-          tma_load(kv0 + s * TILE + p * PANEL, map, p * 64, 0, n * TA_TILE, kh, b, &kv_full[s]);
+          tma_load(stage_at(s) + p * PANEL, map, p * 64, 0, n * TA_TILE, kh, b, &kv_full[s]);
         it++;
         return true;
       };
       bool ok = fetch(&a.k, lo);
-      if (alt && ok && lo + 1 < hi) ok = fetch(&a.k, lo + 1);
-      const int ahead = alt ? 2 : 1;
+      if (ok && lo + 1 < hi) ok = fetch(&a.k, lo + 1);
       for (int n = lo; n < hi && ok; n++) {
         ok = fetch(&a.v, n);
-        if (ok && n + ahead < hi) ok = fetch(&a.k, n + ahead);
+        if (ok && n + 2 < hi) ok = fetch(&a.k, n + 2);
       }
       // nothing may be in flight when the CTA ends
       for (int k = max(0, it - nst); k < it; k++) mbar_drain(&kv_full[k % nst], (k / nst) & 1);
       mbar_drain(&q_full, 0);
     }
   } else if (warp == 17) {
-    // ---- products ----
-    if (lane == 0 && ntile > 0) {
+    // ---- products: each as soon as its operands are there ----
+    const int first = same(lo), tiles = same(ntile);
+    if (tiles > 0) {
+      const uint32_t one = elect(), tm = same(tmem);
       const uint32_t id_s = idesc<BF>(128, 128, false), id_o = idesc<BF>(128, DP, true);
-      int it = 0;
-      auto wait_kv = [&](uint32_t& at) -> bool {
-        const int s = it % nst;
-        at = kv0 + s * TILE;
-        return mbar_wait(&kv_full[s], (it / nst) & 1, abort);
-      };
-      auto scores = [&](int i, uint32_t ktile) {
-        const uint32_t q = base + L::Q + (alt ? 0 : i * TILE);
+      const int step = alt ? 2 : 1;
+      const int end[2] = {same(hi0) - first, same(hi1) - first};     // key tiles count from the first one here
+      int sn[2] = {0, alt ? 1 : 0}, pn[2] = {0, alt ? 1 : 0};        // next key tile of each group's two products
+      int read[2] = {0, 0}, wrote[2] = {0, 0};                       // steps whose products were issued
+      uint64_t t0 = 0;
+      uint32_t idle = 0;
+      bool ok = all_of(mbar_wait(&q_full, 0, abort));
+      while (ok && (pn[0] < end[0] || pn[1] < end[1])) {
+        bool some = false;
 #pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_bf16(tmem + i * 128, desc_k(q, s), desc_k(ktile, s), id_s, s > 0);
-        commit(&s_full[i]);
-      };
-      auto values = [&](int i, uint32_t vtile, bool first) {
-#pragma unroll
-        for (int s = 0; s < 8; s++)
-          mma_ts(tmem + 256 + i * DP, tmem + i * 128 + 8 * s, desc_mn(vtile, s), id_o, s > 0 || !first);
-      };
-      uint32_t kt, vt;
-      bool ok = mbar_wait(&q_full, 0, abort) && wait_kv(kt);
-      fence_after();
-      if (!alt) {
-        if (ok) {
-          if (lo < hi0) scores(0, kt);
-          if (lo < hi1) scores(1, kt);
-          commit(&kv_empty[it % nst]);
-          it++;
-        }
-        for (int n = lo; n < hi && ok; n++) {
-          ok = wait_kv(vt);
-          if (!ok) break;
-          const int vs = it++ % nst;
-          bool have_k = false;
-          for (int i = 0; i < 2 && ok; i++) {
-            const int end = i ? hi1 : hi0;
-            if (n < end) {
-              ok = mbar_wait(&p_full[i], (n - lo) & 1, abort);
-              if (!ok) break;
+        for (int i = 0; i < 2; i++) {
+          const int n = sn[i];
+          if (n < end[i]) {
+            const int k = n < 2 ? n : 2 * n - 1, st = k % nst;       // this key tile in the order of the copies
+            if (all_of((read[i] == 0 || mbar_test(&s_read[i], (read[i] - 1) & 1)) && mbar_test(&kv_full[st], (k / nst) & 1))) {
               fence_after();
-              values(i, vt, n == lo);
-              if (n + 1 == end) commit(&o_full[i]);
-            }
-            if (n + 1 < end) {
-              if (!have_k) ok = wait_kv(kt);
-              if (!ok) break;
-              have_k = true;
-              scores(i, kt);
+              const uint32_t q = base + L::Q + (alt ? 0 : i * TILE), kt = stage_at(st);
+#pragma unroll
+              for (int s = 0; s < DP / 16; s++) mma_ss(tm + i * 128, desc_k(q, s), desc_k(kt, s), id_s, s > 0, one);
+              commit_one(&s_full[i], one);
+              read[i]++;
+              sn[i] += step;
+              if (alt || n >= end[i ^ 1] || sn[i ^ 1] > n) commit_one(&kv_empty[st], one);
+              some = true;
             }
           }
-          if (!ok) break;
-          commit(&kv_empty[vs]);
-          if (have_k) commit(&kv_empty[it++ % nst]);
+          const int m = pn[i];
+          if (m < end[i] && m < sn[i]) {
+            const int k = min(tiles, m + 2) + m, st = k % nst;       // and this value tile
+            if (all_of(mbar_test(&p_full[i], wrote[i] & 1) && mbar_test(&kv_full[st], (k / nst) & 1))) {
+              fence_after();
+              const uint32_t pt = base + L::P + i * L::PTILE, vt = stage_at(st);
+#pragma unroll
+              for (int s = 0; s < 8; s++)
+                mma_ss(tm + 256 + i * DP, desc_k(pt, s), desc_mn(vt, s), id_o, s > 0 || wrote[i] > 0, one);
+              commit_one(&pv_done[i], one);
+              wrote[i]++;
+              pn[i] += step;
+              if (alt || m >= end[i ^ 1] || pn[i ^ 1] > m) commit_one(&kv_empty[st], one);
+              some = true;
+            }
+          }
         }
-      } else {
-        for (int i = 0; i < 2 && ok && lo + i < hi; i++) {
-          if (i) ok = wait_kv(kt);
-          if (!ok) break;
-          scores(i, kt);
-          commit(&kv_empty[it++ % nst]);
-        }
-        for (int n = lo; n < hi && ok; n++) {
-          const int i = (n - lo) & 1;
-          ok = wait_kv(vt) && mbar_wait(&p_full[i], ((n - lo) >> 1) & 1, abort);
-          if (!ok) break;
-          fence_after();
-          values(i, vt, n - lo < 2);
-          if (n + 2 >= hi) commit(&o_full[i]);
-          commit(&kv_empty[it++ % nst]);
-          if (n + 2 < hi) {
-            ok = wait_kv(kt);
-            if (!ok) break;
-            scores(i, kt);
-            commit(&kv_empty[it++ % nst]);
+        if (some) {
+          idle = 0;
+        } else {                                                     // bounded, as every wait
+          if (idle++ == 0) t0 = globaltimer();
+          if ((idle & 63) == 0 && all_of(*abort || globaltimer() - t0 > WAIT_NS)) {
+            ok = false;
+            dead = 1;
           }
         }
       }
       if (!ok) {
-        commit(&gone);
+        commit_one(&gone, one);
         mbar_drain(&gone, 0);
       }
     }
@@ -405,6 +429,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     const int i = wg, pair = 1 + i * 4 + (warp & 3);         // named barrier of the two warps with this warp's rows
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;      // TMEM lane 32 (w % 4) in bits 16 and up
     const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * DP + half * (DP / 2);
+    const uint32_t prow = base + L::P + i * L::PTILE + half * PANEL + r * 128;   // this thread's 64 weights: a panel's row
     const bool capped = a.softcap > 0.f;
     const Cap cap(a.scale, capped ? a.softcap : 1.f);
     const float f0 = a.scale * LOG2E;
@@ -412,12 +437,14 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     // without cap and bias the scores stay products (of a positive scale) until the exponential
     const bool units = capped || a.slopes != nullptr || !(f0 > 0.f);
     const float f = units ? 1.f : f0, lazy = 8.f / f;
+    // capped, unbiased bf16 scores: 0 in the maximum's place
+    const bool fixed = BF && capped && a.slopes == nullptr && a.softcap <= 44.f;
     int lim = a.Skv;
     if (a.causal) lim = min(lim, max(pos + 1, a.prefix ? a.prefix[b] : 0));
     const int first_pos = (a.pack > 1 ? 0 : qt * TA_TILE) + off;
     int full = a.Skv;                                        // keys below it are seen by every row, documents apart
     if (a.causal) full = min(full, max(first_pos + 1, a.prefix ? a.prefix[b] : 0));
-    float m = -INFINITY, l = 0.f;
+    float m = fixed ? 0.f : -INFINITY, l = 0.f;
     const int step = alt ? 2 : 1, end = i ? hi1 : hi0;
     int cnt = 0;
     // a wait that gives up (dead is set) only spoils values: every barrier below is still passed
@@ -429,6 +456,8 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       ld_x32(ts + half * 64, v);
       ld_x32(ts + half * 64 + 32, v + 32);
       ld_wait();
+      fence_before();
+      mbar_arrive(&s_read[i]);
       const int j0 = n * TA_TILE + half * 64;
       bool masked = (n + 1) * TA_TILE > full, padded = false;
       if (a.docs) {
@@ -449,31 +478,25 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         for (int c = 0; c < 64; c++) v[c] = __fmaf_rn(-slope, fabsf(d0 - (float)c), v[c]);
       }
       if (masked) {
-        if (a.docs) {
-          const int* dj = a.docs + (int64_t)b * a.Skv + j0;
-          const int left = a.Skv - j0;
+        uint32_t see[2];
+        first_bits<64>(see, lim - j0);
+        if (a.docs) same_doc<64>(see, a.docs + (int64_t)b * a.Skv + j0, a.Skv - j0, doc);
 #pragma unroll
-          for (int c = 0; c < 64; c++) {
-            const int d = c < left ? dj[c] : -1;
-            if (j0 + c >= lim || d != doc || doc < 0) v[c] = -INFINITY;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 64; c++)
-            if (j0 + c >= lim) v[c] = -INFINITY;
-        }
+        for (int c = 0; c < 64; c++)
+          if (!(see[c >> 5] & (1u << (c & 31)))) v[c] = -INFINITY;
       }
+      if (!fixed) {
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int c = 0; c < 64; c += 8)
 #pragma unroll
         for (int e = 0; e < 4; e++) top[e] = max3(top[e], v[c + 2 * e], v[c + 2 * e + 1]);
-      float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      // The row's maximum over both threads; the two sets of words by turns, so one barrier does.  It also lets the
-      // weights overwrite scores that the other thread has read.
-      exchange[cnt & 1][i][half][r] = mx;
+      const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      // the row's maximum over both threads; two sets of words by turns, so one barrier does
+      uint16_t* const at = exchange + (cnt & 1) * 512 + i * 256 + r;
+      at[half * 128] = __bfloat16_as_ushort(__float2bfloat16_ru(mine));
       bar_sync(pair, 64);
-      mx = fmaxf(mx, exchange[cnt & 1][i][half ^ 1][r]);
+      const float mx = fmaxf(__bfloat162float(__ushort_as_bfloat16(at[0])), __bfloat162float(__ushort_as_bfloat16(at[128])));
       const bool grow = cnt == 0 || mx > m + lazy;
       if (__any_sync(0xffffffffu, grow)) {   // the same in both warps of these rows
         const float mn = grow ? fmaxf(m, mx) : m;
@@ -481,6 +504,9 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         l *= k;
         m = mn;
         if (cnt > 0) {
+          mbar_wait(&pv_done[i], (cnt - 1) & 1, abort);
+          __syncwarp();
+          fence_after();
 #pragma unroll
           for (int c = 0; c < DP / 2; c += 16) {   // 16 at a time: the scores are live
             float o[16];
@@ -491,24 +517,32 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
             for (int e = 0; e < 16; e++) w[e] = __float_as_uint(o[e] * k);
             st_x16(to + c, w);
           }
+          st_wait();
         }
+      }
       }
       const float mf = m == -INFINITY ? 0.f : m * f;
       u64 sum[2] = {0, 0};
       const u64 ff = f2::splat(f), shift = f2::splat(-mf);
+      if (cnt > 0) {   // the product before has read the weights' tile
+        mbar_wait(&pv_done[i], (cnt - 1) & 1, abort);
+        __syncwarp();
+      }
 #pragma unroll
-      for (int c = 0; c < 2; c++) {
-        uint32_t p[16];
+      for (int u = 0; u < 8; u++) {
+        uint32_t p[4];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int e = 0; e < 8; e += 2) {
           float x, y;
-          f2::unpack(f2::fma(f2::pack(v[32 * c + e], v[32 * c + e + 1]), ff, shift), x, y);
+          f2::unpack(f2::fma(f2::pack(v[8 * u + e], v[8 * u + e + 1]), ff, shift), x, y);
           x = ex2(x);
           y = ex2(y);
           sum[(e >> 1) & 1] = f2::add(sum[(e >> 1) & 1], f2::pack(x, y));
           p[e >> 1] = pack16<BF>(x, y);
         }
-        st_x16(ts + half * 32 + 16 * c, p);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + ((u ^ (r & 7)) << 4)), "r"(p[0]), "r"(p[1]),
+                     "r"(p[2]), "r"(p[3])
+                     : "memory");
       }
       {
         float x, y;
@@ -516,23 +550,27 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         l += x + y;
       }
       if (padded) {   // padding may hold NaN, and 0 NaN is NaN: its value rows become zeros
-        const int d = n - lo, k = alt ? min(ntile, d + 2) + d : 1 + 2 * d;   // this value tile in the order of the copies
+        const int d = n - lo, k = min(ntile, d + 2) + d;   // this value tile in the order of the copies
         const int j = n * TA_TILE + r;
         mbar_wait(&kv_full[k % nst], (k / nst) & 1, abort);
-        if (half == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(kv0 + (k % nst) * TILE, r);
+        if (half == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(stage_at(k % nst), r);
         __syncwarp();
       }
-      st_wait();
+      fence_async_smem();
       fence_before();
       mbar_arrive(&p_full[i]);
     }
-    if (cnt > 0) mbar_wait(&o_full[i], 0, abort);
+    if (cnt > 0) mbar_wait(&pv_done[i], (cnt - 1) & 1, abort);
     if (ntile > 0) mbar_wait(&q_full, 0, abort);   // a group without key tiles still reuses its query tile below
     __syncwarp();
     fence_after();
-    exchange[cnt & 1][i][half][r] = l;
-    bar_sync(pair, 64);
-    l = half ? exchange[cnt & 1][i][0][r] + l : l + exchange[cnt & 1][i][1][r];
+    {   // the row's sum, by way of the weights' tile, which is no longer read
+      float* const at = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + L::P + i * L::PTILE) + r;
+      bar_sync(9 + i, 256);
+      at[half * 128] = l;
+      bar_sync(pair, 64);
+      l = at[0] + at[128];
+    }
     if (valid && !isfinite(l) && half == 0 && a.status) atomicOr(a.status, DA_STATUS_NONFINITE);
     __syncwarp();
     if (!alt) {
@@ -627,12 +665,20 @@ __global__ void __launch_bounds__(128) ta_join_kernel(const __grid_constant__ Ta
 template <int DP, bool BF>
 cudaError_t ta_forward(const TaArgs& a, cudaStream_t st) {
   using L = TaFwdSmem<DP>;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(ta_fwd_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  // up to 1024 bytes of static shared memory leave the tiles their alignment within the 227 KB of a CTA
+  static int bytes = 0;
+  static const cudaError_t ready = [] {
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, ta_fwd_kernel<DP, BF>);
+    if (e != cudaSuccess) return e;
+    if (at.sharedSizeBytes > 1024) return cudaErrorInvalidConfiguration;
+    bytes = L::END + 1024 - (int)at.sharedSizeBytes;
+    return cudaFuncSetAttribute(ta_fwd_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  }();
   if (ready != cudaSuccess) return ready;
   const int HB = a.B * (a.Hq / a.pack);
   const unsigned grid = (unsigned)HB * (a.splits > 0 ? a.splits : (a.qtiles + 1) / 2);
-  ta_fwd_kernel<DP, BF><<<grid, TA_FWD_THREADS, L::BYTES, st>>>(a);
+  ta_fwd_kernel<DP, BF><<<grid, TA_FWD_THREADS, bytes, st>>>(a);
   if (a.splits > 0) {
     const int64_t rows = (int64_t)HB * a.pack * a.Sq;
     ta_join_kernel<DP, BF><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);

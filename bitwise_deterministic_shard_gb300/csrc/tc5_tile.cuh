@@ -37,13 +37,41 @@ __host__ __device__ constexpr uint32_t idesc(int m, int n, bool b_mn) {
   return BF ? idesc_bf16(m, n, b_mn) : idesc_f16(m, n, b_mn);
 }
 
+// Products and commits are issued by whole warps with one elected lane.  A tcgen05.mma takes its descriptors from uniform
+// registers: in code that only one lane runs the compiler has to move every one of them there (measured 79 to
+// 160 cycles a product of 128 x 128 x 16); in code that the warp runs together, on values it can tell are the same in
+// all lanes, they are computed there (64 cycles, the tensor cores' rate).  same() makes a value such a one.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int same(int x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t same(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ bool all_of(bool x) { return __all_sync(0xffffffffu, x); }
+
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one));
+}
 // D[tmem] (+)= A[tmem] * B[smem], A 16-bit elements, two in a 32-bit column
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+                                       uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one));
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(one)
+      : "memory");
 }
 
 // box of a rank-5 tensor map -> shared memory; completion counted on bar
@@ -65,6 +93,16 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// Whether the phase of that parity is complete; never suspends the thread.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Wait for a copy or commit of this thread whatever became of the rest of the CTA: a CTA that gives up
 // still ends with nothing in flight.  Bounded (20 ms) like every wait.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
