@@ -24,7 +24,7 @@ struct TaArgs {
   const TaBounds* qbounds;            // backward: [B, query tiles] with docs
   const int* prefix;                  // [B] or null
   float* lse;                         // [B, Hq, Sq], natural logarithm
-  float2* rows;                       // backward: [B, Hq, query tiles x 128] (lse log2 e, delta); +inf, 0 for a
+  float* rows;                        // backward: [B, Hq, query tiles][2][128] (-lse log2 e), (-delta); -inf, 0 for a
                                       // row that sees nothing and past the last query
   float* part;                        // split forward: sums [2 splits][B Hkv][128][DP], then (max, total) pairs
   void* out;                          // join of the split forward: strides of b, h, s
@@ -55,7 +55,7 @@ struct TaRowsArgs {
   const void* out;
   const void* grad;
   const float* lse;
-  float2* rows;
+  float* rows;
   int64_t os[3], gs[3];
   int B, Hq, Sq, D, qtiles, bf;
 };

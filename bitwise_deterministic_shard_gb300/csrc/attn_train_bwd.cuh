@@ -13,11 +13,12 @@
 // tile of 128 queries and runs over the keys.  That is eight products a tile pair (seven without
 // E) instead of the five of a single kernel whose dq would be added by atomics in any order.
 //
-// Eight warps compute: a TMEM lane (tile row) has two threads, each with 64 of the 128 columns.
+// Sixteen warps compute: a TMEM lane (tile row) has four threads, each with 32 of the 128 columns.
 // One warp copies, one issues the products:
 //   keys kept:    S^T = K Q^T;  dP^T = V G^T;  dV += P^T G;  dK += dS^T Q      TMEM 2 x 128 + 2 x D
 //   queries kept: S = Q K^T;    dP = G V^T;    E += P K;      dQ += dS K       TMEM 2 x 128 + 2 x D
-// P and dS overwrite, as 16-bit A operands, the scores and products they came from.  The tensor cores run
+// P and dS overwrite, as 16-bit A operands, the scores and products they came from (each thread's 32 columns
+// become the first 16 of the same 32, so no thread writes what another still reads).  The tensor cores run
 // the products of a step in the shadow of the other half of it: dV or E and the next S while dS is
 // computed, dK or dQ and the next dP while the next P is.  P and dS are rounded to the inputs' type, the sums
 // are binary32.
@@ -52,18 +53,55 @@ __device__ __forceinline__ int2 query_range(const TaArgs& a, int b, int n) {
 
 }  // namespace ta
 
+constexpr int TA_BWD_THREADS = 640;   // registers: 640 x 96 at launch = 128 x 32 + 512 x 112
+
 template <int DP>
 struct TaBwdSmem {
   static constexpr int TILE = DP / 64 * tc5::PANEL;
   static constexpr int NST = 2;
-  // two kept tiles, then stages of two tiles and 128 (lse, delta) pairs
+  // two kept tiles, then stages of two tiles and 128 (-lse), 128 (-delta) of the queries
   static constexpr int KEEP = 0, ST = 2 * TILE, STAGE = 2 * TILE + 1024, END = ST + NST * STAGE;
   static constexpr int BYTES = END + 1024;
 };
 
+namespace ta {
+// the columns of a 16-deep step of the second products' A operand, within its 128 columns of TMEM
+__device__ __forceinline__ uint32_t a_at(int s) { return (s >> 1) * 32 + (s & 1) * 8; }
+
+// The second products of a step wait for their operand, the first ones of the next step follow them.
+template <int DP, bool BF>
+struct Products {
+  uint32_t ts, tp, t1, t2, one;           // scores, products with the gradient; the two sums
+  uint32_t id_s, id_o;
+  __device__ __forceinline__ void first(uint32_t d, uint32_t a, uint32_t b, uint64_t* bar) const {
+    using namespace tc5;
+#pragma unroll
+    for (int s = 0; s < DP / 16; s++) mma_ss(d, desc_k(a, s), desc_k(b, s), id_s, s > 0, one);
+    commit_one(bar, one);
+  }
+  __device__ __forceinline__ void second(uint32_t d, uint32_t a, uint32_t b, bool sum) const {
+    using namespace tc5;
+#pragma unroll
+    for (int s = 0; s < 8; s++) mma_ts(d, a + a_at(s), desc_mn(b, s), id_o, s > 0 || sum, one);
+  }
+};
+
+// What turns a product of a query and a key into a score in log2 units, and that into the cap's derivative
+// 1 - tanh^2 = 1 + inv2 score^2.
+struct Scores {
+  Cap cap;
+  float f0, inv2;         // without a cap; minus one over the square of the cap's factor
+  bool capped;
+  __device__ __forceinline__ Scores(const TaArgs& a)
+      : cap(a.scale, a.softcap > 0.f ? a.softcap : 1.f), f0(a.scale * LOG2E), capped(a.softcap > 0.f) {
+    inv2 = -1.f / (cap.f * cap.f);
+  }
+};
+}  // namespace ta
+
 // ---- keys kept: dK and dV ----
 template <int DP, bool BF>
-__global__ void __launch_bounds__(320, 1) ta_dkv_kernel(const __grid_constant__ TaArgs a) {
+__global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_constant__ TaArgs a) {
   using namespace tc5;
   using namespace ta;
   using L = TaBwdSmem<DP>;
@@ -89,14 +127,14 @@ __global__ void __launch_bounds__(320, 1) ta_dkv_kernel(const __grid_constant__ 
     }
     mbar_init(&s_full, 1);
     mbar_init(&dp_full, 1);
-    mbar_init(&p_full, 256);
-    mbar_init(&ds_full, 256);
+    mbar_init(&p_full, 512);
+    mbar_init(&ds_full, 512);
     mbar_init(&done, 1);
     mbar_init(&gone, 1);
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(&tmem_at, 512);
-  if (warp == 8) {
+  if (warp == 17) tmem_alloc(&tmem_at, 512);
+  if (warp == 16) {
     const int2 r = query_range(a, b, n);
     if (lane == 0) {
       range[0] = r.x;
@@ -109,154 +147,153 @@ __global__ void __launch_bounds__(320, 1) ta_dkv_kernel(const __grid_constant__ 
   const uint32_t tmem = tmem_at;
   const int q0 = range[0], nq = range[1] - q0, total = nq * a.group;
 
-  if (warp == 8) {
-    if (lane == 0 && total > 0) {
-      mbar_expect_tx(&kv_full, 2 * TILE);
-      for (int p = 0; p < DP / 64; p++) {
-        tma_load(base + L::KEEP + p * PANEL, &a.k, p * 64, 0, n * TA_TILE, kh, b, &kv_full);
-        tma_load(base + L::KEEP + TILE + p * PANEL, &a.v, p * 64, 0, n * TA_TILE, kh, b, &kv_full);
-      }
-      bool ok = true;
-      int it = 0;
-      for (; it < total; it++) {
-        const int s = it % NST, h = kh * a.group + it / nq, q = q0 + it % nq;
-        if (it >= NST) ok = mbar_wait(&q_empty[s], ((it / NST) - 1) & 1, abort);
-        if (!ok) break;
-        const uint32_t at = base + L::ST + s * L::STAGE;
-        mbar_expect_tx(&q_full[s], 2 * TILE + 1024);
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");
+    if (warp == 16) {
+      if (lane == 0 && total > 0) {
+        mbar_expect_tx(&kv_full, 2 * TILE);
         for (int p = 0; p < DP / 64; p++) {
-          tma_load(at + p * PANEL, &a.q, p * 64, 0, q * TA_TILE, h, b, &q_full[s]);
-          tma_load(at + TILE + p * PANEL, &a.go, p * 64, 0, q * TA_TILE, h, b, &q_full[s]);
+          tma_load(base + L::KEEP + p * PANEL, &a.k, p * 64, 0, n * TA_TILE, kh, b, &kv_full);
+          tma_load(base + L::KEEP + TILE + p * PANEL, &a.v, p * 64, 0, n * TA_TILE, kh, b, &kv_full);
         }
-        bulk_g2s(gen + L::ST + s * L::STAGE + 2 * TILE, a.rows + (((int64_t)b * a.Hq + h) * a.qtiles + q) * TA_TILE, 1024,
-                 &q_full[s]);
-      }
-      for (int k = max(0, it - NST); k < it; k++) mbar_drain(&q_full[k % NST], (k / NST) & 1);
-      mbar_drain(&kv_full, 0);
-    }
-  } else if (warp == 9) {
-    const int steps = same(total);
-    if (steps > 0) {
-      const uint32_t one = elect(), tm = same(tmem);
-      const uint32_t id_s = idesc<BF>(128, 128, false), id_o = idesc<BF>(128, DP, true);
-      const uint32_t ts = tm, tp = tm + 128, tv = tm + 256, tk = tm + 256 + DP;
-      const uint32_t ktile = base + L::KEEP, vtile = ktile + TILE;
-      auto stage = [&](int it) { return base + L::ST + (it % NST) * L::STAGE; };
-      auto scores = [&](int it) {
-#pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_ss(ts, desc_k(ktile, s), desc_k(stage(it), s), id_s, s > 0, one);
-        commit_one(&s_full, one);
-      };
-      auto grads = [&](int it) {
-#pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_ss(tp, desc_k(vtile, s), desc_k(stage(it) + TILE, s), id_s, s > 0, one);
-        commit_one(&dp_full, one);
-      };
-      bool ok = all_of(mbar_wait(&kv_full, 0, abort) && mbar_wait(&q_full[0], 0, abort));
-      if (ok) {
-        fence_after();
-        scores(0);
-        grads(0);
-      }
-      for (int it = 0; it < steps && ok; it++) {
-        ok = all_of(mbar_wait(&p_full, it & 1, abort));
-        if (!ok) break;
-        fence_after();
-#pragma unroll
-        for (int s = 0; s < 8; s++) mma_ts(tv, ts + 8 * s, desc_mn(stage(it) + TILE, s), id_o, s > 0 || it > 0, one);
-        if (it + 1 < steps) {
-          ok = all_of(mbar_wait(&q_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+        bool ok = true;
+        int it = 0;
+        for (; it < total; it++) {
+          const int s = it % NST, h = kh * a.group + it / nq, q = q0 + it % nq;
+          if (it >= NST) ok = mbar_wait(&q_empty[s], ((it / NST) - 1) & 1, abort);
           if (!ok) break;
-          scores(it + 1);
+          const uint32_t at = base + L::ST + s * L::STAGE;
+          mbar_expect_tx(&q_full[s], 2 * TILE + 1024);
+          for (int p = 0; p < DP / 64; p++) {
+            tma_load(at + p * PANEL, &a.q, p * 64, 0, q * TA_TILE, h, b, &q_full[s]);
+            tma_load(at + TILE + p * PANEL, &a.go, p * 64, 0, q * TA_TILE, h, b, &q_full[s]);
+          }
+          bulk_g2s(gen + L::ST + s * L::STAGE + 2 * TILE, a.rows + (((int64_t)b * a.Hq + h) * a.qtiles + q) * 256, 1024,
+                   &q_full[s]);
         }
-        ok = all_of(mbar_wait(&ds_full, it & 1, abort));
-        if (!ok) break;
-        fence_after();
-#pragma unroll
-        for (int s = 0; s < 8; s++) mma_ts(tk, tp + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0, one);
-        commit_one(&q_empty[it % NST], one);
-        if (it + 1 < steps) grads(it + 1);
+        for (int k = max(0, it - NST); k < it; k++) mbar_drain(&q_full[k % NST], (k / NST) & 1);
+        mbar_drain(&kv_full, 0);
       }
-      commit_one(&done, one);
-      if (!ok) {
-        commit_one(&gone, one);
-        mbar_drain(&gone, 0);
+    } else if (warp == 17) {
+      const int steps = same(total);
+      if (steps > 0) {
+        const uint32_t tm = same(tmem);
+        const Products<DP, BF> go{tm, tm + 128, tm + 256, tm + 256 + DP, elect(), idesc<BF>(128, 128, false), idesc<BF>(128, DP, true)};
+        const uint32_t ktile = base + L::KEEP, vtile = ktile + TILE, st0 = base + L::ST;
+        bool ok = all_of(mbar_wait(&kv_full, 0, abort) && mbar_wait(&q_full[0], 0, abort));
+        if (ok) {
+          fence_after();
+          go.first(go.ts, ktile, st0, &s_full);
+          go.first(go.tp, vtile, st0 + TILE, &dp_full);
+        }
+        for (int it = 0; it < steps && ok; it++) {
+          const uint32_t st = st0 + (it % NST) * L::STAGE, next = st0 + ((it + 1) % NST) * L::STAGE;
+          ok = all_of(mbar_wait(&p_full, it & 1, abort));
+          if (!ok) break;
+          fence_after();
+          go.second(go.t1, go.ts, st + TILE, it > 0);
+          if (it + 1 < steps) {
+            ok = all_of(mbar_wait(&q_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+            if (!ok) break;
+            go.first(go.ts, ktile, next, &s_full);
+          }
+          ok = all_of(mbar_wait(&ds_full, it & 1, abort));
+          if (!ok) break;
+          fence_after();
+          go.second(go.t2, go.tp, st, it > 0);
+          commit_one(&q_empty[it % NST], go.one);
+          if (it + 1 < steps) go.first(go.tp, vtile, next + TILE, &dp_full);
+        }
+        commit_one(&done, go.one);
+        if (!ok) {
+          commit_one(&gone, go.one);
+          mbar_drain(&gone, 0);
+        }
       }
     }
   } else {
-    const int r = threadIdx.x & 127, half = threadIdx.x >> 7, j = n * TA_TILE + r;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;" ::: "memory");
+    const int r = threadIdx.x & 127, part = threadIdx.x >> 7, j = n * TA_TILE + r;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes, tp = ts + 128;
-    const bool cap = a.softcap > 0.f;
-    const float capx = cap ? a.scale / a.softcap : 0.f;
-    const float f0 = (cap ? a.softcap : a.scale) * LOG2E;
+    const uint32_t ts = tmem + lanes + part * 32, tp = ts + 128;
+    const Scores sc(a);
     const bool free_key = !a.causal || (a.prefix && j < a.prefix[b]);
     const int doc = a.docs && j < a.Skv ? a.docs[(int64_t)b * a.Skv + j] : -1;
     TaBounds kb{};
     if (a.docs) kb = a.bounds[(int64_t)b * a.ktiles + n];
     const int free_below = a.causal && a.prefix ? a.prefix[b] : a.causal ? 0 : 0x7fffffff;
-    // a wait that gives up (dead is set) only spoils values: every barrier below is still passed
+    // a wait that gives up (dead is set) only spoils values
     for (int it = 0; it < total; it++) {
       const int q = q0 + it % nq, h = kh * a.group + it / nq;
       const int pos0 = q * TA_TILE + off;
-      const float slope = a.slopes ? a.slopes[h] * LOG2E : 0.f;
       bool padded = false, masked = (n + 1) * TA_TILE > a.Skv || ((n + 1) * TA_TILE - 1 > pos0 && (n + 1) * TA_TILE > free_below);
       if (a.docs) {
         const TaBounds qb = a.qbounds[(int64_t)b * a.qtiles + q];
         padded = kb.neg || qb.neg;
         masked |= padded || kb.lo != kb.hi || qb.lo != qb.hi || kb.lo != qb.lo;
       }
-      const float4* rows = reinterpret_cast<const float4*>(gen + L::ST + (it % NST) * L::STAGE + 2 * TILE) + half * 32;
-      mbar_wait(&s_full, it & 1, abort);
+      const float* rows = reinterpret_cast<const float*>(gen + L::ST + (it % NST) * L::STAGE + 2 * TILE) + part * 32;
       mbar_wait(&q_full[it % NST], (it / NST) & 1, abort);
+      mbar_wait(&s_full, it & 1, abort);
       __syncwarp();
       fence_after();
-      float v[64];
-      ld_x32(ts + half * 64, v);
-      ld_x32(ts + half * 64 + 32, v + 32);
+      float v[32];
+      ld_x32(ts, v);
       ld_wait();
-      // P may be written over the scores once both halves of the row have been read
-      bar_sync(1 + (warp & 3), 64);
-      const float d0 = (float)(pos0 + half * 64 - j);
-      const int cmin = free_key ? -1 : j - pos0 - half * 64;   // the columns below it are hidden
-      const int* dq = a.docs + (a.docs ? (int64_t)b * a.Skv + pos0 + half * 64 : 0);
-      const int left = a.Sq - q * TA_TILE - half * 64;
-#pragma unroll
-      for (int g = 0; g < 2; g++) {
-        uint32_t p16[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int c = 32 * g + e;
-          const float4 row = rows[c >> 1];        // lse, delta of two queries
-          float pp[2];
-#pragma unroll
-          for (int k = 0; k < 2; k++) {
-            float x = v[c + k], dc = 1.f;
-            if (cap) {
-              x = tanh_any(x * capx);
-              dc = __fmaf_rn(-x, x, 1.f);
-            }
-            float s = __fmaf_rn(x, f0, -(k ? row.z : row.x));
-            if (a.slopes) s = __fmaf_rn(-slope, fabsf(d0 + (float)(c + k)), s);
-            float p = ex2(s);
-            dc *= p;
-            if (masked) {
-              bool see = c + k >= cmin && j < a.Skv;
-              if (a.docs) see = see && c + k < left && doc >= 0 && dq[c + k] == doc;
-              p = see ? p : 0.f;
-              dc = see ? dc : 0.f;
-            }
-            pp[k] = p;
-            v[c + k] = dc;
-          }
-          p16[e >> 1] = pack16<BF>(pp[0], pp[1]);
+      uint32_t see[1] = {0xffffffffu};
+      if (masked) {
+        if (!free_key) {
+          first_bits<32>(see, j - pos0 - part * 32);   // the columns before it are hidden
+          see[0] = ~see[0];
         }
-        st_x16(ts + half * 32 + 16 * g, p16);
+        if (j >= a.Skv) see[0] = 0;
+        if (a.docs) same_doc<32>(see, a.docs + (int64_t)b * a.Skv + pos0 + part * 32, a.Sq - q * TA_TILE - part * 32, doc);
+      }
+      if (sc.capped) {
+        sc.cap.apply<32>(v);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) f2::unpack(f2::mul(f2::pack(v[c], v[c + 1]), f2::splat(sc.f0)), v[c], v[c + 1]);
+      }
+      float p[32];
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const ulonglong2 shift = *reinterpret_cast<const ulonglong2*>(rows + c);   // -lse of four queries
+        f2::unpack(f2::add(f2::pack(v[c], v[c + 1]), shift.x), p[c], p[c + 1]);
+        f2::unpack(f2::add(f2::pack(v[c + 2], v[c + 3]), shift.y), p[c + 2], p[c + 3]);
+      }
+      if (a.slopes) {
+        const float slope = a.slopes[h] * LOG2E, d0 = (float)(pos0 + part * 32 - j);
+#pragma unroll
+        for (int c = 0; c < 32; c++) p[c] = __fmaf_rn(-slope, fabsf(d0 + (float)c), p[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 32; c++) p[c] = ex2(p[c]);
+      if (sc.capped) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const u64 y = f2::pack(v[c], v[c + 1]);
+          f2::unpack(f2::mul(f2::pack(p[c], p[c + 1]), f2::fma(f2::mul(y, y), f2::splat(sc.inv2), f2::splat(1.f))), v[c], v[c + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; c++) v[c] = p[c];
+      }
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 32; c++)
+          if (!(see[0] & (1u << c))) p[c] = v[c] = 0.f;
+      }
+      {
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) w[c >> 1] = pack16<BF>(p[c], p[c + 1]);
+        st_x16(ts, w);
       }
       if (padded) {   // padding may hold NaN, and 0 NaN is NaN: its query and gradient rows become zeros
         const int i = q * TA_TILE + r;
-        if (i < a.Sq && a.docs[(int64_t)b * a.Skv + i + off] < 0)
-          zero_row<DP>(base + L::ST + (it % NST) * L::STAGE + half * TILE, r);
+        if (part < 2 && i < a.Sq && a.docs[(int64_t)b * a.Skv + i + off] < 0)
+          zero_row<DP>(base + L::ST + (it % NST) * L::STAGE + part * TILE, r);
         __syncwarp();
       }
       st_wait();
@@ -265,25 +302,25 @@ __global__ void __launch_bounds__(320, 1) ta_dkv_kernel(const __grid_constant__ 
       mbar_wait(&dp_full, it & 1, abort);
       __syncwarp();
       fence_after();
-      float w[64];
-      ld_x32(tp + half * 64, w);
-      ld_x32(tp + half * 64 + 32, w + 32);
+      float w[32];
+      ld_x32(tp, w);
       ld_wait();
-      bar_sync(1 + (warp & 3), 64);
       if (padded) {
 #pragma unroll
-        for (int c = 0; c < 64; c++) w[c] = v[c] == 0.f ? 0.f : w[c];
+        for (int c = 0; c < 32; c++) w[c] = v[c] == 0.f ? 0.f : w[c];
       }
+      {
+        uint32_t d[16];
 #pragma unroll
-      for (int g = 0; g < 2; g++) {
-        uint32_t d16[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int c = 32 * g + e;
-          const float4 row = rows[c >> 1];
-          d16[e >> 1] = pack16<BF>(v[c] * (w[c] - row.y), v[c + 1] * (w[c + 1] - row.w));
+        for (int c = 0; c < 32; c += 4) {
+          const ulonglong2 less = *reinterpret_cast<const ulonglong2*>(rows + 128 + c);   // -delta of four queries
+          float x, y;
+          f2::unpack(f2::mul(f2::pack(v[c], v[c + 1]), f2::add(f2::pack(w[c], w[c + 1]), less.x)), x, y);
+          d[c >> 1] = pack16<BF>(x, y);
+          f2::unpack(f2::mul(f2::pack(v[c + 2], v[c + 3]), f2::add(f2::pack(w[c + 2], w[c + 3]), less.y)), x, y);
+          d[(c >> 1) + 1] = pack16<BF>(x, y);
         }
-        st_x16(tp + half * 32 + 16 * g, d16);
+        st_x16(tp, d);
       }
       st_wait();
       fence_before();
@@ -293,11 +330,12 @@ __global__ void __launch_bounds__(320, 1) ta_dkv_kernel(const __grid_constant__ 
     __syncwarp();
     fence_after();
     // dK over the keys' tile, dV over the values': both are no longer read
-    const uint32_t kt = base + L::KEEP, vt = kt + TILE;
-    row_out<BF, DP / 2>(vt, tmem + lanes + 256, tmem + lanes + 256, r, half * (DP / 2), 1.f, 0.f, total > 0);
-    row_out<BF, DP / 2>(kt, tmem + lanes + 256 + DP, tmem + lanes + 256 + DP, r, half * (DP / 2), a.scale, 0.f, total > 0);
+    const uint32_t kt = base + L::KEEP, vt = kt + TILE, acc = tmem + lanes + 256;
+    constexpr int HALF = DP / 2;
+    if (part < 2) row_out<BF, HALF>(vt, acc, acc, r, part * HALF, 1.f, 0.f, total > 0);
+    else row_out<BF, HALF>(kt, acc + DP, acc + DP, r, (part - 2) * HALF, a.scale, 0.f, total > 0);
     fence_async_smem();
-    bar_sync(5, 256);
+    bar_sync(5, 512);
     if (threadIdx.x == 0 && !dead) {
       for (int p = 0; p < DP / 64; p++)
         if (p * 64 < a.D) {
@@ -307,17 +345,18 @@ __global__ void __launch_bounds__(320, 1) ta_dkv_kernel(const __grid_constant__ 
       tma_store_commit();
       tma_store_wait();
     }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");   // as the control group, for what follows
   }
   fence_before();
   __syncthreads();
   fence_after();
   if (threadIdx.x == 0 && dead && a.status) atomicOr(a.status, DA_STATUS_TIMEOUT);
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // ---- queries kept: dQ ----
 template <int DP, bool BF>
-__global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ TaArgs a) {
+__global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_constant__ TaArgs a) {
   using namespace tc5;
   using namespace ta;
   using L = TaBwdSmem<DP>;
@@ -326,7 +365,7 @@ __global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ T
   __shared__ uint64_t q_full, kv_full[NST], kv_empty[NST], s_full, dp_full, p_full, ds_full, done, gone;
   __shared__ uint32_t tmem_at;
   __shared__ int dead, range[2];
-  __shared__ float delta_sum[2][128];
+  __shared__ float delta_sum[4][128];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &dead;
@@ -342,14 +381,14 @@ __global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ T
     }
     mbar_init(&s_full, 1);
     mbar_init(&dp_full, 1);
-    mbar_init(&p_full, 256);
-    mbar_init(&ds_full, 256);
+    mbar_init(&p_full, 512);
+    mbar_init(&ds_full, 512);
     mbar_init(&done, 1);
     mbar_init(&gone, 1);
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(&tmem_at, 512);
-  if (warp == 8) {
+  if (warp == 17) tmem_alloc(&tmem_at, 512);
+  if (warp == 16) {
     TaBounds qb{};
     if (a.docs) qb = a.qbounds[(int64_t)b * a.qtiles + q];
     const int2 r = key_range(a, b, pos0, min(pos0 + TA_TILE, a.Skv) - 1, qb.lo, qb.hi);
@@ -364,89 +403,77 @@ __global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ T
   const uint32_t tmem = tmem_at;
   const int n0 = range[0], total = range[1] - n0;
 
-  if (warp == 8) {
-    if (lane == 0 && total > 0) {
-      mbar_expect_tx(&q_full, 2 * TILE);
-      for (int p = 0; p < DP / 64; p++) {
-        tma_load(base + L::KEEP + p * PANEL, &a.q, p * 64, 0, q * TA_TILE, h, b, &q_full);
-        tma_load(base + L::KEEP + TILE + p * PANEL, &a.go, p * 64, 0, q * TA_TILE, h, b, &q_full);
-      }
-      bool ok = true;
-      int it = 0;
-      for (; it < total; it++) {
-        const int s = it % NST;
-        if (it >= NST) ok = mbar_wait(&kv_empty[s], ((it / NST) - 1) & 1, abort);
-        if (!ok) break;
-        const uint32_t at = base + L::ST + s * L::STAGE;
-        mbar_expect_tx(&kv_full[s], 2 * TILE);
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");
+    if (warp == 16) {
+      if (lane == 0 && total > 0) {
+        mbar_expect_tx(&q_full, 2 * TILE);
         for (int p = 0; p < DP / 64; p++) {
-          tma_load(at + p * PANEL, &a.k, p * 64, 0, (n0 + it) * TA_TILE, kh, b, &kv_full[s]);
-          tma_load(at + TILE + p * PANEL, &a.v, p * 64, 0, (n0 + it) * TA_TILE, kh, b, &kv_full[s]);
+          tma_load(base + L::KEEP + p * PANEL, &a.q, p * 64, 0, q * TA_TILE, h, b, &q_full);
+          tma_load(base + L::KEEP + TILE + p * PANEL, &a.go, p * 64, 0, q * TA_TILE, h, b, &q_full);
         }
-      }
-      for (int k = max(0, it - NST); k < it; k++) mbar_drain(&kv_full[k % NST], (k / NST) & 1);
-      mbar_drain(&q_full, 0);
-    }
-  } else if (warp == 9) {
-    const int steps = same(total);
-    if (steps > 0) {
-      const uint32_t one = elect(), tm = same(tmem);
-      const uint32_t id_s = idesc<BF>(128, 128, false), id_o = idesc<BF>(128, DP, true);
-      const uint32_t ts = tm, tp = tm + 128, tq = tm + 256, te = tm + 256 + DP;
-      const uint32_t qtile = base + L::KEEP, gtile = qtile + TILE;
-      auto stage = [&](int it) { return base + L::ST + (it % NST) * L::STAGE; };
-      auto scores = [&](int it) {
-#pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_ss(ts, desc_k(qtile, s), desc_k(stage(it), s), id_s, s > 0, one);
-        commit_one(&s_full, one);
-      };
-      auto grads = [&](int it) {
-#pragma unroll
-        for (int s = 0; s < DP / 16; s++) mma_ss(tp, desc_k(gtile, s), desc_k(stage(it) + TILE, s), id_s, s > 0, one);
-        commit_one(&dp_full, one);
-      };
-      bool ok = all_of(mbar_wait(&q_full, 0, abort) && mbar_wait(&kv_full[0], 0, abort));
-      if (ok) {
-        fence_after();
-        scores(0);
-        grads(0);
-      }
-      for (int it = 0; it < steps && ok; it++) {
-        ok = all_of(mbar_wait(&p_full, it & 1, abort));
-        if (!ok) break;
-        fence_after();
-#pragma unroll
-        for (int s = 0; s < 8; s++) mma_ts(te, ts + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0, one);
-        if (it + 1 < steps) {
-          ok = all_of(mbar_wait(&kv_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+        bool ok = true;
+        int it = 0;
+        for (; it < total; it++) {
+          const int s = it % NST;
+          if (it >= NST) ok = mbar_wait(&kv_empty[s], ((it / NST) - 1) & 1, abort);
           if (!ok) break;
-          scores(it + 1);
+          const uint32_t at = base + L::ST + s * L::STAGE;
+          mbar_expect_tx(&kv_full[s], 2 * TILE);
+          for (int p = 0; p < DP / 64; p++) {
+            tma_load(at + p * PANEL, &a.k, p * 64, 0, (n0 + it) * TA_TILE, kh, b, &kv_full[s]);
+            tma_load(at + TILE + p * PANEL, &a.v, p * 64, 0, (n0 + it) * TA_TILE, kh, b, &kv_full[s]);
+          }
         }
-        ok = all_of(mbar_wait(&ds_full, it & 1, abort));
-        if (!ok) break;
-        fence_after();
-#pragma unroll
-        for (int s = 0; s < 8; s++) mma_ts(tq, tp + 8 * s, desc_mn(stage(it), s), id_o, s > 0 || it > 0, one);
-        commit_one(&kv_empty[it % NST], one);
-        if (it + 1 < steps) grads(it + 1);
+        for (int k = max(0, it - NST); k < it; k++) mbar_drain(&kv_full[k % NST], (k / NST) & 1);
+        mbar_drain(&q_full, 0);
       }
-      commit_one(&done, one);
-      if (!ok) {
-        commit_one(&gone, one);
-        mbar_drain(&gone, 0);
+    } else if (warp == 17) {
+      const int steps = same(total);
+      if (steps > 0) {
+        const uint32_t tm = same(tmem);
+        const Products<DP, BF> go{tm, tm + 128, tm + 256 + DP, tm + 256, elect(), idesc<BF>(128, 128, false), idesc<BF>(128, DP, true)};
+        const uint32_t qtile = base + L::KEEP, gtile = qtile + TILE, st0 = base + L::ST;
+        bool ok = all_of(mbar_wait(&q_full, 0, abort) && mbar_wait(&kv_full[0], 0, abort));
+        if (ok) {
+          fence_after();
+          go.first(go.ts, qtile, st0, &s_full);
+          go.first(go.tp, gtile, st0 + TILE, &dp_full);
+        }
+        for (int it = 0; it < steps && ok; it++) {
+          const uint32_t st = st0 + (it % NST) * L::STAGE, next = st0 + ((it + 1) % NST) * L::STAGE;
+          ok = all_of(mbar_wait(&p_full, it & 1, abort));
+          if (!ok) break;
+          fence_after();
+          go.second(go.t1, go.ts, st, it > 0);
+          if (it + 1 < steps) {
+            ok = all_of(mbar_wait(&kv_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+            if (!ok) break;
+            go.first(go.ts, qtile, next, &s_full);
+          }
+          ok = all_of(mbar_wait(&ds_full, it & 1, abort));
+          if (!ok) break;
+          fence_after();
+          go.second(go.t2, go.tp, st, it > 0);
+          commit_one(&kv_empty[it % NST], go.one);
+          if (it + 1 < steps) go.first(go.tp, gtile, next + TILE, &dp_full);
+        }
+        commit_one(&done, go.one);
+        if (!ok) {
+          commit_one(&gone, go.one);
+          mbar_drain(&gone, 0);
+        }
       }
     }
   } else {
-    const int r = threadIdx.x & 127, half = threadIdx.x >> 7, qi = q * TA_TILE + r, pos = pos0 + r;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;" ::: "memory");
+    const int r = threadIdx.x & 127, part = threadIdx.x >> 7, qi = q * TA_TILE + r, pos = pos0 + r;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes, tp = ts + 128;
-    const bool cap = a.softcap > 0.f;
-    const float capx = cap ? a.scale / a.softcap : 0.f;
-    const float f0 = (cap ? a.softcap : a.scale) * LOG2E;
+    const uint32_t ts = tmem + lanes + part * 32, tp = ts + 128;
+    const Scores sc(a);
     const float slope = a.slopes ? a.slopes[h] * LOG2E : 0.f;
-    float2* const my_row = a.rows + ((int64_t)b * a.Hq + h) * a.qtiles * TA_TILE + qi;
-    const float2 row = *my_row;
-    float delta[4] = {0.f, 0.f, 0.f, 0.f};
+    float* const my_row = a.rows + (((int64_t)b * a.Hq + h) * a.qtiles + q) * 256 + r;
+    const float shift = my_row[0], less = my_row[128];      // -lse, -delta
     const int doc = a.docs && qi < a.Sq ? a.docs[(int64_t)b * a.Skv + pos] : -1;
     TaBounds qb{};
     if (a.docs) qb = a.qbounds[(int64_t)b * a.qtiles + q];
@@ -456,8 +483,9 @@ __global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ T
       lim = min(lim, max(pos + 1, pre));
       full = min(full, max(pos0 + 1, pre));
     }
+    u64 delta[2] = {0, 0};
     for (int it = 0; it < total; it++) {   // a wait that gives up only spoils values, as above
-      const int n = n0 + it, j0 = n * TA_TILE + half * 64;
+      const int n = n0 + it, j0 = n * TA_TILE + part * 32;
       bool padded = false, masked = (n + 1) * TA_TILE > full;
       if (a.docs) {
         const TaBounds kb = a.bounds[(int64_t)b * a.ktiles + n];
@@ -467,47 +495,55 @@ __global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ T
       mbar_wait(&s_full, it & 1, abort);
       __syncwarp();
       fence_after();
-      float v[64];
-      ld_x32(ts + half * 64, v);
-      ld_x32(ts + half * 64 + 32, v + 32);
+      float v[32];
+      ld_x32(ts, v);
       ld_wait();
-      bar_sync(1 + (warp & 3), 64);
-      const float d0 = (float)(pos - j0);
-      const int* dj = a.docs + (a.docs ? (int64_t)b * a.Skv + j0 : 0);
-      const int left = a.Skv - j0;
-      uint32_t hidden[2] = {0, 0};
+      uint32_t see[1] = {0xffffffffu};
+      if (masked) {
+        first_bits<32>(see, lim - j0);
+        if (a.docs) same_doc<32>(see, a.docs + (int64_t)b * a.Skv + j0, a.Skv - j0, doc);
+      }
+      float p[32];
+      const u64 sh = f2::splat(shift);
+      if (sc.capped) {
+        sc.cap.apply<32>(v);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) f2::unpack(f2::add(f2::pack(v[c], v[c + 1]), sh), p[c], p[c + 1]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) f2::unpack(f2::fma(f2::pack(v[c], v[c + 1]), f2::splat(sc.f0), sh), p[c], p[c + 1]);
+      }
+      if (a.slopes) {
+        const float d0 = (float)(pos - j0);
+#pragma unroll
+        for (int c = 0; c < 32; c++) p[c] = __fmaf_rn(-slope, fabsf(d0 - (float)c), p[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 32; c++) p[c] = ex2(p[c]);
+      if (sc.capped) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const u64 y = f2::pack(v[c], v[c + 1]);
+          f2::unpack(f2::mul(f2::pack(p[c], p[c + 1]), f2::fma(f2::mul(y, y), f2::splat(sc.inv2), f2::splat(1.f))), v[c], v[c + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; c++) v[c] = p[c];
+      }
       if (masked) {
 #pragma unroll
-        for (int c = 0; c < 64; c++) {
-          bool see = j0 + c < lim;
-          if (a.docs) see = see && c < left && doc >= 0 && dj[c] == doc;
-          hidden[c >> 5] |= (see ? 0u : 1u) << (c & 31);
-        }
+        for (int c = 0; c < 32; c++)
+          if (!(see[0] & (1u << c))) p[c] = v[c] = 0.f;
       }
-      float p[64];
+      {
+        uint32_t w[16];
 #pragma unroll
-      for (int g = 0; g < 2; g++) {
-        uint32_t p16[16];
-#pragma unroll
-        for (int e = 0; e < 32; e++) {
-          const int c = 32 * g + e;
-          float x = v[c], dc = 1.f;
-          if (cap) {
-            x = tanh_any(x * capx);
-            dc = __fmaf_rn(-x, x, 1.f);
-          }
-          float y = __fmaf_rn(x, f0, -row.x);
-          if (a.slopes) y = __fmaf_rn(-slope, fabsf(d0 - (float)c), y);
-          p[c] = ex2(y);
-          v[c] = p[c] * dc;
-          if (masked && (hidden[g] >> e & 1)) p[c] = v[c] = 0.f;
-          if (e & 1) p16[e >> 1] = pack16<BF>(v[c - 1], v[c]);
-        }
-        st_x16(ts + half * 32 + 16 * g, p16);
+        for (int c = 0; c < 32; c += 2) w[c >> 1] = pack16<BF>(v[c], v[c + 1]);
+        st_x16(ts, w);
       }
       if (padded) {   // padding may hold NaN: its key rows become zeros before a product sums over them
         const int j = n * TA_TILE + r;
-        if (half == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(base + L::ST + (it % NST) * L::STAGE, r);
+        if (part == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(base + L::ST + (it % NST) * L::STAGE, r);
         __syncwarp();
       }
       st_wait();
@@ -516,27 +552,27 @@ __global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ T
       mbar_wait(&dp_full, it & 1, abort);
       __syncwarp();
       fence_after();
-      float w[64];
-      ld_x32(tp + half * 64, w);
-      ld_x32(tp + half * 64 + 32, w + 32);
-      ld_wait();
-      bar_sync(1 + (warp & 3), 64);
-      if (padded) {
+      uint32_t d[16];
 #pragma unroll
-        for (int c = 0; c < 64; c++) w[c] = p[c] == 0.f ? 0.f : w[c];
-      }
+      for (int g = 0; g < 2; g++) {      // 16 at a time: weights and factors are live
+        float w[16];
+        ld_x16(tp + 16 * g, w);
+        ld_wait();
+        if (padded) {
 #pragma unroll
-      for (int c = 0; c < 64; c++) delta[c & 3] = __fmaf_rn(p[c], w[c], delta[c & 3]);
-#pragma unroll
-      for (int g = 0; g < 2; g++) {
-        uint32_t d16[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int c = 32 * g + e;
-          d16[e >> 1] = pack16<BF>(v[c] * (w[c] - row.y), v[c + 1] * (w[c + 1] - row.y));
+          for (int c = 0; c < 16; c++) w[c] = p[16 * g + c] == 0.f ? 0.f : w[c];
         }
-        st_x16(tp + half * 32 + 16 * g, d16);
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+          const int k = 16 * g + c;
+          const u64 x = f2::pack(w[c], w[c + 1]);
+          delta[(c >> 1) & 1] = f2::fma(f2::pack(p[k], p[k + 1]), x, delta[(c >> 1) & 1]);
+          float y, z;
+          f2::unpack(f2::mul(f2::pack(v[k], v[k + 1]), f2::add(x, f2::splat(less))), y, z);
+          d[k >> 1] = pack16<BF>(y, z);
+        }
       }
+      st_x16(tp, d);
       st_wait();
       fence_before();
       mbar_arrive(&ds_full);
@@ -546,26 +582,33 @@ __global__ void __launch_bounds__(320, 1) ta_dq_kernel(const __grid_constant__ T
     fence_after();
     // The sums were taken with delta from the rounded output; with D = sum p dp the gradient is
     // scale (sum ds k - (D - delta) sum p (1 - tanh^2) k).  D goes to the other kernel too.
-    delta_sum[half][r] = (delta[0] + delta[1]) + (delta[2] + delta[3]);
-    bar_sync(5, 256);
-    const float exact = delta_sum[0][r] + delta_sum[1][r];
-    if (half == 0 && !dead) my_row->y = exact;
-    const uint32_t qt = base + L::KEEP;
-    row_out<BF, DP / 2>(qt, tmem + lanes + 256, tmem + lanes + 256 + DP, r, half * (DP / 2), a.scale, row.y - exact, total > 0);
+    {
+      float x, y;
+      f2::unpack(f2::add(delta[0], delta[1]), x, y);
+      delta_sum[part][r] = x + y;
+    }
+    bar_sync(5, 512);
+    const float exact = (delta_sum[0][r] + delta_sum[1][r]) + (delta_sum[2][r] + delta_sum[3][r]);
+    if (part == 0 && !dead) my_row[128] = -exact;
+    __syncwarp();
+    const uint32_t qt = base + L::KEEP, acc = tmem + lanes + 256;
+    if (DP == 128) row_out<BF, 32>(qt, acc, acc + DP, r, part * 32, a.scale, -less - exact, total > 0);
+    else if (part < 2) row_out<BF, 32>(qt, acc, acc + DP, r, part * 32, a.scale, -less - exact, total > 0);
     fence_async_smem();
-    bar_sync(5, 256);
+    bar_sync(5, 512);
     if (threadIdx.x == 0 && !dead) {
       for (int p = 0; p < DP / 64; p++)
         if (p * 64 < a.D) tma_store(&a.dq, qt + p * PANEL, p * 64, 0, q * TA_TILE, h, b);
       tma_store_commit();
       tma_store_wait();
     }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");
   }
   fence_before();
   __syncthreads();
   fence_after();
   if (threadIdx.x == 0 && dead && a.status) atomicOr(a.status, DA_STATUS_TIMEOUT);
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 template <int DP, bool BF>
@@ -574,7 +617,7 @@ cudaError_t ta_dkv(const TaArgs& a, cudaStream_t st) {
   static const cudaError_t ready =
       cudaFuncSetAttribute(ta_dkv_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (ready != cudaSuccess) return ready;
-  ta_dkv_kernel<DP, BF><<<(unsigned)(a.B * a.Hkv) * a.ktiles, 320, L::BYTES, st>>>(a);
+  ta_dkv_kernel<DP, BF><<<(unsigned)(a.B * a.Hkv) * a.ktiles, TA_BWD_THREADS, L::BYTES, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -585,7 +628,7 @@ cudaError_t ta_dq(const TaArgs& a, cudaStream_t st) {
       cudaFuncSetAttribute(ta_dq_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (ready != cudaSuccess) return ready;
   if (a.qtiles == 0) return cudaSuccess;
-  ta_dq_kernel<DP, BF><<<(unsigned)(a.B * a.Hq) * a.qtiles, 320, L::BYTES, st>>>(a);
+  ta_dq_kernel<DP, BF><<<(unsigned)(a.B * a.Hq) * a.qtiles, TA_BWD_THREADS, L::BYTES, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(128) ta_bounds_kernel(const int* docs, int Skv
   if (lane == 0) out[(int64_t)blockIdx.y * tiles + w] = TaBounds{lo, max(hi, -1), neg};
 }
 
-// What the backward passes take of a query row: its lse in log2 units and delta = sum out * grad.
+// What the backward passes take of a query row: minus its lse in log2 units and minus delta = sum out * grad.
 // Eight threads a row, 16-byte loads; bound by reading out and grad once.
 template <typename T>
 __global__ void __launch_bounds__(256) ta_rows_kernel(const TaRowsArgs a) {
@@ -56,7 +56,9 @@ __global__ void __launch_bounds__(256) ta_rows_kernel(const TaRowsArgs a) {
   if (u == 0) {
     const float l = i < a.Sq ? a.lse[bh * a.Sq + i] : -INFINITY;
     const bool none = l == -INFINITY;
-    a.rows[row] = make_float2(none ? INFINITY : l * 1.4426950408889634f, none ? 0.f : s);
+    float* const at = a.rows + (row / TA_TILE) * 256 + row % TA_TILE;
+    at[0] = none ? -INFINITY : -l * 1.4426950408889634f;
+    at[128] = none ? 0.f : -s;
   }
 }
 

@@ -139,7 +139,7 @@ Ws layout(const TaArgs& a, bool backward) {
   w.part = w.qbounds + round_up(a.docs && backward ? (size_t)a.B * a.qtiles * sizeof(TaBounds) : 0);
   size_t more = 0;
   if (backward) {
-    more = (size_t)a.B * a.Hq * a.qtiles * TA_TILE * sizeof(float2);
+    more = (size_t)a.B * a.Hq * a.qtiles * TA_TILE * 2 * sizeof(float);
   } else if (const int s = split_rule(a)) {
     more = (size_t)2 * s * a.B * (a.Hq / a.pack) * TA_TILE * (head_width(a.D) + 2) * 4;
   }
@@ -219,7 +219,7 @@ DA_EXPORT int dta_backward(const dta_desc* d, const da_tensor* out, const float*
   if (!aligned(ws, 256)) return DA_EALIGN;
   if (a.B == 0 || a.Skv == 0) return DA_OK;
   cudaStream_t st = (cudaStream_t)stream;
-  float2* rows = reinterpret_cast<float2*>((char*)ws + w.part);
+  float* rows = reinterpret_cast<float*>((char*)ws + w.part);
   a.rows = rows;
   a.bounds = reinterpret_cast<const TaBounds*>((char*)ws + w.bounds);
   a.qbounds = reinterpret_cast<const TaBounds*>((char*)ws + w.qbounds);
