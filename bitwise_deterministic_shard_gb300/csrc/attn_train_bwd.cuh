@@ -17,11 +17,11 @@
 // One warp copies, one issues the products:
 //   keys kept:    S^T = K Q^T;  dP^T = V G^T;  dV += P^T G;  dK += dS^T Q      TMEM 2 x 128 + 2 x D
 //   queries kept: S = Q K^T;    dP = G V^T;    E += P K;      dQ += dS K       TMEM 2 x 128 + 2 x D
-// P and dS overwrite, as 16-bit A operands, the scores and products they came from (each thread's 32 columns
-// become the first 16 of the same 32, so no thread writes what another still reads).  The tensor cores run
-// the products of a step in the shadow of the other half of it: dV or E and the next S while dS is
-// computed, dK or dQ and the next dP while the next P is.  P and dS are rounded to the inputs' type, the sums
-// are binary32.
+// P (times the cap's derivative for E) goes to shared memory as an A operand, so the next scores are computed as soon
+// as the present ones are read (over the scores in TMEM it held them up by 1200 of 4500 cycles a step).  dS
+// overwrites, as 16-bit A operand, the products it came from: each thread's 32 columns become the first 16 of the
+// same 32, so no thread writes what another still reads; the next dP follows dK or dQ in the shadow of the next P.
+// P and dS are rounded to the inputs' type, the sums are binary32.
 #pragma once
 #include "../../include/detattn.h"
 #include "attn_train.h"
@@ -59,16 +59,14 @@ template <int DP>
 struct TaBwdSmem {
   static constexpr int TILE = DP / 64 * tc5::PANEL;
   static constexpr int NST = 2;
-  // two kept tiles, then stages of two tiles and 128 (-lse), 128 (-delta) of the queries
-  static constexpr int KEEP = 0, ST = 2 * TILE, STAGE = 2 * TILE + 1024, END = ST + NST * STAGE;
-  static constexpr int BYTES = END + 1024;
+  // two kept tiles, stages of two tiles and 128 (-lse), 128 (-delta) of the queries, a tile of weights
+  static constexpr int KEEP = 0, ST = 2 * TILE, STAGE = 2 * TILE + 1024, P = ST + NST * STAGE, END = P + 2 * tc5::PANEL;
 };
 
 namespace ta {
 // the columns of a 16-deep step of the second products' A operand, within its 128 columns of TMEM
 __device__ __forceinline__ uint32_t a_at(int s) { return (s >> 1) * 32 + (s & 1) * 8; }
 
-// The second products of a step wait for their operand, the first ones of the next step follow them.
 template <int DP, bool BF>
 struct Products {
   uint32_t ts, tp, t1, t2, one;           // scores, products with the gradient; the two sums
@@ -79,12 +77,31 @@ struct Products {
     for (int s = 0; s < DP / 16; s++) mma_ss(d, desc_k(a, s), desc_k(b, s), id_s, s > 0, one);
     commit_one(bar, one);
   }
-  __device__ __forceinline__ void second(uint32_t d, uint32_t a, uint32_t b, bool sum) const {
+  __device__ __forceinline__ void weights(uint32_t a, uint32_t b, bool sum, uint64_t* bar) const {
     using namespace tc5;
 #pragma unroll
-    for (int s = 0; s < 8; s++) mma_ts(d, a + a_at(s), desc_mn(b, s), id_o, s > 0 || sum, one);
+    for (int s = 0; s < 8; s++) mma_ss(t1, desc_k(a, s), desc_mn(b, s), id_o, s > 0 || sum, one);
+    commit_one(bar, one);
+  }
+  __device__ __forceinline__ void grads(uint32_t b, bool sum) const {
+    using namespace tc5;
+#pragma unroll
+    for (int s = 0; s < 8; s++) mma_ts(t2, tp + a_at(s), desc_mn(b, s), id_o, s > 0 || sum, one);
   }
 };
+
+// A thread's 32 weights of row r: half a panel's row
+template <bool BF>
+__device__ __forceinline__ void put_weights(uint32_t tile, int r, int part, const float* p) {
+  using namespace tc5;
+  const uint32_t row = tile + (part >> 1) * PANEL + r * 128;
+#pragma unroll
+  for (int u = 0; u < 4; u++)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((((part & 1) * 4 + u) ^ (r & 7)) << 4)),
+                 "r"(pack16<BF>(p[8 * u], p[8 * u + 1])), "r"(pack16<BF>(p[8 * u + 2], p[8 * u + 3])),
+                 "r"(pack16<BF>(p[8 * u + 4], p[8 * u + 5])), "r"(pack16<BF>(p[8 * u + 6], p[8 * u + 7]))
+                 : "memory");
+}
 
 // What turns a product of a query and a key into a score in log2 units, and that into the cap's derivative
 // 1 - tanh^2 = 1 + inv2 score^2.
@@ -107,7 +124,7 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
   using L = TaBwdSmem<DP>;
   constexpr int NST = L::NST, TILE = L::TILE;
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t kv_full, q_full[NST], q_empty[NST], s_full, dp_full, p_full, ds_full, done, gone;
+  __shared__ uint64_t kv_full, q_full[NST], q_empty[NST], s_full, s_read, dp_full, p_full, p_read, ds_full, done, gone;
   __shared__ uint32_t tmem_at;
   __shared__ int dead, range[2];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
@@ -126,6 +143,8 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
       mbar_init(&q_empty[s], 1);
     }
     mbar_init(&s_full, 1);
+    mbar_init(&s_read, 512);
+    mbar_init(&p_read, 1);
     mbar_init(&dp_full, 1);
     mbar_init(&p_full, 512);
     mbar_init(&ds_full, 512);
@@ -188,19 +207,20 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
         }
         for (int it = 0; it < steps && ok; it++) {
           const uint32_t st = st0 + (it % NST) * L::STAGE, next = st0 + ((it + 1) % NST) * L::STAGE;
+          if (it + 1 < steps) {
+            ok = all_of(mbar_wait(&s_read, it & 1, abort) && mbar_wait(&q_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+            if (!ok) break;
+            fence_after();
+            go.first(go.ts, ktile, next, &s_full);
+          }
           ok = all_of(mbar_wait(&p_full, it & 1, abort));
           if (!ok) break;
           fence_after();
-          go.second(go.t1, go.ts, st + TILE, it > 0);
-          if (it + 1 < steps) {
-            ok = all_of(mbar_wait(&q_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
-            if (!ok) break;
-            go.first(go.ts, ktile, next, &s_full);
-          }
+          go.weights(base + L::P, st + TILE, it > 0, &p_read);
           ok = all_of(mbar_wait(&ds_full, it & 1, abort));
           if (!ok) break;
           fence_after();
-          go.second(go.t2, go.tp, st, it > 0);
+          go.grads(st, it > 0);
           commit_one(&q_empty[it % NST], go.one);
           if (it + 1 < steps) go.first(go.tp, vtile, next + TILE, &dp_full);
         }
@@ -240,6 +260,8 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
       float v[32];
       ld_x32(ts, v);
       ld_wait();
+      fence_before();
+      mbar_arrive(&s_read);
       uint32_t see[1] = {0xffffffffu};
       if (masked) {
         if (!free_key) {
@@ -284,20 +306,15 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
         for (int c = 0; c < 32; c++)
           if (!(see[0] & (1u << c))) p[c] = v[c] = 0.f;
       }
-      {
-        uint32_t w[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) w[c >> 1] = pack16<BF>(p[c], p[c + 1]);
-        st_x16(ts, w);
-      }
+      if (it > 0) mbar_wait(&p_read, (it - 1) & 1, abort);
+      put_weights<BF>(base + L::P, r, part, p);
       if (padded) {   // padding may hold NaN, and 0 NaN is NaN: its query and gradient rows become zeros
         const int i = q * TA_TILE + r;
         if (part < 2 && i < a.Sq && a.docs[(int64_t)b * a.Skv + i + off] < 0)
           zero_row<DP>(base + L::ST + (it % NST) * L::STAGE + part * TILE, r);
         __syncwarp();
       }
-      st_wait();
-      fence_before();
+      fence_async_smem();
       mbar_arrive(&p_full);
       mbar_wait(&dp_full, it & 1, abort);
       __syncwarp();
@@ -362,10 +379,9 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
   using L = TaBwdSmem<DP>;
   constexpr int NST = L::NST, TILE = L::TILE;
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t q_full, kv_full[NST], kv_empty[NST], s_full, dp_full, p_full, ds_full, done, gone;
+  __shared__ uint64_t q_full, kv_full[NST], kv_empty[NST], s_full, s_read, dp_full, p_full, p_read, ds_full, done, gone;
   __shared__ uint32_t tmem_at;
   __shared__ int dead, range[2];
-  __shared__ float delta_sum[4][128];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &dead;
@@ -380,6 +396,8 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
       mbar_init(&kv_empty[s], 1);
     }
     mbar_init(&s_full, 1);
+    mbar_init(&s_read, 512);
+    mbar_init(&p_read, 1);
     mbar_init(&dp_full, 1);
     mbar_init(&p_full, 512);
     mbar_init(&ds_full, 512);
@@ -442,19 +460,20 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
         }
         for (int it = 0; it < steps && ok; it++) {
           const uint32_t st = st0 + (it % NST) * L::STAGE, next = st0 + ((it + 1) % NST) * L::STAGE;
+          if (it + 1 < steps) {
+            ok = all_of(mbar_wait(&s_read, it & 1, abort) && mbar_wait(&kv_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+            if (!ok) break;
+            fence_after();
+            go.first(go.ts, qtile, next, &s_full);
+          }
           ok = all_of(mbar_wait(&p_full, it & 1, abort));
           if (!ok) break;
           fence_after();
-          go.second(go.t1, go.ts, st, it > 0);
-          if (it + 1 < steps) {
-            ok = all_of(mbar_wait(&kv_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
-            if (!ok) break;
-            go.first(go.ts, qtile, next, &s_full);
-          }
+          go.weights(base + L::P, st, it > 0, &p_read);
           ok = all_of(mbar_wait(&ds_full, it & 1, abort));
           if (!ok) break;
           fence_after();
-          go.second(go.t2, go.tp, st, it > 0);
+          go.grads(st, it > 0);
           commit_one(&kv_empty[it % NST], go.one);
           if (it + 1 < steps) go.first(go.tp, gtile, next + TILE, &dp_full);
         }
@@ -498,6 +517,8 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
       float v[32];
       ld_x32(ts, v);
       ld_wait();
+      fence_before();
+      mbar_arrive(&s_read);
       uint32_t see[1] = {0xffffffffu};
       if (masked) {
         first_bits<32>(see, lim - j0);
@@ -535,19 +556,14 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
         for (int c = 0; c < 32; c++)
           if (!(see[0] & (1u << c))) p[c] = v[c] = 0.f;
       }
-      {
-        uint32_t w[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) w[c >> 1] = pack16<BF>(v[c], v[c + 1]);
-        st_x16(ts, w);
-      }
+      if (it > 0) mbar_wait(&p_read, (it - 1) & 1, abort);
+      put_weights<BF>(base + L::P, r, part, v);
       if (padded) {   // padding may hold NaN: its key rows become zeros before a product sums over them
         const int j = n * TA_TILE + r;
         if (part == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(base + L::ST + (it % NST) * L::STAGE, r);
         __syncwarp();
       }
-      st_wait();
-      fence_before();
+      fence_async_smem();
       mbar_arrive(&p_full);
       mbar_wait(&dp_full, it & 1, abort);
       __syncwarp();
@@ -580,15 +596,16 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
     if (total > 0) mbar_wait(&done, 0, abort);
     __syncwarp();
     fence_after();
+    float* const sums = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + L::P);   // the weights' tile is no longer read
     // The sums were taken with delta from the rounded output; with D = sum p dp the gradient is
     // scale (sum ds k - (D - delta) sum p (1 - tanh^2) k).  D goes to the other kernel too.
     {
       float x, y;
       f2::unpack(f2::add(delta[0], delta[1]), x, y);
-      delta_sum[part][r] = x + y;
+      sums[part * 128 + r] = x + y;
     }
     bar_sync(5, 512);
-    const float exact = (delta_sum[0][r] + delta_sum[1][r]) + (delta_sum[2][r] + delta_sum[3][r]);
+    const float exact = (sums[r] + sums[128 + r]) + (sums[256 + r] + sums[384 + r]);
     if (part == 0 && !dead) my_row[128] = -exact;
     __syncwarp();
     const uint32_t qt = base + L::KEEP, acc = tmem + lanes + 256;
@@ -614,21 +631,21 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
 template <int DP, bool BF>
 cudaError_t ta_dkv(const TaArgs& a, cudaStream_t st) {
   using L = TaBwdSmem<DP>;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(ta_dkv_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  static int bytes = 0;
+  static const cudaError_t ready = tile_smem(ta_dkv_kernel<DP, BF>, L::END, &bytes);
   if (ready != cudaSuccess) return ready;
-  ta_dkv_kernel<DP, BF><<<(unsigned)(a.B * a.Hkv) * a.ktiles, TA_BWD_THREADS, L::BYTES, st>>>(a);
+  ta_dkv_kernel<DP, BF><<<(unsigned)(a.B * a.Hkv) * a.ktiles, TA_BWD_THREADS, bytes, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int DP, bool BF>
 cudaError_t ta_dq(const TaArgs& a, cudaStream_t st) {
   using L = TaBwdSmem<DP>;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(ta_dq_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  static int bytes = 0;
+  static const cudaError_t ready = tile_smem(ta_dq_kernel<DP, BF>, L::END, &bytes);
   if (ready != cudaSuccess) return ready;
   if (a.qtiles == 0) return cudaSuccess;
-  ta_dq_kernel<DP, BF><<<(unsigned)(a.B * a.Hq) * a.qtiles, TA_BWD_THREADS, L::BYTES, st>>>(a);
+  ta_dq_kernel<DP, BF><<<(unsigned)(a.B * a.Hq) * a.qtiles, TA_BWD_THREADS, bytes, st>>>(a);
   return cudaGetLastError();
 }
 

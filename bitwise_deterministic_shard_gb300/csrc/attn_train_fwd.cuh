@@ -57,27 +57,37 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // Scores of a row in log2 units: f tanh(k t) with a cap (k = scale / cap, f = cap log2 e), else f t (f = scale log2 e).
 //
 // tanh of any argument: 1 - 2 / (1 + e^2x), two operations of the special function unit, 2^-22 absolute.  On
-// [-1, 1], where the scores of a capped model nearly always are: x P(x^2), P of degree 5 fitted for the least
-// greatest error (least squares with weights moved toward the largest errors), 3.1e-7 absolute with
-// binary32 steps, on the packed multiplier; k and f are folded into the coefficients.  The special
-// function unit would otherwise bound the kernel: three of its operations a score instead of one.
+// [-1, 1], where the scores of a capped model nearly always are: x P(x^2), P of degree 5, or of degree 3 on
+// [-0.5, 0.5], fitted for the least greatest error (least squares with weights moved toward the largest
+// errors), 3.1e-7 and 1.6e-7 absolute with binary32 steps, on the packed multiplier; k and f are folded into the
+// coefficients.  The special function unit would otherwise bound the kernels: three of its operations a score
+// instead of one.
 __device__ __forceinline__ float tanh_any(float x) {
   return __fmaf_rn(-2.f, tc5::rcp(1.f + tc5::ex2(x * (2.f * LOG2E))), 1.f);
 }
 struct Cap {
-  float c[6], k, f, most;   // most: the largest |t| that the polynomial takes, 0 where its coefficients would over- or underflow
+  float c[6], s[4], k, f, most;   // most: the largest |t| that the polynomial takes, 0 where its coefficients would over- or underflow
   __device__ __forceinline__ Cap(float scale, float cap) {
     k = scale / cap;
     f = cap * LOG2E;
     const float a = fabsf(k);
     most = a >= 0x1p-12f && a <= 0x1p10f ? 1.f / a : 0.f;
     constexpr float p[6] = {0x1.ffff96p-1f, -0x1.553ce0p-2f, 0x1.0f6ea4p-3f, -0x1.a191cep-5f, 0x1.0803b2p-6f, -0x1.742c6ap-9f};
+    constexpr float q[4] = {0x1.ffffb2p-1f, -0x1.55341ap-2f, 0x1.0d366ap-3f, -0x1.634ea8p-5f};
     float power = k;
 #pragma unroll
     for (int i = 0; i < 6; i++) {
       c[i] = p[i] * power * f;
+      if (i < 4) s[i] = q[i] * power * f;
       power *= k * k;
     }
+  }
+  __device__ __forceinline__ u64 smaller2(u64 t) const {
+    const u64 z = f2::mul(t, t);
+    u64 p = f2::fma(f2::splat(s[3]), z, f2::splat(s[2]));
+    p = f2::fma(p, z, f2::splat(s[1]));
+    p = f2::fma(p, z, f2::splat(s[0]));
+    return f2::mul(t, p);
   }
   __device__ __forceinline__ u64 small2(u64 t) const {
     const u64 z = f2::mul(t, t);
@@ -97,12 +107,16 @@ struct Cap {
       m[0] = max3_abs(m[0], v[i], v[i + 1]);
       m[1] = max3_abs(m[1], v[i + 2], v[i + 3]);
     }
-    if (__any_sync(0xffffffffu, !(fmaxf(m[0], m[1]) <= most))) {
+    const float top = fmaxf(m[0], m[1]);
+    if (__all_sync(0xffffffffu, top <= 0.5f * most)) {
 #pragma unroll
-      for (int i = 0; i < N; i++) v[i] = f * tanh_any(v[i] * k);
-    } else {
+      for (int i = 0; i < N; i += 2) f2::unpack(smaller2(f2::pack(v[i], v[i + 1])), v[i], v[i + 1]);
+    } else if (__all_sync(0xffffffffu, top <= most)) {
 #pragma unroll
       for (int i = 0; i < N; i += 2) f2::unpack(small2(f2::pack(v[i], v[i + 1])), v[i], v[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i++) v[i] = f * tanh_any(v[i] * k);
     }
   }
 };
@@ -662,19 +676,23 @@ __global__ void __launch_bounds__(128) ta_join_kernel(const __grid_constant__ Ta
     a.lse[((int64_t)b * a.Hq + head) * a.Sq + qi] = l > 0.f ? (top + log2f(l)) * ta::LN2 : l == 0.f ? -INFINITY : l;
 }
 
+// Dynamic shared memory of a kernel with `tiles` bytes of 1024-byte aligned tiles: with up to 1024 bytes of static shared
+// memory before them the tiles are aligned within the 227 KB of a CTA.
+template <typename K>
+cudaError_t tile_smem(K kernel, int tiles, int* bytes) {
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+  if (e != cudaSuccess) return e;
+  if (at.sharedSizeBytes > 1024) return cudaErrorInvalidConfiguration;
+  *bytes = tiles + 1024 - (int)at.sharedSizeBytes;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, *bytes);
+}
+
 template <int DP, bool BF>
 cudaError_t ta_forward(const TaArgs& a, cudaStream_t st) {
   using L = TaFwdSmem<DP>;
-  // up to 1024 bytes of static shared memory leave the tiles their alignment within the 227 KB of a CTA
   static int bytes = 0;
-  static const cudaError_t ready = [] {
-    cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, ta_fwd_kernel<DP, BF>);
-    if (e != cudaSuccess) return e;
-    if (at.sharedSizeBytes > 1024) return cudaErrorInvalidConfiguration;
-    bytes = L::END + 1024 - (int)at.sharedSizeBytes;
-    return cudaFuncSetAttribute(ta_fwd_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  }();
+  static const cudaError_t ready = tile_smem(ta_fwd_kernel<DP, BF>, L::END, &bytes);
   if (ready != cudaSuccess) return ready;
   const int HB = a.B * (a.Hq / a.pack);
   const unsigned grid = (unsigned)HB * (a.splits > 0 ? a.splits : (a.qtiles + 1) / 2);
