@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
   using L = TaBwdSmem<DP>;
   constexpr int NST = L::NST, TILE = L::TILE;
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t kv_full, q_full[NST], q_empty[NST], s_full, s_read, dp_full, p_full, p_read, ds_full, done, gone;
+  __shared__ uint64_t kv_full, q_full[NST], q_empty[NST], g_full[NST], g_empty[NST], s_full, s_read, dp_full, p_full, p_read, ds_full, done, gone;
   __shared__ uint32_t tmem_at;
   __shared__ int dead, range[2];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
@@ -141,6 +141,8 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
     for (int s = 0; s < NST; s++) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
+      mbar_init(&g_full[s], 1);
+      mbar_init(&g_empty[s], 1);
     }
     mbar_init(&s_full, 1);
     mbar_init(&s_read, 512);
@@ -175,22 +177,35 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
           tma_load(base + L::KEEP + p * PANEL, &a.k, p * 64, 0, n * TA_TILE, kh, b, &kv_full);
           tma_load(base + L::KEEP + TILE + p * PANEL, &a.v, p * 64, 0, n * TA_TILE, kh, b, &kv_full);
         }
-        bool ok = true;
-        int it = 0;
-        for (; it < total; it++) {
+        // a query tile stays until its second product, a gradient tile goes after its first and dV: apart, so that the next
+        // scores only wait for the former
+        const auto query = [&](int it) -> bool {
           const int s = it % NST, h = kh * a.group + it / nq, q = q0 + it % nq;
-          if (it >= NST) ok = mbar_wait(&q_empty[s], ((it / NST) - 1) & 1, abort);
-          if (!ok) break;
+          if (it >= NST && !mbar_wait(&q_empty[s], ((it / NST) - 1) & 1, abort)) return false;
           const uint32_t at = base + L::ST + s * L::STAGE;
-          mbar_expect_tx(&q_full[s], 2 * TILE + 1024);
-          for (int p = 0; p < DP / 64; p++) {
-            tma_load(at + p * PANEL, &a.q, p * 64, 0, q * TA_TILE, h, b, &q_full[s]);
-            tma_load(at + TILE + p * PANEL, &a.go, p * 64, 0, q * TA_TILE, h, b, &q_full[s]);
-          }
+          mbar_expect_tx(&q_full[s], TILE + 1024);
+          for (int p = 0; p < DP / 64; p++) tma_load(at + p * PANEL, &a.q, p * 64, 0, q * TA_TILE, h, b, &q_full[s]);
           bulk_g2s(gen + L::ST + s * L::STAGE + 2 * TILE, a.rows + (((int64_t)b * a.Hq + h) * a.qtiles + q) * 256, 1024,
                    &q_full[s]);
+          return true;
+        };
+        const auto gradient = [&](int it) -> bool {
+          const int s = it % NST, h = kh * a.group + it / nq, q = q0 + it % nq;
+          if (it >= NST && !mbar_wait(&g_empty[s], ((it / NST) - 1) & 1, abort)) return false;
+          const uint32_t at = base + L::ST + s * L::STAGE + TILE;
+          mbar_expect_tx(&g_full[s], TILE);
+          for (int p = 0; p < DP / 64; p++) tma_load(at + p * PANEL, &a.go, p * 64, 0, q * TA_TILE, h, b, &g_full[s]);
+          return true;
+        };
+        int nqt = 0, ngt = 0;
+        if (query(0)) nqt++;
+        while (ngt < total && gradient(ngt)) {
+          ngt++;
+          if (nqt < total && !query(nqt)) break;
+          if (nqt < total) nqt++;
         }
-        for (int k = max(0, it - NST); k < it; k++) mbar_drain(&q_full[k % NST], (k / NST) & 1);
+        for (int k = max(0, nqt - NST); k < nqt; k++) mbar_drain(&q_full[k % NST], (k / NST) & 1);
+        for (int k = max(0, ngt - NST); k < ngt; k++) mbar_drain(&g_full[k % NST], (k / NST) & 1);
         mbar_drain(&kv_full, 0);
       }
     } else if (warp == 17) {
@@ -203,7 +218,8 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
         if (ok) {
           fence_after();
           go.first(go.ts, ktile, st0, &s_full);
-          go.first(go.tp, vtile, st0 + TILE, &dp_full);
+          ok = all_of(mbar_wait(&g_full[0], 0, abort));
+          if (ok) go.first(go.tp, vtile, st0 + TILE, &dp_full);
         }
         for (int it = 0; it < steps && ok; it++) {
           const uint32_t st = st0 + (it % NST) * L::STAGE, next = st0 + ((it + 1) % NST) * L::STAGE;
@@ -217,12 +233,16 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
           if (!ok) break;
           fence_after();
           go.weights(base + L::P, st + TILE, it > 0, &p_read);
+          commit_one(&g_empty[it % NST], go.one);
           ok = all_of(mbar_wait(&ds_full, it & 1, abort));
           if (!ok) break;
           fence_after();
           go.grads(st, it > 0);
           commit_one(&q_empty[it % NST], go.one);
-          if (it + 1 < steps) go.first(go.tp, vtile, next + TILE, &dp_full);
+          if (it + 1 < steps) {
+            ok = all_of(mbar_wait(&g_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+            if (ok) go.first(go.tp, vtile, next + TILE, &dp_full);
+          }
         }
         commit_one(&done, go.one);
         if (!ok) {
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
   using L = TaBwdSmem<DP>;
   constexpr int NST = L::NST, TILE = L::TILE;
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t q_full, kv_full[NST], kv_empty[NST], s_full, s_read, dp_full, p_full, p_read, ds_full, done, gone;
+  __shared__ uint64_t q_full, k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full, s_read, dp_full, p_full, p_read, ds_full, done, gone;
   __shared__ uint32_t tmem_at;
   __shared__ int dead, range[2];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
@@ -392,8 +412,10 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
     dead = 0;
     mbar_init(&q_full, 1);
     for (int s = 0; s < NST; s++) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
     }
     mbar_init(&s_full, 1);
     mbar_init(&s_read, 512);
@@ -430,20 +452,23 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
           tma_load(base + L::KEEP + p * PANEL, &a.q, p * 64, 0, q * TA_TILE, h, b, &q_full);
           tma_load(base + L::KEEP + TILE + p * PANEL, &a.go, p * 64, 0, q * TA_TILE, h, b, &q_full);
         }
-        bool ok = true;
-        int it = 0;
-        for (; it < total; it++) {
+        const auto fetch = [&](const CUtensorMap* map, int it, int at, uint64_t* full, uint64_t* empty) -> bool {
           const int s = it % NST;
-          if (it >= NST) ok = mbar_wait(&kv_empty[s], ((it / NST) - 1) & 1, abort);
-          if (!ok) break;
-          const uint32_t at = base + L::ST + s * L::STAGE;
-          mbar_expect_tx(&kv_full[s], 2 * TILE);
-          for (int p = 0; p < DP / 64; p++) {
-            tma_load(at + p * PANEL, &a.k, p * 64, 0, (n0 + it) * TA_TILE, kh, b, &kv_full[s]);
-            tma_load(at + TILE + p * PANEL, &a.v, p * 64, 0, (n0 + it) * TA_TILE, kh, b, &kv_full[s]);
-          }
+          if (it >= NST && !mbar_wait(&empty[s], ((it / NST) - 1) & 1, abort)) return false;
+          mbar_expect_tx(&full[s], TILE);
+          for (int p = 0; p < DP / 64; p++)
+            tma_load(base + L::ST + s * L::STAGE + at + p * PANEL, map, p * 64, 0, (n0 + it) * TA_TILE, kh, b, &full[s]);
+          return true;
+        };
+        int nk = 0, nv = 0;
+        if (fetch(&a.k, 0, 0, k_full, k_empty)) nk++;
+        while (nv < total && fetch(&a.v, nv, TILE, v_full, v_empty)) {
+          nv++;
+          if (nk < total && !fetch(&a.k, nk, 0, k_full, k_empty)) break;
+          if (nk < total) nk++;
         }
-        for (int k = max(0, it - NST); k < it; k++) mbar_drain(&kv_full[k % NST], (k / NST) & 1);
+        for (int k = max(0, nk - NST); k < nk; k++) mbar_drain(&k_full[k % NST], (k / NST) & 1);
+        for (int k = max(0, nv - NST); k < nv; k++) mbar_drain(&v_full[k % NST], (k / NST) & 1);
         mbar_drain(&q_full, 0);
       }
     } else if (warp == 17) {
@@ -452,16 +477,20 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
         const uint32_t tm = same(tmem);
         const Products<DP, BF> go{tm, tm + 128, tm + 256 + DP, tm + 256, elect(), idesc<BF>(128, 128, false), idesc<BF>(128, DP, true)};
         const uint32_t qtile = base + L::KEEP, gtile = qtile + TILE, st0 = base + L::ST;
-        bool ok = all_of(mbar_wait(&q_full, 0, abort) && mbar_wait(&kv_full[0], 0, abort));
+        bool ok = all_of(mbar_wait(&q_full, 0, abort) && mbar_wait(&k_full[0], 0, abort));
         if (ok) {
           fence_after();
           go.first(go.ts, qtile, st0, &s_full);
-          go.first(go.tp, gtile, st0 + TILE, &dp_full);
+          ok = all_of(mbar_wait(&v_full[0], 0, abort));
+          if (ok) {
+            go.first(go.tp, gtile, st0 + TILE, &dp_full);
+            commit_one(&v_empty[0], go.one);
+          }
         }
         for (int it = 0; it < steps && ok; it++) {
           const uint32_t st = st0 + (it % NST) * L::STAGE, next = st0 + ((it + 1) % NST) * L::STAGE;
           if (it + 1 < steps) {
-            ok = all_of(mbar_wait(&s_read, it & 1, abort) && mbar_wait(&kv_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+            ok = all_of(mbar_wait(&s_read, it & 1, abort) && mbar_wait(&k_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
             if (!ok) break;
             fence_after();
             go.first(go.ts, qtile, next, &s_full);
@@ -474,8 +503,13 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
           if (!ok) break;
           fence_after();
           go.grads(st, it > 0);
-          commit_one(&kv_empty[it % NST], go.one);
-          if (it + 1 < steps) go.first(go.tp, gtile, next + TILE, &dp_full);
+          commit_one(&k_empty[it % NST], go.one);
+          if (it + 1 < steps) {
+            ok = all_of(mbar_wait(&v_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
+            if (!ok) break;
+            go.first(go.tp, gtile, next + TILE, &dp_full);
+            commit_one(&v_empty[(it + 1) % NST], go.one);
+          }
         }
         commit_one(&done, go.one);
         if (!ok) {
