@@ -24,10 +24,10 @@ struct TaArgs {
   const TaBounds* qbounds;            // backward: [B, query tiles] with docs
   const int* prefix;                  // [B] or null
   float* lse;                         // [B, Hq, Sq], natural logarithm
-  float* rows;                        // backward: [B, Hq, query tiles][2][128] (-lse log2 e), (-delta); -inf, 0 for a
-                                      // row that sees nothing and past the last query
+  float* rows;                        // backward, from the dq kernel to the other: [B, Hq, query tiles][2][128]
+                                      // (-lse log2 e), (-delta); -inf, 0 for a row that sees nothing and past the last query
   float* part;                        // split forward: sums [2 splits][B Hkv][128][DP], then (max, total) pairs
-  void* out;                          // join of the split forward: strides of b, h, s
+  void* out;                          // join of the split forward; strides of b, h, s
   int64_t os[3];
   int* status;
   int B, Hq, Hkv, Sq, Skv, D;
@@ -48,17 +48,7 @@ template <int DP, bool BF>
 cudaError_t ta_dkv(const TaArgs& a, cudaStream_t st);
 template <int DP, bool BF>
 cudaError_t ta_dq(const TaArgs& a, cudaStream_t st);
-// tiles of the last S tokens of each row of docs [B, Skv]
-cudaError_t ta_bounds(const int* docs, int B, int Skv, int S, TaBounds* out, cudaStream_t st);
-// the rows array: delta = sum over d of out * grad; strides of b, h, s in elements
-struct TaRowsArgs {
-  const void* out;
-  const void* grad;
-  const float* lse;
-  float* rows;
-  int64_t os[3], gs[3];
-  int B, Hq, Sq, D, qtiles, bf;
-};
-cudaError_t ta_rows(const TaRowsArgs& a, cudaStream_t st);
+// bounds of the key tiles and, unless null, of the tiles of the last Sq tokens (the queries)
+cudaError_t ta_bounds(const int* docs, int B, int Skv, int Sq, TaBounds* keys, TaBounds* queries, cudaStream_t st);
 
 }  // namespace detattn

@@ -26,6 +26,7 @@
 #include "../../include/detattn.h"
 #include "attn_train.h"
 #include "attn_train_fwd.cuh"
+#include "train_math.cuh"
 
 namespace detattn {
 
@@ -447,10 +448,11 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");
     if (warp == 16) {
       if (lane == 0 && total > 0) {
-        mbar_expect_tx(&q_full, 2 * TILE);
+        mbar_expect_tx(&q_full, 3 * TILE);
         for (int p = 0; p < DP / 64; p++) {
           tma_load(base + L::KEEP + p * PANEL, &a.q, p * 64, 0, q * TA_TILE, h, b, &q_full);
           tma_load(base + L::KEEP + TILE + p * PANEL, &a.go, p * 64, 0, q * TA_TILE, h, b, &q_full);
+          tma_load(base + L::P + p * PANEL, &a.o, p * 64, 0, q * TA_TILE, h, b, &q_full);
         }
         const auto fetch = [&](const CUtensorMap* map, int it, int at, uint64_t* full, uint64_t* empty) -> bool {
           const int s = it % NST;
@@ -526,7 +528,38 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
     const Scores sc(a);
     const float slope = a.slopes ? a.slopes[h] * LOG2E : 0.f;
     float* const my_row = a.rows + (((int64_t)b * a.Hq + h) * a.qtiles + q) * 256 + r;
-    const float shift = my_row[0], less = my_row[128];      // -lse, -delta
+    float* const sums = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + L::P);   // the weights' tile, when it is free
+    // -lse and, from the rounded output, -delta: a quarter of the row's dimensions a thread.  The output's tile was copied
+    // to the weights'; its words are read, then the quarters' sums take its place.
+    float shift = -INFINITY, less;
+    {
+      using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+      if (qi < a.Sq) {
+        const float l = a.lse[((int64_t)b * a.Hq + h) * a.Sq + qi];
+        if (l != -INFINITY) shift = -l * LOG2E;
+      }
+      float s = 0.f;
+      if (total > 0) {
+        mbar_wait(&q_full, 0, abort);
+        const unsigned char* const o = raw + (base - smem_addr(raw)) + L::P;
+        const unsigned char* const g = raw + (base - smem_addr(raw)) + L::KEEP + TILE;
+#pragma unroll
+        for (int k = 0; k < DP / 32; k++) {
+          const int u = part * (DP / 32) + k, at = (u >> 3) * PANEL + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+          Run<T, 8> x, y;
+          x.load((const T*)(o + at));
+          y.load((const T*)(g + at));
+#pragma unroll
+          for (int e = 0; e < 8; e++) s = __fmaf_rn(x.get(e), y.get(e), s);
+        }
+      }
+      __syncwarp();
+      bar_sync(5, 512);
+      sums[part * 128 + r] = s;
+      bar_sync(5, 512);
+      less = shift == -INFINITY ? 0.f : -((sums[r] + sums[128 + r]) + (sums[256 + r] + sums[384 + r]));
+      bar_sync(5, 512);
+    }
     const int doc = a.docs && qi < a.Sq ? a.docs[(int64_t)b * a.Skv + pos] : -1;
     TaBounds qb{};
     if (a.docs) qb = a.qbounds[(int64_t)b * a.qtiles + q];
@@ -630,7 +663,6 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
     if (total > 0) mbar_wait(&done, 0, abort);
     __syncwarp();
     fence_after();
-    float* const sums = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + L::P);   // the weights' tile is no longer read
     // The sums were taken with delta from the rounded output; with D = sum p dp the gradient is
     // scale (sum ds k - (D - delta) sum p (1 - tanh^2) k).  D goes to the other kernel too.
     {
@@ -640,7 +672,10 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
     }
     bar_sync(5, 512);
     const float exact = (sums[r] + sums[128 + r]) + (sums[256 + r] + sums[384 + r]);
-    if (part == 0 && !dead) my_row[128] = -exact;
+    if (part == 0 && !dead) {
+      my_row[0] = shift;
+      my_row[128] = -exact;
+    }
     __syncwarp();
     const uint32_t qt = base + L::KEEP, acc = tmem + lanes + 256;
     if (DP == 128) row_out<BF, 32>(qt, acc, acc + DP, r, part * 32, a.scale, -less - exact, total > 0);

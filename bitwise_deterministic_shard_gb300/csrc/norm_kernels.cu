@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(G == 32 ? 32 * WARP_ROWS : G, fwd_ctas(G)) nor
     for (int i = 0; i < VEC / 2; i++) y.set2(i, f2::fma(f2::mul(f2::add(x.get2(k, i), off), rstd2), w[i], b[i]));
     store_vec<T, G, AL>((T*)a.y + row * a.ys, cols, t, k, y);
   }
-  if (t == 0) {
+  if (t == 0 && a.mean) {
     a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormArgs a) {
     const float b = !a.b ? 0.f : wf ? ((const float*)a.b)[c] : Elem<T>::get(((const T*)a.b)[c]);
     y[c] = Elem<T>::put(__fmaf_rn((Elem<T>::get(x[c]) - mean) * rstd, w, b));
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && a.mean) {
     a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(G, 512 / G) norm_fwd_stream_kernel(const NormA
             y.set2(i, f2::fma(f2::mul(f2::add(x.get2(i), f2::splat(-mean[r])), f2::splat(rstd)), w[k][i], b[k][i]));
           store_vec<T, G, true>((T*)a.y + (row + r) * a.ys, cols, t, k, y);
         }
-        if (t == 0) {
+        if (t == 0 && a.mean) {
           a.mean[row + r] = mean[r];
           a.rstd[row + r] = rstd;
         }

@@ -197,7 +197,7 @@ DA_EXPORT int dta_forward(const dta_desc* d, const da_tensor* out, float* lse, v
   if (!tensor_map(&a.q, d->q, a.pack, a.qrows) || !tensor_map(&a.o, *out, a.pack, a.qrows) ||
       !tensor_map(&a.k, d->k, 1, TA_TILE) || !tensor_map(&a.v, d->v, 1, TA_TILE))
     return DA_ECUDA;
-  if (a.docs && (e = launched(ta_bounds(a.docs, a.B, a.Skv, a.Skv, const_cast<TaBounds*>(a.bounds), st)))) return e;
+  if (a.docs && (e = launched(ta_bounds(a.docs, a.B, a.Skv, a.Sq, const_cast<TaBounds*>(a.bounds), nullptr, st)))) return e;
   const bool bf = d->q.dtype == DA_BF16;
   if (head_width(a.D) == 64) return launched(bf ? ta_forward<64, true>(a, st) : ta_forward<64, false>(a, st));
   return launched(bf ? ta_forward<128, true>(a, st) : ta_forward<128, false>(a, st));
@@ -219,31 +219,23 @@ DA_EXPORT int dta_backward(const dta_desc* d, const da_tensor* out, const float*
   if (!aligned(ws, 256)) return DA_EALIGN;
   if (a.B == 0 || a.Skv == 0) return DA_OK;
   cudaStream_t st = (cudaStream_t)stream;
-  float* rows = reinterpret_cast<float*>((char*)ws + w.part);
-  a.rows = rows;
+  a.rows = reinterpret_cast<float*>((char*)ws + w.part);
   a.bounds = reinterpret_cast<const TaBounds*>((char*)ws + w.bounds);
   a.qbounds = reinterpret_cast<const TaBounds*>((char*)ws + w.qbounds);
   if (!tensor_map(&a.k, d->k, 1, TA_TILE) || !tensor_map(&a.v, d->v, 1, TA_TILE) || !tensor_map(&a.dk, *dk, 1, TA_TILE) ||
       !tensor_map(&a.dv, *dv, 1, TA_TILE))
     return DA_ECUDA;
   if (a.Sq > 0 && (!tensor_map(&a.q, d->q, 1, TA_TILE) || !tensor_map(&a.go, *grad, 1, TA_TILE) ||
+                   !tensor_map(&a.o, *out, 1, TA_TILE) ||
                    !tensor_map(&a.dq, *dq, 1, TA_TILE)))
     return DA_ECUDA;
-  if (a.docs) {
-    if ((e = launched(ta_bounds(a.docs, a.B, a.Skv, a.Skv, const_cast<TaBounds*>(a.bounds), st)))) return e;
-    if ((e = launched(ta_bounds(a.docs, a.B, a.Skv, a.Sq, const_cast<TaBounds*>(a.qbounds), st)))) return e;
-  }
+  if (a.docs && (e = launched(ta_bounds(a.docs, a.B, a.Skv, a.Sq, const_cast<TaBounds*>(a.bounds),
+                                       const_cast<TaBounds*>(a.qbounds), st))))
+    return e;
   const bool bf = d->q.dtype == DA_BF16;
-  TaRowsArgs r;
-  r.out = out->ptr; r.grad = grad->ptr; r.lse = lse; r.rows = rows;
-  for (int i = 0; i < 3; i++) {
-    r.os[i] = out->stride[i];
-    r.gs[i] = grad->stride[i];
-  }
-  r.B = a.B; r.Hq = a.Hq; r.Sq = a.Sq; r.D = a.D; r.qtiles = a.qtiles; r.bf = bf;
-  if ((e = launched(ta_rows(r, st)))) return e;
+  a.lse = const_cast<float*>(lse);
   const bool narrow = head_width(a.D) == 64;
-  // dq first: it leaves the rows array's delta as the other kernel takes it
+  // dq first: it leaves the rows array that the other kernel takes
   e = launched(narrow ? bf ? ta_dq<64, true>(a, st) : ta_dq<64, false>(a, st)
                       : bf ? ta_dq<128, true>(a, st) : ta_dq<128, false>(a, st));
   if (e) return e;
@@ -259,7 +251,7 @@ DA_EXPORT int dln_forward(const da_matrix* x, const void* w, const void* b, int 
     return e;
   if (!(eps >= 0.f) || !std::isfinite(eps)) return DA_EINVAL;
   if (x->rows == 0) return DA_OK;
-  if (!mean || !rstd) return DA_EINVAL;
+  if (!mean != !rstd) return DA_EINVAL;
   if (!aligned(mean, 4) || !aligned(rstd, 4)) return DA_EALIGN;
   NormArgs a;
   std::memset(&a, 0, sizeof(a));

@@ -13,7 +13,7 @@ struct NormArgs {
   void* y;               // forward: y; backward: dx; row stride ys
   const void* w;         // [cols] or null (ones)
   const void* b;         // [cols] or null (zeros); forward only
-  float* mean;           // [rows]
+  float* mean;           // [rows]; forward: with rstd, or null
   float* rstd;           // [rows]
   void* dw;              // [cols] or null; the type of w
   void* db;              // [cols] or null

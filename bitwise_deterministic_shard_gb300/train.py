@@ -112,8 +112,6 @@ def _view(t, code):
 
 
 def _option(t, name, dtype, shape, index):
-    if t is None:
-        return None
     _on(index, name, t)
     if t.dtype != dtype or tuple(t.shape) != shape:
         raise DetAttnError(f"{name} must be {dtype} {list(shape)}")
@@ -122,40 +120,45 @@ def _option(t, name, dtype, shape, index):
 
 class _Attention:
     """Checked arguments of one attention call; keeps the tensors alive while it lives."""
-    __slots__ = ("desc", "keep", "code", "index", "device", "lse_shape")
+    __slots__ = ("desc", "keep", "code", "index", "device", "shape")
 
     def __init__(self, Q, K, V, causal, scale, softcap, slopes, docs, prefix, status):
         _da._cuda(Q, "Q")
         index = self.index = Q.get_device()
-        _on(index, "K", K)
-        _on(index, "V", V)
-        if Q.dim() != 4 or K.dim() != 4 or V.dim() != 4:
+        if K.get_device() != index or V.get_device() != index:
+            raise DetAttnError("Q, K and V must be CUDA tensors on one device")
+        dt, shape, kshape = Q.dtype, Q.shape, K.shape
+        if len(shape) != 4 or len(kshape) != 4 or V.dim() != 4:
             raise DetAttnError("Q, K and V must be [B, H, S, D]")
-        code = self.code = _code(Q, "Q", _HALF)
-        if K.dtype != Q.dtype or V.dtype != Q.dtype:
-            raise DetAttnError("Q, K and V must share one dtype (bf16 or f16)")
-        self.device = Q.device
-        B, Hq, Sq, _ = Q.shape
-        self.lse_shape = (B, Hq, Sq)
-        if slopes is not None and slopes.requires_grad:
-            raise DetAttnError("slopes have no gradient: pass them detached")
-        slopes = _option(slopes, "slopes", torch.float32, (Hq,), index)
-        docs = _option(docs, "docs", torch.int32, (B, K.shape[2]), index)
-        prefix = _option(prefix, "prefix", torch.int32, (B,), index)
-        q, k, v = _ready(Q), _ready(K), _ready(V)
-        self.keep = (q, k, v, slopes, docs, prefix)
+        code = self.code = _HALF.get(dt, 0)
+        if not code or K.dtype != dt or V.dtype != dt:
+            raise DetAttnError(f"Q, K and V must share one dtype (bf16 or f16), not {dt}, {K.dtype}, {V.dtype}")
+        self.device, self.shape = Q.device, shape
+        slopes_at = docs_at = prefix_at = status_at = 0
+        if slopes is not None:
+            if slopes.requires_grad:
+                raise DetAttnError("slopes have no gradient: pass them detached")
+            slopes = _option(slopes, "slopes", torch.float32, (shape[1],), index)
+            slopes_at = slopes.data_ptr()
+        if docs is not None:
+            docs = _option(docs, "docs", torch.int32, (shape[0], kshape[2]), index)
+            docs_at = docs.data_ptr()
+        if prefix is not None:
+            prefix = _option(prefix, "prefix", torch.int32, (shape[0],), index)
+            prefix_at = prefix.data_ptr()
         if status is not None:
             _on(index, "status", status)
-            status = _da._sptr(status).value
-        self.desc = _DESC.pack(q.data_ptr(), code, *q.shape, *q.stride(), k.data_ptr(), code, *k.shape, *k.stride(),
+            status_at = _da._sptr(status).value
+        q, k, v = _ready(Q), _ready(K), _ready(V)
+        self.keep = (q, k, v, slopes, docs, prefix)
+        self.desc = _DESC.pack(q.data_ptr(), code, *shape, *q.stride(), k.data_ptr(), code, *kshape, *k.stride(),
                                v.data_ptr(), code, *v.shape, *v.stride(), 1 if causal else 0,
-                               math.nan if scale is None else scale, softcap, _addr(slopes) or 0, _addr(docs) or 0,
-                               _addr(prefix) or 0, status or 0)
+                               math.nan if scale is None else scale, softcap, slopes_at, docs_at, prefix_at, status_at)
 
 
 def _like(t):
     """An uninitialised tensor of t's layout where that is dense and fit for the kernels, else contiguous."""
-    o = torch.empty_like(t, requires_grad=False)
+    o = torch.empty_like(t)
     return o if _fits(o) else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
@@ -184,7 +187,7 @@ def attention_forward(Q, K, V, causal=False, scale=None, softcap=0.0, slopes=Non
     dimension that is not contiguous, strides or starts off 16 bytes, broadcast dimensions) are copied."""
     A = _Attention(Q, K, V, causal, scale, softcap, slopes, docs, prefix, status)
     out = _given(out, Q, "out")
-    lse = torch.empty(A.lse_shape, dtype=torch.float32, device=A.device) if need_lse else None
+    lse = torch.empty(A.shape[:3], dtype=torch.float32, device=A.device) if need_lse else None
     L = _da.lib()
     need = L.dta_workspace_bytes(A.desc, 0)
     ws = _room(need, workspace, A.device)
@@ -197,14 +200,15 @@ def attention_backward(Q, K, V, out, lse, grad, causal=False, scale=None, softca
     """(dQ, dK, dV) of sum(out * grad) from attention_forward's out and lse; the other arguments as there.
     The gradient of a shared key head is the sum over its query heads, formed in binary32."""
     A = _Attention(Q, K, V, causal, scale, softcap, slopes, docs, prefix, status)
-    for t, name in ((out, "out"), (grad, "grad")):
-        _on(A.index, name, t)
-        if t.dtype != Q.dtype or t.shape != Q.shape:
-            raise DetAttnError(f"{name} must be {Q.dtype} {tuple(Q.shape)}")
-    _on(A.index, "lse", lse)
-    if lse.dtype != torch.float32 or lse.shape != A.lse_shape:
-        raise DetAttnError(f"lse must be f32 {A.lse_shape}")
-    out, grad, lse = _ready(out), _ready(grad), lse.contiguous()
+    index, shape, dt = A.index, A.shape, Q.dtype
+    for t in (out, grad):
+        if t.get_device() != index or t.dtype != dt or t.shape != shape:
+            raise DetAttnError(f"out and grad must be {dt} {tuple(shape)} on Q's device")
+    if lse.get_device() != index or lse.dtype != torch.float32 or lse.shape != shape[:3]:
+        raise DetAttnError(f"lse must be f32 {tuple(shape[:3])} on Q's device")
+    out, grad = _ready(out), _ready(grad)
+    if not lse.is_contiguous():
+        lse = lse.contiguous()
     dq, dk, dv = _like(Q), _like(K), _like(V)
     L, c = _da.lib(), A.code
     need = L.dta_workspace_bytes(A.desc, 1)
@@ -265,39 +269,43 @@ def _rows(t, code, cols):
 
 def _weights(x, weight, bias):
     _da._cuda(x, "x")
-    cols = x.shape[-1] if x.dim() else 0
+    shape, dt = x.shape, x.dtype
+    cols = shape[-1] if shape else 0
     if cols < 1:
         raise DetAttnError("x must be [..., cols] with at least one column")
     code, index = _code(x, "x"), x.get_device()
     wt = None
-    for t, name in ((weight, "weight"), (bias, "bias")):
+    for t in (weight, bias):
         if t is None:
             continue
-        _on(index, name, t)
-        if t.dim() != 1 or t.shape[0] != cols or (t.dtype != x.dtype and t.dtype != torch.float32):
-            raise DetAttnError(f"{name} must be [{cols}] of x's dtype or f32")
-        if wt is not None and t.dtype != wt:
+        kind = t.dtype
+        if t.get_device() != index or t.dim() != 1 or t.shape[0] != cols or (kind != dt and kind != torch.float32):
+            raise DetAttnError(f"weight and bias must be [{cols}] of x's dtype or f32, on its device")
+        if wt is not None and kind != wt:
             raise DetAttnError("weight and bias must share one dtype")
-        wt = t.dtype
-    return cols, code, wt or x.dtype, index
+        wt = kind
+    return cols, code, wt or dt, index
 
 
 def _packed(t):
     return t if t is None or t.is_contiguous() else t.detach().contiguous()
 
 
-def layer_norm_forward(x, weight=None, bias=None, eps=1e-5):
+def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, need_stats=True):
     """Layer norm over the last dimension: (y like x, mean f32, rstd f32, one per row).
-    x [..., cols] f32, bf16 or f16; weight and bias [cols] of x's dtype or f32, or None."""
+    x [..., cols] f32, bf16 or f16; weight and bias [cols] of x's dtype or f32, or None.  mean and rstd, which
+    the backward pass takes, are None without need_stats."""
     cols, code, wt, index = _weights(x, weight, bias)
     X, x = _rows(x, code, cols)
     weight, bias = _packed(weight), _packed(bias)
     shape, dev = x.shape, x.device
     y = torch.empty(shape, dtype=x.dtype, device=dev)
-    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    Y = _MATRIX.pack(y.data_ptr(), code, mean.numel(), cols, cols)
-    _da._check(_da.lib().dln_forward(X, _addr(weight), _addr(bias), _CODES[wt], eps, Y, mean.data_ptr(), rstd.data_ptr(),
+    mean = rstd = None
+    if need_stats:
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    Y = _MATRIX.pack(y.data_ptr(), code, y.numel() // cols, cols, cols)
+    _da._check(_da.lib().dln_forward(X, _addr(weight), _addr(bias), _CODES[wt], eps, Y, _addr(mean), _addr(rstd),
                                      _stream(index)), "layer_norm_forward")
     return y, mean, rstd
 
@@ -306,14 +314,12 @@ def layer_norm_backward(grad, x, weight, mean, rstd, need_weight=True, need_bias
     """(dx, dweight, dbias) from the upstream gradient and layer_norm_forward's mean and rstd; the
     weight gradients are None where not needed, and of weight's dtype (x's without a weight)."""
     cols, code, wt, index = _weights(x, weight, None)
-    _on(index, "grad", grad)
-    if grad.shape != x.shape or grad.dtype != x.dtype:
-        raise DetAttnError("grad must have x's shape and dtype")
+    if grad.get_device() != index or grad.shape != x.shape or grad.dtype != x.dtype:
+        raise DetAttnError("grad must have x's shape, dtype and device")
     rows = x.numel() // cols
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _on(index, name, t)
-        if t.dtype != torch.float32 or t.numel() != rows or not t.is_contiguous():
-            raise DetAttnError(f"{name} must be contiguous f32 with one entry per row")
+    for t in (mean, rstd):
+        if t.get_device() != index or t.dtype != torch.float32 or t.numel() != rows or not t.is_contiguous():
+            raise DetAttnError("mean and rstd must be contiguous f32 with one entry per row, on x's device")
     X, x = _rows(x, code, cols)
     G, grad = _rows(grad, code, cols)
     weight = _packed(weight)
@@ -351,9 +357,10 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """layer_norm_forward's y, with autograd for x, weight and bias."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
+                                    or (bias is not None and bias.requires_grad)):
         return _LayerNorm.apply(x, weight, bias, eps)
-    return layer_norm_forward(x, weight, bias, eps)[0]
+    return layer_norm_forward(x, weight, bias, eps, need_stats=False)[0]
 
 
 # ---------------------------------------------------------------- AdamW
@@ -382,16 +389,16 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     dt, index = params[0].dtype, params[0].get_device()
     code = _code(params[0], "params")
     _da._cuda(params[0], "params")
-    table, at = [], 0
+    table, at, block = [], 0, STATE_BLOCK
     for p, g in zip(params, grads):
-        if p.dtype != dt or p.get_device() != index or not p.is_contiguous():
+        if p.dtype is not dt or p.get_device() != index or not p.is_contiguous():
             raise DetAttnError("params must be contiguous tensors of one dtype on one device")
         m = p.numel()
         if g is not None:
-            if g.dtype != dt or g.numel() != m or g.get_device() != index or not g.is_contiguous():
+            if g.dtype is not dt or g.numel() != m or g.get_device() != index or not g.is_contiguous():
                 raise DetAttnError("grads must be contiguous, of their params' dtype, device and size")
             table += (p.data_ptr(), g.data_ptr(), m, at)
-        at += (m + STATE_BLOCK - 1) // STATE_BLOCK * STATE_BLOCK
+        at += -(-m // block) * block
     bits = 8 if exp_avg.dtype == torch.float8_e4m3fn else 32
     st = torch.float8_e4m3fn if bits == 8 else torch.float32
     for t, name, want, length in ((exp_avg, "exp_avg", st, at), (exp_avg_sq, "exp_avg_sq", st, at),

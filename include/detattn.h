@@ -364,7 +364,7 @@ int dta_backward(const dta_desc* desc, const da_tensor* out, const float* lse, c
 
 /* Layer norm over the columns of x: y = (x - mean) rstd w + b, rstd = 1 / sqrt(var + eps).
  * x, y: [rows, cols] of one type (f32, bf16, f16); w, b: optional device [cols], contiguous, of type
- * wdtype (x's or f32); mean, rstd: device f32 [rows], written. */
+ * wdtype (x's or f32); mean, rstd: device f32 [rows], written for the backward pass, or both NULL. */
 int dln_forward(const da_matrix* x, const void* w, const void* b, int wdtype, float eps, const da_matrix* y, float* mean,
                 float* rstd, da_stream_t stream);
 
