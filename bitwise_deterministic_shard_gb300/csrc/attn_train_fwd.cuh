@@ -28,7 +28,8 @@
 // Few queries (Sq * group <= 128): the heads that share a key head are the rows of one tile, so
 // a cache is read once; both groups take the same queries and every other key tile, and the key range
 // is split over CTAs so that all SMs read.  Each group writes its unnormalised sums, a second
-// kernel joins them in a fixed order.
+// kernel joins them in a fixed order.  Without a split of the keys over CTAs the second group hands its sums to the
+// first within the CTA; calls with few query tiles take this form too, as twice as many CTAs of half the steps.
 #pragma once
 #include "../../include/detattn.h"
 #include "attn_train.h"
@@ -229,7 +230,8 @@ struct TaFwdSmem {
   static constexpr int Q = 0, P = 2 * TILE, KV = P + 2 * PTILE, MAX = KV + NST * TILE, END = MAX + 2048;
 };
 
-template <int DP, bool BF>
+// ALT: both groups share a query tile and take every other key tile
+template <int DP, bool BF, bool ALT>
 __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_constant__ TaArgs a) {
   using namespace tc5;
   using namespace ta;
@@ -248,16 +250,17 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   const int NH = a.Hq / a.pack, HB = a.B * NH;
   const int hb = blockIdx.x % HB, b = hb / NH, h = hb % NH;
   const int kh = a.pack > 1 ? h : h / a.group;
-  const bool alt = a.splits > 0;
-  const int t = alt ? 0 : (int)(gridDim.x / HB) - 1 - blockIdx.x / HB;   // the last queries first: with causal masking the longest
-  const int z = alt ? blockIdx.x / HB : 0;
-  const int nst = alt ? L::MOST : L::NST;
+  constexpr bool alt = ALT;
+  // the last queries first: with causal masking the longest
+  const int bt = blockIdx.x / HB, z = alt ? bt % a.splits : 0;
+  const int t = alt ? a.qtiles - 1 - bt / a.splits : (int)(gridDim.x / HB) - 1 - bt;
+  constexpr int nst = alt ? L::MOST : L::NST;
   // the ring's stages: the split form's last one lies in the second query tile
   const auto stage_at = [&](int s) { return base + (s < L::NST ? L::KV + s * TILE : TILE); };
 
   // this thread's query row (softmax groups)
   const int wg = warp >> 3, half = (warp >> 2) & 1, r = threadIdx.x & 127;
-  const int qt = alt ? 0 : 2 * t + wg;
+  const int qt = alt ? t : 2 * t + wg;
   int qi, head;
   if (a.pack > 1) {
     qi = r / a.pack;
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         for (int p = 0; p < DP / 64; p++) {
           const int at = base + L::Q + i * TILE + p * PANEL;
           if (a.pack > 1) tma_load(at, &a.q, p * 64, 0, 0, h, b, &q_full);   // an empty second tile too
-          else tma_load(at, &a.q, p * 64, 0, min(2 * t + i, a.qtiles - 1) * TA_TILE, h, b, &q_full);
+          else tma_load(at, &a.q, p * 64, 0, min(alt ? t : 2 * t + i, a.qtiles - 1) * TA_TILE, h, b, &q_full);
         }
       int it = 0;
       auto fetch = [&](const CUtensorMap* map, int n) -> bool {
@@ -461,10 +464,27 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     float m = fixed ? 0.f : -INFINITY, l = 0.f;
     const int step = alt ? 2 : 1, end = i ? hi1 : hi0;
     int cnt = 0;
+    // Padding may hold NaN, and 0 NaN is NaN: its value rows become zeros, a row a thread.
+    const auto clean = [&](int n) {
+      const int d = n - lo, k = min(ntile, d + 2) + d;   // this value tile in the order of the copies
+      const int j = n * TA_TILE + r;
+      mbar_wait(&kv_full[k % nst], (k / nst) & 1, abort);
+      if (half == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(stage_at(k % nst), r);
+      __syncwarp();
+    };
+    // a warp without a query leaves its rows of the weights as they are (the products of a row are its own) and only keeps step
+    const bool none = !__any_sync(0xffffffffu, valid);
     // a wait that gives up (dead is set) only spoils values: every barrier below is still passed
     for (int n = lo + (alt ? i : 0); n < end; n += step, cnt++) {
       mbar_wait(&s_full[i], cnt & 1, abort);
       __syncwarp();
+      if (none) {
+        mbar_arrive(&s_read[i]);
+        if (cnt > 0) mbar_wait(&pv_done[i], (cnt - 1) & 1, abort);
+        if (a.docs && a.bounds[(int64_t)b * a.ktiles + n].neg) clean(n);
+        mbar_arrive(&p_full[i]);
+        continue;
+      }
       fence_after();
       float v[64];
       ld_x32(ts + half * 64, v);
@@ -563,13 +583,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         f2::unpack(f2::add(sum[0], sum[1]), x, y);
         l += x + y;
       }
-      if (padded) {   // padding may hold NaN, and 0 NaN is NaN: its value rows become zeros
-        const int d = n - lo, k = min(ntile, d + 2) + d;   // this value tile in the order of the copies
-        const int j = n * TA_TILE + r;
-        mbar_wait(&kv_full[k % nst], (k / nst) & 1, abort);
-        if (half == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(stage_at(k % nst), r);
-        __syncwarp();
-      }
+      if (padded) clean(n);
       fence_async_smem();
       fence_before();
       mbar_arrive(&p_full[i]);
@@ -587,41 +601,96 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     }
     if (valid && !isfinite(l) && half == 0 && a.status) atomicOr(a.status, DA_STATUS_NONFINITE);
     __syncwarp();
-    if (!alt) {
+    float lse = l > 0.f ? (m * f + log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
+    if (alt && a.splits == 1) {
+      // one CTA holds all keys: the second group hands its sums to the first through the weights' tiles
+      unsigned char* const room = raw + (base - smem_addr(raw)) + L::P;
+      float2* const stat = reinterpret_cast<float2*>(exchange);
+      const auto at = [&](int c) { return reinterpret_cast<float4*>(room + r * (DP * 4) + (((half * (DP / 2) + c) >> 2) ^ (r & 7)) * 16); };
+      bar_sync(11, 512);
+      if (i == 1) {
+        if (half == 0) stat[r] = make_float2(m * f, l);
+        if (cnt > 0) {
+#pragma unroll 1
+          for (int c = 0; c < DP / 2; c += 16) {
+            float x[16];
+            ld_x16(to + c, x);
+            ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) *at(c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+        }
+      }
+      bar_sync(11, 512);
+      if (i == 0) {
+        const float2 other = stat[r];
+        const float m0 = m * f, top = fmaxf(l != 0.f ? m0 : -INFINITY, other.y != 0.f ? other.x : -INFINITY);
+        const float k0 = l != 0.f ? ex2(m0 - top) : 0.f, k1 = other.y != 0.f ? ex2(other.x - top) : 0.f;
+        const float all = l * k0 + other.y * k1, inv = all > 0.f ? 1.f / all : all;
+        lse = all > 0.f ? (top + log2f(all)) * LN2 : all == 0.f ? -INFINITY : all;
+        const bool more = ntile > 1;
+        const uint32_t tile = base + L::Q;
+#pragma unroll 1
+        for (int c = 0; c < DP / 2; c += 16) {
+          float x[16];
+          if (cnt > 0) {
+            ld_x16(to + c, x);
+            ld_wait();
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (more && k1 > 0.f) y = *at(c + e);
+            const float o[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int w = 0; w < 4; w++) x[e + w] = (cnt > 0 ? __fmaf_rn(x[e + w], k0, o[w] * k1) : 0.f) * inv;
+          }
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            const int col = half * (DP / 2) + c + 8 * u;
+            const uint32_t to_smem = tile + (col >> 6) * PANEL + r * 128 + ((((col & 63) >> 3) ^ (r & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to_smem), "r"(pack16<BF>(x[8 * u], x[8 * u + 1])),
+                         "r"(pack16<BF>(x[8 * u + 2], x[8 * u + 3])), "r"(pack16<BF>(x[8 * u + 4], x[8 * u + 5])),
+                         "r"(pack16<BF>(x[8 * u + 6], x[8 * u + 7]))
+                         : "memory");
+          }
+        }
+      }
+    } else if (!alt) {
       const uint32_t tile = base + L::Q + i * TILE;
       row_out<BF, DP / 2>(tile, tmem + lanes + 256 + i * DP, tmem + lanes + 256 + i * DP, r, half * (DP / 2),
                           l > 0.f ? 1.f / l : l, 0.f, cnt > 0);   // a row that sees nothing: zeros times zero
+    }
+    if (!alt || a.splits == 1) {
+      const bool mine = qt < a.qtiles && !(alt && i == 1);
       fence_async_smem();
       bar_sync(9 + i, 256);
-      if (r == 0 && half == 0 && qt < a.qtiles && !dead) {
+      if (r == 0 && half == 0 && mine && !dead) {
+        const uint32_t tile = base + L::Q + (alt ? 0 : i * TILE);
         for (int p = 0; p < DP / 64; p++)
           if (p * 64 < a.D) {
-            if (a.pack > 1) {
-              if (i == 0) tma_store(&a.o, tile + p * PANEL, p * 64, 0, 0, h, b);
-            } else {
-              tma_store(&a.o, tile + p * PANEL, p * 64, 0, qt * TA_TILE, h, b);
-            }
+            if (a.pack > 1) tma_store(&a.o, tile + p * PANEL, p * 64, 0, 0, h, b);
+            else tma_store(&a.o, tile + p * PANEL, p * 64, 0, qt * TA_TILE, h, b);
           }
         tma_store_commit();
         tma_store_wait();
       }
-      if (a.lse && half == 0 && valid && qt < a.qtiles)
-        a.lse[((int64_t)b * a.Hq + head) * a.Sq + qi] = l > 0.f ? (m * f + log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
+      if (a.lse && half == 0 && valid && mine) a.lse[((int64_t)b * a.Hq + head) * a.Sq + qi] = lse;
     } else {
       const int64_t row = ((int64_t)(2 * z + i) * HB + hb) * TA_TILE + r;
       float* o = a.part + row * DP + half * (DP / 2);
       float2* ml = reinterpret_cast<float2*>(a.part + (int64_t)2 * a.splits * HB * TA_TILE * DP) + row;
       if (valid && half == 0) *ml = make_float2(m * f, l);
-#pragma unroll
-      for (int c = 0; c < DP / 2; c += 32) {
-        float x[32];
+#pragma unroll 1
+      for (int c = 0; c < DP / 2; c += 16) {
+        float x[16];
         if (cnt > 0) {
-          ld_x32(to + c, x);
+          ld_x16(to + c, x);
           ld_wait();
         }
         if (valid && cnt > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
+          for (int e = 0; e < 16; e += 4)
             *reinterpret_cast<float4*>(o + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         }
       }
@@ -691,13 +760,16 @@ cudaError_t tile_smem(K kernel, int tiles, int* bytes) {
 template <int DP, bool BF>
 cudaError_t ta_forward(const TaArgs& a, cudaStream_t st) {
   using L = TaFwdSmem<DP>;
-  static int bytes = 0;
-  static const cudaError_t ready = tile_smem(ta_fwd_kernel<DP, BF>, L::END, &bytes);
-  if (ready != cudaSuccess) return ready;
+  static int bytes[2] = {};
+  static const cudaError_t ready[2] = {tile_smem(ta_fwd_kernel<DP, BF, false>, L::END, &bytes[0]),
+                                       tile_smem(ta_fwd_kernel<DP, BF, true>, L::END, &bytes[1])};
+  const bool alt = a.splits > 0;
+  if (ready[alt] != cudaSuccess) return ready[alt];
   const int HB = a.B * (a.Hq / a.pack);
-  const unsigned grid = (unsigned)HB * (a.splits > 0 ? a.splits : (a.qtiles + 1) / 2);
-  ta_fwd_kernel<DP, BF><<<grid, TA_FWD_THREADS, bytes, st>>>(a);
-  if (a.splits > 0) {
+  const unsigned grid = (unsigned)HB * (alt ? a.splits * a.qtiles : (a.qtiles + 1) / 2);
+  if (alt) ta_fwd_kernel<DP, BF, true><<<grid, TA_FWD_THREADS, bytes[1], st>>>(a);
+  else ta_fwd_kernel<DP, BF, false><<<grid, TA_FWD_THREADS, bytes[0], st>>>(a);
+  if (a.splits > 1) {
     const int64_t rows = (int64_t)HB * a.pack * a.Sq;
     ta_join_kernel<DP, BF><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);
   }

@@ -19,17 +19,18 @@ namespace tc5 {
 
 constexpr int PANEL = 128 * 128;   // bytes
 
-constexpr uint64_t SW128 = ((uint64_t)1 << 46) | ((uint64_t)2 << 61);   // descriptor version, 128-byte swizzle
+// The descriptor's high word: groups of 8 rows are 1024 bytes apart, descriptor version, 128-byte swizzle.  Its low word is
+// the address in 16-byte units (under 2^14) and the leading offset, so a step is one 32-bit addition.
+constexpr uint32_t DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)DESC_HI << 32) | lo; }
 
-// columns [16 s, 16 s + 16) of a tile, contracted over the columns: groups of 8 rows are 1024 bytes apart
+// columns [16 s, 16 s + 16) of a tile, contracted over the columns
 __device__ __forceinline__ uint64_t desc_k(uint32_t tile, int s) {
-  const uint32_t at = tile + (s >> 2) * PANEL + (s & 3) * 32;
-  return SW128 | ((uint64_t)((at >> 4) & 0x3FFF)) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32);
+  return desc_of((tile >> 4) + (uint32_t)(((s >> 2) * PANEL + (s & 3) * 32) / 16 + (1 << 16)));
 }
-// rows [16 s, 16 s + 16), contracted over the rows: panels PANEL apart, groups of 8 rows 1024 bytes
+// rows [16 s, 16 s + 16), contracted over the rows: panels PANEL apart
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int s) {
-  const uint32_t at = tile + s * 2048;
-  return SW128 | ((uint64_t)((at >> 4) & 0x3FFF)) | ((uint64_t)(PANEL >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32);
+  return desc_of((tile >> 4) + (uint32_t)(s * 2048 / 16 + ((PANEL >> 4) << 16)));
 }
 
 template <bool BF>

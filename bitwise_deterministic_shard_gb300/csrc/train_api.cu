@@ -111,16 +111,21 @@ void shapes(const dta_desc* d, TaArgs& a, bool backward) {
 
 int head_width(int D) { return D <= 64 ? 64 : 128; }
 
-// Key ranges of the split forward: one tile of queries a head group, and enough key tiles that the
-// SMs would idle.  A function of the sizes alone (152 SMs), so the order of the sums is too.
+// Key ranges of the forward pass in the form whose groups share a query tile, 0 for the form with a tile each.  A
+// function of the sizes alone (152 SMs), so the order of the sums is too.
+//   One tile of queries a head group (few queries): so many ranges that rounds of CTAs times a CTA's steps
+//   are least; filling the pipeline and the join cost about four key tiles more.
+//   Else the shared form, unsplit, where the other would leave half of the SMs without a CTA (18 heads of 777 queries: 22.6
+//   against 24.6 us); with more CTAs its second reading of the keys costs more (16 heads of 4096: 120 against 92 us).
+constexpr int TA_SHARED = 152 / 2;
 int split_rule(const TaArgs& a) {
-  if (a.qtiles > 1 || a.ktiles < 4) return 0;
   const int64_t units = (int64_t)a.B * (a.Hq / a.pack);
+  if (a.ktiles < 2) return 0;
+  if (a.qtiles > 1 || a.ktiles < 4) return units * ((a.qtiles + 1) / 2) <= TA_SHARED ? 1 : 0;
   int best = 1;
   int64_t least = INT64_MAX;
   for (int s = 1; s <= a.ktiles / 2 && s <= 64; s++) {
-    // rounds of CTAs times a CTA's key tiles; filling the pipeline and the join cost about four tiles more
-    const int64_t cost = ((units * s + 151) / 152) * ((a.ktiles + s - 1) / s + 4);
+    const int64_t cost = ((units * s + 151) / 152) * ((a.ktiles + s - 1) / s + (s > 1 ? 4 : 2));
     if (cost < least) {
       least = cost;
       best = s;
@@ -140,7 +145,7 @@ Ws layout(const TaArgs& a, bool backward) {
   size_t more = 0;
   if (backward) {
     more = (size_t)a.B * a.Hq * a.qtiles * TA_TILE * 2 * sizeof(float);
-  } else if (const int s = split_rule(a)) {
+  } else if (const int s = split_rule(a); s > 1) {
     more = (size_t)2 * s * a.B * (a.Hq / a.pack) * TA_TILE * (head_width(a.D) + 2) * 4;
   }
   w.total = w.part + round_up(more);

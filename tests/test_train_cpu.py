@@ -93,7 +93,7 @@ def test_workspace_of_the_split_forward_is_bounded(L):
             if Skv < 512:
                 assert n == 0
             else:
-                assert 0 < n <= 2 * 64 * B * 2 * 128 * 130 * 4 + 512
+                assert (B > 8 or n > 0) and n <= 2 * 64 * B * 2 * 128 * 130 * 4 + 512     # many requests: no split, no sums
 
 
 def _matrix(rows=4, cols=10, dtype=0, stride=None, ptr=4096):
