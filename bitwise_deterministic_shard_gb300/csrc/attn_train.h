@@ -15,6 +15,13 @@ struct TaBounds {
   int lo, hi, neg;
 };
 
+// f tanh(k t) of a product t, in log2 units: f = softcap log2 e, k = scale / softcap.  Odd polynomials f k t P((k t)^2) with k
+// and f folded into the coefficients, each twice for the packed arithmetic: c up to |t| = most, s up to least.
+struct TaCap {
+  unsigned long long c[6], s[4];
+  float k, f, most, least;
+};
+
 struct TaArgs {
   // rank-5 maps {D, heads of the box's group, S, groups, B}, boxes of 64 columns
   CUtensorMap q, k, v, o, go, dq, dk, dv;
@@ -40,6 +47,7 @@ struct TaArgs {
   int splits;                         // > 0: key ranges, each CTA's two softmax groups on every other tile
   float scale;                        // of the products
   float softcap;
+  TaCap cap;
 };
 
 template <int DP, bool BF>

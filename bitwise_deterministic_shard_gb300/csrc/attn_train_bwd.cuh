@@ -111,8 +111,8 @@ struct Scores {
   float f0, inv2;         // without a cap; minus one over the square of the cap's factor
   bool capped;
   __device__ __forceinline__ Scores(const TaArgs& a)
-      : cap(a.scale, a.softcap > 0.f ? a.softcap : 1.f), f0(a.scale * LOG2E), capped(a.softcap > 0.f) {
-    inv2 = -1.f / (cap.f * cap.f);
+      : cap(a), f0(a.scale * LOG2E), capped(a.softcap > 0.f) {
+    inv2 = -1.f / (a.cap.f * a.cap.f);
   }
 };
 }  // namespace ta

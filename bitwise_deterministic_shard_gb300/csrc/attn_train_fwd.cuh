@@ -67,36 +67,22 @@ __device__ __forceinline__ float tanh_any(float x) {
   return __fmaf_rn(-2.f, tc5::rcp(1.f + tc5::ex2(x * (2.f * LOG2E))), 1.f);
 }
 struct Cap {
-  float c[6], s[4], k, f, most;   // most: the largest |t| that the polynomial takes, 0 where its coefficients would over- or underflow
-  __device__ __forceinline__ Cap(float scale, float cap) {
-    k = scale / cap;
-    f = cap * LOG2E;
-    const float a = fabsf(k);
-    most = a >= 0x1p-12f && a <= 0x1p10f ? 1.f / a : 0.f;
-    constexpr float p[6] = {0x1.ffff96p-1f, -0x1.553ce0p-2f, 0x1.0f6ea4p-3f, -0x1.a191cep-5f, 0x1.0803b2p-6f, -0x1.742c6ap-9f};
-    constexpr float q[4] = {0x1.ffffb2p-1f, -0x1.55341ap-2f, 0x1.0d366ap-3f, -0x1.634ea8p-5f};
-    float power = k;
-#pragma unroll
-    for (int i = 0; i < 6; i++) {
-      c[i] = p[i] * power * f;
-      if (i < 4) s[i] = q[i] * power * f;
-      power *= k * k;
-    }
-  }
+  const TaCap& c;   // in the kernel's parameters: constant-bank operands, no registers
+  __device__ __forceinline__ Cap(const TaArgs& a) : c(a.cap) {}
   __device__ __forceinline__ u64 smaller2(u64 t) const {
     const u64 z = f2::mul(t, t);
-    u64 p = f2::fma(f2::splat(s[3]), z, f2::splat(s[2]));
-    p = f2::fma(p, z, f2::splat(s[1]));
-    p = f2::fma(p, z, f2::splat(s[0]));
+    u64 p = f2::fma(c.s[3], z, c.s[2]);
+    p = f2::fma(p, z, c.s[1]);
+    p = f2::fma(p, z, c.s[0]);
     return f2::mul(t, p);
   }
   __device__ __forceinline__ u64 small2(u64 t) const {
     const u64 z = f2::mul(t, t);
-    u64 p = f2::fma(f2::splat(c[5]), z, f2::splat(c[4]));
-    p = f2::fma(p, z, f2::splat(c[3]));
-    p = f2::fma(p, z, f2::splat(c[2]));
-    p = f2::fma(p, z, f2::splat(c[1]));
-    p = f2::fma(p, z, f2::splat(c[0]));
+    u64 p = f2::fma(c.c[5], z, c.c[4]);
+    p = f2::fma(p, z, c.c[3]);
+    p = f2::fma(p, z, c.c[2]);
+    p = f2::fma(p, z, c.c[1]);
+    p = f2::fma(p, z, c.c[0]);
     return f2::mul(t, p);
   }
   // v <- f tanh(k v) for N scores of each lane; the warp decides which form it takes
@@ -109,15 +95,15 @@ struct Cap {
       m[1] = max3_abs(m[1], v[i + 2], v[i + 3]);
     }
     const float top = fmaxf(m[0], m[1]);
-    if (__all_sync(0xffffffffu, top <= 0.5f * most)) {
+    if (__all_sync(0xffffffffu, top <= c.least)) {
 #pragma unroll
       for (int i = 0; i < N; i += 2) f2::unpack(smaller2(f2::pack(v[i], v[i + 1])), v[i], v[i + 1]);
-    } else if (__all_sync(0xffffffffu, top <= most)) {
+    } else if (__all_sync(0xffffffffu, top <= c.most)) {
 #pragma unroll
       for (int i = 0; i < N; i += 2) f2::unpack(small2(f2::pack(v[i], v[i + 1])), v[i], v[i + 1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; i++) v[i] = f * tanh_any(v[i] * k);
+      for (int i = 0; i < N; i++) v[i] = c.f * tanh_any(v[i] * c.k);
     }
   }
 };
@@ -448,7 +434,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * DP + half * (DP / 2);
     const uint32_t prow = base + L::P + i * L::PTILE + half * PANEL + r * 128;   // this thread's 64 weights: a panel's row
     const bool capped = a.softcap > 0.f;
-    const Cap cap(a.scale, capped ? a.softcap : 1.f);
+    const Cap cap(a);
     const float f0 = a.scale * LOG2E;
     const float slope = a.slopes && valid ? a.slopes[head] * LOG2E : 0.f;
     // without cap and bias the scores stay products (of a positive scale) until the exponential

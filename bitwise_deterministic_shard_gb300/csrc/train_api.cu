@@ -94,6 +94,39 @@ bool tensor_map(CUtensorMap* m, const da_tensor& t, int pack, int rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The cap's coefficients (see attn_train_fwd.cuh): fitted for the least greatest error, least squares with weights moved
+// toward the largest errors.
+TaCap cap_of(float scale, float softcap) {
+  constexpr double full[6] = {0x1.ffff96p-1, -0x1.553ce0p-2, 0x1.0f6ea4p-3, -0x1.a191cep-5, 0x1.0803b2p-6, -0x1.742c6ap-9};
+  constexpr double less[4] = {0x1.ffffb2p-1, -0x1.55341ap-2, 0x1.0d366ap-3, -0x1.634ea8p-5};
+  const auto twice = [](double x) {
+    const float f = (float)x;
+    uint32_t b;
+    std::memcpy(&b, &f, 4);
+    return ((unsigned long long)b << 32) | b;
+  };
+  TaCap c;
+  std::memset(&c, 0, sizeof(c));
+  if (!(softcap > 0.f)) {
+    c.f = 1.f;
+    return c;
+  }
+  const double k = (double)scale / softcap, f = softcap * 1.4426950408889634;
+  double power = k * f;
+  for (int i = 0; i < 6; i++) {
+    c.c[i] = twice(full[i] * power);
+    if (i < 4) c.s[i] = twice(less[i] * power);
+    power *= k * k;
+  }
+  c.k = (float)k;
+  c.f = (float)f;
+  // beyond these factors a coefficient could leave binary32's range: the general form then takes every score
+  const double a = std::fabs(k);
+  c.most = a >= 0x1p-12 && a <= 0x1p10 ? (float)(1 / a) : 0.f;
+  c.least = 0.5f * c.most;
+  return c;
+}
+
 void shapes(const dta_desc* d, TaArgs& a, bool backward) {
   std::memset(&a, 0, sizeof(a));
   a.B = (int)d->q.B; a.Hq = (int)d->q.H; a.Hkv = (int)d->k.H;
@@ -106,6 +139,7 @@ void shapes(const dta_desc* d, TaArgs& a, bool backward) {
   a.causal = d->causal ? 1 : 0;
   a.scale = std::isnan(d->scale) ? (float)(1.0 / std::sqrt((double)d->q.D)) : d->scale;
   a.softcap = d->softcap;
+  a.cap = cap_of(a.scale, a.softcap);
   a.slopes = d->slopes; a.docs = d->docs; a.prefix = d->prefix; a.status = d->dev_status;
 }
 
