@@ -9,6 +9,7 @@
 // variance is the centred sum, not a difference of sums.  Variants, by the 16-byte vectors of a row:
 //   aligned, 129 to 1024 vectors, many rows: streaming CTAs (below) that copy the next rows while they work
 //     on the present ones and keep the weights in registers;
+//   not aligned, more than 128 vectors up to 8192 columns: staged CTAs (below), except f32 forward;
 //   otherwise, up to 128 vectors: a warp a row; up to 2048: a CTA a row (forward) or a run of rows (backward),
 //     rows that do not start and end on 16 bytes element by element, the threads of a warp on
 //     neighbouring elements (a warp's access is still one run);
@@ -19,7 +20,7 @@
 // multiplier and adder.
 // 8192 x 4096 bf16, f32 weights: forward 30 us (0.65 of the measured copy bandwidth; 46 with a CTA a row that
 // reads the weights again for each, 49 with a warp a row), backward 48 us with the sum of the partial rows
-// (0.62; 79 + 5 and 59 so).  3001 x 5003 f32, unaligned: 27 and 59 us (0.66, 0.45).
+// (0.62; 79 + 5 and 59 so).  3001 x 5003 f32, unaligned: 27 and 45 us (0.66, 0.59).
 #include <algorithm>
 
 #include "../../include/detattn.h"
@@ -672,6 +673,184 @@ __global__ void __launch_bounds__(G, 512 / G) norm_bwd_stream_kernel(const NormA
   }
 }
 
+// ---- staged variants: rows that do not start and end on 16 bytes, of more than 128 vectors up to 8192 columns ----
+//
+// The 16-byte units that hold a row (a few bytes of its neighbour before it; cut at its end) are copied to shared
+// memory, from where the threads read their own columns element by element, t + j G of thread t: every
+// global read stays 16 bytes wide and is in flight without a register.  Otherwise as the streaming variants.
+// Against the variants that read single elements: 8192 x 4097 bf16 forward 80 -> 68 us, backward 128 -> 90;
+// 3001 x 5003 f32 backward 54 -> 45; 20000 x 1501 bf16 53 -> 43 and 121 -> 72; what bounds 16-bit rows now is the
+// single-element shared-memory reads and stores.
+
+// copies the row of `cols` elements at p to the buffer at `to`; the row starts p % 16 bytes into it
+template <typename T, int G>
+__device__ __forceinline__ void stage_row(uint32_t to, const T* p, int cols) {
+  const uintptr_t at = (uintptr_t)p;
+  const int off = (int)(at & 15), bytes = off + cols * (int)sizeof(T);
+  const char* from = (const char*)(at - off);
+  for (int c = threadIdx.x * 16; c < bytes; c += G * 16) {
+    const int left = bytes - c;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + c), "l"(from + c), "r"(left < 16 ? left : 16) : "memory");
+  }
+}
+template <typename T>
+__device__ __forceinline__ float staged(uint32_t at) {
+  if constexpr (sizeof(T) == 4) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+  } else {
+    uint16_t b;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(at));
+    return Elem<T>::get(*reinterpret_cast<const T*>(&b));
+  }
+}
+// elements j and j + 1 of the thread, zero past the end
+template <typename T, int G>
+__device__ __forceinline__ u64 staged2(uint32_t row, int j, int cols) {
+  const int c = threadIdx.x + j * G;
+  return f2::pack(c < cols ? staged<T>(row + c * (int)sizeof(T)) : 0.f,
+                  c + G < cols ? staged<T>(row + (c + G) * (int)sizeof(T)) : 0.f);
+}
+template <typename T, int G>
+__device__ __forceinline__ void put2(T* row, int j, int cols, u64 v) {
+  float a, b;
+  f2::unpack(v, a, b);
+  const int c = threadIdx.x + j * G;
+  if (c < cols) row[c] = Elem<T>::put(a);
+  if (c + G < cols) row[c + G] = Elem<T>::put(b);
+}
+template <typename T, int G>
+__device__ __forceinline__ u64 weight2(const void* w, bool f32, float none, int j, int cols) {
+  const int c = threadIdx.x + j * G;
+  const auto one = [&](int k) { return k >= cols ? 0.f : f32 ? ((const float*)w)[k] : Elem<T>::get(((const T*)w)[k]); };
+  return w ? f2::pack(one(c), one(c + G)) : f2::splat(none);
+}
+
+template <typename T, int G, int NJ>
+__global__ void __launch_bounds__(G, 1024 / G) norm_fwd_staged_kernel(const NormArgs a, int room) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float sh[2 * (G / 32)];
+  const int cols = (int)a.cols, t = threadIdx.x;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const bool wf = a.wdtype == DA_F32;
+  const float n = (float)a.cols;
+  u64 w[NJ / 2], b[NJ / 2];
+#pragma unroll
+  for (int j = 0; j < NJ; j += 2) {
+    w[j / 2] = weight2<T, G>(a.w, wf, 1.f, j, cols);
+    b[j / 2] = weight2<T, G>(a.b, wf, 0.f, j, cols);
+  }
+  const auto fetch = [&](int64_t row, int st) {
+    if (row < a.rows) stage_row<T, G>(base + st * room, (const T*)a.x + row * a.xs, cols);
+    copy_commit();
+  };
+  int64_t row = blockIdx.x;
+  for (int s = 0; s < 2; s++) fetch(row + (int64_t)s * gridDim.x, s);
+  int st = 0;
+  for (; row < a.rows; row += gridDim.x) {
+    copy_wait<1>();
+    __syncthreads();
+    fetch(row + 2 * (int64_t)gridDim.x, st == 0 ? 2 : st - 1);   // the buffer of the row before, which all have left
+    const T* p = (const T*)a.x + row * a.xs;
+    const uint32_t x = base + st * room + (int)((uintptr_t)p & 15);
+    u64 s = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; j += 2) s = f2::add(s, staged2<T, G>(x, j, cols));
+    float v[1] = {both(s)};
+    cta_sums<G, 1>(v, sh, 0);
+    const float mean = __fdiv_rn(v[0], n);
+    s = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; j += 2) {
+      float d, e;
+      f2::unpack(f2::add(staged2<T, G>(x, j, cols), f2::splat(-mean)), d, e);
+      const u64 k = f2::pack(t + j * G < cols ? d : 0.f, t + (j + 1) * G < cols ? e : 0.f);
+      s = f2::fma(k, k, s);
+    }
+    v[0] = both(s);
+    cta_sums<G, 1>(v, sh, 1);
+    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(v[0], n) + a.eps));
+    T* y = (T*)a.y + row * a.ys;
+#pragma unroll
+    for (int j = 0; j < NJ; j += 2)
+      put2<T, G>(y, j, cols, f2::fma(f2::mul(f2::add(staged2<T, G>(x, j, cols), f2::splat(-mean)), f2::splat(rstd)), w[j / 2], b[j / 2]));
+    if (t == 0 && a.mean) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+    st = st == 2 ? 0 : st + 1;
+  }
+}
+
+template <typename T, int G, int NJ>
+__global__ void __launch_bounds__(G, 512 / G) norm_bwd_staged_kernel(const NormArgs a, int64_t per, int room) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float sh[4 * (G / 32)];
+  const int cols = (int)a.cols;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const bool wf = a.wdtype == DA_F32;
+  const int64_t r0 = (int64_t)blockIdx.x * per, r1 = min(r0 + per, a.rows);
+  const float inv_n = __fdiv_rn(1.f, (float)a.cols);
+  u64 w[NJ / 2], gw[NJ / 2], gb[NJ / 2];
+#pragma unroll
+  for (int j = 0; j < NJ; j += 2) {
+    w[j / 2] = weight2<T, G>(a.w, wf, 1.f, j, cols);
+    gw[j / 2] = gb[j / 2] = 0;
+  }
+  const auto fetch = [&](int64_t row, int st) {
+    if (row < r1) {
+      stage_row<T, G>(base + st * 2 * room, (const T*)a.x + row * a.xs, cols);
+      stage_row<T, G>(base + (st * 2 + 1) * room, (const T*)a.dy + row * a.dys, cols);
+    }
+    copy_commit();
+  };
+  for (int s = 0; s < 2; s++) fetch(r0 + s, s);
+  float nmean = a.mean[r0], nrstd = a.rstd[r0];
+  int st = 0, turn = 0;
+  for (int64_t row = r0; row < r1; row++, turn ^= 1) {
+    const float mean = nmean, rstd = nrstd;
+    if (row + 1 < r1) {
+      nmean = a.mean[row + 1];
+      nrstd = a.rstd[row + 1];
+    }
+    copy_wait<1>();
+    __syncthreads();
+    fetch(row + 2, st == 0 ? 2 : st - 1);
+    const uint32_t x = base + st * 2 * room + (int)((uintptr_t)((const T*)a.x + row * a.xs) & 15);
+    const uint32_t dy = base + (st * 2 + 1) * room + (int)((uintptr_t)((const T*)a.dy + row * a.dys) & 15);
+    const u64 off = f2::splat(-mean), rr = f2::splat(rstd);
+    u64 t1 = 0, t2 = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; j += 2) {
+      const u64 d = staged2<T, G>(dy, j, cols), h = f2::mul(f2::add(staged2<T, G>(x, j, cols), off), rr);
+      const u64 ad = f2::mul(d, w[j / 2]);
+      gw[j / 2] = f2::fma(d, h, gw[j / 2]);   // past the row's end d is zero
+      gb[j / 2] = f2::add(gb[j / 2], d);
+      t1 = f2::add(t1, ad);
+      t2 = f2::fma(ad, h, t2);
+    }
+    float s[2] = {both(t1), both(t2)};
+    cta_sums<G, 2>(s, sh, turn);
+    const u64 m1 = f2::splat(-s[0] * inv_n), m2 = f2::splat(-s[1] * inv_n);
+    T* dx = (T*)a.y + row * a.ys;
+#pragma unroll
+    for (int j = 0; j < NJ; j += 2) {
+      const u64 h = f2::mul(f2::add(staged2<T, G>(x, j, cols), off), rr);
+      put2<T, G>(dx, j, cols, f2::mul(f2::fma(h, m2, f2::fma(staged2<T, G>(dy, j, cols), w[j / 2], m1)), rr));
+    }
+    st = st == 2 ? 0 : st + 1;
+  }
+  if (!a.part) return;
+  float* pw = a.part + (int64_t)blockIdx.x * a.cols;
+  float* pb = pw + (int64_t)gridDim.x * a.cols;
+#pragma unroll
+  for (int j = 0; j < NJ; j += 2) {
+    put2<float, G>(pw, j, cols, gw[j / 2]);
+    put2<float, G>(pb, j, cols, gb[j / 2]);
+  }
+}
+
 // dw and db from the partial rows: 32 columns a CTA, 32 warps over the rows, then the warps' sums
 // in their order.  blockIdx.y: 0 dw, 1 db.
 template <typename W>
@@ -710,23 +889,44 @@ void bwd_go(const NormArgs& a, bool al, unsigned grid, int64_t per, cudaStream_t
   else norm_bwd_kernel<T, G, NV, R, false><<<grid, threads, 0, st>>>(a, per);
 }
 
+// a launch whose shared memory could not be allowed fails, and the caller sees that
 template <typename T, int G, int R, int ST>
-cudaError_t fwd_stream(const NormArgs& a, cudaStream_t st) {
+void fwd_stream(const NormArgs& a, cudaStream_t st) {
   constexpr int bytes = ST * R * 2 * G * 16;
   static const cudaError_t ready =
       cudaFuncSetAttribute(norm_fwd_stream_kernel<T, G, 2, R, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (ready != cudaSuccess) return ready;
+  (void)ready;
   norm_fwd_stream_kernel<T, G, 2, R, ST><<<(unsigned)std::min<int64_t>(152 * 512 / G, (a.rows + R - 1) / R), G, bytes, st>>>(a);
-  return cudaSuccess;
 }
 template <typename T, int G, int R, int ST>
-cudaError_t bwd_stream(const NormArgs& a, unsigned grid, int64_t per, cudaStream_t st) {
+void bwd_stream(const NormArgs& a, unsigned grid, int64_t per, cudaStream_t st) {
   constexpr int bytes = ST * R * 2 * G * 32;
   static const cudaError_t ready =
       cudaFuncSetAttribute(norm_bwd_stream_kernel<T, G, 2, R, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (ready != cudaSuccess) return ready;
+  (void)ready;
   norm_bwd_stream_kernel<T, G, 2, R, ST><<<grid, G, bytes, st>>>(a, per);
-  return cudaSuccess;
+}
+
+// bytes of a staged row's buffer
+template <typename T>
+int staged_room(const NormArgs& a) {
+  return ((int)a.cols * (int)sizeof(T) + 31) / 16 * 16;
+}
+template <typename T, int G, int NJ>
+void fwd_staged(const NormArgs& a, cudaStream_t st) {
+  static const cudaError_t ready = cudaFuncSetAttribute(norm_fwd_staged_kernel<T, G, NJ>,
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * (G * NJ * 4 + 32));
+  (void)ready;
+  const int room = staged_room<T>(a);
+  norm_fwd_staged_kernel<T, G, NJ><<<(unsigned)std::min<int64_t>(152 * 1024 / G, a.rows), G, 3 * room, st>>>(a, room);
+}
+template <typename T, int G, int NJ>
+void bwd_staged(const NormArgs& a, unsigned grid, int64_t per, cudaStream_t st) {
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(norm_bwd_staged_kernel<T, G, NJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, 6 * (G * NJ * 4 + 32));
+  (void)ready;
+  const int room = staged_room<T>(a);
+  norm_bwd_staged_kernel<T, G, NJ><<<grid, G, 6 * room, st>>>(a, per, room);
 }
 
 template <typename T>
@@ -738,6 +938,17 @@ void fwd(const NormArgs& a, cudaStream_t st) {
     if (nv <= 256) fwd_stream<T, 128, 2, 2>(a, st);
     else if (nv <= 512) fwd_stream<T, 256, 2, 2>(a, st);
     else fwd_stream<T, 512, 2, 2>(a, st);
+    return;
+  }
+  if constexpr (sizeof(T) == 2)   // f32's single-element reads are 128 bytes a warp: 27 us against 33 (3001 x 5003)
+  if (!al && nv > 128 && a.cols <= 8192 && al16(a.x) && a.rows >= 304) {
+    if (a.cols <= 1024) fwd_staged<T, 128, 8>(a, st);
+    else if (a.cols <= 1536) fwd_staged<T, 128, 12>(a, st);
+    else if (a.cols <= 2048) fwd_staged<T, 256, 8>(a, st);
+    else if (a.cols <= 3072) fwd_staged<T, 256, 12>(a, st);
+    else if (a.cols <= 4096) fwd_staged<T, 512, 8>(a, st);
+    else if (a.cols <= 6144) fwd_staged<T, 512, 12>(a, st);
+    else fwd_staged<T, 512, 16>(a, st);
     return;
   }
   if (nv <= 32) fwd_go<T, 32, 1>(a, al, st);
@@ -758,6 +969,16 @@ void bwd(const NormArgs& a, unsigned grid, int64_t per, cudaStream_t st) {
     if (nv <= 256) bwd_stream<T, 128, 2, 2>(a, grid, per, st);
     else if (nv <= 512) bwd_stream<T, 256, 2, 2>(a, grid, per, st);
     else bwd_stream<T, 512, 2, 2>(a, grid, per, st);
+    return;
+  }
+  if (!al && nv > 128 && (sizeof(T) == 2 || a.cols > 1024) && a.cols <= 8192 && al16(a.x) && al16(a.dy)) {
+    if (a.cols <= 1024) bwd_staged<T, 128, 8>(a, grid, per, st);
+    else if (a.cols <= 1536) bwd_staged<T, 128, 12>(a, grid, per, st);
+    else if (a.cols <= 2048) bwd_staged<T, 256, 8>(a, grid, per, st);
+    else if (a.cols <= 3072) bwd_staged<T, 256, 12>(a, grid, per, st);
+    else if (a.cols <= 4096) bwd_staged<T, 512, 8>(a, grid, per, st);
+    else if (a.cols <= 6144) bwd_staged<T, 512, 12>(a, grid, per, st);
+    else bwd_staged<T, 512, 16>(a, grid, per, st);
     return;
   }
   if (nv <= 32) bwd_go<T, 32, 1, 2>(a, al, grid, per, st);

@@ -92,6 +92,25 @@ def test_attention_options(shape, opts):
         _attn_check(q, k, v, go, **{**kw, "causal": False})
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", [(8, 12, 4, 257, 257, 128), (2, 40, 8, 385, 400, 64), (40, 4, 2, 40, 300, 96), (90, 2, 1, 1, 200, 128),
+                                   (3, 30, 10, 513, 513, 72)])
+@pytest.mark.parametrize("opts", ["plain", "cap", "all"])
+def test_attention_many_heads(shape, opts, dtype):
+    """Enough query tiles that each group of a CTA has one of its own (few of them share a CTA's groups)."""
+    B, Hq, Hkv, Sq, Skv, D = shape
+    q, k, v, go = _attn_inputs(*shape, dtype, seed=11)
+    kw = {"causal": opts != "plain"}
+    if opts != "plain":
+        kw["softcap"] = 30.0
+    if opts == "all":
+        kw["slopes"] = torch.linspace(0.0, 0.4, Hq, device="cuda")
+        ids = (torch.arange(Skv) * 3 // Skv).repeat(B, 1).int()
+        ids[:, Skv // 4:Skv // 4 + 5] = -1
+        kw["docs"] = ids.cuda()
+    _attn_check(q, k, v, go, **kw)
+
+
 @pytest.mark.parametrize("kind", ["none visible", "one token documents", "scattered", "rows"])
 def test_attention_documents(kind):
     S = 300
@@ -281,6 +300,14 @@ def test_layer_norm(rows, cols, gap, dtype, wdtype):
         _close(got, r[n], tol[n], n)
     again = da.layer_norm_backward(dy, x, w, mean, rstd)
     assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
+
+
+@pytest.mark.parametrize("dtype, wdtype", [(torch.float32, torch.float32), (torch.bfloat16, torch.float32), (torch.float16, torch.float16)])
+@pytest.mark.parametrize("rows, cols, gap", [(1300, 1100, 0), (1230, 2048, 0), (1250, 4096, 8), (1217, 8192, 0), (400, 1100, 4), (310, 2501, 3),
+                                             (307, 1501, 0), (305, 6001, 0), (333, 8190, 2), (1, 5003, 0)])
+def test_layer_norm_many_rows(rows, cols, gap, dtype, wdtype):
+    """The streaming and the staged variants, which take many rows, with a last run that is shorter."""
+    test_layer_norm(rows, cols, gap, dtype, wdtype)
 
 
 def test_layer_norm_without_weights_and_shapes():
