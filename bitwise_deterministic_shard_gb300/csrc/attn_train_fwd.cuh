@@ -19,7 +19,9 @@
 // that four softmax warps a scheduler leave open.
 //
 // The weights are rounded to the inputs' 16-bit type (the tensor cores take both operands in one
-// type); the sum of the weights and the output are binary32.  The maximum is moved only when
+// type); the sum of the weights and the output are binary32.  The output is divided by the sum of the rounded weights where
+// a row has few keys (their roundings then largely cancel: 96 queries, output 2.5e-3 -> 2.0e-3 off; over many keys they do
+// not, and the sum costs 1.5 operations a score), lse is formed from the unrounded sum always.  The maximum is moved only when
 // it grows by more than 2^8: until then weights are at most 2^8 too large, which the division by
 // their sum undoes exactly, and the output needs no rescaling.  Capped bf16 scores without a bias need no
 // maximum: they lie within +-cap, so with a cap of at most 44 (2^+-64) nothing over- or underflows in
@@ -447,7 +449,8 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     const int first_pos = (a.pack > 1 ? 0 : qt * TA_TILE) + off;
     int full = a.Skv;                                        // keys below it are seen by every row, documents apart
     if (a.causal) full = min(full, max(first_pos + 1, a.prefix ? a.prefix[b] : 0));
-    float m = fixed ? 0.f : -INFINITY, l = 0.f;
+    float m = fixed ? 0.f : -INFINITY, l = 0.f, lr = 0.f;   // lr: of the rounded weights, with few key tiles
+    const bool few = ntile <= 4 && !(alt && a.splits > 1);
     const int step = alt ? 2 : 1, end = i ? hi1 : hi0;
     int cnt = 0;
     // Padding may hold NaN, and 0 NaN is NaN: its value rows become zeros, a row a thread.
@@ -522,6 +525,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         const float mn = grow ? fmaxf(m, mx) : m;
         const float k = mn == m ? 1.f : ex2((m - mn) * f);
         l *= k;
+        lr *= k;
         m = mn;
         if (cnt > 0) {
           mbar_wait(&pv_done[i], (cnt - 1) & 1, abort);
@@ -542,17 +546,17 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       }
       }
       const float mf = m == -INFINITY ? 0.f : m * f;
-      u64 sum[2] = {0, 0};
+      u64 sum[2] = {0, 0}, rounded = 0;
       const u64 ff = f2::splat(f), shift = f2::splat(-mf);
       if (cnt > 0) {   // the product before has read the weights' tile
         mbar_wait(&pv_done[i], (cnt - 1) & 1, abort);
         __syncwarp();
       }
 #pragma unroll
-      for (int u = 0; u < 8; u++) {
-        uint32_t p[4];
+      for (int u = 0; u < 8; u += 4) {
+        uint32_t p[16];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
+        for (int e = 0; e < 32; e += 2) {
           float x, y;
           f2::unpack(f2::fma(f2::pack(v[8 * u + e], v[8 * u + e + 1]), ff, shift), x, y);
           x = ex2(x);
@@ -560,14 +564,22 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
           sum[(e >> 1) & 1] = f2::add(sum[(e >> 1) & 1], f2::pack(x, y));
           p[e >> 1] = pack16<BF>(x, y);
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + ((u ^ (r & 7)) << 4)), "r"(p[0]), "r"(p[1]),
-                     "r"(p[2]), "r"(p[3])
-                     : "memory");
+        if (few) {
+#pragma unroll
+          for (int e = 0; e < 16; e++) rounded = f2::add(rounded, unpack16<BF>(p[e]));
+        }
+#pragma unroll
+        for (int w = 0; w < 4; w++)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + (((u + w) ^ (r & 7)) << 4)), "r"(p[4 * w]),
+                       "r"(p[4 * w + 1]), "r"(p[4 * w + 2]), "r"(p[4 * w + 3])
+                       : "memory");
       }
       {
         float x, y;
         f2::unpack(f2::add(sum[0], sum[1]), x, y);
         l += x + y;
+        f2::unpack(rounded, x, y);
+        lr += x + y;
       }
       if (padded) clean(n);
       fence_async_smem();
@@ -582,8 +594,10 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       float* const at = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + L::P + i * L::PTILE) + r;
       bar_sync(9 + i, 256);
       at[half * 128] = l;
+      at[256 + half * 128] = lr;
       bar_sync(pair, 64);
       l = at[0] + at[128];
+      lr = few ? at[256] + at[384] : l;
     }
     if (valid && !isfinite(l) && half == 0 && a.status) atomicOr(a.status, DA_STATUS_NONFINITE);
     __syncwarp();
@@ -591,11 +605,11 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     if (alt && a.splits == 1) {
       // one CTA holds all keys: the second group hands its sums to the first through the weights' tiles
       unsigned char* const room = raw + (base - smem_addr(raw)) + L::P;
-      float2* const stat = reinterpret_cast<float2*>(exchange);
+      float4* const stat = reinterpret_cast<float4*>(exchange);
       const auto at = [&](int c) { return reinterpret_cast<float4*>(room + r * (DP * 4) + (((half * (DP / 2) + c) >> 2) ^ (r & 7)) * 16); };
       bar_sync(11, 512);
       if (i == 1) {
-        if (half == 0) stat[r] = make_float2(m * f, l);
+        if (half == 0) stat[r] = make_float4(m * f, l, lr, 0.f);
         if (cnt > 0) {
 #pragma unroll 1
           for (int c = 0; c < DP / 2; c += 16) {
@@ -609,10 +623,10 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       }
       bar_sync(11, 512);
       if (i == 0) {
-        const float2 other = stat[r];
+        const float4 other = stat[r];
         const float m0 = m * f, top = fmaxf(l != 0.f ? m0 : -INFINITY, other.y != 0.f ? other.x : -INFINITY);
         const float k0 = l != 0.f ? ex2(m0 - top) : 0.f, k1 = other.y != 0.f ? ex2(other.x - top) : 0.f;
-        const float all = l * k0 + other.y * k1, inv = all > 0.f ? 1.f / all : all;
+        const float all = l * k0 + other.y * k1, by = lr * k0 + other.z * k1, inv = by > 0.f ? 1.f / by : by;
         lse = all > 0.f ? (top + log2f(all)) * LN2 : all == 0.f ? -INFINITY : all;
         const bool more = ntile > 1;
         const uint32_t tile = base + L::Q;
@@ -645,7 +659,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     } else if (!alt) {
       const uint32_t tile = base + L::Q + i * TILE;
       row_out<BF, DP / 2>(tile, tmem + lanes + 256 + i * DP, tmem + lanes + 256 + i * DP, r, half * (DP / 2),
-                          l > 0.f ? 1.f / l : l, 0.f, cnt > 0);   // a row that sees nothing: zeros times zero
+                          lr > 0.f ? 1.f / lr : lr, 0.f, cnt > 0);   // a row that sees nothing: zeros times zero
     }
     if (!alt || a.splits == 1) {
       const bool mine = qt < a.qtiles && !(alt && i == 1);

@@ -148,6 +148,15 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {   // two 16-bit
   else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+template <bool BF>
+__device__ __forceinline__ unsigned long long unpack16(uint32_t w) {   // the packed binary32 pair of two 16-bit floats
+  float2 f;
+  if constexpr (BF) f = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  else f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(f.x), "f"(f.y));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {   // 2^x, 2^-inf = 0; error 2^-22 relative
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
