@@ -40,6 +40,7 @@
 #include "attn_train.h"
 #include "pack2.cuh"
 #include "tc5_tile.cuh"
+#include "tile_ring.h"
 
 namespace detattn {
 namespace ta {
@@ -217,7 +218,7 @@ struct TaFwdSmem {
   static constexpr int TILE = DP / 64 * tc5::PANEL, PTILE = 2 * tc5::PANEL;
   // two query tiles, two tiles of weights and a ring of key and value tiles (the split form has one query tile and
   // a stage more), then the rows' maxima
-  static constexpr int NST = DP == 128 ? 3 : 7, MOST = NST + 1;
+  static constexpr int NST = DP == 128 ? 3 : 7, MOST = NST + 1;   // MOST is a multiple of 4
   static constexpr int Q = 0, P = 2 * TILE, KV = P + 2 * PTILE, MAX = KV + NST * TILE, END = MAX + 2048;
 };
 
@@ -346,24 +347,27 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
           if (a.pack > 1) tma_load(at, &a.q, p * 64, 0, 0, h, b, &q_full);   // an empty second tile too
           else tma_load(at, &a.q, p * 64, 0, min(alt ? t : 2 * t + i, a.qtiles - 1) * TA_TILE, h, b, &q_full);
         }
-      int it = 0;
-      auto fetch = [&](const CUtensorMap* map, int n) -> bool {
-        const int s = it % nst;
-        if (it >= nst && !mbar_wait(&kv_empty[s], ((it / nst) - 1) & 1, abort)) return false;
+      uint32_t used = 0, odd = 0;                                    // a bit a stage: filled, its last fill's parity
+      auto fetch = [&](const CUtensorMap* map, int k, int n) -> bool {
+        const int s = k % nst;
+        if (k >= nst && !mbar_wait(&kv_empty[s], ((k / nst) - 1) & 1, abort)) return false;
         mbar_expect_tx(&kv_full[s], TILE);
         for (int p = 0; p < DP / 64; p++)
           tma_load(stage_at(s) + p * PANEL, map, p * 64, 0, n * TA_TILE, kh, b, &kv_full[s]);
-        it++;
+        used |= 1u << s;
+        odd = (odd & ~(1u << s)) | (uint32_t)((k / nst) & 1) << s;
         return true;
       };
-      bool ok = fetch(&a.k, lo);
-      if (ok && lo + 1 < hi) ok = fetch(&a.k, lo + 1);
+      bool ok = fetch(&a.k, key_place<ALT>(0), lo);
+      if (ok && lo + 1 < hi) ok = fetch(&a.k, key_place<ALT>(1), lo + 1);
       for (int n = lo; n < hi && ok; n++) {
-        ok = fetch(&a.v, n);
-        if (ok && n + 2 < hi) ok = fetch(&a.k, n + 2);
+        ok = fetch(&a.v, value_place<ALT>(n - lo, ntile), n);
+        if (ok && n + 2 < hi) ok = fetch(&a.k, key_place<ALT>(n + 2 - lo), n + 2);
       }
       // nothing may be in flight when the CTA ends
-      for (int k = max(0, it - nst); k < it; k++) mbar_drain(&kv_full[k % nst], (k / nst) & 1);
+#pragma unroll 1
+      for (int s = 0; s < nst; s++)
+        if (used >> s & 1) mbar_drain(&kv_full[s], odd >> s & 1);
       mbar_drain(&q_full, 0);
     }
   } else if (warp == 17) {
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
         for (int i = 0; i < 2; i++) {
           const int n = sn[i];
           if (n < end[i]) {
-            const int k = n < 2 ? n : 2 * n - 1, st = k % nst;       // this key tile in the order of the copies
+            const int k = key_place<ALT>(n), st = k % nst;
             if (all_of((read[i] == 0 || mbar_test(&s_read[i], (read[i] - 1) & 1)) && mbar_test(&kv_full[st], (k / nst) & 1))) {
               fence_after();
               const uint32_t q = base + L::Q + (alt ? 0 : i * TILE), kt = stage_at(st);
@@ -394,13 +398,14 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
               commit_one(&s_full[i], one);
               read[i]++;
               sn[i] += step;
-              if (alt || n >= end[i ^ 1] || sn[i ^ 1] > n) commit_one(&kv_empty[st], one);
+              // only where the copies wait for it: no arrival is left when the CTA ends
+              if ((alt || n >= end[i ^ 1] || sn[i ^ 1] > n) && !last_place(k, tiles, nst)) commit_one(&kv_empty[st], one);
               some = true;
             }
           }
           const int m = pn[i];
           if (m < end[i] && m < sn[i]) {
-            const int k = min(tiles, m + 2) + m, st = k % nst;       // and this value tile
+            const int k = value_place<ALT>(m, tiles), st = k % nst;
             if (all_of(mbar_test(&p_full[i], wrote[i] & 1) && mbar_test(&kv_full[st], (k / nst) & 1))) {
               fence_after();
               const uint32_t pt = base + L::P + i * L::PTILE, vt = stage_at(st);
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
               commit_one(&pv_done[i], one);
               wrote[i]++;
               pn[i] += step;
-              if (alt || m >= end[i ^ 1] || pn[i ^ 1] > m) commit_one(&kv_empty[st], one);
+              if ((alt || m >= end[i ^ 1] || pn[i ^ 1] > m) && !last_place(k, tiles, nst)) commit_one(&kv_empty[st], one);
               some = true;
             }
           }
@@ -458,8 +463,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     int cnt = 0;
     // Padding may hold NaN, and 0 NaN is NaN: its value rows become zeros, a row a thread.
     const auto clean = [&](int n) {
-      const int d = n - lo, k = min(ntile, d + 2) + d;   // this value tile in the order of the copies
-      const int j = n * TA_TILE + r;
+      const int k = value_place<ALT>(n - lo, ntile), j = n * TA_TILE + r;
       mbar_wait(&kv_full[k % nst], (k / nst) & 1, abort);
       if (half == 0 && j < a.Skv && a.docs[(int64_t)b * a.Skv + j] < 0) zero_row<DP>(stage_at(k % nst), r);
       __syncwarp();

@@ -256,6 +256,23 @@ def test_attention_rows_do_not_depend_on_the_batch():
     assert torch.equal(out[1:2], o1) and torch.equal(lse[1:2], l1)
 
 
+@pytest.mark.parametrize("B, Hq, Hkv, Sq, S, D, dtype", [(16, 32, 8, 1, 4096, 128, torch.bfloat16), (19, 32, 8, 2, 2000, 64, torch.float16),
+                                                         (40, 16, 16, 1, 1500, 128, torch.bfloat16), (64, 8, 8, 5, 700, 72, torch.bfloat16)])
+def test_attention_many_requests_of_few_queries(B, Hq, Hkv, Sq, S, D, dtype):
+    """More CTAs than SMs, each reading a cache of its own from memory: tiles arrive in any order, nothing may depend on it."""
+    q, k, v, go = _attn_inputs(B, Hq, Hkv, Sq, S, D, dtype, seed=B, heavy=False)
+    st = da.new_status()
+    out, lse = da.attention_forward(q, k, v, causal=True, status=st)
+    assert da.read_status(st) == 0
+    for _ in range(40):
+        again = da.attention_forward(q, k, v, causal=True, status=st)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert da.read_status(st) == 0
+    b = slice(B - 2, B)
+    r = R.attention(q[b], k[b], v[b], go[b], causal=True)
+    _close(out[b], r["out"], R.attention_tolerance(r, dtype)["out"], "out")
+
+
 def test_attention_empty():
     for B, Sq, Skv in ((0, 5, 5), (1, 0, 0), (1, 0, 7)):
         q = torch.zeros(B, 2, Sq, 64, device="cuda", dtype=torch.bfloat16)
