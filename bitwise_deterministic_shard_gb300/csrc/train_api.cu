@@ -147,8 +147,10 @@ int head_width(int D) { return D <= 64 ? 64 : 128; }
 
 // Key ranges of the forward pass in the form whose groups share a query tile, 0 for the form with a tile each.  A
 // function of the sizes alone (152 SMs), so the order of the sums is too.
-//   One tile of queries a head group (few queries): so many ranges that rounds of CTAs times a CTA's steps
-//   are least; filling the pipeline and the join cost about four key tiles more.
+//   One tile of queries a head group (few queries): so many ranges that rounds of CTAs times a CTA's key tiles are least, where
+//   filling the pipeline and the join cost about four key tiles more (0.8 us each) and every range two thirds of one in
+//   the join: 2 key heads of 32768 keys 34 us in 16 or 24 ranges, 49 in 64, 224 in one; 32 of them 93 us in 4, 106 in 8;
+//   512 keys 12.9 us in one range, 12.8 to 14.1 in two.
 //   Else the shared form, unsplit, where the other would leave half of the SMs without a CTA (18 heads of 777 queries: 22.6
 //   against 24.6 us); with more CTAs its second reading of the keys costs more (16 heads of 4096: 120 against 92 us).
 constexpr int TA_SHARED = 152 / 2;
@@ -159,7 +161,7 @@ int split_rule(const TaArgs& a) {
   int best = 1;
   int64_t least = INT64_MAX;
   for (int s = 1; s <= a.ktiles / 2 && s <= 64; s++) {
-    const int64_t cost = ((units * s + 151) / 152) * ((a.ktiles + s - 1) / s + (s > 1 ? 4 : 2));
+    const int64_t cost = 3 * ((units * s + 151) / 152) * ((a.ktiles + s - 1) / s + (s > 1 ? 4 : 2)) + 2 * s;   // in thirds of a tile
     if (cost < least) {
       least = cost;
       best = s;

@@ -90,7 +90,7 @@ def test_workspace_of_the_split_forward_is_bounded(L):
         for Skv in (1, 127, 512, 8192, 131072):
             d = _desc(B=B, Hq=8, Hkv=2, Sq=1, Skv=Skv, D=128)
             n = L.dta_workspace_bytes(C.byref(d), 0)
-            if Skv < 512:
+            if Skv <= 512:                       # up to four tiles are not worth a join
                 assert n == 0
             else:
                 assert (B > 8 or n > 0) and n <= 2 * 64 * B * 2 * 128 * 130 * 4 + 512     # many requests: no split, no sums
