@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
       put_weights<BF>(base + L::P, r, part, p);
       if (padded) {   // padding may hold NaN, and 0 NaN is NaN: its query and gradient rows become zeros
         const int i = q * TA_TILE + r;
+        mbar_wait(&g_full[it % NST], (it / NST) & 1, abort);   // the scores only needed the query tile
         if (part < 2 && i < a.Sq && a.docs[(int64_t)b * a.Skv + i + off] < 0)
           zero_row<DP>(base + L::ST + (it % NST) * L::STAGE + part * TILE, r);
         __syncwarp();

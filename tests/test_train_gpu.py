@@ -151,6 +151,28 @@ def test_attention_padding_may_hold_anything(S, Sq, D):
     assert da.read_status(st) == 0
 
 
+def test_attention_padding_of_many_tiles():
+    """Each tile holds padding, and tiles arrive in any order: their rows become zeros after they arrived, not before."""
+    B, S = 8, 2600
+    q, k, v, go = _attn_inputs(B, 16, 8, S, S, 128, torch.bfloat16, seed=6, heavy=False)
+    ids = (torch.arange(S) // 500).int().repeat(B, 1)
+    ids[:, ::50] = -1
+    docs, st = ids.cuda(), da.new_status()
+    for t in (q, k, v, go):
+        t[:, :, ::50] = 0
+    kw = dict(docs=docs, causal=True, status=st)
+    out, lse = da.attention_forward(q, k, v, **kw)
+    want = da.attention_backward(q, k, v, out, lse, go, **kw)
+    for t in (q, k, v, go):
+        t[:, :, ::50] = float("nan")
+    for _ in range(10):
+        o, l = da.attention_forward(q, k, v, **kw)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+        for x, y in zip(da.attention_backward(q, k, v, o, l, go, **kw), want):
+            assert torch.equal(x, y)
+    assert da.read_status(st) == 0
+
+
 @pytest.mark.parametrize("layout", ["bshd", "wide", "odd", "last"])
 def test_attention_layouts(layout):
     q, k, v, go = _attn_inputs(2, 4, 2, 200, 200, 64, torch.bfloat16, seed=4, layout=layout)
