@@ -241,12 +241,12 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
           if (!ok) break;
           fence_after();
           go.weights(base + L::P, st + TILE, it > 0, &p_read);
-          commit_one(&g_empty[it % NST], go.one);
+          if (it + NST < steps) commit_one(&g_empty[it % NST], go.one);   // only where the copies wait for it, as below
           ok = all_of(mbar_wait(&ds_full, it & 1, abort));
           if (!ok) break;
           fence_after();
           go.grads(st, it > 0);
-          commit_one(&q_empty[it % NST], go.one);
+          if (it + NST < steps) commit_one(&q_empty[it % NST], go.one);
           if (it + 1 < steps) {
             ok = all_of(mbar_wait(&g_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
             if (ok) go.first(go.tp, vtile, next + TILE, &dp_full);
@@ -372,7 +372,10 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
       fence_before();
       mbar_arrive(&ds_full);
     }
-    if (total > 0) mbar_wait(&done, 0, abort);
+    if (total > 0) {   // every product is done and no arrival is left when the CTA ends
+      mbar_wait(&p_read, (total - 1) & 1, abort);
+      mbar_wait(&done, 0, abort);
+    }
     __syncwarp();
     fence_after();
     // dK over the keys' tile, dV over the values': both are no longer read
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
           ok = all_of(mbar_wait(&v_full[0], 0, abort));
           if (ok) {
             go.first(go.tp, gtile, st0 + TILE, &dp_full);
-            commit_one(&v_empty[0], go.one);
+            if (NST < steps) commit_one(&v_empty[0], go.one);   // only where the copies wait for it, as below
           }
         }
         for (int it = 0; it < steps && ok; it++) {
@@ -513,12 +516,12 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
           if (!ok) break;
           fence_after();
           go.grads(st, it > 0);
-          commit_one(&k_empty[it % NST], go.one);
+          if (it + NST < steps) commit_one(&k_empty[it % NST], go.one);
           if (it + 1 < steps) {
             ok = all_of(mbar_wait(&v_full[(it + 1) % NST], ((it + 1) / NST) & 1, abort));
             if (!ok) break;
             go.first(go.tp, gtile, next + TILE, &dp_full);
-            commit_one(&v_empty[(it + 1) % NST], go.one);
+            if (it + 1 + NST < steps) commit_one(&v_empty[(it + 1) % NST], go.one);
           }
         }
         commit_one(&done, go.one);
@@ -668,7 +671,10 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
       fence_before();
       mbar_arrive(&ds_full);
     }
-    if (total > 0) mbar_wait(&done, 0, abort);
+    if (total > 0) {   // every product is done and no arrival is left when the CTA ends
+      mbar_wait(&p_read, (total - 1) & 1, abort);
+      mbar_wait(&done, 0, abort);
+    }
     __syncwarp();
     fence_after();
     // The sums were taken with delta from the rounded output; with D = sum p dp the gradient is
