@@ -33,7 +33,7 @@ struct TaArgs {
   float* lse;                         // [B, Hq, Sq], natural logarithm
   float* rows;                        // backward, from the dq kernel to the other: [B, Hq, query tiles][2][128]
                                       // (-lse log2 e), (-delta); -inf, 0 for a row that sees nothing and past the last query
-  float* part;                        // split forward: sums [2 splits][B Hkv][128][DP], then (max, total) pairs
+  float* part;                        // split forward: sums [2 splits][B Hkv][128][DP], then (max, total, total of the rounded weights, 0)
   void* out;                          // join of the split forward; strides of b, h, s
   int64_t os[3];
   int* status;

@@ -22,8 +22,9 @@
 //
 // The weights are rounded to the inputs' 16-bit type (the tensor cores take both operands in one
 // type); the sum of the weights and the output are binary32.  The output is divided by the sum of the rounded weights where
-// a row has few keys (their roundings then largely cancel: 96 queries, output 2.5e-3 -> 2.0e-3 off; over many keys they do
-// not, and the sum costs 1.5 operations a score), lse is formed from the unrounded sum always.  The maximum is moved only when
+// a row may have few keys that count: few key tiles, a distance bias (their roundings then largely cancel: 96
+// queries, output 2.5e-3 -> 2.0e-3 off) and, as it costs nothing there, the form below; over many keys they do
+// not cancel, and the sum costs 1.5 operations a score.  lse is formed from the unrounded sum always.  The maximum is moved only when
 // it grows by more than 2^8: until then weights are at most 2^8 too large, which the division by
 // their sum undoes exactly, and the output needs no rescaling.  Capped bf16 scores without a bias need no
 // maximum: they lie within +-cap, so with a cap of at most 32 (weights of 2^+-46) and values below 2^64 nothing overflows in
@@ -457,8 +458,8 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     const int first_pos = (a.pack > 1 ? 0 : qt * TA_TILE) + off;
     int full = a.Skv;                                        // keys below it are seen by every row, documents apart
     if (a.causal) full = min(full, max(first_pos + 1, a.prefix ? a.prefix[b] : 0));
-    float m = fixed ? 0.f : -INFINITY, l = 0.f, lr = 0.f;   // lr: of the rounded weights, with few key tiles
-    const bool few = ntile <= 4 && !(alt && a.splits > 1);
+    float m = fixed ? 0.f : -INFINITY, l = 0.f, lr = 0.f;   // lr: of the rounded weights
+    const bool few = alt || ntile <= 4 || a.slopes != nullptr;
     const int step = alt ? 2 : 1, end = i ? hi1 : hi0;
     int cnt = 0;
     // Padding may hold NaN, and 0 NaN is NaN: its value rows become zeros, a row a thread.
@@ -686,8 +687,8 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     } else {
       const int64_t row = ((int64_t)(2 * z + i) * HB + hb) * TA_TILE + r;
       float* o = a.part + row * DP + half * (DP / 2);
-      float2* ml = reinterpret_cast<float2*>(a.part + (int64_t)2 * a.splits * HB * TA_TILE * DP) + row;
-      if (valid && half == 0) *ml = make_float2(m * f, l);
+      float4* stat = reinterpret_cast<float4*>(a.part + (int64_t)2 * a.splits * HB * TA_TILE * DP) + row;
+      if (valid && half == 0) *stat = make_float4(m * f, l, lr, 0.f);
 #pragma unroll 1
       for (int c = 0; c < DP / 2; c += 16) {
         float x[16];
@@ -721,27 +722,28 @@ __global__ void __launch_bounds__(128) ta_join_kernel(const __grid_constant__ Ta
   if (w >= (int64_t)HB * a.pack * a.Sq) return;
   const int rows = a.pack * a.Sq, hb = (int)(w / rows), r = (int)(w % rows);
   const int b = hb / NH, qi = r / a.pack, head = hb % NH * a.pack + r % a.pack;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + (int64_t)np * HB * TA_TILE * DP);
+  const float4* ml = reinterpret_cast<const float4*>(a.part + (int64_t)np * HB * TA_TILE * DP);
   float top = -INFINITY;
   for (int p = lane; p < np; p += 32) top = fmaxf(top, ml[((int64_t)p * HB + hb) * TA_TILE + r].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   constexpr int E = DP / 32;
-  float sum[E] = {}, l = 0.f;
+  float sum[E] = {}, l = 0.f, lr = 0.f;
 #pragma unroll 4
   for (int p = 0; p < np; p++) {
     const int64_t row = ((int64_t)p * HB + hb) * TA_TILE + r;
-    const float2 x = ml[row];
+    const float4 x = ml[row];
     const bool some = x.y != 0.f;                 // a range without visible keys wrote no sums
     const float k = some ? ex2(x.x - top) : 0.f;
     l = __fmaf_rn(x.y, k, l);
+    lr = __fmaf_rn(x.z, k, lr);
 #pragma unroll
     for (int e = 0; e < E; e++) {
       const float o = some ? a.part[row * DP + lane * E + e] : 0.f;
       sum[e] = __fmaf_rn(o, k, sum[e]);
     }
   }
-  const float inv = l > 0.f ? 1.f / l : l;        // NaN stays
+  const float inv = lr > 0.f ? 1.f / lr : lr;     // NaN stays
   uint16_t* out = (uint16_t*)a.out + b * a.os[0] + head * a.os[1] + qi * a.os[2];
 #pragma unroll
   for (int e = 0; e < E; e += 2) {

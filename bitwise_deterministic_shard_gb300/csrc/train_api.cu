@@ -182,7 +182,7 @@ Ws layout(const TaArgs& a, bool backward) {
   if (backward) {
     more = (size_t)a.B * a.Hq * a.qtiles * TA_TILE * 2 * sizeof(float);
   } else if (const int s = split_rule(a); s > 1) {
-    more = (size_t)2 * s * a.B * (a.Hq / a.pack) * TA_TILE * (head_width(a.D) + 2) * 4;
+    more = (size_t)2 * s * a.B * (a.Hq / a.pack) * TA_TILE * (head_width(a.D) + 4) * 4;
   }
   w.total = w.part + round_up(more);
   return w;
