@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t q_full, kv_full[L::MOST], kv_empty[L::MOST], s_full[2], s_read[2], p_full[2], pv_done[2], gone;
   __shared__ uint32_t tmem_at;
-  __shared__ int dead, wdoc[16][2], range[2][2], qdoc[2][3];
+  __shared__ int dead, wdoc[16][3], range[2][2], qdoc[2][3];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   // the rows' maxima in the two halves of the keys, as bf16 rounded up (any value near the maximum does): [turn][tile][half][row]
   uint16_t* const exchange = reinterpret_cast<uint16_t*>(raw + (base - smem_addr(raw)) + L::MAX);
@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     const int neg = __any_sync(0xffffffffu, valid && doc < 0);
     if (lane == 0) {
       wdoc[warp][0] = dl;
-      wdoc[warp][1] = neg ? -2 - dh : dh;
+      wdoc[warp][1] = max(dh, -1);
+      wdoc[warp][2] = neg;      // apart: a warp may hold nothing but padding
     }
   }
   fence_before();
@@ -298,13 +299,9 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   if (wg < 2 && (warp & 7) == 0) {
     int dl = 0x7fffffff, dh = -1, neg = 0;
     for (int w = warp; w < warp + 4; w++) {
-      int x = wdoc[w][1];
-      if (x < -1) {
-        neg = 1;
-        x = -2 - x;
-      }
       dl = min(dl, wdoc[w][0]);
-      dh = max(dh, x);
+      dh = max(dh, wdoc[w][1]);
+      neg |= wdoc[w][2];
     }
     const int q0 = (a.pack > 1 ? 0 : qt * TA_TILE) + off;
     const int q1 = (qt >= a.qtiles ? 0 : a.pack > 1 ? a.Sq : min(qt * TA_TILE + TA_TILE, a.Sq)) - 1 + off;   // none: below q0
