@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
   __shared__ uint32_t tmem_at;
   __shared__ int dead, wdoc[16][3], range[2][2], qdoc[2][3];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-  // the rows' maxima in the two halves of the keys, as bf16 rounded up (any value near the maximum does): [turn][tile][half][row]
+  // the rows' maxima in the two halves of the keys, as bf16 rounded up: [turn][tile][half][row]
   uint16_t* const exchange = reinterpret_cast<uint16_t*>(raw + (base - smem_addr(raw)) + L::MAX);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &dead;
@@ -520,22 +520,32 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
 #pragma unroll
         for (int e = 0; e < 4; e++) top[e] = max3(top[e], v[c + 2 * e], v[c + 2 * e + 1]);
       const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      // the row's maximum over both threads; two sets of words by turns, so one barrier does
-      uint16_t* const at = exchange + (cnt & 1) * 512 + i * 256 + r;
-      at[half * 128] = __bfloat16_as_ushort(__float2bfloat16_ru(mine));
-      bar_sync(pair, 64);
-      const float mx = fmaxf(__bfloat162float(__ushort_as_bfloat16(at[0])), __bfloat162float(__ushort_as_bfloat16(at[128])));
-      const bool grow = cnt == 0 || mx > m + lazy;
+      // Whether a row's maximum has to move is asked of both threads' maxima as bf16 rounded up, two sets of words by turns, so
+      // one barrier does.  That is up to 2^-7 of the score above it, so where it moves the maximum itself passes, through the
+      // weights' tile: rows that only these two warps write, free once the product before has read them.
+      const bool first = cnt == 0;
+      bool grow = first;
+      if (!first) {
+        uint16_t* const at = exchange + (cnt & 1) * 512 + i * 256 + r;
+        at[half * 128] = __bfloat16_as_ushort(__float2bfloat16_ru(mine));
+        bar_sync(pair, 64);
+        grow = fmaxf(__bfloat162float(__ushort_as_bfloat16(at[0])), __bfloat162float(__ushort_as_bfloat16(at[128]))) > m + lazy;
+      }
       if (__any_sync(0xffffffffu, grow)) {   // the same in both warps of these rows
-        const float mn = grow ? fmaxf(m, mx) : m;
-        const float k = mn == m ? 1.f : ex2((m - mn) * f);
-        l *= k;
-        lr *= k;
-        m = mn;
-        if (cnt > 0) {
+        if (!first) {
           mbar_wait(&pv_done[i], (cnt - 1) & 1, abort);
           __syncwarp();
           fence_after();
+        }
+        float* const at = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + L::P + i * L::PTILE + (warp & 3) * 4096) + lane;
+        at[half * 32] = mine;
+        bar_sync(pair, 64);
+        const float mn = grow ? fmaxf(m, fmaxf(at[0], at[32])) : m;
+        const float k = mn == m ? 1.f : ex2(m * f - mn * f);   // of the shifts as rounded: the weights were taken with them
+        l *= k;
+        lr *= k;
+        m = mn;
+        if (!first) {
 #pragma unroll
           for (int c = 0; c < DP / 2; c += 16) {   // 16 at a time: the scores are live
             float o[16];
@@ -548,6 +558,7 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
           }
           st_wait();
         }
+        bar_sync(pair, 64);   // both have read the words that the weights take next
       }
       }
       const float mf = m == -INFINITY ? 0.f : m * f;

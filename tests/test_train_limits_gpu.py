@@ -33,3 +33,43 @@ def test_padding_that_fills_whole_warps(S, pad, B, H, causal, pad_id):
     st = da.new_status()
     again = da.attention_forward(q, k, v, causal=causal, docs=docs, status=st)
     assert torch.equal(again[0], out) and torch.equal(again[1], lse) and da.read_status(st) == 0
+
+
+# ---------------------------------------------------------------- scores of any size
+
+def _tall(B, Hq, Hkv, Sq, Skv, dtype, base, late):
+    """Products that are exact in binary32: 16 dimensions give every score +-256 |base| times a power of two (scale 1/4),
+    the others a spread of about 3.5.  late: the first half of the keys without the common part."""
+    g = torch.Generator(device="cuda").manual_seed(int(abs(base) * 2) + Skv)
+    q = torch.randint(-2, 3, (B, Hq, Sq, 64), device="cuda", generator=g).to(dtype)
+    k = torch.randint(-2, 3, (B, Hkv, Skv, 64), device="cuda", generator=g).to(dtype)
+    q[..., :16], k[..., :16] = 64, base
+    if late:
+        k[:, :, :Skv // 2, :16] = 0
+    v, go = (torch.randn(B, h, s, 64, device="cuda", generator=g).to(dtype) for h, s in ((Hkv, Skv), (Hq, Sq)))
+    return q, k, v, go
+
+
+TALL = [(1, 2, 1, 150, 300), (5, 16, 16, 130, 260), (2, 8, 2, 1, 1500), (1, 4, 4, 1, 70)]
+
+
+@pytest.mark.parametrize("late", [False, True])
+@pytest.mark.parametrize("base", [5.0, 11.5, -11.5, 23.5, -23.5, 60.0, -60.0, 156.0, -156.0])   # scores of 1280 to 39936
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", TALL)
+def test_tall_scores(shape, dtype, base, late):
+    """The output's roundings do not depend on the size of the scores; lse is one binary32 number, so the weights that the
+    backward pass forms from it are off by six roundings of it, a factor of a row."""
+    q, k, v, go = _tall(*shape, dtype, base, late)
+    kw = dict(causal=True, scale=0.25)
+    st = da.new_status()
+    out, lse = da.attention_forward(q, k, v, status=st, **kw)
+    r = R.attention(q, k, v, go, **kw)
+    tol, A = R.attention_tolerance(r, dtype), r["abs"]
+    T._close(out, r["out"], tol["out"], "out")
+    assert ((lse.double() - r["lse"]).abs() <= 2.0 ** -17 * (1 + r["lse"].abs())).all()
+    grads = da.attention_backward(q, k, v, out, lse, go, status=st, **kw)
+    e = 6 * 2.0 ** -24 * float(r["lse"].abs().max())
+    for got, n, more in zip(grads, ("dq", "dk", "dv"), (2 * A["dq_rough"], 2 * A["dk_rough"], A["dv"])):
+        T._close(got, r[n], tol[n] + e * more, n)
+    assert da.read_status(st) == 0
