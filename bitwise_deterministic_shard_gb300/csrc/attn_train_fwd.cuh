@@ -284,6 +284,9 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
     mbar_fence_init();
   }
   if (warp == 17) tmem_alloc(&tmem_at, 512);
+  // Rows that the packed heads' query box leaves unfilled (their number need not divide 128): what lies there may not decide
+  // the form of the cap.
+  if (wg == 0 && half == 0 && a.pack > 1 && r >= a.pack * a.qrows) zero_row<DP>(base + L::Q, r);
   if (wg < 2) {
     const int dl = __reduce_min_sync(0xffffffffu, doc < 0 ? 0x7fffffff : doc), dh = __reduce_max_sync(0xffffffffu, doc);
     const int neg = __any_sync(0xffffffffu, valid && doc < 0);

@@ -73,3 +73,26 @@ def test_tall_scores(shape, dtype, base, late):
     for got, n, more in zip(grads, ("dq", "dk", "dv"), (2 * A["dq_rough"], 2 * A["dk_rough"], A["dv"])):
         T._close(got, r[n], tol[n] + e * more, n)
     assert da.read_status(st) == 0
+
+
+# ---------------------------------------------------------------- what may not matter
+
+def _leave_behind(x):
+    """Fills the shared memory of every SM where a query tile lies: a call whose output is x everywhere."""
+    q = torch.full((4, 152, 256, 128), x, device="cuda", dtype=torch.bfloat16)
+    da.attention_forward(q, q, q, scale=0.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("B, Hkv, group, Sq, Skv", [(2, 2, 5, 24, 200), (2, 1, 3, 40, 1200), (1, 2, 7, 18, 90), (90, 2, 5, 25, 130)])
+def test_rows_that_are_no_query(B, Hkv, group, Sq, Skv, dtype):
+    """Heads that do not divide 128 leave rows of the query tile unfilled: what lies there decides nothing."""
+    q, k, v, _ = T._attn_inputs(B, Hkv * group, Hkv, Sq, Skv, 128, dtype, seed=14, heavy=False)
+    kw = dict(causal=True, softcap=30.0)
+    _leave_behind(0.0)
+    want = da.attention_forward(q, k, v, **kw)
+    for x in (300.0, 10.0, 3.0, 1.5, 0.7):
+        for _ in range(4):
+            _leave_behind(x)
+            got = da.attention_forward(q, k, v, **kw)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), x
