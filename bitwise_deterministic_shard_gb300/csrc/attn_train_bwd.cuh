@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dkv_kernel(const __grid_
         if (a.docs) same_doc<32>(see, a.docs + (int64_t)b * a.Skv + pos0 + part * 32, a.Sq - q * TA_TILE - part * 32, doc);
       }
       if (sc.capped) {
-        sc.cap.apply<32>(v);
+        sc.cap.apply<32>(v, !padded);
       } else {
 #pragma unroll
         for (int c = 0; c < 32; c += 2) f2::unpack(f2::mul(f2::pack(v[c], v[c + 1]), f2::splat(sc.f0)), v[c], v[c + 1]);
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
       float p[32];
       const u64 sh = f2::splat(shift);
       if (sc.capped) {
-        sc.cap.apply<32>(v);
+        sc.cap.apply<32>(v, !padded);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) f2::unpack(f2::add(f2::pack(v[c], v[c + 1]), sh), p[c], p[c + 1]);
       } else {

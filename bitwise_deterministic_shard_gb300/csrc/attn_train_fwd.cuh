@@ -92,9 +92,10 @@ struct Cap {
     p = f2::fma(p, z, c.c[0]);
     return f2::mul(t, p);
   }
-  // v <- f tanh(k v) for N scores of each lane; the warp decides which form it takes
+  // v <- f tanh(k v) for N scores of each lane.  The warp decides by its scores which form it takes; where they hold padding,
+  // whose values may be anything, without a vote the one for any argument.
   template <int N>
-  __device__ __forceinline__ void apply(float* v) const {
+  __device__ __forceinline__ void apply(float* v, bool vote) const {
     float m[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
@@ -102,10 +103,10 @@ struct Cap {
       m[1] = max3_abs(m[1], v[i + 2], v[i + 3]);
     }
     const float top = fmaxf(m[0], m[1]);
-    if (__all_sync(0xffffffffu, top <= c.least)) {
+    if (vote && __all_sync(0xffffffffu, top <= c.least)) {
 #pragma unroll
       for (int i = 0; i < N; i += 2) f2::unpack(smaller2(f2::pack(v[i], v[i + 1])), v[i], v[i + 1]);
-    } else if (__all_sync(0xffffffffu, top <= c.most)) {
+    } else if (vote && __all_sync(0xffffffffu, top <= c.most)) {
 #pragma unroll
       for (int i = 0; i < N; i += 2) f2::unpack(small2(f2::pack(v[i], v[i + 1])), v[i], v[i + 1]);
     } else {
@@ -490,15 +491,16 @@ __global__ void __launch_bounds__(TA_FWD_THREADS, 1) ta_fwd_kernel(const __grid_
       fence_before();
       mbar_arrive(&s_read[i]);
       const int j0 = n * TA_TILE + half * 64;
-      bool masked = (n + 1) * TA_TILE > full, padded = false;
+      bool masked = (n + 1) * TA_TILE > full, padded = false, vote = true;   // padded: keys; vote: no padding at all
       if (a.docs) {
         const TaBounds bd = a.bounds[(int64_t)b * a.ktiles + n];
         padded = bd.neg;
-        masked |= bd.neg || bd.lo != bd.hi || bd.lo != qdoc[i][0] || bd.lo != qdoc[i][1] || qdoc[i][2];
+        vote = !(bd.neg || qdoc[i][2]);
+        masked |= !vote || bd.lo != bd.hi || bd.lo != qdoc[i][0] || bd.lo != qdoc[i][1];
       }
       if (capped) {
-        cap.apply<32>(v);
-        cap.apply<32>(v + 32);
+        cap.apply<32>(v, vote);
+        cap.apply<32>(v + 32, vote);
       } else if (units) {
 #pragma unroll
         for (int c = 0; c < 64; c++) v[c] *= f0;

@@ -96,3 +96,25 @@ def test_rows_that_are_no_query(B, Hkv, group, Sq, Skv, dtype):
             _leave_behind(x)
             got = da.attention_forward(q, k, v, **kw)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), x
+
+
+@pytest.mark.parametrize("B, H, Sq", [(1, 4, 320), (6, 16, 320), (2, 8, 1)])
+def test_padding_does_not_matter(B, H, Sq):
+    """Tokens of padding, of any size: the same bytes, whichever form of the cap their scores would take."""
+    S = 320
+    q, k, v, go = T._attn_inputs(B, H, H // 2, Sq, S, 64, torch.bfloat16, seed=15, heavy=False)
+    docs = torch.zeros(B, S, dtype=torch.int32, device="cuda")
+    docs[:, 100:110] = -1
+    kw = dict(causal=True, softcap=30.0, docs=docs)
+
+    def both(q, k):
+        out, lse = da.attention_forward(q, k, v, **kw)
+        return out, lse, *da.attention_backward(q, k, v, out, lse, go, **kw)
+    want = both(q, k)
+    for x in (2.0, 8.0, 300.0, 1e30, float("nan")):
+        kk, qq = k.clone(), q.clone()
+        kk[:, :, 100:110] *= x
+        if Sq == S:
+            qq[:, :, 100:110] *= x
+        for a, b in zip(both(qq, kk), want):
+            assert torch.equal(a, b), x
