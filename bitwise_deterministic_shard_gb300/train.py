@@ -2,7 +2,7 @@
 layer norm, and AdamW over many tensors, each with its gradient where it has one.
 
 Argument marshalling only, as in the package's __init__: the computation runs in the CUDA kernels
-behind include/detattn.h on the current stream, and there is no CPU path.  Every kernel adds in
+behind include/detattn.h on the current stream of the tensors' device, and there is no CPU path.  Every kernel adds in
 an order that depends on the sizes and types alone, so equal calls give equal bytes on every run.
 """
 from __future__ import annotations
@@ -72,8 +72,15 @@ def _on(index, name, t):
         raise DetAttnError(f"{name} is on another device")
 
 
-def _stream(index):
-    return torch._C._cuda_getCurrentRawStream(index)
+def _run(what, index, f, *args):
+    """f(*args, stream) on the current stream of the tensors' device, with that device current: a launch goes to the
+    current one, whichever device its addresses and its stream belong to."""
+    if torch._C._cuda_getDevice() == index:
+        code = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            code = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    _da._check(code, what)
 
 
 def _addr(t):
@@ -191,7 +198,7 @@ def attention_forward(Q, K, V, causal=False, scale=None, softcap=0.0, slopes=Non
     L = _da.lib()
     need = L.dta_workspace_bytes(A.desc, 0)
     ws = _room(need, workspace, A.device)
-    _da._check(L.dta_forward(A.desc, _view(out, A.code), _addr(lse), _addr(ws), need, _stream(A.index)), "attention_forward")
+    _run("attention_forward", A.index, L.dta_forward, A.desc, _view(out, A.code), _addr(lse), _addr(ws), need)
     return out, lse
 
 
@@ -213,8 +220,8 @@ def attention_backward(Q, K, V, out, lse, grad, causal=False, scale=None, softca
     L, c = _da.lib(), A.code
     need = L.dta_workspace_bytes(A.desc, 1)
     ws = _room(need, workspace, A.device)
-    _da._check(L.dta_backward(A.desc, _view(out, c), lse.data_ptr(), _view(grad, c), _view(dq, c), _view(dk, c), _view(dv, c),
-                              _addr(ws), need, _stream(A.index)), "attention_backward")
+    _run("attention_backward", index, L.dta_backward, A.desc, _view(out, c), lse.data_ptr(), _view(grad, c), _view(dq, c),
+         _view(dk, c), _view(dv, c), _addr(ws), need)
     return dq, dk, dv
 
 
@@ -305,8 +312,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, need_stats=True):
         mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     Y = _MATRIX.pack(y.data_ptr(), code, y.numel() // cols, cols, cols)
-    _da._check(_da.lib().dln_forward(X, _addr(weight), _addr(bias), _CODES[wt], eps, Y, _addr(mean), _addr(rstd),
-                                     _stream(index)), "layer_norm_forward")
+    _run("layer_norm_forward", index, _da.lib().dln_forward, X, _addr(weight), _addr(bias), _CODES[wt], eps, Y, _addr(mean),
+         _addr(rstd))
     return y, mean, rstd
 
 
@@ -331,8 +338,8 @@ def layer_norm_backward(grad, x, weight, mean, rstd, need_weight=True, need_bias
     L = _da.lib()
     need = L.dln_workspace_bytes(rows, cols) if need_weight or need_bias else 0
     ws = _room(need, workspace, dev)
-    _da._check(L.dln_backward(G, X, _addr(weight), _CODES[wt], mean.data_ptr(), rstd.data_ptr(), DX, _addr(dw), _addr(db),
-                              _addr(ws), need, _stream(index)), "layer_norm_backward")
+    _run("layer_norm_backward", index, L.dln_backward, G, X, _addr(weight), _CODES[wt], mean.data_ptr(), rstd.data_ptr(), DX,
+         _addr(dw), _addr(db), _addr(ws), need)
     return dx, dw, db
 
 
@@ -414,10 +421,9 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
                                    or grad_scale.get_device() != index):
         raise DetAttnError("grad_scale must be one f32 element on the params' device")
     k = len(table) // 4
-    _da._check(_da.lib().dow_adamw(struct.pack(f"{4 * k}Q", *table), k, code, bits, exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
-                                   _addr(exp_avg_scale), _addr(exp_avg_sq_scale), at,
-                                   _HYPER.pack(lr, betas[0], betas[1], eps, weight_decay, int(step)), _addr(grad_scale),
-                                   _stream(index)), "adamw_step")
+    _run("adamw_step", index, _da.lib().dow_adamw, struct.pack(f"{4 * k}Q", *table), k, code, bits, exp_avg.data_ptr(),
+         exp_avg_sq.data_ptr(), _addr(exp_avg_scale), _addr(exp_avg_sq_scale), at,
+         _HYPER.pack(lr, betas[0], betas[1], eps, weight_decay, int(step)), _addr(grad_scale))
 
 
 class AdamW:

@@ -1,0 +1,64 @@
+"""What the binding of the training operators does around the library's calls, with a stub in the library's place: the device and
+stream that a call goes to, what it takes as a workspace, what autograd is told."""
+import contextlib
+import math
+
+import pytest
+import torch
+
+import bitwise_deterministic_shard_gb300 as da
+from bitwise_deterministic_shard_gb300 import train
+
+
+class _Stub:
+    """Answers every call with 0 (no workspace, no error) and notes it beside the device that was current."""
+
+    def __init__(self):
+        self.calls, self.current = [], 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, self.current, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def stub(monkeypatch):
+    """CPU tensors as those of device -1 (what their get_device says), device 0 current."""
+    s = _Stub()
+
+    @contextlib.contextmanager
+    def device(index):
+        before, s.current = s.current, index
+        yield
+        s.current = before
+    monkeypatch.setattr(da, "_cuda", lambda t, name: None)
+    monkeypatch.setattr(da, "lib", lambda: s)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: s.current, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+    return s
+
+
+def _qkv():
+    return [torch.zeros(1, h, 8, 64, dtype=torch.bfloat16) for h in (4, 2, 2)]
+
+
+def test_calls_go_to_the_tensors_device(stub):
+    """A raw stream means nothing without its device (0 is the default stream of whichever is current)."""
+    q, k, v = _qkv()
+    x, s = torch.zeros(4, 10), torch.zeros(4)
+    da.attention_forward(q, k, v)
+    da.attention_backward(q, k, v, q, torch.zeros(1, 4, 8), q)
+    da.layer_norm_forward(x)
+    da.layer_norm_backward(x, x, None, s, s)
+    da.adamw_step([s], [s], torch.zeros(256), torch.zeros(256), 1)
+    p = torch.zeros(5)
+    p.grad = torch.zeros(5)
+    da.AdamW([p]).step()
+    launches = [c for c in stub.calls if not c[0].endswith("_bytes")]
+    assert [c[0] for c in launches] == ["dta_forward", "dta_backward", "dln_forward", "dln_backward", "dow_adamw", "dow_adamw"]
+    for name, device, args in launches:
+        assert device == -1 and args[-1] == 1000 - 1, name
+    assert stub.current == 0
