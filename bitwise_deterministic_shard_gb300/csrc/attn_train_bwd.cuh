@@ -714,9 +714,9 @@ __global__ void __launch_bounds__(TA_BWD_THREADS, 1) ta_dq_kernel(const __grid_c
 template <int DP, bool BF>
 cudaError_t ta_dkv(const TaArgs& a, cudaStream_t st) {
   using L = TaBwdSmem<DP>;
-  static int bytes = 0;
-  static const cudaError_t ready = tile_smem(ta_dkv_kernel<DP, BF>, L::END, &bytes);
-  if (ready != cudaSuccess) return ready;
+  static TileSmem smem;
+  int bytes;
+  if (const cudaError_t e = smem.ready(ta_dkv_kernel<DP, BF>, L::END, &bytes)) return e;
   ta_dkv_kernel<DP, BF><<<(unsigned)(a.B * a.Hkv) * a.ktiles, TA_BWD_THREADS, bytes, st>>>(a);
   return cudaGetLastError();
 }
@@ -724,9 +724,9 @@ cudaError_t ta_dkv(const TaArgs& a, cudaStream_t st) {
 template <int DP, bool BF>
 cudaError_t ta_dq(const TaArgs& a, cudaStream_t st) {
   using L = TaBwdSmem<DP>;
-  static int bytes = 0;
-  static const cudaError_t ready = tile_smem(ta_dq_kernel<DP, BF>, L::END, &bytes);
-  if (ready != cudaSuccess) return ready;
+  static TileSmem smem;
+  int bytes;
+  if (const cudaError_t e = smem.ready(ta_dq_kernel<DP, BF>, L::END, &bytes)) return e;
   if (a.qtiles == 0) return cudaSuccess;
   ta_dq_kernel<DP, BF><<<(unsigned)(a.B * a.Hq) * a.qtiles, TA_BWD_THREADS, bytes, st>>>(a);
   return cudaGetLastError();

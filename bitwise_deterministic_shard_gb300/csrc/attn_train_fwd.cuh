@@ -39,6 +39,7 @@
 #pragma once
 #include "../../include/detattn.h"
 #include "attn_train.h"
+#include "device_once.h"
 #include "pack2.cuh"
 #include "tc5_tile.cuh"
 #include "tile_ring.h"
@@ -768,29 +769,38 @@ __global__ void __launch_bounds__(128) ta_join_kernel(const __grid_constant__ Ta
 }
 
 // Dynamic shared memory of a kernel with `tiles` bytes of 1024-byte aligned tiles: with up to 1024 bytes of static shared
-// memory before them the tiles are aligned within the 227 KB of a CTA.
-template <typename K>
-cudaError_t tile_smem(K kernel, int tiles, int* bytes) {
-  cudaFuncAttributes at;
-  const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
-  if (e != cudaSuccess) return e;
-  if (at.sharedSizeBytes > 1024) return cudaErrorInvalidConfiguration;
-  *bytes = tiles + 1024 - (int)at.sharedSizeBytes;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, *bytes);
-}
+// memory before them the tiles are aligned within the 227 KB of a CTA.  One object a kernel.
+class TileSmem {
+  DeviceOnce once;
+  std::atomic<int> fixed{-1};   // bytes of static shared memory: the kernel's, on every device
+
+ public:
+  template <typename K>
+  cudaError_t ready(K kernel, int tiles, int* bytes) {
+    int before = fixed.load(std::memory_order_relaxed);
+    if (before < 0) {
+      cudaFuncAttributes at;
+      const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+      if (e != cudaSuccess) return e;
+      if (at.sharedSizeBytes > 1024) return cudaErrorInvalidConfiguration;
+      fixed.store(before = (int)at.sharedSizeBytes, std::memory_order_relaxed);
+    }
+    *bytes = tiles + 1024 - before;
+    return allow_smem(once, kernel, *bytes);
+  }
+};
 
 template <int DP, bool BF>
 cudaError_t ta_forward(const TaArgs& a, cudaStream_t st) {
   using L = TaFwdSmem<DP>;
-  static int bytes[2] = {};
-  static const cudaError_t ready[2] = {tile_smem(ta_fwd_kernel<DP, BF, false>, L::END, &bytes[0]),
-                                       tile_smem(ta_fwd_kernel<DP, BF, true>, L::END, &bytes[1])};
+  static TileSmem smem[2];
   const bool alt = a.splits > 0;
-  if (ready[alt] != cudaSuccess) return ready[alt];
+  int bytes;
+  const auto kernel = alt ? ta_fwd_kernel<DP, BF, true> : ta_fwd_kernel<DP, BF, false>;
+  if (const cudaError_t e = smem[alt].ready(kernel, L::END, &bytes)) return e;
   const int HB = a.B * (a.Hq / a.pack);
   const unsigned grid = (unsigned)HB * (alt ? a.splits * a.qtiles : (a.qtiles + 1) / 2);
-  if (alt) ta_fwd_kernel<DP, BF, true><<<grid, TA_FWD_THREADS, bytes[1], st>>>(a);
-  else ta_fwd_kernel<DP, BF, false><<<grid, TA_FWD_THREADS, bytes[0], st>>>(a);
+  kernel<<<grid, TA_FWD_THREADS, bytes, st>>>(a);
   if (a.splits > 1) {
     const int64_t rows = (int64_t)HB * a.pack * a.Sq;
     ta_join_kernel<DP, BF><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);

@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "../../include/detattn.h"
+#include "device_once.h"
 #include "train_kernels.h"
 #include "train_math.cuh"
 
@@ -893,17 +894,15 @@ void bwd_go(const NormArgs& a, bool al, unsigned grid, int64_t per, cudaStream_t
 template <typename T, int G, int R, int ST>
 void fwd_stream(const NormArgs& a, cudaStream_t st) {
   constexpr int bytes = ST * R * 2 * G * 16;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(norm_fwd_stream_kernel<T, G, 2, R, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  (void)ready;
+  static DeviceOnce once;
+  (void)allow_smem(once, norm_fwd_stream_kernel<T, G, 2, R, ST>, bytes);
   norm_fwd_stream_kernel<T, G, 2, R, ST><<<(unsigned)std::min<int64_t>(152 * 512 / G, (a.rows + R - 1) / R), G, bytes, st>>>(a);
 }
 template <typename T, int G, int R, int ST>
 void bwd_stream(const NormArgs& a, unsigned grid, int64_t per, cudaStream_t st) {
   constexpr int bytes = ST * R * 2 * G * 32;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(norm_bwd_stream_kernel<T, G, 2, R, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  (void)ready;
+  static DeviceOnce once;
+  (void)allow_smem(once, norm_bwd_stream_kernel<T, G, 2, R, ST>, bytes);
   norm_bwd_stream_kernel<T, G, 2, R, ST><<<grid, G, bytes, st>>>(a, per);
 }
 
@@ -914,17 +913,15 @@ int staged_room(const NormArgs& a) {
 }
 template <typename T, int G, int NJ>
 void fwd_staged(const NormArgs& a, cudaStream_t st) {
-  static const cudaError_t ready = cudaFuncSetAttribute(norm_fwd_staged_kernel<T, G, NJ>,
-                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * (G * NJ * 4 + 32));
-  (void)ready;
+  static DeviceOnce once;
+  (void)allow_smem(once, norm_fwd_staged_kernel<T, G, NJ>, 3 * (G * NJ * 4 + 32));
   const int room = staged_room<T>(a);
   norm_fwd_staged_kernel<T, G, NJ><<<(unsigned)std::min<int64_t>(152 * 1024 / G, a.rows), G, 3 * room, st>>>(a, room);
 }
 template <typename T, int G, int NJ>
 void bwd_staged(const NormArgs& a, unsigned grid, int64_t per, cudaStream_t st) {
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(norm_bwd_staged_kernel<T, G, NJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, 6 * (G * NJ * 4 + 32));
-  (void)ready;
+  static DeviceOnce once;
+  (void)allow_smem(once, norm_bwd_staged_kernel<T, G, NJ>, 6 * (G * NJ * 4 + 32));
   const int room = staged_room<T>(a);
   norm_bwd_staged_kernel<T, G, NJ><<<grid, G, 6 * room, st>>>(a, per, room);
 }
