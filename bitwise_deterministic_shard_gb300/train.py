@@ -317,10 +317,15 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, need_stats=True):
     return y, mean, rstd
 
 
-def layer_norm_backward(grad, x, weight, mean, rstd, need_weight=True, need_bias=True, workspace=None):
+def layer_norm_backward(grad, x, weight, mean, rstd, need_weight=True, need_bias=True, workspace=None, weight_dtype=None):
     """(dx, dweight, dbias) from the upstream gradient and layer_norm_forward's mean and rstd; the
-    weight gradients are None where not needed, and of weight's dtype (x's without a weight)."""
+    weight gradients are None where not needed, and of weight's dtype; without a weight of weight_dtype, x's or f32
+    (None: x's), such as the dtype of a bias that has no weight beside it."""
     cols, code, wt, index = _weights(x, weight, None)
+    if weight_dtype is not None and weight_dtype != wt:
+        if weight is not None or weight_dtype != torch.float32:
+            raise DetAttnError("weight_dtype must be weight's dtype, without a weight x's or f32")
+        wt = weight_dtype
     if grad.get_device() != index or grad.shape != x.shape or grad.dtype != x.dtype:
         raise DetAttnError("grad must have x's shape, dtype and device")
     rows = x.numel() // cols
@@ -356,9 +361,8 @@ class _LayerNorm(torch.autograd.Function):
     def backward(ctx, grad):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx, dw, db = layer_norm_backward(grad, x, weight, mean, rstd, need[1], need[2])
-        if db is not None and db.dtype != ctx.bias_dtype:
-            db = db.to(ctx.bias_dtype)
+        dx, dw, db = layer_norm_backward(grad, x, weight, mean, rstd, need[1], need[2],
+                                         weight_dtype=ctx.bias_dtype if need[2] else None)
         return dx if need[0] else None, dw, db, None
 
 

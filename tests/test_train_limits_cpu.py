@@ -62,3 +62,16 @@ def test_calls_go_to_the_tensors_device(stub):
     for name, device, args in launches:
         assert device == -1 and args[-1] == 1000 - 1, name
     assert stub.current == 0
+
+
+# ---------------------------------------------------------------- layer norm
+
+def test_layer_norm_weight_dtype(stub):
+    x, s, w = torch.zeros(4, 10, dtype=torch.bfloat16), torch.zeros(4), torch.zeros(10)
+    for weight, want, got in ((None, None, torch.bfloat16), (None, torch.float32, torch.float32), (None, x.dtype, x.dtype),
+                              (w, None, torch.float32), (w, torch.float32, torch.float32), (w.bfloat16(), None, x.dtype)):
+        _, dw, db = da.layer_norm_backward(x, x, weight, s, s, weight_dtype=want)
+        assert dw.dtype == db.dtype == got and stub.calls[-1][2][3] == train._CODES[got]
+    for weight, want in ((w, x.dtype), (w.bfloat16(), torch.float32), (None, torch.float16), (None, torch.float64)):
+        with pytest.raises(da.DetAttnError):
+            da.layer_norm_backward(x, x, weight, s, s, weight_dtype=want)

@@ -118,3 +118,17 @@ def test_padding_does_not_matter(B, H, Sq):
             qq[:, :, 100:110] *= x
         for a, b in zip(both(qq, kk), want):
             assert torch.equal(a, b), x
+
+
+# ---------------------------------------------------------------- layer norm
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_layer_norm_bias_keeps_its_type(dtype):
+    """An f32 bias beside 16-bit rows without a weight: its gradient is a binary32 sum, not a 16-bit one."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(700, 300, device="cuda", generator=g).to(dtype)
+    dy = (torch.randn(700, 300, device="cuda", generator=g) + 200).to(dtype)     # sums of 140000, beyond f16
+    b = torch.zeros(300, device="cuda", requires_grad=True)
+    da.layer_norm(x, None, b).backward(dy)
+    r = R.layer_norm(x, None, b.detach(), dy)
+    T._close(b.grad, r["db"], R.layer_norm_tolerance(r, dtype, torch.float32, 700, 300)["db"], "db")
