@@ -3,7 +3,8 @@ layer norm, and AdamW over many tensors, each with its gradient where it has one
 
 Argument marshalling only, as in the package's __init__: the computation runs in the CUDA kernels
 behind include/detattn.h on the current stream of the tensors' device, and there is no CPU path.  Every kernel adds in
-an order that depends on the sizes and types alone, so equal calls give equal bytes on every run.
+an order that depends on the sizes, types and options and, for layer norm, on what starts on 16 bytes, so equal calls (for
+layer norm: on equally aligned tensors) give equal bytes on every run.
 """
 from __future__ import annotations
 
@@ -301,7 +302,8 @@ def _packed(t):
 def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, need_stats=True):
     """Layer norm over the last dimension: (y like x, mean f32, rstd f32, one per row).
     x [..., cols] f32, bf16 or f16; weight and bias [cols] of x's dtype or f32, or None.  mean and rstd, which
-    the backward pass takes, are None without need_stats."""
+    the backward pass takes, are None without need_stats.  Rows, weight and bias that all start on 16 bytes are added up in
+    another order than others: the same values in a shifted view can differ in low bits."""
     cols, code, wt, index = _weights(x, weight, bias)
     X, x = _rows(x, code, cols)
     weight, bias = _packed(weight), _packed(bias)

@@ -132,3 +132,25 @@ def test_layer_norm_bias_keeps_its_type(dtype):
     da.layer_norm(x, None, b).backward(dy)
     r = R.layer_norm(x, None, b.detach(), dy)
     T._close(b.grad, r["db"], R.layer_norm_tolerance(r, dtype, torch.float32, 700, 300)["db"], "db")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows, cols, gap", [(1300, 1100, 0), (400, 1101, 3), (300, 600, 0), (5, 9000, 7)])
+def test_layer_norm_bytes_with_the_same_alignment(rows, cols, gap, dtype):
+    """Equal values whose rows start alike relative to 16 bytes give equal bytes, wherever they lie."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, dy = (torch.randn(rows, cols, device="cuda", generator=g).to(dtype) for _ in range(2))
+    w, b = (torch.randn(cols, device="cuda", generator=g) for _ in range(2))
+
+    def both(x, dy):
+        y, mean, rstd = da.layer_norm_forward(x, w, b)
+        return y, mean, rstd, *da.layer_norm_backward(dy, x, w, mean, rstd)
+
+    def placed(t, pad):
+        room = torch.empty(pad + rows * (cols + gap), device="cuda", dtype=dtype)
+        p = room[pad:].view(rows, cols + gap)[:, :cols]
+        return p.copy_(t)
+    want = both(placed(x, 0), placed(dy, 0))
+    for pad in (64, 4096):
+        for p, q in zip(both(placed(x, pad), placed(dy, pad)), want):
+            assert torch.equal(p, q)
