@@ -84,6 +84,17 @@ def _run(what, index, f, *args):
     _da._check(code, what)
 
 
+def _tracked(*ts):
+    """Whether autograd may follow any of ts: backward, or forward mode, whose tensors do not require a gradient (its
+    functions then refuse, as they have no forward-mode derivative)."""
+    if torch.autograd.forward_ad._current_level >= 0:
+        return True
+    for t in ts:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -245,7 +256,7 @@ def attention(Q, K, V, causal=False, scale=None, softcap=0.0, slopes=None, docs=
     CUDA graph calls attention_backward itself, as with any autograd function whose leaves live in
     an eager graph too.)"""
     kw = dict(causal=causal, scale=scale, softcap=softcap, slopes=slopes, docs=docs, prefix=prefix, status=status)
-    if torch.is_grad_enabled() and (Q.requires_grad or K.requires_grad or V.requires_grad):
+    if _tracked(Q, K, V):
         return _AttentionFn.apply(Q, K, V, kw)
     return attention_forward(Q, K, V, need_lse=False, **kw)[0]
 
@@ -370,8 +381,7 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """layer_norm_forward's y, with autograd for x, weight and bias."""
-    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
-                                    or (bias is not None and bias.requires_grad)):
+    if _tracked(x, weight, bias):
         return _LayerNorm.apply(x, weight, bias, eps)
     return layer_norm_forward(x, weight, bias, eps, need_stats=False)[0]
 

@@ -75,3 +75,26 @@ def test_layer_norm_weight_dtype(stub):
     for weight, want in ((w, x.dtype), (w.bfloat16(), torch.float32), (None, torch.float16), (None, torch.float64)):
         with pytest.raises(da.DetAttnError):
             da.layer_norm_backward(x, x, weight, s, s, weight_dtype=want)
+
+
+# ---------------------------------------------------------------- autograd
+
+def test_forward_mode_is_refused_not_dropped(stub):
+    """A dual tensor does not require a gradient; its tangent may not get lost on the way past the autograd functions."""
+    q, k, v = _qkv()
+    x, w, b = torch.zeros(4, 10), torch.ones(10), torch.zeros(10)
+    with torch.autograd.forward_ad.dual_level():
+        def dual(t):
+            return torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad):
+                for i in range(3):
+                    args = [q, k, v]
+                    args[i] = dual(args[i])
+                    with pytest.raises(Exception, match="jvp|forward"):
+                        da.attention(*args)
+                    args = [x, w, b]
+                    args[i] = dual(args[i])
+                    with pytest.raises(Exception, match="jvp|forward"):
+                        da.layer_norm(*args)
+                assert da.attention(q, k, v).shape == q.shape and da.layer_norm(x, w, b).shape == x.shape
