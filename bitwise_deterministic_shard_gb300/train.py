@@ -239,26 +239,28 @@ def attention_backward(Q, K, V, out, lse, grad, causal=False, scale=None, softca
 
 class _AttentionFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, Q, K, V, kw):
-        out, lse = attention_forward(Q, K, V, **kw)
-        ctx.save_for_backward(Q, K, V, out, lse)
+    def forward(ctx, Q, K, V, slopes, docs, prefix, kw):
+        out, lse = attention_forward(Q, K, V, slopes=slopes, docs=docs, prefix=prefix, **kw)
+        ctx.save_for_backward(Q, K, V, out, lse, slopes, docs, prefix)   # a change in place of any of them is refused
         ctx.kw = kw
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        return (*attention_backward(*ctx.saved_tensors, grad, **ctx.kw), None)
+        Q, K, V, out, lse, slopes, docs, prefix = ctx.saved_tensors
+        return (*attention_backward(Q, K, V, out, lse, grad, slopes=slopes, docs=docs, prefix=prefix, **ctx.kw),
+                None, None, None, None)
 
 
 def attention(Q, K, V, causal=False, scale=None, softcap=0.0, slopes=None, docs=None, prefix=None, status=None):
     """attention_forward's output, with autograd for Q, K and V.  (A backward pass that is captured into a
     CUDA graph calls attention_backward itself, as with any autograd function whose leaves live in
     an eager graph too.)"""
-    kw = dict(causal=causal, scale=scale, softcap=softcap, slopes=slopes, docs=docs, prefix=prefix, status=status)
+    kw = dict(causal=causal, scale=scale, softcap=softcap, status=status)
     if _tracked(Q, K, V):
-        return _AttentionFn.apply(Q, K, V, kw)
-    return attention_forward(Q, K, V, need_lse=False, **kw)[0]
+        return _AttentionFn.apply(Q, K, V, slopes, docs, prefix, kw)
+    return attention_forward(Q, K, V, slopes=slopes, docs=docs, prefix=prefix, need_lse=False, **kw)[0]
 
 
 # ---------------------------------------------------------------- layer norm

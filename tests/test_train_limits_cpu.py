@@ -98,3 +98,17 @@ def test_forward_mode_is_refused_not_dropped(stub):
                     with pytest.raises(Exception, match="jvp|forward"):
                         da.layer_norm(*args)
                 assert da.attention(q, k, v).shape == q.shape and da.layer_norm(x, w, b).shape == x.shape
+
+
+def test_masks_and_slopes_may_not_change_before_the_backward_pass(stub):
+    S, opts = 8, dict(docs=lambda: torch.zeros(1, 8, dtype=torch.int32), prefix=lambda: torch.zeros(1, dtype=torch.int32),
+                      slopes=lambda: torch.zeros(4))
+    for name, make in opts.items():
+        q, k, v = (t.requires_grad_(True) for t in _qkv())
+        t = make()
+        out = da.attention(q, k, v, causal=True, **{name: t})
+        out.sum().backward(retain_graph=True)
+        assert q.grad.shape == q.shape and stub.calls[-1][0] == "dta_backward"
+        t.add_(1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out.sum().backward()
