@@ -95,6 +95,11 @@ def _tracked(*ts):
     return False
 
 
+def _written(ts):
+    """Tells autograd of writes that went through addresses: a graph that saved one of ts refuses to go backward."""
+    torch.autograd.graph.increment_version(ts)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -205,12 +210,14 @@ def attention_forward(Q, K, V, causal=False, scale=None, softcap=0.0, slopes=Non
     key head, split over the GPU.  out takes Q's layout.  Tensors that the kernels cannot address (a last
     dimension that is not contiguous, strides or starts off 16 bytes, broadcast dimensions) are copied."""
     A = _Attention(Q, K, V, causal, scale, softcap, slopes, docs, prefix, status)
-    out = _given(out, Q, "out")
+    given, out = out, _given(out, Q, "out")
     lse = torch.empty(A.shape[:3], dtype=torch.float32, device=A.device) if need_lse else None
     L = _da.lib()
     need = L.dta_workspace_bytes(A.desc, 0)
     ws = _room(need, workspace, A.device)
     _run("attention_forward", A.index, L.dta_forward, A.desc, _view(out, A.code), _addr(lse), _addr(ws), need)
+    if given is not None:
+        _written(out)
     return out, lse
 
 
@@ -414,7 +421,7 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     dt, index = params[0].dtype, params[0].get_device()
     code = _code(params[0], "params")
     _da._cuda(params[0], "params")
-    table, at, block = [], 0, STATE_BLOCK
+    table, moved, at, block = [], [], 0, STATE_BLOCK
     for p, g in zip(params, grads):
         if p.dtype is not dt or p.get_device() != index or not p.is_contiguous():
             raise DetAttnError("params must be contiguous tensors of one dtype on one device")
@@ -423,18 +430,20 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
             if g.dtype is not dt or g.numel() != m or g.get_device() != index or not g.is_contiguous():
                 raise DetAttnError("grads must be contiguous, of their params' dtype, device and size")
             table += (p.data_ptr(), g.data_ptr(), m, at)
-        at += -(-m // block) * block
-    bits = 8 if exp_avg.dtype == torch.float8_e4m3fn else 32
-    st = torch.float8_e4m3fn if bits == 8 else torch.float32
-    for t, name, want, length in ((exp_avg, "exp_avg", st, at), (exp_avg_sq, "exp_avg_sq", st, at),
-                                  (exp_avg_scale, "exp_avg_scale", torch.float32, at // STATE_BLOCK),
-                                  (exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, at // STATE_BLOCK)):
-        if bits == 32 and name.endswith("scale"):
-            if t is not None:
-                raise DetAttnError("scales go with 8-bit states")
-            continue
-        if t is None or t.dtype != want or t.numel() != length or not t.is_contiguous() or t.get_device() != index:
-            raise DetAttnError(f"{name} must be contiguous {want} [{length}] on the params' device")
+            moved.append(p)
+        at += (m + block - 1) // block * block
+    states = (exp_avg, exp_avg_sq)
+    if exp_avg.dtype == torch.float8_e4m3fn:
+        bits, scales = 8, (exp_avg_scale, exp_avg_sq_scale)
+    else:
+        bits, scales = 32, ()
+        if exp_avg_scale is not None or exp_avg_sq_scale is not None:
+            raise DetAttnError("scales go with 8-bit states")
+    for ts, want, length in ((states, torch.float8_e4m3fn if bits == 8 else torch.float32, at), (scales, torch.float32, at // block)):
+        for t in ts:
+            if t is None or t.dtype != want or t.numel() != length or not t.is_contiguous() or t.get_device() != index:
+                raise DetAttnError(f"exp_avg{'_scale' if ts is scales else ''} and exp_avg_sq{'_scale' if ts is scales else ''} "
+                                   f"must be contiguous {want} [{length}] on the params' device")
     if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                    or grad_scale.get_device() != index):
         raise DetAttnError("grad_scale must be one f32 element on the params' device")
@@ -442,6 +451,9 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     _run("adamw_step", index, _da.lib().dow_adamw, struct.pack(f"{4 * k}Q", *table), k, code, bits, exp_avg.data_ptr(),
          exp_avg_sq.data_ptr(), _addr(exp_avg_scale), _addr(exp_avg_sq_scale), at,
          _HYPER.pack(lr, betas[0], betas[1], eps, weight_decay, int(step)), _addr(grad_scale))
+    moved += states
+    moved += scales
+    _written(moved)
 
 
 class AdamW:

@@ -112,3 +112,24 @@ def test_masks_and_slopes_may_not_change_before_the_backward_pass(stub):
         t.add_(1)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             out.sum().backward()
+
+
+def test_writes_through_addresses_are_seen(stub):
+    """What the library writes in place counts as an in-place change: a graph that saved it refuses to go backward."""
+    p, late = torch.ones(300, requires_grad=True), torch.ones(5, requires_grad=True)
+    m, v, scale = torch.zeros(768), torch.zeros(768), torch.ones(1)
+    y = (p * p).sum() + (late * late).sum()
+    before = [t._version for t in (p, late, m, v, scale)]
+    with torch.no_grad():
+        da.adamw_step([p, late], [torch.ones(300), None], m, v, 1, grad_scale=scale)
+    assert [t._version - b for t, b in zip((p, late, m, v, scale), before)] == [1, 0, 1, 1, 0]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    m8, s = torch.zeros(768).to(torch.float8_e4m3fn), [torch.zeros(3) for _ in range(2)]
+    v8 = m8.clone()
+    da.adamw_step([p.detach(), late.detach()], [torch.ones(300), torch.ones(5)], m8, v8, 1, exp_avg_scale=s[0], exp_avg_sq_scale=s[1])
+    assert all(t._version for t in (m8, v8, *s))
+    q, k, v = _qkv()
+    out = torch.empty_like(q)
+    da.attention_forward(q, k, v, out=out)
+    assert out._version == 1
