@@ -16,10 +16,12 @@ struct TaBounds {
 };
 
 // f tanh(k t) of a product t, in log2 units: f = softcap log2 e, k = scale / softcap.  Odd polynomials f k t P((k t)^2) with k
-// and f folded into the coefficients, each twice for the packed arithmetic: c up to |t| = most, s up to least.
+// and f folded into the coefficients, each twice for the packed arithmetic: c up to |t| = most, s up to least.  far: a cap of more
+// than 4096 times the scale, s tanh's series.
 struct TaCap {
   unsigned long long c[6], s[4];
   float k, f, most, least;
+  int far;
 };
 
 struct TaArgs {

@@ -94,9 +94,10 @@ struct Cap {
     return f2::mul(t, p);
   }
   // v <- f tanh(k v) for N scores of each lane.  The warp decides by its scores which form it takes; where they hold padding,
-  // whose values may be anything, without a vote the one for any argument.
+  // whose values may be anything, without a vote the one for any argument (unless that is too far off: 2^-22 of a far cap).
   template <int N>
-  __device__ __forceinline__ void apply(float* v, bool vote) const {
+  __device__ __forceinline__ void apply(float* v, bool clean) const {
+    const bool vote = clean || c.far;
     float m[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; i += 4) {

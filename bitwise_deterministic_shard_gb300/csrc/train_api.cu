@@ -46,7 +46,8 @@ int check(const dta_desc* d) {
   if (d->q.H % d->k.H != 0 || d->q.S > d->k.S) return DA_ESHAPE;
   if (d->q.B * d->q.H * (d->k.S / TA_TILE + 1) > (int64_t)1 << 30) return DA_ESHAPE;   // CTAs of a launch
   if (!std::isnan(d->scale) && !std::isfinite(d->scale)) return DA_EINVAL;
-  if (!(d->softcap >= 0.f) || !std::isfinite(d->softcap)) return DA_EINVAL;
+  // beyond these the cap's factors, their squares or the scale over it leave binary32's range
+  if (d->softcap != 0.f && (!(d->softcap >= 0x1p-60f && d->softcap <= 0x1p60f) || std::fabs(d->scale) > 0x1p60f)) return DA_EINVAL;
   if (d->prefix && !d->causal) return DA_EINVAL;
   if (!aligned(d->slopes, 4) || !aligned(d->docs, 4) || !aligned(d->prefix, 4) || !aligned(d->dev_status, 4))
     return DA_EALIGN;
@@ -120,10 +121,27 @@ TaCap cap_of(float scale, float softcap) {
   }
   c.k = (float)k;
   c.f = (float)f;
-  // beyond these factors a coefficient could leave binary32's range: the general form then takes every score
+  // Beyond these factors a coefficient could leave binary32's range, and an error in units of the cap would be one of many
+  // scores (2^-22 of a cap of 10^5 is 0.02).
   const double a = std::fabs(k);
-  c.most = a >= 0x1p-12 && a <= 0x1p10 ? (float)(1 / a) : 0.f;
-  c.least = 0.5f * c.most;
+  if (a >= 0x1p-12 && a <= 0x1p10) {
+    c.most = (float)(1 / a);
+    c.least = 0.5f * c.most;
+  } else if (a > 0x1p10) {
+    c.most = c.least = -1.f;   // the general form, for a score of 0 too
+  } else {
+    // A cap of more than 4096 times the scale: tanh's series, as many terms as binary32 holds, up to where the next one is 2^-22
+    // of the value; the scores beyond (a quarter to a 32nd of the cap) take the general form.
+    constexpr double series[4] = {1, -1. / 3, 2. / 15, -17. / 315};
+    const int terms = a >= 0x1p-20 ? 4 : a >= 0x1p-30 ? 3 : 2;
+    power = k * f;
+    for (int i = 0; i < 4; i++) {
+      c.s[i] = twice(i < terms ? series[i] * power : 0);
+      power *= k * k;
+    }
+    c.far = 1;
+    c.most = c.least = (float)std::min((terms == 4 ? 0x1p-2 : terms == 3 ? 0x1p-3 : 0x1p-5) / a, 0x1p60);
+  }
   return c;
 }
 

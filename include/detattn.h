@@ -336,6 +336,8 @@ int da_probe_bounded_wait(int32_t* dev_status, da_stream_t stream);
  * Hq % Hkv == 0.  Pointers are 16-byte aligned and the strides of b, h and s multiples of 8
  * elements (where the dimension is longer than 1), not zero.
  *   t = scale q.k;  u = softcap > 0 ? softcap tanh(t / softcap) : t;  s = u - slopes[h] |pos_i - j|
+ * A capped score is within 2^-21 softcap of that; with softcap above 4096 |scale| within 2^-21 of itself as long as 32
+ * neighbouring queries' and 32 keys' scores all lie below a 32nd of it (one beyond makes theirs 2^-21 softcap again).
  * Query i sees key j when (not causal, or j <= pos_i, or j < prefix[b]) and, with docs,
  * docs[b][j] == docs[b][pos_i] >= 0.  A query that sees nothing gets a zero output, an lse of -inf and
  * zero gradients.  Tokens with a negative id may hold any bits, NaN among them; other inputs must
@@ -344,7 +346,7 @@ typedef struct {
   da_tensor q, k, v;
   int32_t causal;
   float scale;            /* NaN selects 1/sqrt(D) */
-  float softcap;          /* 0: scores are not capped; else positive and finite */
+  float softcap;          /* 0: scores are not capped; else 2^-60 to 2^60, with |scale| up to 2^60 */
   const float* slopes;    /* optional device f32 [Hq]: the score falls by slopes[h] per position of distance */
   const int32_t* docs;    /* optional device int32 [B, Skv]: document of each token, negative: padding */
   const int32_t* prefix;  /* optional device int32 [B], needs causal: keys below it are seen by all queries */

@@ -1,13 +1,19 @@
 """What the binding of the training operators does around the library's calls, with a stub in the library's place: the device and
 stream that a call goes to, what it takes as a workspace, what autograd is told."""
 import contextlib
+import ctypes
 import math
+import os
+import sys
 
 import pytest
 import torch
 
 import bitwise_deterministic_shard_gb300 as da
 from bitwise_deterministic_shard_gb300 import train
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import test_train_cpu as T  # noqa: E402
 
 
 class _Stub:
@@ -133,3 +139,16 @@ def test_writes_through_addresses_are_seen(stub):
     out = torch.empty_like(q)
     da.attention_forward(q, k, v, out=out)
     assert out._version == 1
+
+
+# ---------------------------------------------------------------- caps
+
+@pytest.mark.parametrize("softcap, scale, code", [(0.0, 2.0 ** 100, 5), (2.0 ** -60, math.nan, 5), (2.0 ** 60, -2.0 ** 60, 5), (2.0 ** -61, math.nan, 1),
+                                                  (2.0 ** 61, math.nan, 1), (-30.0, math.nan, 1), (30.0, 2.0 ** 61, 1), (1e-40, math.nan, 1)])
+def test_caps_beyond_the_factors_range_are_refused(softcap, scale, code):
+    """5: the arguments passed, and the workspace, which is missing, is asked for."""
+    from bitwise_deterministic_shard_gb300 import build
+    build.build()
+    L, d, o = da.lib(), T._desc(Skv=4096, Sq=1), T._desc(Skv=4096, Sq=1)
+    d.softcap, d.scale = softcap, scale
+    assert L.dta_forward(ctypes.byref(d), ctypes.byref(o.q), None, None, 0, None) == code

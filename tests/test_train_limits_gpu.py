@@ -75,6 +75,46 @@ def test_tall_scores(shape, dtype, base, late):
     assert da.read_status(st) == 0
 
 
+# ---------------------------------------------------------------- caps of any size
+
+@pytest.mark.parametrize("shape", [(1, 4, 2, 200, 300, 64), (6, 16, 16, 130, 260, 64), (2, 8, 2, 1, 1500, 128)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("cap", [1e-3, 0.1, 31.0, 32.0, 33.0, 50.0, 300.0, 400.0, 1e4, 1e5, 1e6, 1e9])
+def test_caps(shape, dtype, cap):
+    """The capped score is off by 2^-21 of the cap where it is a good part of the cap, and by 2^-22 of itself below a quarter
+    of a cap beyond 4096 times the scale, where every score here lies."""
+    q, k, v, go = T._attn_inputs(*shape, dtype, seed=12)
+    kw = dict(causal=True, softcap=cap)
+    st = da.new_status()
+    out, lse = da.attention_forward(q, k, v, status=st, **kw)
+    dq, dk, dv = da.attention_backward(q, k, v, out, lse, go, status=st, **kw)
+    assert da.read_status(st) == 0
+    r = R.attention(q, k, v, go, **kw)
+    tol, A = R.attention_tolerance(r, dtype), r["abs"]
+    e = min(cap, 362.0) * 2.0 ** -21
+    for got, n, more in ((out, "out", 2 * A["out"]), (dq, "dq", 4 * A["dq_rough"]), (dk, "dk", 4 * A["dk_rough"]), (dv, "dv", 2 * A["dv"])):
+        T._close(got, r[n], tol[n] + e * more, n)
+    assert ((lse.double() - r["lse"]).abs() <= 2.0 ** -17 * (1 + r["lse"].abs()) + e).all()
+
+
+def test_a_large_cap_is_no_cap():
+    """u = t - t^3 / (3 cap^2): at 1e6 the scores of up to 2^6 are the products to 2^-24 of them, so lse is the one without a
+    cap up to the roundings of both."""
+    q, k, v, _ = T._attn_inputs(2, 4, 2, 200, 300, 64, torch.bfloat16, seed=13)
+    want = da.attention_forward(q, k, v)[1]
+    for cap in (1e6, 1e9, 1e15):
+        lse = da.attention_forward(q, k, v, softcap=cap)[1]
+        assert ((lse - want).abs() <= 2.0 ** -18 * (1 + want.abs())).all(), cap
+
+
+@pytest.mark.parametrize("cap", [1e-8, 1e-12])
+def test_scores_of_zero_under_a_tiny_cap(cap):
+    """Without a score other than 0 every key weighs the same."""
+    q = torch.zeros(1, 2, 200, 64, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.randn(1, 2, 200, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    T._attn_check(q, k, v, torch.randn_like(q), softcap=cap)
+
+
 # ---------------------------------------------------------------- what may not matter
 
 def _leave_behind(x):
