@@ -7,8 +7,8 @@
 // undo = 1 / sqrt(1 - b2^t), rate = lr / (1 - b1^t); p rounded once more to its own type.
 //
 // 8-bit states: a block of 256 elements of a tensor holds e4m3 values and one f32 scale,
-// max |x| / 448 over the block (0 below 2^-100, where the block's values become zero); x = value *
-// scale.  Of the second moment its square root is kept, which halves the exponents it spans;
+// max |x| / 448 over the block's finite x (0 below 2^-100, where the block's values become zero); x = value *
+// scale; an x that is not finite becomes NaN.  Of the second moment its square root is kept, which halves the exponents it spans;
 // a root above zero never becomes zero (it would leave m / eps), it takes the smallest value.
 //
 // What bounds it: HBM.  f32 states move 28 bytes an element, 8-bit ones with bf16 parameters
@@ -225,8 +225,21 @@ __global__ void __launch_bounds__(256, 6) adamw8_kernel(const __grid_constant__ 
         if (at + k * 128 + e < size) p[k * 128 + e] = P[k].bits(e);
     }
   }
-  const float mt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
-  const float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
+  float mt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
+  float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
+  if (fmaxf(mt, vt) == INFINITY) {   // an infinity would be the block's scale: it stays in its own element, as NaN
+    const auto finite_top = [](float (&x)[8]) {
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        if (fabsf(x[e]) == INFINITY) x[e] = __uint_as_float(0x7fffffffu);
+        top = fmaxf(top, fabsf(x[e]));
+      }
+      return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    };
+    mt = finite_top(M);
+    vt = finite_top(R);
+  }
   const bool ml = mt >= 0x1p-100f, vl = vt >= 0x1p-100f;
   const float mi = ml ? __fdiv_rn(448.f, mt) : 0.f, vi = vl ? __fdiv_rn(448.f, vt) : 0.f;
   const float floor = vl ? 0x1p-9f : 0.f;

@@ -409,7 +409,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     params, grads: contiguous tensors of one dtype (f32, bf16, f16); a grad of None leaves its tensor as it is.
     exp_avg, exp_avg_sq: [adamw_state_len(params)], tensor after tensor, each from the next multiple of
     STATE_BLOCK on: f32, or float8_e4m3fn with f32 scales [len / STATE_BLOCK] in exp_avg_scale and
-    exp_avg_sq_scale (exp_avg_sq then holds the square root; zeros, scales included, are the initial state).
+    exp_avg_sq_scale (exp_avg_sq then holds the square root; zeros, scales included, are the initial state;
+    what is not finite becomes NaN in its own element).
     step: 1 on the first call.  grad_scale: optional f32 CUDA scalar that multiplies every gradient.
     Every operation is rounded once to binary32; the hyperparameters are baked into the launch, so a
     captured graph replays this step's."""

@@ -398,8 +398,8 @@ typedef struct {
  *   g = grad (times *grad_scale when given);  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) (g g)
  *   p = p (1 - lr wd) - lr / (1 - b1^step) * (m / (sqrt(v) / sqrt(1 - b2^step) + eps))
  * state_bits 32: m, v are device f32 [state_len].  state_bits 8: m, v are device e4m3 [state_len] with
- * a f32 scale for each 256 elements (m_scale, v_scale: [state_len / 256], scale = largest magnitude
- * / 448); v holds the square root, in which a value above zero never becomes zero; elements of a
+ * a f32 scale for each 256 elements (m_scale, v_scale: [state_len / 256], scale = largest finite magnitude
+ * / 448, what is not finite becoming NaN); v holds the square root, in which a value above zero never becomes zero; elements of a
  * tensor's last block past its end become zero.  state_len is a multiple of 256. */
 int dow_adamw(const dow_tensor* tensors, int n, int dtype, int state_bits, void* m, void* v, float* m_scale,
               float* v_scale, int64_t state_len, const dow_hyper* hyper, const float* grad_scale, da_stream_t stream);

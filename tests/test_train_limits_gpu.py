@@ -194,3 +194,33 @@ def test_layer_norm_bytes_with_the_same_alignment(rows, cols, gap, dtype):
     for pad in (64, 4096):
         for p, q in zip(both(placed(x, pad), placed(dy, pad)), want):
             assert torch.equal(p, q)
+
+
+# ---------------------------------------------------------------- AdamW
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan"), 1e25])
+def test_adamw_8bit_keeps_an_infinity_to_itself(bad, dtype):
+    """A gradient that is not finite, or whose square is not, spoils its own element of an 8-bit block and no other."""
+    g = torch.Generator().manual_seed(3)
+    ps = [torch.randn(1000, generator=g).to(dtype).cuda() for _ in range(2)]
+    ps[1].copy_(ps[0])
+    opts = [da.AdamW([p], state_bits=8, **T.H) for p in ps]
+    for step in range(3):
+        gr = torch.randn(1000, generator=g).to(dtype).cuda()
+        for p, x in zip(ps, (0.0, bad)):
+            p.grad = gr.clone()
+            p.grad[300] = x if step == 0 else 0.0
+        for o in opts:
+            o.step()
+    rest = torch.arange(1000, device="cuda") != 300
+    assert torch.isfinite(ps[1][rest]).all()
+    if bad == 1e25:                  # a finite first moment, under whose scale the block's others become zero
+        return
+    assert torch.equal(ps[0][rest], ps[1][rest])
+    a, b = (o.groups[0] for o in opts)
+    rest = torch.arange(1024, device="cuda") != 300
+    for n in ("exp_avg", "exp_avg_sq"):
+        assert torch.equal(a[n].view(torch.uint8)[rest], b[n].view(torch.uint8)[rest])
+    for n in ("exp_avg_scale", "exp_avg_sq_scale"):
+        assert torch.equal(a[n], b[n])
