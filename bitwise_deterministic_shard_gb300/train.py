@@ -458,13 +458,15 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
 
 
 class AdamW:
-    """AdamW over a list of parameters, grouped by dtype, with f32 or 8-bit states (adamw_step)."""
+    """AdamW over a list of parameters, grouped by dtype and device, with f32 or 8-bit states (adamw_step).  steps counts the
+    calls of step; a parameter's own steps are those in which it had a gradient (missed, a list a group, counts the others), and
+    one without leaves it and its states as they are."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32):
         if state_bits not in (8, 32):
             raise DetAttnError("state_bits must be 8 or 32")
         self.hyper = dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay)
-        self.state_bits, self.steps, self.groups = state_bits, 0, []
+        self.state_bits, self.steps, self.groups, self.missed = state_bits, 0, [], []
         by = {}
         for p in params:
             by.setdefault((p.dtype, p.device), []).append(p)
@@ -475,15 +477,30 @@ class AdamW:
             if state_bits == 8:
                 g["exp_avg_scale"], g["exp_avg_sq_scale"] = torch.zeros((2, n // STATE_BLOCK), device=dev).unbind(0)
             self.groups.append(g)
+            self.missed.append([0] * len(ps))
 
     def step(self, grad_scale=None):
         self.steps += 1
-        for g in self.groups:
-            ps = g["params"]
+        for g, missed in zip(self.groups, self.missed):
+            ps, grads, none = g["params"], [], 0
+            for p in ps:
+                x = p.grad
+                if x is None:
+                    none += 1
+                elif not x.is_contiguous():
+                    x = x.contiguous()
+                grads.append(x)
+            if none == len(ps):
+                kinds = ()
+            elif len(kinds := set(missed)) > 1:
+                kinds = sorted({m for m, x in zip(missed, grads) if x is not None})
             with torch.no_grad():
-                adamw_step(ps, [None if p.grad is None else p.grad.contiguous() for p in ps], g["exp_avg"], g["exp_avg_sq"],
-                           self.steps, exp_avg_scale=g.get("exp_avg_scale"), exp_avg_sq_scale=g.get("exp_avg_sq_scale"),
-                           grad_scale=grad_scale, **self.hyper)
+                for m in kinds:   # one launch where all began together
+                    adamw_step(ps, grads if len(kinds) == 1 else [x if k == m else None for k, x in zip(missed, grads)], g["exp_avg"],
+                               g["exp_avg_sq"], self.steps - m, exp_avg_scale=g.get("exp_avg_scale"),
+                               exp_avg_sq_scale=g.get("exp_avg_sq_scale"), grad_scale=grad_scale, **self.hyper)
+            if none:
+                missed[:] = [k + (x is None) for k, x in zip(missed, grads)]
 
     def zero_grad(self):
         for g in self.groups:

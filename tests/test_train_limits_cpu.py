@@ -152,3 +152,20 @@ def test_caps_beyond_the_factors_range_are_refused(softcap, scale, code):
     L, d, o = da.lib(), T._desc(Skv=4096, Sq=1), T._desc(Skv=4096, Sq=1)
     d.softcap, d.scale = softcap, scale
     assert L.dta_forward(ctypes.byref(d), ctypes.byref(o.q), None, None, 0, None) == code
+
+
+# ---------------------------------------------------------------- AdamW
+
+def test_adamw_counts_each_parameters_steps(stub):
+    """Parameters with as many steps behind them share a launch; none without a gradient counts."""
+    ps = [torch.zeros(n) for n in (5, 300, 7)]
+    opt = da.AdamW(ps)
+    launches = []
+    for have in ((0,), (0, 1), (1,), (0, 1, 2), ()):
+        for i, p in enumerate(ps):
+            p.grad = torch.ones_like(p) if i in have else None
+        before = len(stub.calls)
+        opt.step()
+        launches.append([(args[1], train._HYPER.unpack(args[9])[-1]) for _, _, args in stub.calls[before:]])
+    assert launches == [[(1, 1)], [(1, 2), (1, 1)], [(1, 2)], [(2, 3), (1, 1)], []]
+    assert opt.missed == [[2, 2, 4]] and opt.steps == 5

@@ -224,3 +224,22 @@ def test_adamw_8bit_keeps_an_infinity_to_itself(bad, dtype):
         assert torch.equal(a[n].view(torch.uint8)[rest], b[n].view(torch.uint8)[rest])
     for n in ("exp_avg_scale", "exp_avg_sq_scale"):
         assert torch.equal(a[n], b[n])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_first_gradient_that_comes_late(bits):
+    """A parameter's bias correction counts its own steps: with a first gradient in the third step it moves as one whose
+    first step this is."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(500, generator=g).cuda()
+    a, late, fresh = x.clone(), x.clone(), x.clone()
+    opt, other = da.AdamW([a, late], state_bits=bits, **T.H), da.AdamW([fresh], state_bits=bits, **T.H)
+    for step in range(5):
+        gr = torch.randn(500, generator=g).cuda()
+        a.grad = gr
+        late.grad = gr if step >= 2 else None
+        opt.step()
+        if step >= 2:
+            fresh.grad = gr
+            other.step()
+    assert torch.equal(late, fresh) and not torch.equal(a, late)
