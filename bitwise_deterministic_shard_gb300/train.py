@@ -465,6 +465,9 @@ class AdamW:
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32):
         if state_bits not in (8, 32):
             raise DetAttnError("state_bits must be 8 or 32")
+        params = list(params)
+        if len({id(p) for p in params}) != len(params):
+            raise DetAttnError("a parameter is given twice: both entries would write it at once")
         self.hyper = dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay)
         self.state_bits, self.steps, self.groups, self.missed = state_bits, 0, [], []
         by = {}

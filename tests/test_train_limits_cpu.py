@@ -169,3 +169,9 @@ def test_adamw_counts_each_parameters_steps(stub):
         launches.append([(args[1], train._HYPER.unpack(args[9])[-1]) for _, _, args in stub.calls[before:]])
     assert launches == [[(1, 1)], [(1, 2), (1, 1)], [(1, 2)], [(2, 3), (1, 1)], []]
     assert opt.missed == [[2, 2, 4]] and opt.steps == 5
+
+
+def test_adamw_refuses_a_parameter_given_twice(stub):
+    p = torch.zeros(5)
+    with pytest.raises(da.DetAttnError):
+        da.AdamW([p, torch.zeros(5), p])
