@@ -104,9 +104,13 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _room(need, ws, device):
+def _room(need, ws, device, index):
+    """ws where it holds need bytes, else a new workspace."""
     if ws is None or ws.numel() * ws.element_size() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _on(index, "workspace", ws)
+    if not ws.is_contiguous():
+        raise DetAttnError("workspace must be contiguous")
     return ws
 
 
@@ -214,7 +218,7 @@ def attention_forward(Q, K, V, causal=False, scale=None, softcap=0.0, slopes=Non
     lse = torch.empty(A.shape[:3], dtype=torch.float32, device=A.device) if need_lse else None
     L = _da.lib()
     need = L.dta_workspace_bytes(A.desc, 0)
-    ws = _room(need, workspace, A.device)
+    ws = _room(need, workspace, A.device, A.index)
     _run("attention_forward", A.index, L.dta_forward, A.desc, _view(out, A.code), _addr(lse), _addr(ws), need)
     if given is not None:
         _written(out)
@@ -238,7 +242,7 @@ def attention_backward(Q, K, V, out, lse, grad, causal=False, scale=None, softca
     dq, dk, dv = _like(Q), _like(K), _like(V)
     L, c = _da.lib(), A.code
     need = L.dta_workspace_bytes(A.desc, 1)
-    ws = _room(need, workspace, A.device)
+    ws = _room(need, workspace, A.device, A.index)
     _run("attention_backward", index, L.dta_backward, A.desc, _view(out, c), lse.data_ptr(), _view(grad, c), _view(dq, c),
          _view(dk, c), _view(dv, c), _addr(ws), need)
     return dq, dk, dv
@@ -364,7 +368,7 @@ def layer_norm_backward(grad, x, weight, mean, rstd, need_weight=True, need_bias
     db = torch.empty(cols, dtype=wt, device=dev) if need_bias else None
     L = _da.lib()
     need = L.dln_workspace_bytes(rows, cols) if need_weight or need_bias else 0
-    ws = _room(need, workspace, dev)
+    ws = _room(need, workspace, dev, index)
     _run("layer_norm_backward", index, L.dln_backward, G, X, _addr(weight), _CODES[wt], mean.data_ptr(), rstd.data_ptr(), DX,
          _addr(dw), _addr(db), _addr(ws), need)
     return dx, dw, db

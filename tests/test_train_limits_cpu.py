@@ -175,3 +175,35 @@ def test_adamw_refuses_a_parameter_given_twice(stub):
     p = torch.zeros(5)
     with pytest.raises(da.DetAttnError):
         da.AdamW([p, torch.zeros(5), p])
+
+
+# ---------------------------------------------------------------- workspaces
+
+def test_workspaces_are_checked(stub, monkeypatch):
+    """A given workspace goes to the kernels as an address: it has to lie on the tensors' device and in one piece."""
+    q, k, v = _qkv()
+    s, x, lse = torch.zeros(4), torch.zeros(4, 10), torch.zeros(1, 4, 8)
+    for name in ("dta_workspace_bytes", "dln_workspace_bytes"):
+        setattr(stub, name, lambda *args: 4096)
+    good, small = torch.zeros(4096, dtype=torch.uint8), torch.zeros(100)
+    pieces = (torch.zeros(4, 8192, dtype=torch.uint8)[:, ::2], torch.zeros(1).expand(9000))
+    calls = [lambda w: da.attention_forward(q, k, v, workspace=w), lambda w: da.attention_backward(q, k, v, q, lse, q, workspace=w),
+             lambda w: da.layer_norm_backward(x, x, None, s, s, workspace=w)]
+    for call in calls:
+        for w in (good, None, small):                               # one that is too small is replaced, as elsewhere in the package
+            call(w)
+        assert len(stub.calls) == 3
+        stub.calls.clear()
+        for w in pieces:
+            with pytest.raises(da.DetAttnError):
+                call(w)
+    elsewhere = torch.zeros(4096, dtype=torch.uint8, device="meta")
+
+    def cuda(t, name):
+        if t is elsewhere:
+            raise da.DetAttnError(f"{name} must be a CUDA tensor")
+    monkeypatch.setattr(da, "_cuda", cuda)
+    for call in calls:
+        with pytest.raises(da.DetAttnError, match="workspace"):
+            call(elsewhere)
+    assert not stub.calls
