@@ -159,7 +159,8 @@ __device__ __forceinline__ void load_words(Run<T, E>& r, const T* p, int64_t i, 
 
 // One warp a block of 256 elements.  Parameter and gradient stay packed words until their turn: registers, and
 // with them the warps whose loads are in flight, bound this kernel beside the arithmetic of the roots and
-// divisions.  144 M bf16 parameters: 328 us (4.4 TB/s) at 6 CTAs an SM, 331 at 5, 343 with spills at 8; 482 with
+// divisions.  144 M bf16 parameters: 329 us (4.4 TB/s) at 6 CTAs an SM (328 before
+// infinities were kept apart, then 331 at 5, 343 with spills at 8); 482 with
 // the operands unpacked first (4 CTAs), 650 with two blocks a warp (2 CTAs).
 template <typename T>
 __global__ void __launch_bounds__(256, 6) adamw8_kernel(const __grid_constant__ AdamWArgs a) {

@@ -25,8 +25,8 @@
 //
 // What bounds it: four products a tile pair in each kernel (2048 cycles; their shared-memory operands with the copies and
 // P take about 2500) beside 1700 cycles of FP32 arithmetic with a cap, in steps of 3900 cycles: sixteen warps that pass the
-// same phases together.  4096 causal, 16 heads, D 128, bf16, cap 30: dq 119 us, dk and dv 121 us (tensor pipe 52 and 50 %, issue
-// slots 56 and 54 % of the cycles); eight warps of 64 columns with tanh from the special function unit took 341 each.
+// same phases together.  4096 causal, 16 heads, D 128, bf16, cap 30: dq 120 us, dk and dv 126 us (tensor pipe 52 and 50 %, issue
+// slots 56 and 55 % of the cycles); eight warps of 64 columns with tanh from the special function unit took 341 each.
 // Many CTAs of few steps (packed documents) pay about 3 us each for their start and end, and with shared key heads the
 // longest of the dk and dv kernel's few CTAs set its end.
 #pragma once

@@ -16,8 +16,8 @@
 //
 // What bounds it: the softmax's arithmetic (per score 7 to 9 cycles of the FP32 pipe with a cap, 2 without, 4 of the
 // special function unit, against 8 of the tensor cores for two products of D = 128) and the latencies
-// that four softmax warps a scheduler leave open.  4096 causal, 16 heads, D 128, bf16, cap 30: 79 us, 870 TFLOP/s, 0.46 of the
-// measured matrix rate; tensor pipe 41 % and issue slots 52 % of the cycles (one thread a row 107 us; weights over the scores
+// that four softmax warps a scheduler leave open.  4096 causal, 16 heads, D 128, bf16, cap 30: 80 us, 859 TFLOP/s, 0.45 of the
+// measured matrix rate; tensor pipe 40 % and issue slots 54 % of the cycles (one thread a row 107 us; weights over the scores
 // in TMEM 108; the products issued by one lane 109; spilling control warps 94; the coefficients in registers 81).
 //
 // The weights are rounded to the inputs' 16-bit type (the tensor cores take both operands in one
@@ -70,7 +70,8 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // [-0.5, 0.5], fitted for the least greatest error (least squares with weights moved toward the largest
 // errors), 3.1e-7 and 1.6e-7 absolute with binary32 steps, on the packed multiplier; k and f are folded into the
 // coefficients.  The special function unit would otherwise bound the kernels: three of its operations a score
-// instead of one.
+// instead of one.  Scores beyond the cap pay that: 4096 causal, cap 30, forward 118 us against 78, the backward kernels 294
+// against 241 (71 and 214 without a cap).
 __device__ __forceinline__ float tanh_any(float x) {
   return __fmaf_rn(-2.f, tc5::rcp(1.f + tc5::ex2(x * (2.f * LOG2E))), 1.f);
 }

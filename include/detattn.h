@@ -341,7 +341,10 @@ int da_probe_bounded_wait(int32_t* dev_status, da_stream_t stream);
  * Query i sees key j when (not causal, or j <= pos_i, or j < prefix[b]) and, with docs,
  * docs[b][j] == docs[b][pos_i] >= 0.  A query that sees nothing gets a zero output, an lse of -inf and
  * zero gradients.  Tokens with a negative id may hold any bits, NaN among them; other inputs must
- * be finite (a row whose sum is not sets DA_STATUS_NONFINITE). */
+ * be finite (a row whose sum is not sets DA_STATUS_NONFINITE), values below 2^64.  Attention's weights and, in the
+ * backward pass, the gradients of the products q.k are rounded to the inputs' type: with f16 these must stay below
+ * 65504.  Scores may have any size; lse is one binary32 number, so the backward pass's weights are off by some
+ * 2^-21 of it. */
 typedef struct {
   da_tensor q, k, v;
   int32_t causal;
