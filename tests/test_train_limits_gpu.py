@@ -3,7 +3,6 @@ warps, values that may not matter, infinite gradients, gradients that come late.
 import os
 import sys
 
-import numpy as np
 import pytest
 import torch
 
