@@ -100,6 +100,7 @@ def lib():
                   "dce_finalize_shard", "dce_backward_shard", "da_rowmax_cached", "da_accumulate_finalize_cached"):
             getattr(L, f).restype = C.c_int
         train.declare(L)
+        decoder.declare(L)
         _lib = L
     return _lib
 
@@ -745,3 +746,5 @@ def probe_int_mac_rate(iters=4096, nblocks=None):
 from . import train  # noqa: E402  (needs the helpers above)
 from .train import (AdamW, adamw_state_len, adamw_step, attention, attention_backward,  # noqa: E402,F401
                     attention_forward, layer_norm, layer_norm_backward, layer_norm_forward)
+from . import decoder  # noqa: E402
+from .decoder import gated_linear, gated_linear_backward, gated_linear_forward  # noqa: E402,F401

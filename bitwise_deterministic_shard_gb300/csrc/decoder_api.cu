@@ -1,0 +1,162 @@
+// Host side of the operators at the ends and in the middle of a decoder (include/detattn.h): argument
+// checks, workspace layout, tensor maps and launches.
+#include <cmath>
+#include <cstring>
+
+#include "../../include/detattn.h"
+#include "decoder_kernels.h"
+
+using namespace detattn;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
+int launched(cudaError_t e) { return e == cudaSuccess ? DA_OK : DA_ECUDA; }
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static const EncodeFn fn = []() -> EncodeFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// boxes of 64 columns x `rows` rows of a matrix of 16-bit elements
+bool tensor_map(CUtensorMap* m, const void* at, int dtype, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
+  const EncodeFn fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? stride : cols) * 2};   // one row: not used, but must be valid
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  const CUtensorMapDataType type = dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(m, type, 2, const_cast<void*>(at), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool tensor_map(CUtensorMap* m, const da_matrix& x, int box_rows) {
+  return tensor_map(m, x.ptr, x.dtype, x.rows, x.cols, x.row_stride, box_rows);
+}
+
+// ---- gated feed-forward ----
+constexpr int64_t kMaxRows = (int64_t)1 << 24;
+
+int check(const da_matrix* x) {   // a matrix that tensor maps and 16-byte accesses can take
+  if (!x) return DA_EINVAL;
+  if (x->dtype != DA_BF16 && x->dtype != DA_F16) return DA_EDTYPE;
+  if (x->rows < 0 || x->cols < 8 || x->cols % 8 || x->rows > kMaxRows || x->cols > kMaxRows) return DA_ESHAPE;
+  if (x->rows > 1 && (x->row_stride < x->cols || x->row_stride >= ((int64_t)1 << 38))) return DA_ESHAPE;
+  if (x->rows > 0 && !x->ptr) return DA_EINVAL;
+  if (!aligned(x->ptr, 16) || (x->rows > 1 && x->row_stride % 8)) return DA_EALIGN;
+  return DA_OK;
+}
+int check(const da_matrix* x, int dtype, int64_t rows, int64_t cols) {
+  const int e = check(x);
+  if (e) return e;
+  if (x->dtype != dtype) return DA_EDTYPE;
+  return x->rows == rows && x->cols == cols ? DA_OK : DA_ESHAPE;
+}
+int check(const da_matrix* x, const da_matrix* wg, const da_matrix* wu) {
+  int e = check(x);
+  if (e || (e = check(wg)) || (e = check(wu, wg->dtype, wg->rows, wg->cols))) return e;
+  if (wg->dtype != x->dtype) return DA_EDTYPE;
+  if (wg->cols != x->cols || wg->rows < 8 || wg->rows % 8) return DA_ESHAPE;
+  // tiles of a launch
+  if (((x->rows >> 8) + 1) * ((wg->rows >> 7) + 1) > (int64_t)1 << 30 || ((wg->rows >> 7) + 2) * ((wg->cols >> 8) + 1) > (int64_t)1 << 30)
+    return DA_ESHAPE;
+  return DA_OK;
+}
+int64_t stride(const da_matrix& x) { return x.rows > 1 ? x.row_stride : x.cols; }
+
+}  // namespace
+
+#define DA_EXPORT __attribute__((visibility("default")))
+
+extern "C" {
+
+DA_EXPORT size_t dgl_saved_bytes(int64_t tokens, int64_t hidden) {
+  return tokens < 0 || hidden < 0 || tokens > kMaxRows || hidden > kMaxRows ? 0 : gl_saved_bytes(tokens, hidden);
+}
+
+DA_EXPORT int dgl_forward(const da_matrix* x, const da_matrix* wg, const da_matrix* wu, int activation, const da_matrix* h,
+                          void* saved, int32_t* dev_status, da_stream_t stream) {
+  int e = check(x, wg, wu);
+  if (e || (e = check(h, x->dtype, x->rows, wg->rows))) return e;
+  if (activation < DGL_SILU || activation > DGL_RELU) return DA_EINVAL;
+  if (!aligned(saved, 16) || !aligned(dev_status, 4)) return DA_EALIGN;
+  if (x->rows == 0) return DA_OK;
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool bf = x->dtype == DA_BF16;
+  if (x->rows <= GL_FEW && !saved) {
+    const GlFewArgs f = {x->ptr, wg->ptr, wu->ptr, const_cast<void*>(h->ptr), stride(*x), stride(*wg), stride(*wu), stride(*h),
+                         (int)x->rows, (int)x->cols, (int)wg->rows, activation};
+    return launched(bf ? gl_few<true>(f, st) : gl_few<false>(f, st));
+  }
+  GlArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.T = (int)x->rows; a.D = (int)x->cols; a.F = (int)wg->rows;
+  a.out[0] = const_cast<void*>(h->ptr); a.os[0] = stride(*h);
+  a.saved = static_cast<unsigned char*>(saved);
+  a.activation = activation;
+  a.status = dev_status;
+  if (!tensor_map(&a.a[0], *x, 128) || !tensor_map(&a.b[0], *wg, 128) || !tensor_map(&a.b[1], *wu, 128)) return DA_ECUDA;
+  return launched(bf ? gl_forward<true>(a, st) : gl_forward<false>(a, st));
+}
+
+DA_EXPORT size_t dgl_workspace_bytes(int64_t tokens, int64_t hidden) {
+  return tokens < 0 || hidden < 0 || tokens > kMaxRows || hidden > kMaxRows ? 0 : round_up((size_t)4 * tokens * hidden);
+}
+
+DA_EXPORT int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_matrix* wg, const da_matrix* wu, const void* saved,
+                           const da_matrix* dx, const da_matrix* dwg, const da_matrix* dwu, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, da_stream_t stream) {
+  int e = check(x, wg, wu);
+  if (e || (e = check(dh, x->dtype, x->rows, wg->rows))) return e;
+  if (dx && (e = check(dx, x->dtype, x->rows, x->cols))) return e;
+  if (!dwg != !dwu) return DA_EINVAL;
+  if (dwg && ((e = check(dwg, x->dtype, wg->rows, wg->cols)) || (e = check(dwu, x->dtype, wg->rows, wg->cols)))) return e;
+  const int64_t T = x->rows, D = x->cols, F = wg->rows;
+  if (T > 0 && !saved) return DA_EINVAL;
+  const size_t need = dgl_workspace_bytes(T, F);
+  if (need > 0 && (!ws || ws_bytes < need)) return DA_EWORKSPACE;
+  if (!aligned(saved, 16) || !aligned(ws, 256) || !aligned(dev_status, 4)) return DA_EALIGN;
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool bf = x->dtype == DA_BF16;
+  if (T == 0) {   // sums of nothing
+    for (const da_matrix* w : {dwg, dwu})
+      if (w && (e = launched(cudaMemset2DAsync(const_cast<void*>(w->ptr), 2 * stride(*w), 0, 2 * D, F, st)))) return e;
+    return DA_OK;
+  }
+  if (!dx && !dwg) return DA_OK;
+  uint16_t* const dg = static_cast<uint16_t*>(ws);
+  const GlScaleArgs s = {dh->ptr, stride(*dh), static_cast<const unsigned char*>(saved), dg, T, F};
+  if ((e = launched(bf ? gl_scale<true>(s, st) : gl_scale<false>(s, st)))) return e;
+  GlArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.T = (int)T; a.D = (int)D; a.F = (int)F;
+  a.status = dev_status;
+  if (dx) {
+    for (int i = 0; i < 2; i++)
+      if (!tensor_map(&a.a[i], dg + i * T * F, x->dtype, T, F, F, 128) || !tensor_map(&a.b[i], i ? *wu : *wg, 64)) return DA_ECUDA;
+    a.out[0] = const_cast<void*>(dx->ptr); a.os[0] = stride(*dx);
+    if ((e = launched(bf ? gl_dx<true>(a, st) : gl_dx<false>(a, st)))) return e;
+  }
+  if (dwg) {
+    for (int i = 0; i < 2; i++) {
+      if (!tensor_map(&a.a[i], dg + i * T * F, x->dtype, T, F, F, 64)) return DA_ECUDA;
+      a.out[i] = const_cast<void*>((i ? dwu : dwg)->ptr); a.os[i] = stride(*(i ? dwu : dwg));
+    }
+    if (!tensor_map(&a.b[0], *x, 64)) return DA_ECUDA;
+    return launched(bf ? gl_dw<true>(a, st) : gl_dw<false>(a, st));
+  }
+  return DA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,10 @@
+// The gated feed-forward kernels, bf16 operands.
+#include "gated_kernels.cuh"
+
+namespace detattn {
+template cudaError_t gl_forward<true>(const GlArgs&, cudaStream_t);
+template cudaError_t gl_dx<true>(const GlArgs&, cudaStream_t);
+template cudaError_t gl_dw<true>(const GlArgs&, cudaStream_t);
+template cudaError_t gl_few<true>(const GlFewArgs&, cudaStream_t);
+template cudaError_t gl_scale<true>(const GlScaleArgs&, cudaStream_t);
+}  // namespace detattn

@@ -1,0 +1,218 @@
+// Matrix products on pairs of SMs (tcgen05, cta_group::2) for the gated feed-forward operator:
+// tiles of 256 x 256 of the result, one pair a tile at a time, fed by tensor-map copies.
+//
+// A cluster of two CTAs works on one tile: each CTA holds 128 of the rows of A and 128 of the rows of B for a step of 64 of
+// the contracted dimension, the leader's products read both CTAs' shared memory and write 128 rows x 256 columns of
+// binary32 sums into each CTA's TMEM.  Per SM and step that is 32 KB of copies for 256 x 256 x 64 / 2 products, 512 cycles of the
+// tensor cores: a single SM with a tile of its own of 128 x 256 would need 48 KB, more than its share of the L2's rate.
+//
+// One warp copies (a ring of 7 steps, 224 KB), one of the leader issues the products, eight warps take the finished sums from TMEM.
+// Two tiles of sums fit (2 x 256 columns), so a tile's results are taken while the next one's products run.  The grid is as
+// many pairs as the GPU holds; each takes every (number of pairs)-th tile.  All sums of a result are one chain of products in the
+// order of the contracted dimension: no split, no atomics.
+//
+// Operands lie in shared memory as the 128-byte swizzle writes them: contracted over the contiguous dimension (K-major: 128 rows of
+// 64 elements) or over the rows (MN-major: two panels of 64 rows of 64 elements), so no operand is ever transposed.
+#pragma once
+#include "tc5_tile.cuh"
+
+namespace detattn {
+namespace pair {
+
+constexpr int BK = 64;                    // contracted elements of a step
+constexpr int HALF = 128 * BK * 2;        // bytes of one operand's half in a CTA
+constexpr int STAGE = 2 * HALF, STAGES = 7;
+constexpr int SMEM = STAGES * STAGE + 1024;
+constexpr int TAKERS = 8;                 // warps that take results
+constexpr int THREADS = (TAKERS + 2) * 32;
+constexpr int TILE_M = 256, TILE_N = 256;
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// the leader's address of a place in this CTA's shared memory
+__device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// A bounded wait whose arrivals may come from the other CTA.
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t at = tc5::smem_addr(bar);
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; it < (1u << 30); it++) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (it == 0) t0 = tc5::globaltimer();
+    if ((it & 15) == 15 && (*abort || tc5::globaltimer() - t0 > tc5::WAIT_NS)) break;
+  }
+  *abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {   // one whole warp of each CTA of the pair
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc5::smem_addr(dst)), "r"(ncols));
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols));
+}
+// box of a rank-2 tensor map -> this CTA's shared memory, completion counted on a barrier of the leader
+__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t leader_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(leader_bar)
+      : "memory");
+}
+// D[tmem of both] (+)= A[both CTAs' smem] * B[both CTAs' smem]; issued by one lane of the leader
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                                    uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one));
+}
+// arrive on bar in both CTAs once every product issued so far has completed
+__device__ __forceinline__ void commit_both(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\tsetp.ne.u32 q, %1, 0;\n\tmov.b16 m, 3;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          tc5::smem_addr(bar)),
+      "r"(one)
+      : "memory");
+}
+
+// 256 x 256 x 16 products of a type, either operand MN-major
+template <bool BF>
+__host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
+  return (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         ((uint32_t)(TILE_N >> 3) << 17) | ((uint32_t)(TILE_M >> 4) << 24);
+}
+// contracted elements [16 s, 16 s + 16) of an operand's half
+template <bool MN>
+__device__ __forceinline__ uint64_t desc(uint32_t tile, int s) {
+  if constexpr (MN) return tc5::desc_of((tile >> 4) + (uint32_t)(s * 2048 / 16 + ((HALF / 2 >> 4) << 16)));
+  else return tc5::desc_of((tile >> 4) + (uint32_t)(s * 32 / 16 + (1 << 16)));
+}
+
+struct Shared {   // beside the ring
+  uint64_t full[STAGES], empty[STAGES], done[2], taken[2];
+  uint32_t tmem;
+  int dead;
+};
+
+// The tile of an index: runs of 8 tile rows, column after column, so that the pairs at work at one time read few rows of both
+// operands.
+__device__ __forceinline__ int2 tile_of(int t, int mt, int nt) {
+  const int g = t / (8 * nt), r = t - g * 8 * nt, rows = min(8, mt - 8 * g);
+  return make_int2(8 * g + r % rows, r / rows);
+}
+
+// The products of all tiles of this pair.
+//   load(tile, step, a, b, leader_bar): copies this CTA's halves of a step (HALF bytes each) to the addresses a and b
+//   take(tile, columns): takes a tile's sums; columns: TMEM address of this warp's lanes; calls `release()` when it
+//     has read them
+// steps: steps of a tile, the same for all.
+template <bool BF, bool A_MN, bool B_MN, typename Load, typename Take>
+__device__ __forceinline__ void run(Shared& sh, unsigned char* raw, int tiles, int steps, int32_t* status, Load load, Take take) {
+  using namespace tc5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  volatile int* abort = &sh.dead;
+  const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    sh.dead = 0;
+    for (int s = 0; s < STAGES; s++) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&sh.done[i], 1);
+      mbar_init(&sh.taken[i], 2 * TAKERS);
+    }
+    mbar_fence_init();
+  }
+  if (warp == TAKERS + 1) tmem_alloc(&sh.tmem, 512);
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == TAKERS) {
+    if (lane == 0) {
+      int k = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += pairs)
+        for (int n = 0; n < steps; n++, k++) {
+          const int s = k % STAGES;
+          if (k >= STAGES && !(ok = wait_pair(&sh.empty[s], (k / STAGES - 1) & 1, abort))) break;
+          const uint32_t at = base + s * STAGE;
+          if (rank == 0) mbar_expect_tx(&sh.full[s], 2 * STAGE);
+          load(t, n, at, at + HALF, at_leader(smem_addr(&sh.full[s])));
+        }
+      // every step's products are done, so nothing is in flight when the CTA ends
+      for (int j = max(0, k - STAGES); j < k && ok; j++) ok = wait_pair(&sh.empty[j % STAGES], (j / STAGES) & 1, abort);
+      if (!ok)   // given up: what was copied arrives at the leader
+        for (int j = max(0, k - STAGES); j < k && rank == 0; j++) mbar_drain(&sh.full[j % STAGES], (j / STAGES) & 1);
+    }
+  } else if (warp == TAKERS + 1) {
+    if (rank == 0) {
+      const uint32_t one = elect(), tm = same(tmem);
+      constexpr uint32_t id = idesc<BF>(A_MN, B_MN);
+      int k = 0, i = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += pairs, i++) {
+        if (i >= 2 && !(ok = all_of(wait_pair(&sh.taken[i & 1], ((i >> 1) - 1) & 1, abort)))) break;
+        fence_after();
+        for (int n = 0; n < steps; n++, k++) {
+          const int s = same(k % STAGES);
+          if (!(ok = all_of(wait_pair(&sh.full[s], (k / STAGES) & 1, abort)))) break;
+          fence_after();
+          const uint32_t at = same(base) + s * STAGE;
+#pragma unroll
+          for (int j = 0; j < BK / 16; j++)
+            mma(tm + (i & 1) * 256, desc<A_MN>(at, j), desc<B_MN>(at + HALF, j), id, n > 0 || j > 0, one);
+          commit_both(&sh.empty[s], one);
+        }
+        if (ok) commit_both(&sh.done[i & 1], one);
+      }
+    }
+  } else {
+    int i = 0;
+    for (int t = first; t < tiles; t += pairs, i++) {
+      if (!all_of(wait_pair(&sh.done[i & 1], (i >> 1) & 1, abort))) break;
+      fence_after();
+      const uint32_t bar = at_leader(smem_addr(&sh.taken[i & 1]));
+      take(t, tmem + ((uint32_t)(warp & 3) << 21) + (i & 1) * 256, [&] {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(bar);
+      });
+    }
+  }
+  __syncwarp();
+  fence_before();
+  cluster_sync();   // the leader's products have read the other CTA's shared memory, all sums are taken
+  fence_after();
+  if (warp == TAKERS + 1) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && sh.dead && status) atomicOr(status, DA_STATUS_TIMEOUT);
+}
+
+}  // namespace pair
+}  // namespace detattn

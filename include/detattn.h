@@ -407,6 +407,35 @@ typedef struct {
 int dow_adamw(const dow_tensor* tensors, int n, int dtype, int state_bits, void* m, void* v, float* m_scale,
               float* v_scale, int64_t state_len, const dow_hyper* hyper, const float* grad_scale, da_stream_t stream);
 
+/* ---- Operators at the ends and in the middle of a decoder ----------------------------------
+ * Gated feed-forward projections, embedding lookup and log probabilities, each with its gradient.  As the training operators
+ * above they compute in binary32 in a fixed order: no atomics add values, and the order depends on the sizes and types
+ * given (an embedding row's gradient: on the places of its own tokens alone), so equal calls give equal bytes on every run.  The
+ * conventions above hold. */
+
+/* activations */
+#define DGL_SILU 0        /* g / (1 + exp(-g)) */
+#define DGL_GELU 1        /* g Phi(g) */
+#define DGL_GELU_TANH 2   /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+#define DGL_RELU 3        /* max(g, 0) */
+
+/* h = act(x wg^T) (x wu^T): x [tokens, width], wg and wu [hidden, width], h [tokens, hidden], all bf16 or all f16.  width and
+ * hidden are multiples of 8, pointers 16-byte aligned, row strides multiples of 8 elements.  The products are binary32 sums; h is
+ * rounded once.  saved: optional device memory of dgl_saved_bytes(tokens, hidden), 16-byte aligned, which the backward
+ * pass takes (act(g) and act'(g) u, 24 bits of each binary32 value).  Up to 8 tokens without saved, the sums are in another
+ * order than with more tokens or with saved. */
+size_t dgl_saved_bytes(int64_t tokens, int64_t hidden);
+int dgl_forward(const da_matrix* x, const da_matrix* wg, const da_matrix* wu, int activation, const da_matrix* h, void* saved,
+                int32_t* dev_status, da_stream_t stream);
+
+/* Gradients of sum(h dh) from the forward's saved factors: dx like x, dwg and dwu like wg and wu; dx may be NULL, and dwg and dwu
+ * both may be.  The gradients of the two products are rounded to the inputs' type before the products with the weights and
+ * with x (with f16 they must stay below 65504).  ws: dgl_workspace_bytes(tokens, hidden), 256-byte aligned. */
+size_t dgl_workspace_bytes(int64_t tokens, int64_t hidden);
+int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_matrix* wg, const da_matrix* wu, const void* saved,
+                 const da_matrix* dx, const da_matrix* dwg, const da_matrix* dwu, void* ws, size_t ws_bytes, int32_t* dev_status,
+                 da_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
