@@ -747,4 +747,5 @@ from . import train  # noqa: E402  (needs the helpers above)
 from .train import (AdamW, adamw_state_len, adamw_step, attention, attention_backward,  # noqa: E402,F401
                     attention_forward, layer_norm, layer_norm_backward, layer_norm_forward)
 from . import decoder  # noqa: E402
-from .decoder import gated_linear, gated_linear_backward, gated_linear_forward  # noqa: E402,F401
+from .decoder import (LogProbs, embedding, embedding_backward, embedding_forward, gated_linear,  # noqa: E402,F401
+                      gated_linear_backward, gated_linear_forward, log_probs, log_probs_backward, log_probs_forward)

@@ -75,6 +75,51 @@ int check(const da_matrix* x, const da_matrix* wg, const da_matrix* wu) {
 }
 int64_t stride(const da_matrix& x) { return x.rows > 1 ? x.row_stride : x.cols; }
 
+// ---- log probabilities and embedding ----
+size_t size_of(int dtype) { return dtype == DA_F32 ? 4 : 2; }
+int check_rows(const da_matrix* x) {
+  if (!x) return DA_EINVAL;
+  if (x->dtype != DA_F32 && x->dtype != DA_BF16 && x->dtype != DA_F16) return DA_EDTYPE;
+  if (x->rows < 0 || x->cols < 1 || (x->rows > 1 && (x->row_stride < x->cols || x->row_stride >= ((int64_t)1 << 40)))) return DA_ESHAPE;
+  if (x->rows > ((int64_t)1 << 31) - 2 || x->cols > (int64_t)1 << 30) return DA_ESHAPE;
+  if (x->rows > 0 && !x->ptr) return DA_EINVAL;
+  return aligned(x->ptr, size_of(x->dtype)) ? DA_OK : DA_EALIGN;
+}
+int check_logits(const da_matrix* x, float temperature) {
+  const int e = check_rows(x);
+  if (e) return e;
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature)) return DA_EINVAL;
+  return x->rows * (x->cols / 4096 + 8) >= (int64_t)1 << 31 ? DA_ESHAPE : DA_OK;   // CTAs of a launch
+}
+int check_ids(const void* ids, int bits, int64_t n, const da_matrix* like) {
+  if (bits != 32 && bits != 64) return DA_EINVAL;
+  if (n > 0 && !ids) return DA_EINVAL;
+  if (!aligned(ids, bits / 8)) return DA_EALIGN;
+  return n * (like->cols / 128 + 1) >= (int64_t)1 << 33 ? DA_ESHAPE : DA_OK;       // warps of a launch
+}
+struct EmWs {
+  size_t key[2], pos[2], unit, count, part, total;
+};
+EmWs em_layout(int64_t n, int64_t cols) {
+  EmWs w;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round_up(bytes);
+    return here;
+  };
+  const bool small = n <= EM_SMALL;
+  for (int i = 0; i < 2; i++) {
+    w.key[i] = take(small && i ? 0 : (size_t)n * 4);
+    w.pos[i] = take(small && i ? 0 : (size_t)n * 4);
+  }
+  w.unit = take((size_t)n * 4);
+  w.count = take(small ? 0 : (size_t)((n + EM_BLOCK - 1) / EM_BLOCK) * EM_BINS * 4);
+  w.part = take(n <= EM_CHUNK ? 0 : (size_t)2 * (n / EM_CHUNK + 1) * cols * 4);
+  w.total = at;
+  return w;
+}
+
 }  // namespace
 
 #define DA_EXPORT __attribute__((visibility("default")))
@@ -157,6 +202,94 @@ DA_EXPORT int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_mat
     return launched(bf ? gl_dw<true>(a, st) : gl_dw<false>(a, st));
   }
   return DA_OK;
+}
+
+DA_EXPORT int dlp_forward(const da_matrix* logits, const int64_t* targets, float temperature, int top, float* log_probs,
+                          float* entropy, float* saved, float* top_log_probs, int64_t* top_indices, int32_t* dev_status,
+                          da_stream_t stream) {
+  const int e = check_logits(logits, temperature);
+  if (e) return e;
+  if (top < 0 || top > LP_TOP || top > logits->cols) return DA_EINVAL;
+  if (logits->rows == 0) return DA_OK;
+  if (!targets || !log_probs || !entropy || (top > 0 && (!top_log_probs || !top_indices))) return DA_EINVAL;
+  if (!aligned(targets, 8) || !aligned(top_indices, 8) || !aligned(log_probs, 4) || !aligned(entropy, 4) || !aligned(saved, 4) ||
+      !aligned(top_log_probs, 4) || !aligned(dev_status, 4))
+    return DA_EALIGN;
+  LpArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = logits->ptr; a.targets = targets; a.lp = log_probs; a.entropy = entropy; a.stats = saved;
+  a.top_lp = top_log_probs; a.top_index = top_indices;
+  a.rows = logits->rows; a.xs = stride(*logits); a.cols = (uint32_t)logits->cols;
+  a.top = top; a.dtype = logits->dtype; a.temperature = temperature; a.status = dev_status;
+  return launched(launch_log_probs(a, (cudaStream_t)stream));
+}
+
+DA_EXPORT int dlp_backward(const da_matrix* logits, const int64_t* targets, const float* saved, const float* grad,
+                           const float* grad_entropy, float temperature, const da_matrix* dlogits, da_stream_t stream) {
+  int e = check_logits(logits, temperature);
+  if (e || (e = check_rows(dlogits))) return e;
+  if (dlogits->dtype != logits->dtype) return DA_EDTYPE;
+  if (dlogits->rows != logits->rows || dlogits->cols != logits->cols) return DA_ESHAPE;
+  if (logits->rows == 0) return DA_OK;
+  if (!targets || !saved) return DA_EINVAL;
+  if (!aligned(targets, 8) || !aligned(saved, 4) || !aligned(grad, 4) || !aligned(grad_entropy, 4)) return DA_EALIGN;
+  LpGradArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = logits->ptr; a.targets = targets; a.stats = saved; a.grad = grad; a.grad_entropy = grad_entropy;
+  a.dx = const_cast<void*>(dlogits->ptr);
+  a.rows = logits->rows; a.xs = stride(*logits); a.ds = stride(*dlogits); a.cols = (uint32_t)logits->cols;
+  a.dtype = logits->dtype; a.temperature = temperature;
+  return launched(launch_log_probs_grad(a, (cudaStream_t)stream));
+}
+
+DA_EXPORT int dte_forward(const void* ids, int id_bits, const da_matrix* w, float scale, const da_matrix* y, int32_t* dev_status,
+                          da_stream_t stream) {
+  int e = check_rows(w);
+  if (e || (e = check_rows(y))) return e;
+  if (y->dtype != w->dtype) return DA_EDTYPE;
+  if (y->cols != w->cols || w->rows < 1) return DA_ESHAPE;
+  if ((e = check_ids(ids, id_bits, y->rows, w))) return e;
+  if (!std::isfinite(scale)) return DA_EINVAL;
+  if (!aligned(dev_status, 4)) return DA_EALIGN;
+  if (y->rows == 0) return DA_OK;
+  EmArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.ids = ids; a.wide = id_bits == 64; a.w = w->ptr; a.y = const_cast<void*>(y->ptr);
+  a.n = y->rows; a.rows = w->rows; a.cols = w->cols; a.ws = stride(*w); a.ys = stride(*y);
+  a.padding = -1; a.scale = scale; a.dtype = w->dtype; a.status = dev_status;
+  return launched(launch_embedding(a, (cudaStream_t)stream));
+}
+
+DA_EXPORT size_t dte_workspace_bytes(int64_t n, int64_t cols) {
+  if (n < 0 || n > ((int64_t)1 << 31) - 2 || cols < 1 || cols > (int64_t)1 << 30) return 0;
+  return em_layout(n, cols).total;
+}
+
+DA_EXPORT int dte_backward(const void* ids, int id_bits, const da_matrix* dy, float scale, int64_t padding, const da_matrix* dw,
+                           void* ws, size_t ws_bytes, int32_t* dev_status, da_stream_t stream) {
+  int e = check_rows(dw);
+  if (e || (e = check_rows(dy))) return e;
+  if (dy->dtype != dw->dtype) return DA_EDTYPE;
+  if (dy->cols != dw->cols || dw->rows < 1) return DA_ESHAPE;
+  if ((e = check_ids(ids, id_bits, dy->rows, dw))) return e;
+  if (!std::isfinite(scale) || padding < -1 || padding >= dw->rows) return DA_EINVAL;
+  const EmWs w = em_layout(dy->rows, dy->cols);
+  if (w.total > 0 && (!ws || ws_bytes < w.total)) return DA_EWORKSPACE;
+  if (!aligned(ws, 256) || !aligned(dev_status, 4)) return DA_EALIGN;
+  EmArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.ids = ids; a.wide = id_bits == 64; a.dy = dy->ptr; a.dw = const_cast<void*>(dw->ptr);
+  a.n = dy->rows; a.rows = dw->rows; a.cols = dw->cols; a.ws = stride(*dw); a.ys = stride(*dy);
+  a.padding = padding; a.scale = scale; a.dtype = dw->dtype; a.status = dev_status;
+  char* const p = static_cast<char*>(ws);
+  for (int i = 0; i < 2; i++) {
+    a.key[i] = reinterpret_cast<uint32_t*>(p + w.key[i]);
+    a.pos[i] = reinterpret_cast<uint32_t*>(p + w.pos[i]);
+  }
+  a.unit = reinterpret_cast<uint32_t*>(p + w.unit);
+  a.count = reinterpret_cast<uint32_t*>(p + w.count);
+  a.part = reinterpret_cast<float*>(p + w.part);
+  return launched(launch_embedding_grad(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -49,4 +49,65 @@ cudaError_t gl_few(const GlFewArgs& a, cudaStream_t st);
 template <bool BF>
 cudaError_t gl_scale(const GlScaleArgs& a, cudaStream_t st);
 
+// ---- log probabilities ----
+constexpr int LP_TOP = 32;       // most alternatives of a row
+
+struct LpArgs {
+  const void* x;                 // [rows, cols], row stride xs
+  const int64_t* targets;        // [rows]
+  float* lp;                     // [rows]
+  float* entropy;                // [rows]
+  float* stats;                  // [rows][3] or null: reference and sum (log2 units, see log_prob_kernels.cu), entropy
+  float* top_lp;                 // [rows, top]
+  int64_t* top_index;
+  int64_t rows, xs;
+  uint32_t cols;
+  int top;
+  int dtype;
+  float temperature;
+  int* status;
+};
+struct LpGradArgs {
+  const void* x;
+  const int64_t* targets;
+  const float* stats;
+  const float* grad;             // [rows] or null
+  const float* grad_entropy;     // [rows] or null
+  void* dx;                      // [rows, cols], row stride ds
+  int64_t rows, xs, ds;
+  uint32_t cols;
+  int dtype;
+  float temperature;
+};
+cudaError_t launch_log_probs(const LpArgs& a, cudaStream_t st);
+cudaError_t launch_log_probs_grad(const LpGradArgs& a, cudaStream_t st);
+
+// ---- embedding ----
+constexpr int EM_CHUNK = 64;     // tokens of a row whose sum is one chain
+constexpr int EM_SMALL = 16384;  // tokens that one CTA sorts in shared memory
+constexpr int EM_BLOCK = 4096;   // tokens of a CTA of the passes of a longer sort
+constexpr int EM_BINS = 512;     // values of a digit
+
+struct EmArgs {
+  const void* ids;               // [n], int32 or int64
+  int wide;                      // int64
+  const void* w;                 // lookup: [rows, cols], row stride ws
+  void* y;                       // lookup: [n, cols], row stride ys
+  const void* dy;                // gradient: [n, cols], row stride ys
+  void* dw;                      // gradient: [rows, cols], row stride ws
+  int64_t n, rows, cols, ws, ys;
+  int64_t padding;               // its tokens give no gradient; -1: none
+  float scale;
+  int dtype;
+  int* status;
+  // workspace of the gradient
+  uint32_t* key[2];              // [n] ids in sorted order (rows: no gradient), and of the pass before
+  uint32_t* pos[2];              // [n] their tokens
+  uint32_t* count;               // longer sorts: [EM_BINS][blocks]
+  uint32_t* unit;                // [n]: tokens of the chunk that starts here, 0: none; bit 31: one of several
+  float* part;                   // [2 (n / EM_CHUNK + 1)][cols] sums of such chunks
+};
+cudaError_t launch_embedding(const EmArgs& a, cudaStream_t st);
+cudaError_t launch_embedding_grad(const EmArgs& a, cudaStream_t st);
+
 }  // namespace detattn

@@ -1,0 +1,512 @@
+// Embedding lookup with scaling and its gradient by sorted tokens.
+//
+//   y[i] = scale w[id_i];   dw[v] = scale (sum over i with id_i = v, in order of i, of dy[i])
+//
+// What bounds both: HBM.  The lookup reads the named rows and writes one a token; the gradient reads dy once and writes every
+// row of dw, most of them zeros for a large vocabulary.
+//
+// Gradient: the tokens are sorted by id, stably, by counting digits of up to 9 bits from the lowest on (two passes up to 2^18
+// rows).  Up to 16384 tokens one CTA does that in shared memory while the others fill dw with zeros; longer ones take three
+// launches a pass, the zeros beside the first.  Each warp's rank of a token among those of its digit comes from a match over the
+// warp and its counters, so the order never depends on which thread came first.  Then a chunk of up to 64 tokens of a row is one
+// warp's chain of binary32 additions for each of its columns, in order of the tokens; rows of more leave their chunks' sums in the
+// workspace, and a last kernel adds these, eight runs of chunks in order and then the eight.  So a row's bits depend on its own
+// tokens alone, and no atomics add values.
+#include <algorithm>
+
+#include "../../include/detattn.h"
+#include "decoder_kernels.h"
+#include "device_once.h"
+#include "train_math.cuh"
+
+namespace detattn {
+namespace {
+
+constexpr uint32_t LONG = 0x80000000u;   // of a unit: one of several chunks of its row
+
+__device__ __forceinline__ int64_t id_at(const EmArgs& a, int64_t i) {
+  return a.wide ? static_cast<const int64_t*>(a.ids)[i] : (int64_t) static_cast<const int32_t*>(a.ids)[i];
+}
+
+// ---- lookup: a warp 8 runs (of 16 bytes or one element a lane) of a token ----
+template <typename T, bool AL>
+__global__ void __launch_bounds__(256) em_lookup_kernel(const __grid_constant__ EmArgs a, uint32_t pieces) {
+  constexpr int VEC = AL ? Elem<T>::VEC : 1, U = 4;
+  const int lane = threadIdx.x & 31;
+  const uint64_t w = ((uint64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+  const int64_t i = w / pieces, c0 = (int64_t)(w % pieces) * 32 * VEC * U;
+  if (i >= a.n) return;
+  const int64_t id = id_at(a, i);
+  const bool known = id >= 0 && id < a.rows;
+  if (!known && lane == 0 && c0 == 0 && a.status) atomicOr(a.status, DA_STATUS_BAD_TARGET);
+  const T* const from = static_cast<const T*>(a.w) + (known ? id : 0) * a.ws;
+  T* const to = static_cast<T*>(a.y) + i * a.ys;
+  if constexpr (AL) {
+    Run<T, VEC> r[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t c = c0 + (u * 32 + lane) * VEC;
+      r[u].zero();
+      if (known && c < a.cols) r[u].load(from + c);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t c = c0 + (u * 32 + lane) * VEC;
+      if (a.scale != 1.f) {
+        float v[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; e++) v[e] = r[u].get(e) * a.scale;
+        r[u].set(v);
+      }
+      if (c < a.cols) r[u].store(to + c);
+    }
+  } else {
+    T r[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t c = c0 + u * 32 + lane;
+      r[u] = known && c < a.cols ? from[c] : Elem<T>::put(0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t c = c0 + u * 32 + lane;
+      if (c < a.cols) to[c] = a.scale == 1.f ? r[u] : Elem<T>::put(Elem<T>::get(r[u]) * a.scale);
+    }
+  }
+}
+
+// ---- sort ----
+__device__ __forceinline__ uint32_t key_at(const EmArgs& a, int64_t i) {   // rows: gives no gradient
+  const int64_t id = id_at(a, i);
+  if (id < 0 || id >= a.rows) {
+    if (a.status) atomicOr(a.status, DA_STATUS_BAD_TARGET);
+    return (uint32_t)a.rows;
+  }
+  return id == a.padding ? (uint32_t)a.rows : (uint32_t)id;
+}
+// zeros over this CTA's share (of `share` CTAs) of a contiguous dw
+template <int THREADS>
+__device__ __forceinline__ void fill_zeros(const EmArgs& a, uint32_t cta, uint32_t share) {
+  const int64_t bytes = a.rows * a.cols * (a.dtype == DA_F32 ? 4 : 2);
+  unsigned char* const p = static_cast<unsigned char*>(a.dw);
+  const int64_t head = min(bytes, (int64_t)(-reinterpret_cast<intptr_t>(p) & 15)), body = (bytes - head) / 16;
+  for (int64_t i = (int64_t)cta * THREADS + threadIdx.x; i < body; i += (int64_t)share * THREADS)
+    reinterpret_cast<uint4*>(p + head)[i] = make_uint4(0, 0, 0, 0);
+  if (cta == 0 && threadIdx.x < 32) {
+    if (threadIdx.x < head) p[threadIdx.x] = 0;
+    const int64_t tail = head + body * 16 + threadIdx.x;
+    if (tail < bytes) p[tail] = 0;
+  }
+}
+
+// A warp's tokens of one digit each: this lane's rank among equal digits of lower lanes, and whether it is their last.
+__device__ __forceinline__ uint32_t rank_of(uint32_t digit, bool& last) {
+  const uint32_t same = __match_any_sync(0xffffffffu, digit), lane = threadIdx.x & 31;
+  last = same >> lane == 1;
+  return __popc(same & ((1u << lane) - 1));
+}
+
+// One CTA (the first) sorts up to EM_SMALL tokens; the others fill zeros.
+constexpr int SORT_THREADS = 1024, SORT_WARPS = 32;
+struct SortSmall {
+  uint32_t key[EM_SMALL];
+  uint16_t pos[2][EM_SMALL];
+  uint16_t hist[SORT_WARPS][EM_BINS];
+  uint32_t base[EM_BINS], warps[32];
+};
+
+__global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_constant__ EmArgs a, int passes, int bits) {
+  if (blockIdx.x > 0) {
+    fill_zeros<SORT_THREADS>(a, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  extern __shared__ unsigned char raw[];
+  SortSmall& s = *reinterpret_cast<SortSmall*>(raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = (int)a.n;
+  const int per = ((n + SORT_THREADS - 1) / SORT_THREADS) * 32, i0 = warp * per, i1 = min(n, i0 + per);   // a warp's run of places
+  for (int i = tid; i < n; i += SORT_THREADS) s.key[i] = key_at(a, i);
+  __syncthreads();
+  for (int p = 0; p < passes; p++) {
+    const int shift = p * bits;
+    const uint32_t mask = (1u << bits) - 1;
+    const uint16_t* const from = s.pos[(p + 1) & 1];
+    uint16_t* const to = s.pos[p & 1];
+    for (int b = lane; b <= (int)mask; b += 32) s.hist[warp][b] = 0;
+    __syncwarp();
+    for (int i = i0; i < i1; i += 32) {
+      const int at = i + lane;
+      const bool live = at < i1;
+      const uint32_t d = live ? s.key[p ? from[at] : at] >> shift & mask : EM_BINS;
+      bool last;
+      const uint32_t rank = rank_of(d, last);
+      if (live && last) s.hist[warp][d] += rank + 1;
+      __syncwarp();
+    }
+    __syncthreads();
+    // places before each digit, and within it before each warp
+    uint32_t total = 0;
+    if (tid <= (int)mask)
+      for (int w = 0; w < SORT_WARPS; w++) {
+        const uint32_t c = s.hist[w][tid];
+        s.hist[w][tid] = (uint16_t)total;
+        total += c;
+      }
+    uint32_t sum = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    if (lane == 31) s.warps[warp] = sum;
+    __syncthreads();
+    if (tid <= (int)mask) {
+      uint32_t before = sum - total;
+      for (int w = 0; w < warp; w++) before += s.warps[w];
+      s.base[tid] = before;
+    }
+    __syncthreads();
+    for (int i = i0; i < i1; i += 32) {
+      const int at = i + lane;
+      const bool live = at < i1;
+      const int place = live ? p ? from[at] : at : 0;
+      const uint32_t d = live ? s.key[place] >> shift & mask : EM_BINS;
+      bool last;
+      const uint32_t rank = rank_of(d, last);
+      uint32_t mine = 0;
+      if (live) {
+        mine = s.hist[warp][d];
+        to[s.base[d] + mine + rank] = (uint16_t)place;
+      }
+      __syncwarp();
+      if (live && last) s.hist[warp][d] = (uint16_t)(mine + rank + 1);
+      __syncwarp();
+    }
+    __syncthreads();
+  }
+  const uint16_t* const done = s.pos[(passes - 1) & 1];
+  for (int i = tid; i < n; i += SORT_THREADS) {
+    a.pos[0][i] = done[i];
+    a.key[0][i] = s.key[done[i]];
+  }
+}
+
+// A pass over longer ones.  Counts of a block's digits (the first pass: from the ids; blocks past the tokens' fill zeros).
+constexpr int RADIX_THREADS = 256, RADIX_WARPS = 8, RADIX_RUN = EM_BLOCK / RADIX_WARPS;
+__global__ void __launch_bounds__(RADIX_THREADS) em_count_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int from, int shift, int bits) {
+  if (blockIdx.x >= blocks) {
+    fill_zeros<RADIX_THREADS>(a, blockIdx.x - blocks, gridDim.x - blocks);
+    return;
+  }
+  __shared__ uint32_t hist[EM_BINS];
+  const uint32_t mask = (1u << bits) - 1;
+  for (int b = threadIdx.x; b < EM_BINS; b += RADIX_THREADS) hist[b] = 0;
+  __syncthreads();
+  const int64_t i0 = (int64_t)blockIdx.x * EM_BLOCK, i1 = min(a.n, i0 + EM_BLOCK);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += RADIX_THREADS)
+    atomicAdd(&hist[(from < 0 ? key_at(a, i) : a.key[from][i]) >> shift & mask], 1u);
+  __syncthreads();
+  for (uint32_t b = threadIdx.x; b <= mask; b += RADIX_THREADS) a.count[(size_t)b * blocks + blockIdx.x] = hist[b];
+}
+// Places before each (digit, block): one CTA, a run of counts a thread.
+__global__ void __launch_bounds__(1024) em_scan_kernel(uint32_t* count, int64_t n) {
+  __shared__ uint32_t warps[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t per = (n + 1023) / 1024, i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  uint32_t total = 0;
+  for (int64_t i = i0; i < i1; i++) total += count[i];
+  uint32_t sum = total;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) warps[warp] = sum;
+  __syncthreads();
+  uint32_t before = sum - total;
+  for (int w = 0; w < warp; w++) before += warps[w];
+  for (int64_t i = i0; i < i1; i++) {
+    const uint32_t c = count[i];
+    count[i] = before;
+    before += c;
+  }
+}
+__global__ void __launch_bounds__(RADIX_THREADS) em_scatter_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int from, int to, int shift, int bits) {
+  __shared__ uint32_t hist[RADIX_WARPS][EM_BINS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t mask = (1u << bits) - 1;
+  const int64_t i0 = (int64_t)blockIdx.x * EM_BLOCK + warp * RADIX_RUN, i1 = min(a.n, i0 + RADIX_RUN);
+  uint32_t key[RADIX_RUN / 32];
+  for (int b = lane; b < EM_BINS; b += 32) hist[warp][b] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < RADIX_RUN / 32; k++) {
+    const int64_t i = i0 + k * 32 + lane;
+    key[k] = i < i1 ? from < 0 ? key_at(a, i) : a.key[from][i] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < RADIX_RUN / 32; k++) {
+    const bool live = i0 + k * 32 + lane < i1;
+    const uint32_t d = live ? key[k] >> shift & mask : EM_BINS;
+    bool last;
+    const uint32_t rank = rank_of(d, last);
+    if (live && last) hist[warp][d] += rank + 1;
+    __syncwarp();
+  }
+  __syncthreads();
+  for (uint32_t b = tid; b <= mask; b += RADIX_THREADS) {
+    uint32_t before = a.count[(size_t)b * blocks + blockIdx.x];
+    for (int w = 0; w < RADIX_WARPS; w++) {
+      const uint32_t c = hist[w][b];
+      hist[w][b] = before;
+      before += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < RADIX_RUN / 32; k++) {
+    const int64_t i = i0 + k * 32 + lane;
+    const bool live = i < i1;
+    const uint32_t d = live ? key[k] >> shift & mask : EM_BINS;
+    bool last;
+    const uint32_t rank = rank_of(d, last);
+    uint32_t mine = 0;
+    if (live) {
+      mine = hist[warp][d];
+      a.key[to][mine + rank] = key[k];
+      a.pos[to][mine + rank] = from < 0 ? (uint32_t)i : a.pos[from][i];
+    }
+    __syncwarp();
+    if (live && last) hist[warp][d] = mine + rank + 1;
+    __syncwarp();
+  }
+}
+
+// ---- chunks: a row's sorted tokens from its first on, EM_CHUNK at a time ----
+__global__ void __launch_bounds__(256) em_chunk_kernel(const __grid_constant__ EmArgs a, int from) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.n) return;
+  const uint32_t* const key = a.key[from];
+  const uint32_t k = key[i];
+  uint32_t unit = 0;
+  if (k < a.rows) {
+    int64_t first = i;
+    if (i > 0 && key[i - 1] == k) {   // the first place of k
+      int64_t lo = 0;
+      while (lo < first) {
+        const int64_t mid = (lo + first) >> 1;
+        if (key[mid] < k) lo = mid + 1;
+        else first = mid;
+      }
+    }
+    if ((i - first) % EM_CHUNK == 0) {
+      int64_t end = min(a.n, i + EM_CHUNK), lo = i + 1;
+      const bool more = i > first || (i + EM_CHUNK < a.n && key[i + EM_CHUNK] == k);
+      while (lo < end) {   // the first place past k, at most a chunk on
+        const int64_t mid = (lo + end) >> 1;
+        if (key[mid] == k) lo = mid + 1;
+        else end = mid;
+      }
+      unit = (uint32_t)(end - i) | (more ? LONG : 0);
+    }
+  }
+  a.unit[i] = unit;
+}
+// Where a chunk of several leaves its sum: full ones start at least a chunk apart, and so do the last ones of their rows.
+__device__ __forceinline__ int64_t slot_of(const EmArgs& a, int64_t i, uint32_t len) {
+  return i / EM_CHUNK + (len < EM_CHUNK ? a.n / EM_CHUNK + 1 : 0);
+}
+
+// ---- sums: a warp a chunk's 32 runs (of 16 bytes, or 8 single elements a lane) ----
+template <typename T, bool AL>
+__global__ void __launch_bounds__(256) em_sum_kernel(const __grid_constant__ EmArgs a, int from, uint32_t pieces) {
+  constexpr int VEC = AL ? Elem<T>::VEC : 4, U = 8;
+  const int lane = threadIdx.x & 31;
+  const uint64_t w = ((uint64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+  const int64_t i = w / pieces;
+  if (i >= a.n) return;
+  const uint32_t unit = a.unit[i], len = unit & ~LONG;
+  if (len == 0) return;
+  const int64_t c0 = (int64_t)(w % pieces) * 32 * VEC + (AL ? lane * VEC : lane);
+  const T* const dy = static_cast<const T*>(a.dy) + c0;
+  const uint32_t* const pos = a.pos[from] + i;
+  float sum[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; e++) sum[e] = 0.f;
+  if (c0 < a.cols) {
+    for (uint32_t j = 0; j < len; j += U) {
+      if constexpr (AL) {
+        Run<T, VEC> r[U];
+#pragma unroll
+        for (int u = 0; u < U; u++)
+          if (j + u < len) r[u].load(dy + (int64_t)pos[j + u] * a.ys);
+#pragma unroll
+        for (int u = 0; u < U; u++)
+          if (j + u < len) {
+#pragma unroll
+            for (int e = 0; e < VEC; e++) sum[e] += r[u].get(e);
+          }
+      } else {
+        T r[U][VEC];
+#pragma unroll
+        for (int u = 0; u < U; u++)
+          if (j + u < len) {
+            const T* const at = dy + (int64_t)pos[j + u] * a.ys;
+#pragma unroll
+            for (int e = 0; e < VEC; e++) r[u][e] = c0 + 32 * e < a.cols ? at[32 * e] : Elem<T>::put(0.f);
+          }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+          if (j + u < len) {
+#pragma unroll
+            for (int e = 0; e < VEC; e++) sum[e] += Elem<T>::get(r[u][e]);
+          }
+      }
+    }
+    if (unit & LONG) {
+      float* const to = a.part + slot_of(a, i, len) * a.cols + c0;
+#pragma unroll
+      for (int e = 0; e < VEC; e++)
+        if (AL || c0 + 32 * e < a.cols) to[AL ? e : 32 * e] = sum[e];
+    } else {
+      T* const to = static_cast<T*>(a.dw) + (int64_t)a.key[from][i] * a.ws + c0;
+#pragma unroll
+      for (int e = 0; e < VEC; e++) sum[e] *= a.scale;
+      if constexpr (AL) {
+        Run<T, VEC> o;
+        o.set(sum);
+        o.store(to);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e++)
+          if (c0 + 32 * e < a.cols) to[32 * e] = Elem<T>::put(sum[e]);
+      }
+    }
+  }
+}
+
+// ---- rows of several chunks: a CTA 32 columns, its eight warps a run of the chunks each ----
+template <typename T>
+__global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ EmArgs a, int from) {
+  __shared__ float sums[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the first of several chunks is full, and such ones start at least a chunk apart: at most one within EM_CHUNK places
+  const int64_t i0 = (int64_t)blockIdx.x * EM_CHUNK;
+  const uint32_t* const key = a.key[from];
+  int64_t first = -1;
+  for (int j = 0; j < EM_CHUNK; j += 32) {
+    const int64_t i = i0 + j + lane;
+    const bool is = i < a.n && a.unit[i] == (EM_CHUNK | LONG) && (i == 0 || key[i - 1] != key[i]);
+    const uint32_t who = __ballot_sync(0xffffffffu, is);
+    if (who) first = i0 + j + __ffs(who) - 1;
+  }
+  if (first < 0) return;
+  // chunks of this row: they follow each other, the last one may be shorter
+  const uint32_t k = key[first];
+  int64_t lo = first + EM_CHUNK, end = a.n;
+  while (lo < end) {
+    const int64_t mid = (lo + end) >> 1;
+    if (key[mid] == k) lo = mid + 1;
+    else end = mid;
+  }
+  const int64_t chunks = (end - first + EM_CHUNK - 1) / EM_CHUNK, per = (chunks + 7) / 8;
+  const int64_t q0 = min(chunks, warp * per), q1 = min(chunks, q0 + per);
+  for (int64_t c0 = (int64_t)blockIdx.y * 32; c0 < a.cols; c0 += (int64_t)gridDim.y * 32) {
+    const int64_t c = c0 + lane;
+    float sum = 0.f;
+    if (c < a.cols) {
+      int64_t q = q0;
+      for (; q + 8 <= q1; q += 8) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+          const int64_t i = first + (q + u) * EM_CHUNK;
+          v[u] = a.part[slot_of(a, i, (uint32_t)min((int64_t)EM_CHUNK, end - i)) * a.cols + c];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; u++) sum += v[u];
+      }
+      for (; q < q1; q++) {
+        const int64_t i = first + q * EM_CHUNK;
+        sum += a.part[slot_of(a, i, (uint32_t)min((int64_t)EM_CHUNK, end - i)) * a.cols + c];
+      }
+    }
+    __syncthreads();
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && c < a.cols) {
+      float all = sums[0][lane];
+#pragma unroll
+      for (int w = 1; w < 8; w++) all += sums[w][lane];
+      static_cast<T*>(a.dw)[(int64_t)k * a.ws + c] = Elem<T>::put(all * a.scale);
+    }
+  }
+}
+
+bool rows_aligned(const void* p, int64_t stride, int64_t cols, int es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * es % 16 == 0 && cols * es % 16 == 0;
+}
+
+template <typename T, bool AL>
+cudaError_t lookup(const EmArgs& a, cudaStream_t st) {
+  const int64_t run = 32 * 4 * (AL ? Elem<T>::VEC : 1), pieces = (a.cols + run - 1) / run;
+  em_lookup_kernel<T, AL><<<(unsigned)((a.n * pieces + 7) / 8), 256, 0, st>>>(a, (uint32_t)pieces);
+  return cudaGetLastError();
+}
+template <typename T, bool AL>
+cudaError_t sums(const EmArgs& a, int from, cudaStream_t st) {
+  const int64_t run = 32 * (AL ? Elem<T>::VEC : 4), pieces = (a.cols + run - 1) / run;
+  em_sum_kernel<T, AL><<<(unsigned)((a.n * pieces + 7) / 8), 256, 0, st>>>(a, from, (uint32_t)pieces);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.n <= EM_CHUNK) return e;
+  const dim3 grid((unsigned)((a.n + EM_CHUNK - 1) / EM_CHUNK), (unsigned)std::min<int64_t>((a.cols + 31) / 32, 64));
+  em_join_kernel<T><<<grid, 256, 0, st>>>(a, from);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t gradient(const EmArgs& a, int from, cudaStream_t st) {
+  return rows_aligned(a.dy, a.ys, a.cols, sizeof(T)) && rows_aligned(a.dw, a.ws, a.cols, sizeof(T)) ? sums<T, true>(a, from, st)
+                                                                                                  : sums<T, false>(a, from, st);
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const EmArgs& a, cudaStream_t st) {
+  const int es = a.dtype == DA_F32 ? 4 : 2;
+  const bool al = rows_aligned(a.w, a.ws, a.cols, es) && rows_aligned(a.y, a.ys, a.cols, es);
+  if (a.dtype == DA_F32) return al ? lookup<float, true>(a, st) : lookup<float, false>(a, st);
+  if (a.dtype == DA_BF16) return al ? lookup<__nv_bfloat16, true>(a, st) : lookup<__nv_bfloat16, false>(a, st);
+  return al ? lookup<__half, true>(a, st) : lookup<__half, false>(a, st);
+}
+
+cudaError_t launch_embedding_grad(const EmArgs& a, cudaStream_t st) {
+  const int es = a.dtype == DA_F32 ? 4 : 2;
+  const bool flat = a.rows <= 1 || a.ws == a.cols;
+  cudaError_t e = cudaSuccess;
+  if (!flat || a.n == 0) e = cudaMemset2DAsync(a.dw, (size_t)a.ws * es, 0, (size_t)a.cols * es, (size_t)a.rows, st);
+  if (e != cudaSuccess || a.n == 0) return e;
+  // CTAs that fill zeros: at least 64 KB each, beside the one that sorts one an SM (it takes most of the shared memory)
+  const unsigned fill = flat ? (unsigned)std::min<int64_t>(a.n <= EM_SMALL ? 151 : 152 * 4, a.rows * a.cols * es / 65536 + 1) : 0;
+  int need = 1, from = 0;
+  while (need < 32 && ((uint64_t)1 << need) <= (uint64_t)a.rows) need++;   // bits of the keys 0 .. rows
+  const int passes = (need + 8) / 9, bits = (need + passes - 1) / passes;
+  if (a.n <= EM_SMALL) {
+    static DeviceOnce once;
+    if ((e = allow_smem(once, em_sort_kernel, (int)sizeof(SortSmall))) != cudaSuccess) return e;
+    em_sort_kernel<<<1 + fill, SORT_THREADS, sizeof(SortSmall), st>>>(a, passes, bits);
+  } else {
+    const uint32_t blocks = (uint32_t)((a.n + EM_BLOCK - 1) / EM_BLOCK);
+    for (int p = 0; p < passes; p++) {
+      const int src = p ? (p + 1) & 1 : -1, dst = p & 1, shift = p * bits;
+      em_count_kernel<<<blocks + (p ? 0 : fill), RADIX_THREADS, 0, st>>>(a, blocks, src, shift, bits);
+      em_scan_kernel<<<1, 1024, 0, st>>>(a.count, (int64_t)blocks << bits);
+      em_scatter_kernel<<<blocks, RADIX_THREADS, 0, st>>>(a, blocks, src, dst, shift, bits);
+      from = dst;
+    }
+  }
+  em_chunk_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, st>>>(a, from);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.dtype == DA_F32) return gradient<float>(a, from, st);
+  return a.dtype == DA_BF16 ? gradient<__nv_bfloat16>(a, from, st) : gradient<__half>(a, from, st);
+}
+
+}  // namespace detattn

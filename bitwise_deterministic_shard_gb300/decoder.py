@@ -1,4 +1,5 @@
-"""Operators at the ends and in the middle of a decoder: the gated feed-forward projections, each with its gradient.
+"""Operators at the ends and in the middle of a decoder: embedding lookup, the gated feed-forward projections and
+log probabilities of given tokens with entropy and alternatives, each with its gradient.
 
 Argument marshalling only, as in train.py: the computation runs in the CUDA kernels behind include/detattn.h on the current stream
 of the tensors' device, and there is no CPU path.  Every kernel adds in an order that depends on the sizes and types alone,
@@ -7,14 +8,17 @@ so equal calls give equal bytes on every run.
 from __future__ import annotations
 
 import ctypes as C
+from typing import NamedTuple, Optional
 
 import torch
 
 import bitwise_deterministic_shard_gb300 as _da
 from bitwise_deterministic_shard_gb300 import DetAttnError
-from .train import _HALF, _MATRIX, _addr, _on, _room, _run, _tracked, _written
+from .train import _HALF, _MATRIX, _addr, _code, _on, _room, _run, _tracked, _written
 
-_NAMES = ("dgl_forward", "dgl_backward")
+TOP_MOST = 32         # alternatives of a row in log_probs
+
+_NAMES = ("dgl_forward", "dgl_backward", "dlp_forward", "dlp_backward", "dte_forward", "dte_backward")
 
 
 def declare(L):
@@ -24,6 +28,11 @@ def declare(L):
     L.dgl_workspace_bytes.argtypes, L.dgl_workspace_bytes.restype = [Q, Q], N
     L.dgl_forward.argtypes = [P, P, P, I, P, P, P, P]
     L.dgl_backward.argtypes = [P, P, P, P, P, P, P, P, P, N, P, P]
+    L.dlp_forward.argtypes = [P, P, C.c_float, I, P, P, P, P, P, P, P]
+    L.dlp_backward.argtypes = [P, P, P, P, P, C.c_float, P, P]
+    L.dte_forward.argtypes = [P, I, P, C.c_float, P, P, P]
+    L.dte_workspace_bytes.argtypes, L.dte_workspace_bytes.restype = [Q, Q], N
+    L.dte_backward.argtypes = [P, I, P, C.c_float, Q, P, P, N, P, P]
     for f in _NAMES:
         getattr(L, f).restype = C.c_int
 
@@ -168,3 +177,199 @@ def gated_linear(x, w_gate, w_up, activation="silu", status=None):
     if _tracked(x, w_gate, w_up):
         return _GatedLinear.apply(x, w_gate, w_up, activation, status)
     return gated_linear_forward(x, w_gate, w_up, activation, need_saved=False, status=status)[0]
+
+
+# ---------------------------------------------------------------- log probabilities
+
+class LogProbs(NamedTuple):
+    """Of each row: log_probs of its given token, entropy, and where asked for its most likely tokens [..., top]."""
+    log_probs: torch.Tensor
+    entropy: torch.Tensor
+    top_log_probs: Optional[torch.Tensor]
+    top_indices: Optional[torch.Tensor]
+
+
+def _rows(t, code, cols):
+    """t [..., cols] as the bytes of a matrix, t (itself or a contiguous copy) and the row stride."""
+    run = _run_of_rows(t, cols)
+    if run is None:
+        t, run = t.detach().contiguous(), cols
+    return _MATRIX.pack(t.data_ptr(), code, t.numel() // cols, cols, run), t, run
+
+
+def _logits(logits, targets, temperature):
+    _da._cuda(logits, "logits")
+    if logits.dim() < 1 or logits.shape[-1] < 1:
+        raise DetAttnError("logits must be [..., V] with at least one column")
+    code, index = _code(logits, "logits"), logits.get_device()
+    if targets.get_device() != index or targets.shape != logits.shape[:-1]:
+        raise DetAttnError(f"targets must be {list(logits.shape[:-1])} on the logits' device")
+    if targets.dtype != torch.int64:
+        if targets.dtype.is_floating_point or targets.dtype.is_complex or targets.dtype == torch.bool:
+            raise DetAttnError("targets must be integers")
+        targets = targets.to(torch.int64)
+    if not 0.0 < temperature < float("inf"):
+        raise DetAttnError("temperature must be above 0 and finite")
+    return code, index, targets if targets.is_contiguous() else targets.contiguous()
+
+
+def log_probs_forward(logits, targets, temperature=1.0, top=0, need_saved=True, status=None):
+    """Log probabilities of given tokens, entropies and alternatives: (LogProbs, saved).
+
+    logits [..., V] f32, bf16 or f16; targets [...] integers.  With z = logits / temperature and lse = log sum exp z:
+      log_probs = z[target] - lse (a negative target: no token, 0);  entropy = lse - sum p z
+      top_indices, top_log_probs [..., top]: the top largest logits (up to 32) in order, equal ones by their index; None for 0
+    Results are f32 (indices int64).  A logit of -inf is a token of probability 0; a row of nothing else has entropy 0 and log
+    probabilities of -inf.  saved, which the backward pass takes, is None without need_saved."""
+    code, index, targets = _logits(logits, targets, temperature)
+    shape, V, dev = logits.shape[:-1], logits.shape[-1], logits.device
+    if not 0 <= top <= min(TOP_MOST, V):
+        raise DetAttnError(f"top must be from 0 to {min(TOP_MOST, V)}")
+    status = _status(status, index)
+    X, logits, _ = _rows(logits, code, V)
+    lp, entropy = (torch.empty(shape, dtype=torch.float32, device=dev) for _ in range(2))
+    saved = torch.empty((*shape, 3), dtype=torch.float32, device=dev) if need_saved else None
+    top_lp = top_at = None
+    if top:
+        top_lp = torch.empty((*shape, top), dtype=torch.float32, device=dev)
+        top_at = torch.empty((*shape, top), dtype=torch.int64, device=dev)
+    _run("log_probs_forward", index, _da.lib().dlp_forward, X, targets.data_ptr(), temperature, top, lp.data_ptr(),
+         entropy.data_ptr(), _addr(saved), _addr(top_lp), _addr(top_at), status)
+    return LogProbs(lp, entropy, top_lp, top_at), saved
+
+
+def log_probs_backward(logits, targets, saved, grad, grad_entropy=None, temperature=1.0, out=None):
+    """Gradient of sum(grad * log_probs) + sum(grad_entropy * entropy) (f32 [...], either None: zeros) for the logits, rounded once
+    to their dtype.  out: contiguous memory for it, such as the logits themselves; without it the rows of the result
+    are as far apart as the logits' are, up to 16 bytes."""
+    code, index, targets = _logits(logits, targets, temperature)
+    shape, V, n = logits.shape[:-1], logits.shape[-1], targets.numel()
+    if saved.get_device() != index or saved.dtype != torch.float32 or saved.numel() != 3 * n or not saved.is_contiguous():
+        raise DetAttnError("saved must be what log_probs_forward gave for these logits")
+    grads = []
+    for t, name in ((grad, "grad"), (grad_entropy, "grad_entropy")):
+        if t is not None:
+            if t.get_device() != index or t.dtype != torch.float32 or t.shape != shape:
+                raise DetAttnError(f"{name} must be f32 {list(shape)} on the logits' device")
+            t = t if t.is_contiguous() else t.contiguous()
+        grads.append(t)
+    X, x, run = _rows(logits, code, V)
+    if out is None:
+        step = V + (run - V) % (16 // logits.element_size())    # rows that start on 16 bytes where the logits' do
+        out = torch.empty((*shape, step), dtype=logits.dtype, device=logits.device)
+        given, out = None, out if step == V else out[..., :V]
+    else:
+        _on(index, "out", out)
+        if out.dtype != logits.dtype or out.shape != logits.shape or not out.is_contiguous():
+            raise DetAttnError(f"out must be contiguous {logits.dtype} {list(logits.shape)}")
+        given, step = out, V
+    _run("log_probs_backward", index, _da.lib().dlp_backward, X, targets.data_ptr(), saved.data_ptr(), _addr(grads[0]),
+         _addr(grads[1]), temperature, _MATRIX.pack(out.data_ptr(), code, n, V, step))
+    if given is not None:
+        _written(given)
+    return out
+
+
+class _LogProbs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, temperature, top, status):
+        r, saved = log_probs_forward(logits, targets, temperature, top, status=status)
+        ctx.save_for_backward(logits, targets, saved)
+        ctx.temperature = temperature
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(t for t in r[2:] if t is not None))
+        return tuple(r)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, grad_entropy, *_):
+        logits, targets, saved = ctx.saved_tensors
+        if grad is None and grad_entropy is None:
+            return None, None, None, None, None
+        return log_probs_backward(logits, targets, saved, grad, grad_entropy, ctx.temperature), None, None, None, None
+
+
+def log_probs(logits, targets, temperature=1.0, top=0, status=None):
+    """log_probs_forward's LogProbs, with autograd of log_probs and entropy for the logits (the alternatives have no gradient)."""
+    if _tracked(logits):
+        return LogProbs(*_LogProbs.apply(logits, targets, temperature, top, status))
+    return log_probs_forward(logits, targets, temperature, top, need_saved=False, status=status)[0]
+
+
+# ---------------------------------------------------------------- embedding
+
+def _ids(ids, index):
+    _on(index, "ids", ids)
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise DetAttnError("ids must be int32 or int64")
+    return ids if ids.is_contiguous() else ids.contiguous(), 32 if ids.dtype == torch.int32 else 64
+
+
+def embedding_forward(ids, weight, scale=1.0, out=None, status=None):
+    """Embedding lookup: scale * weight[ids], rounded once (scale 1: the same bits).  ids [...] int32 or int64, weight [rows, cols]
+    f32, bf16 or f16; the result is [..., cols] of weight's dtype.  An id outside [0, rows) gives zeros and sets
+    STATUS_BAD_TARGET."""
+    _da._cuda(weight, "weight")
+    if weight.dim() != 2 or weight.shape[0] < 1 or weight.shape[1] < 1:
+        raise DetAttnError("weight must be [rows, cols] with at least one row and column")
+    code, index, cols = _code(weight, "weight"), weight.get_device(), weight.shape[1]
+    ids, bits = _ids(ids, index)
+    status = _status(status, index)
+    W, weight, _ = _rows(weight, code, cols)
+    shape, given = (*ids.shape, cols), out
+    if out is None:
+        out = torch.empty(shape, dtype=weight.dtype, device=weight.device)
+    else:
+        _on(index, "out", out)
+        if out.dtype != weight.dtype or out.shape != shape or not out.is_contiguous():
+            raise DetAttnError(f"out must be contiguous {weight.dtype} {list(shape)}")
+    _run("embedding_forward", index, _da.lib().dte_forward, ids.data_ptr(), bits, W, scale,
+         _MATRIX.pack(out.data_ptr(), code, ids.numel(), cols, cols), status)
+    if given is not None:
+        _written(given)
+    return out
+
+
+def embedding_backward(grad, ids, rows, scale=1.0, padding_idx=None, workspace=None, status=None):
+    """The gradient [rows, cols] of sum(embedding * grad) for the weight, of grad's dtype: each row the binary32 sum over its own
+    tokens, in order and 64 at a time, rounded once; a row's bits depend on its own tokens alone.  Tokens of id padding_idx
+    give nothing, nor do those outside [0, rows), which set STATUS_BAD_TARGET."""
+    _da._cuda(grad, "grad")
+    if grad.dim() < 1 or grad.shape[:-1] != ids.shape or grad.shape[-1] < 1:
+        raise DetAttnError("grad must be [..., cols] with ids [...]")
+    code, index, cols = _code(grad, "grad"), grad.get_device(), grad.shape[-1]
+    ids, bits = _ids(ids, index)
+    if rows < 1 or (padding_idx is not None and not 0 <= padding_idx < rows):
+        raise DetAttnError("rows must be at least 1, padding_idx None or from 0 to rows - 1")
+    status = _status(status, index)
+    G, grad, _ = _rows(grad, code, cols)
+    dw = torch.empty(rows, cols, dtype=grad.dtype, device=grad.device)
+    L = _da.lib()
+    need = L.dte_workspace_bytes(ids.numel(), cols)
+    ws = _room(need, workspace, grad.device, index)
+    _run("embedding_backward", index, L.dte_backward, ids.data_ptr(), bits, G, scale, -1 if padding_idx is None else padding_idx,
+         _MATRIX.pack(dw.data_ptr(), code, rows, cols, cols), _addr(ws), need, status)
+    return dw
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, weight, scale, padding_idx, status):
+        ctx.save_for_backward(ids)
+        ctx.rows, ctx.scale, ctx.padding_idx, ctx.status = weight.shape[0], scale, padding_idx, status
+        return embedding_forward(ids, weight, scale, status=status)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        ids, = ctx.saved_tensors
+        return None, embedding_backward(grad, ids, ctx.rows, ctx.scale, ctx.padding_idx, status=ctx.status), None, None, None
+
+
+def embedding(ids, weight, scale=1.0, padding_idx=None, status=None):
+    """embedding_forward's lookup, with autograd for weight (tokens of id padding_idx give it no gradient)."""
+    if padding_idx is not None and not 0 <= padding_idx < weight.shape[0]:
+        raise DetAttnError("padding_idx must be None or from 0 to rows - 1")
+    if _tracked(weight):
+        return _Embedding.apply(ids, weight, scale, padding_idx, status)
+    return embedding_forward(ids, weight, scale, status=status)

@@ -436,6 +436,38 @@ int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_matrix* wg, c
                  const da_matrix* dx, const da_matrix* dwg, const da_matrix* dwu, void* ws, size_t ws_bytes, int32_t* dev_status,
                  da_stream_t stream);
 
+/* Log probabilities of given tokens, entropies and the most likely alternatives of rows of logits (f32, bf16, f16; any stride and
+ * start).  With z = logits / temperature (above 0) and lse = log sum exp z, all f32:
+ *   log_probs[i] = z[i][targets[i]] - lse_i  (targets: device int64 [rows]; negative: no token, 0)
+ *   entropy[i] = lse_i - sum_v p_iv z_iv,  p = exp(z - lse)
+ *   top_log_probs, top_indices [rows, top], top up to 32 and cols: the largest logits in order, equal ones by their index
+ * A logit of -inf is a token of probability 0; a row of nothing else has an entropy of 0 and log probabilities of -inf.  A target past
+ * the last column gives NaN and DA_STATUS_BAD_TARGET.  Other logits must be finite: NaN or +inf makes its row's results NaN (its
+ * alternatives unspecified) and sets DA_STATUS_NONFINITE.  saved: optional device f32 [rows, 3] for the backward pass. */
+int dlp_forward(const da_matrix* logits, const int64_t* targets, float temperature, int top, float* log_probs, float* entropy,
+                float* saved, float* top_log_probs, int64_t* top_indices, int32_t* dev_status, da_stream_t stream);
+
+/* Gradient of sum(grad log_probs) + sum(grad_entropy entropy) (device f32 [rows], either may be NULL: zeros), rounded once to the
+ * logits' type:
+ *   dlogits[i][v] = (grad_i ([v == targets[i]] - p_iv) - grad_entropy_i p_iv (log p_iv + entropy_i)) / temperature
+ * zeros for a row of nothing but -inf; a row whose target is outside [0, cols) has the second term alone.  dlogits may be the logits'
+ * own memory. */
+int dlp_backward(const da_matrix* logits, const int64_t* targets, const float* saved, const float* grad, const float* grad_entropy,
+                 float temperature, const da_matrix* dlogits, da_stream_t stream);
+
+/* Embedding lookup y[i] = scale w[ids[i]], rounded once (scale 1: the same bits).  ids: device int32 or int64 (id_bits 32 or 64)
+ * [y's rows]; w [rows, cols], y [n, cols], f32, bf16 or f16.  An id outside [0, rows) gives zeros and DA_STATUS_BAD_TARGET. */
+int dte_forward(const void* ids, int id_bits, const da_matrix* w, float scale, const da_matrix* y, int32_t* dev_status,
+                da_stream_t stream);
+
+/* Its gradient, every row of dw [rows, cols] written: dw[v] = scale (sum over i with ids[i] == v of dy[i]), a binary32 sum in order of
+ * the tokens, 64 at a time, rounded once; the tokens of id `padding` (-1: none) and those outside [0, rows), which set
+ * DA_STATUS_BAD_TARGET, give nothing.  A row's bits depend on its own tokens alone.  ws: dte_workspace_bytes(n, cols),
+ * 256-byte aligned. */
+size_t dte_workspace_bytes(int64_t n, int64_t cols);
+int dte_backward(const void* ids, int id_bits, const da_matrix* dy, float scale, int64_t padding, const da_matrix* dw, void* ws,
+                 size_t ws_bytes, int32_t* dev_status, da_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
