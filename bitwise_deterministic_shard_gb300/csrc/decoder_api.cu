@@ -30,20 +30,18 @@ EncodeFn encoder() {
   return fn;
 }
 
-// boxes of 64 columns x `rows` rows of a matrix of 16-bit elements
-bool tensor_map(CUtensorMap* m, const void* at, int dtype, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
+// boxes of 64 x 64 of a matrix of 16-bit elements
+bool tensor_map(CUtensorMap* m, const void* at, int dtype, int64_t rows, int64_t cols, int64_t stride) {
   const EncodeFn fn = encoder();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? stride : cols) * 2};   // one row: not used, but must be valid
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
   const CUtensorMapDataType type = dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   return fn(m, type, 2, const_cast<void*>(at), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool tensor_map(CUtensorMap* m, const da_matrix& x, int box_rows) {
-  return tensor_map(m, x.ptr, x.dtype, x.rows, x.cols, x.row_stride, box_rows);
-}
+bool tensor_map(CUtensorMap* m, const da_matrix& x) { return tensor_map(m, x.ptr, x.dtype, x.rows, x.cols, x.row_stride); }
 
 // ---- gated feed-forward ----
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
@@ -98,7 +96,7 @@ int check_ids(const void* ids, int bits, int64_t n, const da_matrix* like) {
   return n * (like->cols / 128 + 1) >= (int64_t)1 << 33 ? DA_ESHAPE : DA_OK;       // warps of a launch
 }
 struct EmWs {
-  size_t key[2], pos[2], unit, count, part, total;
+  size_t key[2], pos[2], found, unit, row, count, part, total;
 };
 EmWs em_layout(int64_t n, int64_t cols) {
   EmWs w;
@@ -110,10 +108,12 @@ EmWs em_layout(int64_t n, int64_t cols) {
   };
   const bool small = n <= EM_SMALL;
   for (int i = 0; i < 2; i++) {
-    w.key[i] = take(small && i ? 0 : (size_t)n * 4);
+    w.key[i] = take(small ? 0 : (size_t)n * 4);
     w.pos[i] = take(small && i ? 0 : (size_t)n * 4);
   }
-  w.unit = take((size_t)n * 4);
+  w.found = take(sizeof(EmUnits));
+  w.unit = take((size_t)n * 16);
+  w.row = take(n <= EM_CHUNK ? 0 : (size_t)(n / EM_CHUNK + 1) * 16);
   w.count = take(small ? 0 : (size_t)((n + EM_BLOCK - 1) / EM_BLOCK) * EM_BINS * 4);
   w.part = take(n <= EM_CHUNK ? 0 : (size_t)2 * (n / EM_CHUNK + 1) * cols * 4);
   w.total = at;
@@ -147,11 +147,11 @@ DA_EXPORT int dgl_forward(const da_matrix* x, const da_matrix* wg, const da_matr
   GlArgs a;
   std::memset(&a, 0, sizeof(a));
   a.T = (int)x->rows; a.D = (int)x->cols; a.F = (int)wg->rows;
-  a.out[0] = const_cast<void*>(h->ptr); a.os[0] = stride(*h);
+  a.h = const_cast<void*>(h->ptr); a.hs = stride(*h);
   a.saved = static_cast<unsigned char*>(saved);
   a.activation = activation;
   a.status = dev_status;
-  if (!tensor_map(&a.a[0], *x, 128) || !tensor_map(&a.b[0], *wg, 128) || !tensor_map(&a.b[1], *wu, 128)) return DA_ECUDA;
+  if (!tensor_map(&a.x, *x) || !tensor_map(&a.wg, *wg) || !tensor_map(&a.wu, *wu)) return DA_ECUDA;
   return launched(bf ? gl_forward<true>(a, st) : gl_forward<false>(a, st));
 }
 
@@ -187,21 +187,15 @@ DA_EXPORT int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_mat
   std::memset(&a, 0, sizeof(a));
   a.T = (int)T; a.D = (int)D; a.F = (int)F;
   a.status = dev_status;
-  if (dx) {
-    for (int i = 0; i < 2; i++)
-      if (!tensor_map(&a.a[i], dg + i * T * F, x->dtype, T, F, F, 128) || !tensor_map(&a.b[i], i ? *wu : *wg, 64)) return DA_ECUDA;
-    a.out[0] = const_cast<void*>(dx->ptr); a.os[0] = stride(*dx);
-    if ((e = launched(bf ? gl_dx<true>(a, st) : gl_dx<false>(a, st)))) return e;
-  }
+  if (!tensor_map(&a.x, *x) || !tensor_map(&a.wg, *wg) || !tensor_map(&a.wu, *wu) ||
+      !tensor_map(&a.dg, dg, x->dtype, T, F, F) || !tensor_map(&a.du, dg + T * F, x->dtype, T, F, F))
+    return DA_ECUDA;
+  if (dx) a.dx = const_cast<void*>(dx->ptr), a.dxs = stride(*dx);
   if (dwg) {
-    for (int i = 0; i < 2; i++) {
-      if (!tensor_map(&a.a[i], dg + i * T * F, x->dtype, T, F, F, 64)) return DA_ECUDA;
-      a.out[i] = const_cast<void*>((i ? dwu : dwg)->ptr); a.os[i] = stride(*(i ? dwu : dwg));
-    }
-    if (!tensor_map(&a.b[0], *x, 64)) return DA_ECUDA;
-    return launched(bf ? gl_dw<true>(a, st) : gl_dw<false>(a, st));
+    a.dwg = const_cast<void*>(dwg->ptr), a.dwgs = stride(*dwg);
+    a.dwu = const_cast<void*>(dwu->ptr), a.dwus = stride(*dwu);
   }
-  return DA_OK;
+  return launched(bf ? gl_backward<true>(a, st) : gl_backward<false>(a, st));
 }
 
 DA_EXPORT int dlp_forward(const da_matrix* logits, const int64_t* targets, float temperature, int top, float* log_probs,
@@ -286,7 +280,9 @@ DA_EXPORT int dte_backward(const void* ids, int id_bits, const da_matrix* dy, fl
     a.key[i] = reinterpret_cast<uint32_t*>(p + w.key[i]);
     a.pos[i] = reinterpret_cast<uint32_t*>(p + w.pos[i]);
   }
-  a.unit = reinterpret_cast<uint32_t*>(p + w.unit);
+  a.found = reinterpret_cast<EmUnits*>(p + w.found);
+  a.unit = reinterpret_cast<uint4*>(p + w.unit);
+  a.row = reinterpret_cast<uint4*>(p + w.row);
   a.count = reinterpret_cast<uint32_t*>(p + w.count);
   a.part = reinterpret_cast<float*>(p + w.part);
   return launched(launch_embedding_grad(a, (cudaStream_t)stream));

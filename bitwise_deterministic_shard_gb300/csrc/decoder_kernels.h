@@ -12,9 +12,13 @@ namespace detattn {
 constexpr int GL_FEW = 8;        // tokens up to which the weights are read once by plain loads
 
 struct GlArgs {
-  CUtensorMap a[2], b[2];        // operands of the pair products (see gated_kernels.cuh)
-  void* out[2];                  // forward: h; dx; or dWg and dWu
-  int64_t os[2];                 // their row strides
+  CUtensorMap x, wg, wu;         // boxes of 64 x 64
+  CUtensorMap dg, du;            // backward
+  void* h;                       // forward
+  void* dx;                      // backward; either may be null
+  void* dwg;
+  void* dwu;
+  int64_t hs, dxs, dwgs, dwus;   // row strides
   unsigned char* saved;          // forward: factors of the backward pass, or null
   int T, D, F;                   // tokens, width, hidden units
   int activation;
@@ -35,15 +39,15 @@ struct GlScaleArgs {             // dg = dh p, du = dh q
   void* dg;                      // [T, F], du behind it
   int64_t T, F;
 };
-// The saved factors p and q of [T, F]: the high 16 bits of each binary32 value (p's plane, q's plane), then the next 8.
-inline size_t gl_saved_bytes(int64_t T, int64_t F) { return (size_t)6 * T * F; }
+// The saved factors p and q of [T, F], in planes of rows of F rounded up to 16: the high 16 bits of each binary32 value of p,
+// those of q, then the next 8 bits of p, those of q.
+__host__ __device__ inline int64_t gl_saved_row(int64_t F) { return (F + 15) / 16 * 16; }
+__host__ __device__ inline size_t gl_saved_bytes(int64_t T, int64_t F) { return (size_t)6 * T * gl_saved_row(F); }
 
 template <bool BF>
 cudaError_t gl_forward(const GlArgs& a, cudaStream_t st);
 template <bool BF>
-cudaError_t gl_dx(const GlArgs& a, cudaStream_t st);
-template <bool BF>
-cudaError_t gl_dw(const GlArgs& a, cudaStream_t st);
+cudaError_t gl_backward(const GlArgs& a, cudaStream_t st);
 template <bool BF>
 cudaError_t gl_few(const GlFewArgs& a, cudaStream_t st);
 template <bool BF>
@@ -88,6 +92,12 @@ constexpr int EM_SMALL = 16384;  // tokens that one CTA sorts in shared memory
 constexpr int EM_BLOCK = 4096;   // tokens of a CTA of the passes of a longer sort
 constexpr int EM_BINS = 512;     // values of a digit
 
+constexpr int EM_FEW = 8;        // tokens of a short chunk
+constexpr uint32_t EM_MORE = 0x80000000u;   // of a chunk: one of several of its row
+struct EmUnits {
+  uint32_t few, many, rows;      // short chunks, long ones, rows of several
+};
+
 struct EmArgs {
   const void* ids;               // [n], int32 or int64
   int wide;                      // int64
@@ -101,10 +111,12 @@ struct EmArgs {
   int dtype;
   int* status;
   // workspace of the gradient
-  uint32_t* key[2];              // [n] ids in sorted order (rows: no gradient), and of the pass before
+  uint32_t* key[2];              // longer sorts: [n] ids in sorted order (rows: no gradient), and of the pass before
   uint32_t* pos[2];              // [n] their tokens
   uint32_t* count;               // longer sorts: [EM_BINS][blocks]
-  uint32_t* unit;                // [n]: tokens of the chunk that starts here, 0: none; bit 31: one of several
+  EmUnits* found;
+  uint4* unit;                   // [n]: chunks (first place, tokens and EM_MORE, row): short ones from the front, long ones from the back
+  uint4* row;                    // [n / EM_CHUNK + 1]: rows of several chunks (first place, end, row)
   float* part;                   // [2 (n / EM_CHUNK + 1)][cols] sums of such chunks
 };
 cudaError_t launch_embedding(const EmArgs& a, cudaStream_t st);

@@ -9,9 +9,13 @@
 // rows).  Up to 16384 tokens one CTA does that in shared memory while the others fill dw with zeros; longer ones take three
 // launches a pass, the zeros beside the first.  Each warp's rank of a token among those of its digit comes from a match over the
 // warp and its counters, so the order never depends on which thread came first.  Then a chunk of up to 64 tokens of a row is one
-// warp's chain of binary32 additions for each of its columns, in order of the tokens; rows of more leave their chunks' sums in the
+// chain of binary32 additions for each column, in order of the tokens; rows of more leave their chunks' sums in the
 // workspace, and a last kernel adds these, eight runs of chunks in order and then the eight.  So a row's bits depend on its own
-// tokens alone, and no atomics add values.
+// tokens alone, and no atomics add values (the lists of chunks are filled by atomics: their order is that of the work, not
+// of a sum).
+//
+// A warp takes a short chunk's 1024 16-bit columns at once (its loads are independent), a long one's 256 with eight tokens'
+// loads under way: with one column width for all, 16384 tokens of width 2048 took 64 us instead of ~20.
 #include <algorithm>
 
 #include "../../include/detattn.h"
@@ -21,8 +25,6 @@
 
 namespace detattn {
 namespace {
-
-constexpr uint32_t LONG = 0x80000000u;   // of a unit: one of several chunks of its row
 
 __device__ __forceinline__ int64_t id_at(const EmArgs& a, int64_t i) {
   return a.wide ? static_cast<const int64_t*>(a.ids)[i] : (int64_t) static_cast<const int32_t*>(a.ids)[i];
@@ -110,10 +112,70 @@ __device__ __forceinline__ uint32_t rank_of(uint32_t digit, bool& last) {
 constexpr int SORT_THREADS = 1024, SORT_WARPS = 32;
 struct SortSmall {
   uint32_t key[EM_SMALL];
-  uint16_t pos[2][EM_SMALL];
+  uint16_t pos0[EM_SMALL];
   uint16_t hist[SORT_WARPS][EM_BINS];
+  uint16_t pos1[EM_SMALL];          // in the end the sorted keys lie over the counters and the places no longer used
   uint32_t base[EM_BINS], warps[32];
+  EmUnits found;
 };
+static_assert(sizeof(uint16_t) * (EM_SMALL + SORT_WARPS * EM_BINS) == sizeof(uint32_t) * EM_SMALL, "room for the sorted keys");
+
+// What starts at place i of the sorted keys: a chunk of a row's tokens, or nothing.  Called by whole warps; the counters are atomics.
+__device__ __forceinline__ void find_chunk(const EmArgs& a, const uint32_t* key, int64_t i, int64_t n, EmUnits* found) {
+  uint32_t k = (uint32_t)a.rows, len = 0;
+  bool more = false, start = false;
+  int64_t end = i;
+  if (i < n) k = key[i];
+  if (k < a.rows) {
+    int64_t first = i;
+    bool is = true;
+    if (i > 0 && key[i - 1] == k) {
+      is = i >= EM_CHUNK && key[i - EM_CHUNK] == k;   // else within the first chunk
+      if (is) {                                       // the first place of k
+        int64_t lo = 0;
+        while (lo < first) {
+          const int64_t mid = (lo + first) >> 1;
+          if (key[mid] < k) lo = mid + 1;
+          else first = mid;
+        }
+        is = (i - first) % EM_CHUNK == 0;
+      }
+    }
+    if (is) {
+      start = i == first;
+      int64_t lo = i + 1;
+      end = min(n, i + EM_CHUNK);
+      more = !start || (i + EM_CHUNK < n && key[i + EM_CHUNK] == k);
+      while (lo < end) {   // the first place past k, at most a chunk on
+        const int64_t mid = (lo + end) >> 1;
+        if (key[mid] == k) lo = mid + 1;
+        else end = mid;
+      }
+      len = (uint32_t)(end - i);
+    }
+  }
+  const int lane = threadIdx.x & 31;
+  const auto place = [&](bool mine, uint32_t* counter) {   // of this lane's entry
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    uint32_t at = 0;
+    if (lane == 0 && who) at = atomicAdd(counter, __popc(who));
+    return __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+  };
+  const bool few = len > 0 && len <= EM_FEW && !more, many = len > 0 && !few;
+  const uint32_t f = place(few, &found->few), m = place(many, &found->many), r = place(many && more && start, &found->rows);
+  const uint4 unit = make_uint4((uint32_t)i, len | (more ? EM_MORE : 0), k, 0);
+  if (few) a.unit[f] = unit;
+  if (many) a.unit[n - 1 - m] = unit;
+  if (many && more && start) {
+    int64_t lo = i + EM_CHUNK, hi = n;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (key[mid] == k) lo = mid + 1;
+      else hi = mid;
+    }
+    a.row[r] = make_uint4((uint32_t)i, (uint32_t)hi, k, 0);
+  }
+}
 
 __global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_constant__ EmArgs a, int passes, int bits) {
   if (blockIdx.x > 0) {
@@ -129,8 +191,8 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_c
   for (int p = 0; p < passes; p++) {
     const int shift = p * bits;
     const uint32_t mask = (1u << bits) - 1;
-    const uint16_t* const from = s.pos[(p + 1) & 1];
-    uint16_t* const to = s.pos[p & 1];
+    const uint16_t* const from = p & 1 ? s.pos0 : s.pos1;
+    uint16_t* const to = p & 1 ? s.pos1 : s.pos0;
     for (int b = lane; b <= (int)mask; b += 32) s.hist[warp][b] = 0;
     __syncwarp();
     for (int i = i0; i < i1; i += 32) {
@@ -183,11 +245,17 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_c
     }
     __syncthreads();
   }
-  const uint16_t* const done = s.pos[(passes - 1) & 1];
+  const uint16_t* const done = passes & 1 ? s.pos0 : s.pos1;
+  uint32_t* const sorted = reinterpret_cast<uint32_t*>(passes & 1 ? &s.hist[0][0] : s.pos0);
+  if (tid == 0) s.found = {0, 0, 0};
   for (int i = tid; i < n; i += SORT_THREADS) {
     a.pos[0][i] = done[i];
-    a.key[0][i] = s.key[done[i]];
+    sorted[i] = s.key[done[i]];
   }
+  __syncthreads();
+  for (int i = warp * 32; i < n; i += SORT_THREADS) find_chunk(a, sorted, i + lane, n, &s.found);
+  __syncthreads();
+  if (tid == 0) *a.found = s.found;
 }
 
 // A pass over longer ones.  Counts of a block's digits (the first pass: from the ids; blocks past the tokens' fill zeros).
@@ -208,7 +276,8 @@ __global__ void __launch_bounds__(RADIX_THREADS) em_count_kernel(const __grid_co
   for (uint32_t b = threadIdx.x; b <= mask; b += RADIX_THREADS) a.count[(size_t)b * blocks + blockIdx.x] = hist[b];
 }
 // Places before each (digit, block): one CTA, a run of counts a thread.
-__global__ void __launch_bounds__(1024) em_scan_kernel(uint32_t* count, int64_t n) {
+__global__ void __launch_bounds__(1024) em_scan_kernel(uint32_t* count, int64_t n, EmUnits* found) {
+  if (threadIdx.x == 0) *found = {0, 0, 0};
   __shared__ uint32_t warps[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t per = (n + 1023) / 1024, i0 = min(n, tid * per), i1 = min(n, i0 + per);
@@ -281,163 +350,152 @@ __global__ void __launch_bounds__(RADIX_THREADS) em_scatter_kernel(const __grid_
   }
 }
 
-// ---- chunks: a row's sorted tokens from its first on, EM_CHUNK at a time ----
+// ---- chunks of longer ones ----
 __global__ void __launch_bounds__(256) em_chunk_kernel(const __grid_constant__ EmArgs a, int from) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.n) return;
-  const uint32_t* const key = a.key[from];
-  const uint32_t k = key[i];
-  uint32_t unit = 0;
-  if (k < a.rows) {
-    int64_t first = i;
-    if (i > 0 && key[i - 1] == k) {   // the first place of k
-      int64_t lo = 0;
-      while (lo < first) {
-        const int64_t mid = (lo + first) >> 1;
-        if (key[mid] < k) lo = mid + 1;
-        else first = mid;
-      }
-    }
-    if ((i - first) % EM_CHUNK == 0) {
-      int64_t end = min(a.n, i + EM_CHUNK), lo = i + 1;
-      const bool more = i > first || (i + EM_CHUNK < a.n && key[i + EM_CHUNK] == k);
-      while (lo < end) {   // the first place past k, at most a chunk on
-        const int64_t mid = (lo + end) >> 1;
-        if (key[mid] == k) lo = mid + 1;
-        else end = mid;
-      }
-      unit = (uint32_t)(end - i) | (more ? LONG : 0);
-    }
-  }
-  a.unit[i] = unit;
+  find_chunk(a, a.key[from], (int64_t)blockIdx.x * 256 + threadIdx.x, a.n, a.found);
 }
 // Where a chunk of several leaves its sum: full ones start at least a chunk apart, and so do the last ones of their rows.
 __device__ __forceinline__ int64_t slot_of(const EmArgs& a, int64_t i, uint32_t len) {
   return i / EM_CHUNK + (len < EM_CHUNK ? a.n / EM_CHUNK + 1 : 0);
 }
 
-// ---- sums: a warp a chunk's 32 runs (of 16 bytes, or 8 single elements a lane) ----
-template <typename T, bool AL>
-__global__ void __launch_bounds__(256) em_sum_kernel(const __grid_constant__ EmArgs a, int from, uint32_t pieces) {
-  constexpr int VEC = AL ? Elem<T>::VEC : 4, U = 8;
+// ---- sums ----
+// AL: runs of 16 bytes a lane; else of 4 single elements, neighbouring lanes' beside each other.  C runs of a chunk, R tokens' loads
+// under way.
+template <typename T, bool AL, int C, int R>
+__device__ __forceinline__ void sum_chunk(const EmArgs& a, uint4 unit, int64_t c0, int from) {
+  constexpr int VEC = AL ? Elem<T>::VEC : 4, STRIDE = AL ? 1 : 32;
   const int lane = threadIdx.x & 31;
-  const uint64_t w = ((uint64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
-  const int64_t i = w / pieces;
-  if (i >= a.n) return;
-  const uint32_t unit = a.unit[i], len = unit & ~LONG;
-  if (len == 0) return;
-  const int64_t c0 = (int64_t)(w % pieces) * 32 * VEC + (AL ? lane * VEC : lane);
+  const uint32_t len = unit.y & ~EM_MORE;
+  const uint32_t* const pos = a.pos[from] + unit.x;
+  uint32_t token[EM_CHUNK / 32];
+#pragma unroll
+  for (int i = 0; i < EM_CHUNK / 32; i++) token[i] = i * 32 + lane < len ? pos[i * 32 + lane] : 0;
+  c0 += AL ? lane * VEC : lane;
   const T* const dy = static_cast<const T*>(a.dy) + c0;
-  const uint32_t* const pos = a.pos[from] + i;
-  float sum[VEC];
+  const auto inside = [&](int c, int e) { return c0 + c * 32 * VEC + (AL ? 0 : 32 * e) < a.cols; };
+  float sum[C][VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; e++) sum[e] = 0.f;
-  if (c0 < a.cols) {
-    for (uint32_t j = 0; j < len; j += U) {
-      if constexpr (AL) {
-        Run<T, VEC> r[U];
+  for (int c = 0; c < C; c++)
 #pragma unroll
-        for (int u = 0; u < U; u++)
-          if (j + u < len) r[u].load(dy + (int64_t)pos[j + u] * a.ys);
+    for (int e = 0; e < VEC; e++) sum[c][e] = 0.f;
+  for (uint32_t j = 0; j < len; j += R) {
+    const T* at[R];
 #pragma unroll
-        for (int u = 0; u < U; u++)
-          if (j + u < len) {
-#pragma unroll
-            for (int e = 0; e < VEC; e++) sum[e] += r[u].get(e);
-          }
-      } else {
-        T r[U][VEC];
-#pragma unroll
-        for (int u = 0; u < U; u++)
-          if (j + u < len) {
-            const T* const at = dy + (int64_t)pos[j + u] * a.ys;
-#pragma unroll
-            for (int e = 0; e < VEC; e++) r[u][e] = c0 + 32 * e < a.cols ? at[32 * e] : Elem<T>::put(0.f);
-          }
-#pragma unroll
-        for (int u = 0; u < U; u++)
-          if (j + u < len) {
-#pragma unroll
-            for (int e = 0; e < VEC; e++) sum[e] += Elem<T>::get(r[u][e]);
-          }
-      }
+    for (int u = 0; u < R; u++) {
+      const uint32_t t = j + u;
+      at[u] = dy + (int64_t)__shfl_sync(0xffffffffu, t < 32 ? token[0] : token[1], t & 31) * a.ys;
     }
-    if (unit & LONG) {
-      float* const to = a.part + slot_of(a, i, len) * a.cols + c0;
+    if constexpr (AL) {
+      Run<T, VEC> r[R][C];
+#pragma unroll
+      for (int u = 0; u < R; u++)
+#pragma unroll
+        for (int c = 0; c < C; c++)
+          if (j + u < len && inside(c, 0)) r[u][c].load(at[u] + c * 32 * VEC);
+          else r[u][c].zero();
+#pragma unroll
+      for (int u = 0; u < R; u++)
+        if (j + u < len) {
+#pragma unroll
+          for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int e = 0; e < VEC; e++) sum[c][e] += r[u][c].get(e);
+        }
+    } else {
+      T r[R][C][VEC];
+#pragma unroll
+      for (int u = 0; u < R; u++)
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+          for (int e = 0; e < VEC; e++) r[u][c][e] = j + u < len && inside(c, e) ? at[u][c * 128 + 32 * e] : Elem<T>::put(0.f);
+#pragma unroll
+      for (int u = 0; u < R; u++)
+        if (j + u < len) {
+#pragma unroll
+          for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int e = 0; e < VEC; e++) sum[c][e] += Elem<T>::get(r[u][c][e]);
+        }
+    }
+  }
+  static_assert(EM_CHUNK == 64, "two words of tokens a lane");
+  if (unit.y & EM_MORE) {
+    float* const to = a.part + slot_of(a, unit.x, len) * a.cols + c0;
+#pragma unroll
+    for (int c = 0; c < C; c++)
 #pragma unroll
       for (int e = 0; e < VEC; e++)
-        if (AL || c0 + 32 * e < a.cols) to[AL ? e : 32 * e] = sum[e];
+        if (inside(c, e)) to[c * 32 * VEC + e * STRIDE] = sum[c][e];
+    return;
+  }
+  T* const to = static_cast<T*>(a.dw) + (int64_t)unit.z * a.ws + c0;
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+#pragma unroll
+    for (int e = 0; e < VEC; e++) sum[c][e] *= a.scale;
+    if constexpr (AL) {
+      Run<T, VEC> o;
+      o.set(sum[c]);
+      if (inside(c, 0)) o.store(to + c * 32 * VEC);
     } else {
-      T* const to = static_cast<T*>(a.dw) + (int64_t)a.key[from][i] * a.ws + c0;
 #pragma unroll
-      for (int e = 0; e < VEC; e++) sum[e] *= a.scale;
-      if constexpr (AL) {
-        Run<T, VEC> o;
-        o.set(sum);
-        o.store(to);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; e++)
-          if (c0 + 32 * e < a.cols) to[32 * e] = Elem<T>::put(sum[e]);
-      }
+      for (int e = 0; e < VEC; e++)
+        if (inside(c, e)) to[c * 128 + 32 * e] = Elem<T>::put(sum[c][e]);
     }
   }
 }
+constexpr int SUM_CTAS = 152 * 4;
+template <typename T, bool AL>
+__global__ void __launch_bounds__(256, 3) em_sum_kernel(const __grid_constant__ EmArgs a, int from) {
+  constexpr int RUN = 32 * (AL ? Elem<T>::VEC : 4), WIDE = 4;
+  const EmUnits found = *a.found;
+  const int64_t narrow = (a.cols + RUN - 1) / RUN, wide = (a.cols + WIDE * RUN - 1) / (WIDE * RUN);
+  const int64_t many = found.many * narrow, all = many + found.few * wide, warps = (int64_t)gridDim.x * 8;
+  for (int64_t w = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5; w < all; w += warps) {   // the long ones first
+    if (w < many) sum_chunk<T, AL, 1, 8>(a, a.unit[a.n - 1 - w / narrow], (w % narrow) * RUN, from);
+    else sum_chunk<T, AL, WIDE, 2>(a, a.unit[(w - many) / wide], ((w - many) % wide) * (WIDE * RUN), from);
+  }
+}
 
-// ---- rows of several chunks: a CTA 32 columns, its eight warps a run of the chunks each ----
+// ---- rows of several chunks: a CTA 128 columns of one, its eight warps a run of the chunks each ----
 template <typename T>
-__global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ EmArgs a, int from) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ EmArgs a) {
+  __shared__ float sums[8][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the first of several chunks is full, and such ones start at least a chunk apart: at most one within EM_CHUNK places
-  const int64_t i0 = (int64_t)blockIdx.x * EM_CHUNK;
-  const uint32_t* const key = a.key[from];
-  int64_t first = -1;
-  for (int j = 0; j < EM_CHUNK; j += 32) {
-    const int64_t i = i0 + j + lane;
-    const bool is = i < a.n && a.unit[i] == (EM_CHUNK | LONG) && (i == 0 || key[i - 1] != key[i]);
-    const uint32_t who = __ballot_sync(0xffffffffu, is);
-    if (who) first = i0 + j + __ffs(who) - 1;
-  }
-  if (first < 0) return;
-  // chunks of this row: they follow each other, the last one may be shorter
-  const uint32_t k = key[first];
-  int64_t lo = first + EM_CHUNK, end = a.n;
-  while (lo < end) {
-    const int64_t mid = (lo + end) >> 1;
-    if (key[mid] == k) lo = mid + 1;
-    else end = mid;
-  }
-  const int64_t chunks = (end - first + EM_CHUNK - 1) / EM_CHUNK, per = (chunks + 7) / 8;
-  const int64_t q0 = min(chunks, warp * per), q1 = min(chunks, q0 + per);
-  for (int64_t c0 = (int64_t)blockIdx.y * 32; c0 < a.cols; c0 += (int64_t)gridDim.y * 32) {
-    const int64_t c = c0 + lane;
-    float sum = 0.f;
-    if (c < a.cols) {
-      int64_t q = q0;
-      for (; q + 8 <= q1; q += 8) {
-        float v[8];
+  const int64_t pieces = (a.cols + 127) / 128, all = a.found->rows * pieces;
+  for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
+    const uint4 row = a.row[w / pieces];
+    const int64_t c0 = (w % pieces) * 128 + lane, first = row.x, end = row.y;
+    const int64_t chunks = (end - first + EM_CHUNK - 1) / EM_CHUNK, per = (chunks + 7) / 8;
+    const int64_t q0 = min(chunks, warp * per), q1 = min(chunks, q0 + per);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t q = q0; q < q1; q += 4) {
+      float v[4][4];
 #pragma unroll
-        for (int u = 0; u < 8; u++) {
-          const int64_t i = first + (q + u) * EM_CHUNK;
-          v[u] = a.part[slot_of(a, i, (uint32_t)min((int64_t)EM_CHUNK, end - i)) * a.cols + c];
-        }
+      for (int u = 0; u < 4; u++) {
+        const int64_t i = first + (q + u) * EM_CHUNK;
+        const float* const at = a.part + slot_of(a, i, (uint32_t)min((int64_t)EM_CHUNK, end - i)) * a.cols + c0;
 #pragma unroll
-        for (int u = 0; u < 8; u++) sum += v[u];
+        for (int e = 0; e < 4; e++) v[u][e] = q + u < q1 && c0 + 32 * e < a.cols ? at[32 * e] : 0.f;
       }
-      for (; q < q1; q++) {
-        const int64_t i = first + q * EM_CHUNK;
-        sum += a.part[slot_of(a, i, (uint32_t)min((int64_t)EM_CHUNK, end - i)) * a.cols + c];
-      }
+#pragma unroll
+      for (int u = 0; u < 4; u++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if (q + u < q1) sum[e] += v[u][e];
     }
     __syncthreads();
-    sums[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && c < a.cols) {
-      float all = sums[0][lane];
 #pragma unroll
-      for (int w = 1; w < 8; w++) all += sums[w][lane];
-      static_cast<T*>(a.dw)[(int64_t)k * a.ws + c] = Elem<T>::put(all * a.scale);
+    for (int e = 0; e < 4; e++) sums[warp][32 * e + lane] = sum[e];
+    __syncthreads();
+    const int64_t c = (w % pieces) * 128 + threadIdx.x;
+    if (threadIdx.x < 128 && c < a.cols) {
+      float total = sums[0][threadIdx.x];
+#pragma unroll
+      for (int k = 1; k < 8; k++) total += sums[k][threadIdx.x];
+      static_cast<T*>(a.dw)[(int64_t)row.z * a.ws + c] = Elem<T>::put(total * a.scale);
     }
   }
 }
@@ -454,12 +512,11 @@ cudaError_t lookup(const EmArgs& a, cudaStream_t st) {
 }
 template <typename T, bool AL>
 cudaError_t sums(const EmArgs& a, int from, cudaStream_t st) {
-  const int64_t run = 32 * (AL ? Elem<T>::VEC : 4), pieces = (a.cols + run - 1) / run;
-  em_sum_kernel<T, AL><<<(unsigned)((a.n * pieces + 7) / 8), 256, 0, st>>>(a, from, (uint32_t)pieces);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.n <= EM_CHUNK) return e;
-  const dim3 grid((unsigned)((a.n + EM_CHUNK - 1) / EM_CHUNK), (unsigned)std::min<int64_t>((a.cols + 31) / 32, 64));
-  em_join_kernel<T><<<grid, 256, 0, st>>>(a, from);
+  constexpr int RUN = 32 * (AL ? Elem<T>::VEC : 4);
+  const int64_t most = a.n * ((a.cols + RUN - 1) / RUN);   // warps' items
+  em_sum_kernel<T, AL><<<(unsigned)std::min<int64_t>(SUM_CTAS, (most + 7) / 8), 256, 0, st>>>(a, from);
+  if (a.n > EM_CHUNK)
+    em_join_kernel<T><<<(unsigned)std::min<int64_t>(152 * 2, a.n / EM_CHUNK * ((a.cols + 127) / 128)), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
@@ -498,12 +555,12 @@ cudaError_t launch_embedding_grad(const EmArgs& a, cudaStream_t st) {
     for (int p = 0; p < passes; p++) {
       const int src = p ? (p + 1) & 1 : -1, dst = p & 1, shift = p * bits;
       em_count_kernel<<<blocks + (p ? 0 : fill), RADIX_THREADS, 0, st>>>(a, blocks, src, shift, bits);
-      em_scan_kernel<<<1, 1024, 0, st>>>(a.count, (int64_t)blocks << bits);
+      em_scan_kernel<<<1, 1024, 0, st>>>(a.count, (int64_t)blocks << bits, a.found);
       em_scatter_kernel<<<blocks, RADIX_THREADS, 0, st>>>(a, blocks, src, dst, shift, bits);
       from = dst;
     }
+    em_chunk_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, st>>>(a, from);
   }
-  em_chunk_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, st>>>(a, from);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.dtype == DA_F32) return gradient<float>(a, from, st);
   return a.dtype == DA_BF16 ? gradient<__nv_bfloat16>(a, from, st) : gradient<__half>(a, from, st);

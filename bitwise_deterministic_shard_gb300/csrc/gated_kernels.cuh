@@ -4,13 +4,14 @@
 //   dg = dh p,  du = dh q,  p = act'(g) u,  q = act(g)
 //   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
 //
-// Forward: one kernel of pair products (gemm_pair.cuh).  The 256 rows of its second operand are 128 rows of Wg (one CTA's half)
-// and the same 128 of Wu (the other's), so g and u of a token and hidden unit lie in one TMEM lane, 128 columns apart,
+// Forward: one kernel of pair products (gemm_pair.cuh).  Half the rows of its second operand are rows of Wg (one CTA's half)
+// and the other half the same rows of Wu, so g and u of a token and hidden unit lie in one TMEM lane, half a tile apart,
 // and a thread forms h from them.  For the backward pass it also writes p and q, the only values of the activation that the
 // gradient needs: 24 bits of each (2^-15 of the value left out), as 16 would add a rounding of the size of the result's own to dg
-// and du (dx then 2.9e-3 off in bf16 instead of 2.4e-3; 1.7e-3 is a result only rounded).
-// Backward: dg and du as one pass over dh, p and q, rounded to 16 bits (the tensor cores take operands of one 16-bit type), then two
-// kernels of pair products: dx contracts over both halves of [dg | du] in one chain, dW has the tiles of both weights.
+// and du (dx then 2.9e-3 off in bf16 instead of 2.35e-3; 1.66e-3 is a result only rounded).
+// Backward: dg and du as one pass over dh, p and q, rounded to 16 bits (the tensor cores take operands of one 16-bit type), then one
+// kernel of pair products: dx contracts over both halves of [dg | du] in one chain, dW has the tiles of both weights; the
+// longer tiles come first and the shorter ones fill the pairs up.
 //
 // Up to 8 tokens the forward pass reads the weights once with plain loads instead: a warp a hidden unit.
 #pragma once
@@ -53,143 +54,223 @@ __device__ __forceinline__ void activate(float g, float& a, float& d) {
   }
 }
 
+// copies of N boxes of 64 rows from row r on, contracted elements [k, k + 64): K-major
+template <int N>
+__device__ __forceinline__ void copy_k(uint32_t to, const CUtensorMap* m, int k, int r, uint32_t bar) {
+#pragma unroll
+  for (int i = 0; i < N; i++) pair::load2(to + i * pair::BOX, m, k, r + 64 * i, bar);
+}
+// and of N panels of 64 columns from c on: MN-major
+template <int N>
+__device__ __forceinline__ void copy_mn(uint32_t to, const CUtensorMap* m, int k, int c, uint32_t bar) {
+#pragma unroll
+  for (int i = 0; i < N; i++) pair::load2(to + i * pair::BOX, m, c + 64 * i, k, bar);
+}
+
 // ---- forward ----
-template <bool BF, int ACT, bool SAVE>
+// The factors' rows are staged in shared memory, 32 columns at a time, and written 64 bytes a row by neighbouring lanes: a
+// lane that wrote its own row's pieces would touch 32 lines an instruction (8192 tokens, width 2048, 8192 hidden units: 555 us; the
+// products alone take 300).
+template <bool SAVE>
+constexpr int STAGED = SAVE ? pair::TAKERS * 4096 : 0;   // bytes
+
+// 32 rows of 8 units of 16 bytes, unit u of row r at u ^ (r % 8)
+__device__ __forceinline__ void stage_put(uint32_t stage, int r, int u, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + r * 128 + ((u ^ (r & 7)) << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 stage_get(uint32_t stage, int r, int u) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(stage + r * 128 + ((u ^ (r & 7)) << 4))
+               : "memory");
+  return v;
+}
+// the high halves of 8 binary32 values; the bytes below them of 16
+__device__ __forceinline__ uint4 high_halves(const float* v) {
+  const auto two = [&](int i) { return __byte_perm(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), 0x7632); };
+  return make_uint4(two(0), two(2), two(4), two(6));
+}
+__device__ __forceinline__ uint4 next_bytes(const float* v) {
+  const auto four = [&](int i) {
+    return __byte_perm(__byte_perm(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), 0x0051),
+                       __byte_perm(__float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]), 0x0051), 0x5410);
+  };
+  return make_uint4(four(0), four(4), four(8), four(12));
+}
+
+template <bool BF, int ACT, bool SAVE, int TN>
 __global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl_fwd_kernel(const __grid_constant__ GlArgs a) {
   using namespace tc5;
   extern __shared__ unsigned char raw[];
   __shared__ pair::Shared sh;
-  const int mt = (a.T + 255) / 256, nt = (a.F + 127) / 128, steps = (a.D + pair::BK - 1) / pair::BK;
+  constexpr int HALF = TN / 2;
+  const int mt = (a.T + 255) / 256, nt = (a.F + HALF - 1) / HALF, steps = (a.D + pair::BK - 1) / pair::BK;
   const uint32_t rank = pair::cta_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const size_t n = (size_t)a.T * a.F;
-  pair::run<BF, false, false>(
-      sh, raw, mt * nt, steps, a.status,
-      [&](int t, int k, uint32_t A, uint32_t B, uint32_t bar) {
-        const int2 at = pair::tile_of(t, mt, nt);
-        pair::load2(A, &a.a[0], k * pair::BK, at.x * 256 + rank * 128, bar);
-        pair::load2(B, &a.b[rank], k * pair::BK, at.y * 128, bar);
+  const CUtensorMap* const w = rank ? &a.wu : &a.wg;
+  pair::run<BF, TN, STAGED<SAVE>, false>(
+      sh, raw, a.status,
+      [&](int j) {
+        const int t = (int)(blockIdx.x >> 1) + j * (int)(gridDim.x >> 1);
+        return t < mt * nt ? pair::tile_of(t, mt, nt, 0, steps) : pair::Tile{0, 0, 0, 0};
       },
-      [&](int t, uint32_t tm, auto release) {
-        const int2 at = pair::tile_of(t, mt, nt);
-        const int row = at.x * 256 + rank * 128 + (warp & 3) * 32 + lane;
+      [](int) { return false; },
+      [&](const pair::Tile& t, int k, uint32_t A, uint32_t B, uint32_t bar) {
+        copy_k<2>(A, &a.x, k * pair::BK, t.m * 256 + rank * 128, bar);
+        copy_k<HALF / 64>(B, w, k * pair::BK, t.n * HALF, bar);
+      },
+      [&](const pair::Tile& t, uint32_t tm, uint32_t extra, auto release) {
+        const int row0 = t.m * 256 + rank * 128 + (warp & 3) * 32, row = row0 + lane;
+        const uint32_t stage = extra + warp * 4096;
+        uint16_t* const h = static_cast<uint16_t*>(a.h);
+        const int64_t fp = gl_saved_row(a.F), n = a.T * fp;
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          const int cc = (warp >> 2) * 64 + c, col = at.y * 128 + cc;   // columns of the tile and of h
+        for (int c = 0; c < HALF / 2; c += 32) {
+          const int cc = (warp >> 2) * (HALF / 2) + c, col = t.n * HALF + cc;   // columns of the tile and of h
           float g[32], u[32];
           __syncwarp();   // the loads are the whole warp's
           ld_x32(tm + cc, g);
-          ld_x32(tm + 128 + cc, u);
+          ld_x32(tm + HALF + cc, u);
           ld_wait();
-          if (c == 32) release();
-          if (row >= a.T) continue;
-          uint32_t h[16];
-          const size_t out = (size_t)row * a.F + col;
+          if (c == HALF / 2 - 32) release();
+          if (row0 >= a.T || col >= a.F) continue;   // the same in all lanes
+          float q[32];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float p[8], q[8];
+          for (int e = 0; e < 32; e++) {
+            float d;
+            activate<ACT>(g[e], q[e], d);
+            g[e] = q[e] * u[e];
+            u[e] *= d;
+          }
+          const auto units = [&](int j) {
+            return make_uint4(pack16<BF>(g[8 * j], g[8 * j + 1]), pack16<BF>(g[8 * j + 2], g[8 * j + 3]),
+                              pack16<BF>(g[8 * j + 4], g[8 * j + 5]), pack16<BF>(g[8 * j + 6], g[8 * j + 7]));
+          };
+          if constexpr (SAVE) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-              float d;
-              activate<ACT>(g[e + i], q[i], d);
-              p[i] = d * u[e + i];
-              g[e + i] = q[i] * u[e + i];
+            for (int j = 0; j < 4; j++) {
+              stage_put(stage, lane, j, units(j));
+              stage_put(stage, lane, 4 + j, high_halves(u + 8 * j));
             }
+            __syncwarp();
+            const int un = lane & 7, at = col + (un & 3) * 8;
 #pragma unroll
-            for (int i = 0; i < 4; i++) h[e / 2 + i] = pack16<BF>(g[e + 2 * i], g[e + 2 * i + 1]);
-            if (col + e >= a.F) continue;
-            if constexpr (SAVE) {
-#pragma unroll
-              for (int w = 0; w < 2; w++) {
-                const float* const v = w ? q : p;
-                uint32_t hi[4], lo[2];
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                  hi[i] = __byte_perm(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]), 0x7632);
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-                  lo[i] = __byte_perm(__byte_perm(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), 0x0051),
-                                      __byte_perm(__float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]), 0x0051), 0x5410);
-                *reinterpret_cast<uint4*>(a.saved + 2 * (w * n + out + e)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint2*>(a.saved + 4 * n + w * n + out + e) = make_uint2(lo[0], lo[1]);
+            for (int it = 0; it < 8; it++) {
+              const int r = it * 4 + (lane >> 3);
+              const uint4 v = stage_get(stage, r, un);
+              if (row0 + r < a.T && at < a.F) {
+                if (un < 4) *reinterpret_cast<uint4*>(h + (row0 + r) * a.hs + at) = v;
+                else *reinterpret_cast<uint4*>(a.saved + 2 * ((row0 + r) * fp + at)) = v;
               }
             }
-            uint4* const to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[0]) + (size_t)row * a.os[0] + col + e);
-            *to = make_uint4(h[e / 2], h[e / 2 + 1], h[e / 2 + 2], h[e / 2 + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; j++) stage_put(stage, lane, j, high_halves(q + 8 * j));
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+              stage_put(stage, lane, 4 + j, next_bytes(u + 16 * j));
+              stage_put(stage, lane, 6 + j, next_bytes(q + 16 * j));
+            }
+            __syncwarp();
+            const int lo = col + (un & 1) * 16;
+#pragma unroll
+            for (int it = 0; it < 8; it++) {
+              const int r = it * 4 + (lane >> 3);
+              const uint4 v = stage_get(stage, r, un);
+              if (row0 + r < a.T) {
+                if (un < 4) {
+                  if (at < a.F) *reinterpret_cast<uint4*>(a.saved + 2 * (n + (row0 + r) * fp + at)) = v;
+                } else if (lo < a.F) {
+                  *reinterpret_cast<uint4*>(a.saved + 4 * n + (un < 6 ? 0 : n) + (row0 + r) * fp + lo) = v;
+                }
+              }
+            }
+          } else if (row < a.T) {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              if (col + 8 * j < a.F) *reinterpret_cast<uint4*>(h + row * a.hs + col + 8 * j) = units(j);
           }
         }
       });
 }
 
-// One thread's row of a tile of a plain product: columns [c0, c0 + 128) of the tile.
-template <bool BF, typename Release>
-__device__ __forceinline__ void take_row(uint32_t tm, int c0, uint16_t* out, bool live, int left, Release release) {
+// ---- backward: dx [T, D] = [dg | du] [Wg; Wu] (dg, du K-major), dW [F, D] = dg^T x and du^T x (dg, du MN-major) ----
+// Of na long and nb short tiles, how many steps: each pair takes every P-th long one; the pairs that this leaves short take
+// short ones until they are level (q each), then all pairs do by turns.
+struct Shares {
+  int na, nb, q;
+};
+__device__ __forceinline__ int share(const Shares& s, int j, int p, int P) {   // the pair's j-th tile, -1: none
+  const int r = s.na % P, mine = s.na / P + (p < r);
+  if (j < mine) return j * P + p;
+  j -= mine;
+  int k;
+  if (r == 0) k = j * P + p;
+  else if (p < r) k = s.q * (P - r) + j * P + P - r + p;
+  else if (j < s.q) k = j * (P - r) + p - r;
+  else k = s.q * (P - r) + (j - s.q) * P + p - r;
+  return k < s.nb ? s.na + k : -1;
+}
+
+enum { DX = 0, DW = 1 };
+template <bool BF, int TN>
+__global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl_bwd_kernel(const __grid_constant__ GlArgs a) {
   using namespace tc5;
-#pragma unroll
-  for (int c = 0; c < 128; c += 32) {
-    float v[32];
-    __syncwarp();   // the loads are the whole warp's
-    ld_x32(tm + c0 + c, v);
-    ld_wait();
-    if (c == 96) release();
-    if (!live) continue;
-#pragma unroll
-    for (int e = 0; e < 32; e += 8)
-      if (c0 + c + e < left)
-        *reinterpret_cast<uint4*>(out + c0 + c + e) =
-            make_uint4(pack16<BF>(v[e], v[e + 1]), pack16<BF>(v[e + 2], v[e + 3]), pack16<BF>(v[e + 4], v[e + 5]),
-                       pack16<BF>(v[e + 6], v[e + 7]));
-  }
-}
-
-// ---- dx [T, D] = [dg | du] [Wg; Wu]: a: dg and du (K-major), b: Wg and Wu (MN-major) ----
-template <bool BF>
-__global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl_dx_kernel(const __grid_constant__ GlArgs a) {
   extern __shared__ unsigned char raw[];
   __shared__ pair::Shared sh;
-  const int mt = (a.T + 255) / 256, nt = (a.D + 255) / 256, half = (a.F + pair::BK - 1) / pair::BK;
+  const int tt = (a.T + 255) / 256, ft = (a.F + 255) / 256, nt = (a.D + TN - 1) / TN, half = (a.F + pair::BK - 1) / pair::BK;
+  const int nx = a.dx ? tt * nt : 0, nw = a.dwg ? 2 * ft * nt : 0, sx = 2 * half, sw = (a.T + pair::BK - 1) / pair::BK;
+  const bool x_first = sx >= sw;
+  const Shares shares = x_first ? Shares{nx, nw, sx / sw} : Shares{nw, nx, sw / sx};
   const uint32_t rank = pair::cta_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pair::run<BF, false, true>(
-      sh, raw, mt * nt, 2 * half, a.status,
-      [&](int t, int k, uint32_t A, uint32_t B, uint32_t bar) {
-        const int2 at = pair::tile_of(t, mt, nt);
-        const int w = k >= half, k0 = (k - w * half) * pair::BK, c = at.y * 256 + rank * 128;
-        pair::load2(A, &a.a[w], k0, at.x * 256 + rank * 128, bar);
-        pair::load2(B, &a.b[w], c, k0, bar);
-        pair::load2(B + pair::HALF / 2, &a.b[w], c + 64, k0, bar);
+  pair::run<BF, TN, 0, true>(
+      sh, raw, a.status,
+      [&](int j) {
+        const int t = share(shares, j, blockIdx.x >> 1, gridDim.x >> 1);
+        if (t < 0) return pair::Tile{0, 0, 0, 0};
+        const bool first = t < shares.na;
+        const int i = first ? t : t - shares.na;
+        return first == x_first ? pair::tile_of(i, tt, nt, DX, sx) : pair::tile_of(i, 2 * ft, nt, DW, sw);
       },
-      [&](int t, uint32_t tm, auto release) {
-        const int2 at = pair::tile_of(t, mt, nt);
-        const int row = at.x * 256 + rank * 128 + (warp & 3) * 32 + lane;
-        uint16_t* const out = static_cast<uint16_t*>(a.out[0]) + (size_t)row * a.os[0] + at.y * 256;
-        take_row<BF>(tm, (warp >> 2) * 128, out, row < a.T, a.D - at.y * 256, release);
-      });
-}
-
-// ---- dWg, dWu [F, D] = dg^T x, du^T x: a: dg and du (MN-major), b: x (MN-major) ----
-template <bool BF>
-__global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl_dw_kernel(const __grid_constant__ GlArgs a) {
-  extern __shared__ unsigned char raw[];
-  __shared__ pair::Shared sh;
-  const int half = (a.F + 255) / 256, mt = 2 * half, nt = (a.D + 255) / 256, steps = (a.T + pair::BK - 1) / pair::BK;
-  const uint32_t rank = pair::cta_rank();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pair::run<BF, true, true>(
-      sh, raw, mt * nt, steps, a.status,
-      [&](int t, int k, uint32_t A, uint32_t B, uint32_t bar) {
-        const int2 at = pair::tile_of(t, mt, nt);
-        const int w = at.x >= half, r = (at.x - w * half) * 256 + rank * 128, c = at.y * 256 + rank * 128;
-        pair::load2(A, &a.a[w], r, k * pair::BK, bar);
-        pair::load2(A + pair::HALF / 2, &a.a[w], r + 64, k * pair::BK, bar);
-        pair::load2(B, &a.b[0], c, k * pair::BK, bar);
-        pair::load2(B + pair::HALF / 2, &a.b[0], c + 64, k * pair::BK, bar);
+      [](int kind) { return kind == DW; },
+      [&](const pair::Tile& t, int k, uint32_t A, uint32_t B, uint32_t bar) {
+        const int c = t.n * TN + rank * (TN / 2);
+        if (t.kind == DX) {
+          const bool u = k >= half;
+          const int k0 = (u ? k - half : k) * pair::BK;
+          copy_k<2>(A, u ? &a.du : &a.dg, k0, t.m * 256 + rank * 128, bar);
+          copy_mn<TN / 128>(B, u ? &a.wu : &a.wg, k0, c, bar);
+        } else {
+          const bool u = t.m >= ft;
+          copy_mn<2>(A, u ? &a.du : &a.dg, k * pair::BK, (u ? t.m - ft : t.m) * 256 + rank * 128, bar);
+          copy_mn<TN / 128>(B, &a.x, k * pair::BK, c, bar);
+        }
       },
-      [&](int t, uint32_t tm, auto release) {
-        const int2 at = pair::tile_of(t, mt, nt);
-        const int w = at.x >= half, row = (at.x - w * half) * 256 + rank * 128 + (warp & 3) * 32 + lane;
-        uint16_t* const out = static_cast<uint16_t*>(a.out[w]) + (size_t)row * a.os[w] + at.y * 256;
-        take_row<BF>(tm, (warp >> 2) * 128, out, row < a.F, a.D - at.y * 256, release);
+      [&](const pair::Tile& t, uint32_t tm, uint32_t, auto release) {
+        const bool u = t.kind == DW && t.m >= ft;
+        const int row = (u ? t.m - ft : t.m) * 256 + rank * 128 + (warp & 3) * 32 + lane;
+        const bool live = row < (t.kind == DX ? a.T : a.F);
+        uint16_t* const out = static_cast<uint16_t*>(t.kind == DX ? a.dx : u ? a.dwu : a.dwg) +
+                              row * (t.kind == DX ? a.dxs : u ? a.dwus : a.dwgs);
+#pragma unroll
+        for (int c = 0; c < TN / 2; c += 32) {
+          const int cc = (warp >> 2) * (TN / 2) + c, col = t.n * TN + cc;
+          float v[32];
+          __syncwarp();   // the loads are the whole warp's
+          ld_x32(tm + cc, v);
+          ld_wait();
+          if (c == TN / 2 - 32) release();
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              if (col + e < a.D)
+                *reinterpret_cast<uint4*>(out + col + e) = make_uint4(pack16<BF>(v[e], v[e + 1]), pack16<BF>(v[e + 2], v[e + 3]),
+                                                                      pack16<BF>(v[e + 4], v[e + 5]), pack16<BF>(v[e + 6], v[e + 7]));
+          }
+        }
       });
 }
 
@@ -252,15 +333,16 @@ __global__ void __launch_bounds__(256) gl_few_kernel(const GlFewArgs a) {
 template <bool BF>
 __global__ void __launch_bounds__(256) gl_scale_kernel(const GlScaleArgs a) {
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-  const int64_t n = a.T * a.F, per = a.F / 8, all = n / 8;
+  const int64_t fp = gl_saved_row(a.F), n = a.T * fp, per = a.F / 8, all = a.T * per;
   T* const dg = static_cast<T*>(a.dg);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per, col = (i - row * per) * 8, at = row * fp + col;
     Run<T, 8> r;
-    r.load(static_cast<const T*>(a.dh) + (i / per) * a.ds + (i % per) * 8);
+    r.load(static_cast<const T*>(a.dh) + row * a.ds + col);
 #pragma unroll
     for (int w = 0; w < 2; w++) {
-      const uint4 hi = *reinterpret_cast<const uint4*>(a.saved + 2 * (w * n + 8 * i));
-      const uint2 lo = *reinterpret_cast<const uint2*>(a.saved + 4 * n + w * n + 8 * i);
+      const uint4 hi = *reinterpret_cast<const uint4*>(a.saved + 2 * (w * n + at));
+      const uint2 lo = *reinterpret_cast<const uint2*>(a.saved + 4 * n + w * n + at);
       const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
       float v[8];
 #pragma unroll
@@ -268,34 +350,38 @@ __global__ void __launch_bounds__(256) gl_scale_kernel(const GlScaleArgs a) {
         v[e] = r.get(e) * __uint_as_float((h[e >> 1] >> (16 * (e & 1)) << 16) | ((e < 4 ? lo.x : lo.y) >> (8 * (e & 3)) & 255) << 8);
       Run<T, 8> o;
       o.set(v);
-      o.store(dg + w * n + 8 * i);
+      o.store(dg + w * a.T * a.F + 8 * i);
     }
   }
 }
 
-inline cudaError_t pairs_of_device(int* n) {
-  int device;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, device);
-  *n /= 2;
-  return e;
-}
-
-template <typename K, typename A>
-cudaError_t launch_pairs(DeviceOnce& once, K kernel, int64_t tiles, const A& a, cudaStream_t st) {
-  if (tiles == 0) return cudaSuccess;
-  int pairs;
-  cudaError_t e = pairs_of_device(&pairs);
-  if (e == cudaSuccess) e = allow_smem(once, kernel, pair::SMEM);
+template <typename K>
+cudaError_t launch_pairs(DeviceOnce& once, K kernel, int smem, int64_t tiles, int pairs, const GlArgs& a, cudaStream_t st) {
+  const cudaError_t e = allow_smem(once, kernel, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<2 * (int)(tiles < pairs ? tiles : pairs), pair::THREADS, pair::SMEM, st>>>(a);
+  kernel<<<2 * (int)(tiles < pairs ? tiles : pairs), pair::THREADS, smem, st>>>(a);
   return cudaGetLastError();
 }
+constexpr int PAIRS = 152 / 2;   // of the GPU this is written for: the choice of the tile, and with it no bit, depends on it
 
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <bool BF, int ACT, bool SAVE, int TN>
+cudaError_t forward_as(const GlArgs& a, int64_t tiles, cudaStream_t st) {
+  static DeviceOnce once;
+  return launch_pairs(once, gl_fwd_kernel<BF, ACT, SAVE, TN>, pair::Ring<TN, STAGED<SAVE>>::SMEM, tiles, PAIRS, a, st);
+}
+// The tile: rounds of pairs times a tile's time, a narrow one 0.6 of a wide one (its products take half, its copies 0.75).
 template <bool BF, int ACT, bool SAVE>
 cudaError_t forward_of(const GlArgs& a, cudaStream_t st) {
+  const int64_t mt = ceil_div(a.T, 256), wide = mt * ceil_div(a.F, 128), narrow = mt * ceil_div(a.F, 64);
+  if (5 * ceil_div(wide, PAIRS) > 3 * ceil_div(narrow, PAIRS)) return forward_as<BF, ACT, SAVE, 128>(a, narrow, st);
+  return forward_as<BF, ACT, SAVE, 256>(a, wide, st);
+}
+template <bool BF, int TN>
+cudaError_t backward_as(const GlArgs& a, int64_t tiles, cudaStream_t st) {
   static DeviceOnce once;
-  return launch_pairs(once, gl_fwd_kernel<BF, ACT, SAVE>, (int64_t)((a.T + 255) / 256) * ((a.F + 127) / 128), a, st);
+  return launch_pairs(once, gl_bwd_kernel<BF, TN>, pair::Ring<TN, 0>::SMEM, tiles, PAIRS, a, st);
 }
 template <bool BF, int ACT>
 cudaError_t few_of(const GlFewArgs& a, cudaStream_t st) {
@@ -338,14 +424,19 @@ cudaError_t gl_few(const GlFewArgs& a, cudaStream_t st) {
   }
 }
 template <bool BF>
-cudaError_t gl_dx(const GlArgs& a, cudaStream_t st) {
-  static DeviceOnce once;
-  return gl::launch_pairs(once, gl::gl_dx_kernel<BF>, (int64_t)((a.T + 255) / 256) * ((a.D + 255) / 256), a, st);
-}
-template <bool BF>
-cudaError_t gl_dw(const GlArgs& a, cudaStream_t st) {
-  static DeviceOnce once;
-  return gl::launch_pairs(once, gl::gl_dw_kernel<BF>, (int64_t)2 * ((a.F + 255) / 256) * ((a.D + 255) / 256), a, st);
+cudaError_t gl_backward(const GlArgs& a, cudaStream_t st) {
+  using namespace gl;
+  // steps of the pair with the most, at least those of the longest tile, for tiles of 256 and of 128 columns
+  int64_t tiles[2], most[2];
+  for (int i = 0; i < 2; i++) {
+    const int64_t nt = ceil_div(a.D, i ? 128 : 256), nx = a.dx ? ceil_div(a.T, 256) * nt : 0, nw = a.dwg ? 2 * ceil_div(a.F, 256) * nt : 0;
+    const int64_t sx = 2 * ceil_div(a.F, 64), sw = ceil_div(a.T, 64);
+    const bool x = nx && (sx >= sw || !nw);
+    tiles[i] = nx + nw;
+    const int64_t even = ceil_div(nx * sx + nw * sw, PAIRS), first = x ? ceil_div(nx, PAIRS) * sx : ceil_div(nw, PAIRS) * sw;
+    most[i] = even > first ? even : first;
+  }
+  return 5 * most[0] > 3 * most[1] ? backward_as<BF, 128>(a, tiles[1], st) : backward_as<BF, 256>(a, tiles[0], st);
 }
 template <bool BF>
 cudaError_t gl_scale(const GlScaleArgs& a, cudaStream_t st) {

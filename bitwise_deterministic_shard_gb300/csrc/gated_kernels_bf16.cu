@@ -3,8 +3,7 @@
 
 namespace detattn {
 template cudaError_t gl_forward<true>(const GlArgs&, cudaStream_t);
-template cudaError_t gl_dx<true>(const GlArgs&, cudaStream_t);
-template cudaError_t gl_dw<true>(const GlArgs&, cudaStream_t);
+template cudaError_t gl_backward<true>(const GlArgs&, cudaStream_t);
 template cudaError_t gl_few<true>(const GlFewArgs&, cudaStream_t);
 template cudaError_t gl_scale<true>(const GlScaleArgs&, cudaStream_t);
 }  // namespace detattn

@@ -3,8 +3,7 @@
 
 namespace detattn {
 template cudaError_t gl_forward<false>(const GlArgs&, cudaStream_t);
-template cudaError_t gl_dx<false>(const GlArgs&, cudaStream_t);
-template cudaError_t gl_dw<false>(const GlArgs&, cudaStream_t);
+template cudaError_t gl_backward<false>(const GlArgs&, cudaStream_t);
 template cudaError_t gl_few<false>(const GlFewArgs&, cudaStream_t);
 template cudaError_t gl_scale<false>(const GlScaleArgs&, cudaStream_t);
 }  // namespace detattn

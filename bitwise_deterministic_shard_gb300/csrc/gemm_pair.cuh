@@ -1,18 +1,20 @@
 // Matrix products on pairs of SMs (tcgen05, cta_group::2) for the gated feed-forward operator:
-// tiles of 256 x 256 of the result, one pair a tile at a time, fed by tensor-map copies.
+// tiles of 256 x 256 (or 256 x 128) of the result, one pair a tile at a time, fed by tensor-map copies.
 //
-// A cluster of two CTAs works on one tile: each CTA holds 128 of the rows of A and 128 of the rows of B for a step of 64 of
-// the contracted dimension, the leader's products read both CTAs' shared memory and write 128 rows x 256 columns of
-// binary32 sums into each CTA's TMEM.  Per SM and step that is 32 KB of copies for 256 x 256 x 64 / 2 products, 512 cycles of the
-// tensor cores: a single SM with a tile of its own of 128 x 256 would need 48 KB, more than its share of the L2's rate.
+// A cluster of two CTAs works on one tile: each CTA holds 128 of the rows of A and half of the rows of B for a step of 64 of
+// the contracted dimension, the leader's products read both CTAs' shared memory and write 128 rows of binary32 sums into each
+// CTA's TMEM.  Per SM and step of a 256 x 256 tile that is 32 KB of copies for 512 cycles of the tensor cores: a single SM with a
+// tile of its own of 128 x 256 would need 48 KB, more than its share of the L2's rate.  The narrow tile is for results of so few
+// tiles that the last round of wide ones would leave many pairs idle.
 //
-// One warp copies (a ring of 7 steps, 224 KB), one of the leader issues the products, eight warps take the finished sums from TMEM.
-// Two tiles of sums fit (2 x 256 columns), so a tile's results are taken while the next one's products run.  The grid is as
-// many pairs as the GPU holds; each takes every (number of pairs)-th tile.  All sums of a result are one chain of products in the
-// order of the contracted dimension: no split, no atomics.
+// One warp copies (a ring of steps), one of the leader issues the products, eight warps take the finished sums from TMEM.
+// Two tiles of sums fit, so a tile's results are taken while the next one's products run.  The grid is as
+// many pairs as the GPU holds; which tiles a pair takes is a function of the sizes.  All sums of a result are one chain of
+// products in the order of the contracted dimension: no split, no atomics.
 //
-// Operands lie in shared memory as the 128-byte swizzle writes them: contracted over the contiguous dimension (K-major: 128 rows of
-// 64 elements) or over the rows (MN-major: two panels of 64 rows of 64 elements), so no operand is ever transposed.
+// Operands lie in shared memory as the 128-byte swizzle writes them: contracted over the contiguous dimension (K-major: rows of
+// 64 elements) or over the rows (MN-major: panels of 64 rows of 64 elements), so no operand is ever transposed.  All copies are boxes
+// of 64 x 64 elements: 8 KB, a panel, or 64 rows of a K-major operand.
 #pragma once
 #include "tc5_tile.cuh"
 
@@ -20,12 +22,17 @@ namespace detattn {
 namespace pair {
 
 constexpr int BK = 64;                    // contracted elements of a step
-constexpr int HALF = 128 * BK * 2;        // bytes of one operand's half in a CTA
-constexpr int STAGE = 2 * HALF, STAGES = 7;
-constexpr int SMEM = STAGES * STAGE + 1024;
+constexpr int BOX = 64 * BK * 2;          // bytes of a copy
 constexpr int TAKERS = 8;                 // warps that take results
 constexpr int THREADS = (TAKERS + 2) * 32;
-constexpr int TILE_M = 256, TILE_N = 256;
+
+// TN: columns of a tile (rows of B); EXTRA: bytes of shared memory beside the ring
+template <int TN, int EXTRA>
+struct Ring {
+  static constexpr int A = 2 * BOX, B = TN / 128 * BOX, STAGE = A + B;
+  static constexpr int STAGES = (227 * 1024 - 1024 - 512 - EXTRA) / STAGE;
+  static constexpr int SMEM = STAGES * STAGE + EXTRA + 1024;
+};
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -95,45 +102,49 @@ __device__ __forceinline__ void commit_both(uint64_t* bar, uint32_t one) {
       : "memory");
 }
 
-// 256 x 256 x 16 products of a type, either operand MN-major
-template <bool BF>
-__host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
+// products of a type, 256 x TN x 16, either operand MN-major
+template <bool BF, int TN>
+__device__ __forceinline__ uint32_t idesc(bool a_mn, bool b_mn) {
   return (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
-         ((uint32_t)(TILE_N >> 3) << 17) | ((uint32_t)(TILE_M >> 4) << 24);
+         ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
 }
-// contracted elements [16 s, 16 s + 16) of an operand's half
-template <bool MN>
-__device__ __forceinline__ uint64_t desc(uint32_t tile, int s) {
-  if constexpr (MN) return tc5::desc_of((tile >> 4) + (uint32_t)(s * 2048 / 16 + ((HALF / 2 >> 4) << 16)));
-  else return tc5::desc_of((tile >> 4) + (uint32_t)(s * 32 / 16 + (1 << 16)));
-}
+// low word of the descriptor of an operand's contracted elements [0, 16), and what 16 further on adds
+__device__ __forceinline__ uint32_t desc_lo(uint32_t tile, bool mn) { return (tile >> 4) + (mn ? BOX >> 4 << 16 : 1 << 16); }
+__device__ __forceinline__ uint32_t desc_step(bool mn) { return mn ? 2048 / 16 : 32 / 16; }
 
+constexpr int MOST_STAGES = 10;
 struct Shared {   // beside the ring
-  uint64_t full[STAGES], empty[STAGES], done[2], taken[2];
+  uint64_t full[MOST_STAGES], empty[MOST_STAGES], done[2], taken[2];
   uint32_t tmem;
   int dead;
 };
 
-// The tile of an index: runs of 8 tile rows, column after column, so that the pairs at work at one time read few rows of both
-// operands.
-__device__ __forceinline__ int2 tile_of(int t, int mt, int nt) {
+struct Tile {
+  int kind, m, n, steps;   // steps 0: no more tiles
+};
+// tile t of mt x nt: runs of 8 tile rows, column after column, so that the pairs at work at one time read few rows of both
+// operands
+__device__ __forceinline__ Tile tile_of(int t, int mt, int nt, int kind, int steps) {
   const int g = t / (8 * nt), r = t - g * 8 * nt, rows = min(8, mt - 8 * g);
-  return make_int2(8 * g + r % rows, r / rows);
+  return {kind, 8 * g + r % rows, r / rows, steps};
 }
 
-// The products of all tiles of this pair.
-//   load(tile, step, a, b, leader_bar): copies this CTA's halves of a step (HALF bytes each) to the addresses a and b
-//   take(tile, columns): takes a tile's sums; columns: TMEM address of this warp's lanes; calls `release()` when it
-//     has read them
-// steps: steps of a tile, the same for all.
-template <bool BF, bool A_MN, bool B_MN, typename Load, typename Take>
-__device__ __forceinline__ void run(Shared& sh, unsigned char* raw, int tiles, int steps, int32_t* status, Load load, Take take) {
+// The products of this pair's tiles.
+//   tile(j): the pair's j-th Tile
+//   load(tile, step, a, b, leader_bar): copies this CTA's halves of a step (2 and TN / 128 boxes) to the addresses a and b
+//   take(tile, columns, extra, release): takes a tile's sums; columns: TMEM address of this warp's lanes; extra: address of the
+//     shared memory beside the ring; calls release() when it has read them
+// a_mn(kind): whether A is MN-major; B is with B_MN.
+template <bool BF, int TN, int EXTRA, bool B_MN, typename Next, typename Major, typename Load, typename Take>
+__device__ __forceinline__ void run(Shared& sh, unsigned char* raw, int32_t* status, Next tile, Major a_mn, Load load, Take take) {
   using namespace tc5;
+  using R = Ring<TN, EXTRA>;
+  constexpr int STAGES = R::STAGES;
+  static_assert(STAGES <= MOST_STAGES, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   volatile int* abort = &sh.dead;
-  const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     sh.dead = 0;
@@ -158,14 +169,17 @@ __device__ __forceinline__ void run(Shared& sh, unsigned char* raw, int tiles, i
     if (lane == 0) {
       int k = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += pairs)
-        for (int n = 0; n < steps; n++, k++) {
+      for (int j = 0; ok; j++) {
+        const Tile t = tile(j);
+        if (t.steps == 0) break;
+        for (int n = 0; n < t.steps; n++, k++) {
           const int s = k % STAGES;
           if (k >= STAGES && !(ok = wait_pair(&sh.empty[s], (k / STAGES - 1) & 1, abort))) break;
-          const uint32_t at = base + s * STAGE;
-          if (rank == 0) mbar_expect_tx(&sh.full[s], 2 * STAGE);
-          load(t, n, at, at + HALF, at_leader(smem_addr(&sh.full[s])));
+          const uint32_t at = base + s * R::STAGE;
+          if (rank == 0) mbar_expect_tx(&sh.full[s], 2 * R::STAGE);
+          load(t, n, at, at + R::A, at_leader(smem_addr(&sh.full[s])));
         }
+      }
       // every step's products are done, so nothing is in flight when the CTA ends
       for (int j = max(0, k - STAGES); j < k && ok; j++) ok = wait_pair(&sh.empty[j % STAGES], (j / STAGES) & 1, abort);
       if (!ok)   // given up: what was copied arrives at the leader
@@ -174,32 +188,36 @@ __device__ __forceinline__ void run(Shared& sh, unsigned char* raw, int tiles, i
   } else if (warp == TAKERS + 1) {
     if (rank == 0) {
       const uint32_t one = elect(), tm = same(tmem);
-      constexpr uint32_t id = idesc<BF>(A_MN, B_MN);
-      int k = 0, i = 0;
+      int k = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += pairs, i++) {
+      for (int i = 0; ok; i++) {
+        const Tile t = tile(i);
+        const int steps = same(t.steps);
+        if (steps == 0) break;
+        const bool mn = a_mn(same(t.kind));
+        const uint32_t id = idesc<BF, TN>(mn, B_MN), sa = desc_step(mn), sb = desc_step(B_MN);
         if (i >= 2 && !(ok = all_of(wait_pair(&sh.taken[i & 1], ((i >> 1) - 1) & 1, abort)))) break;
         fence_after();
         for (int n = 0; n < steps; n++, k++) {
           const int s = same(k % STAGES);
           if (!(ok = all_of(wait_pair(&sh.full[s], (k / STAGES) & 1, abort)))) break;
           fence_after();
-          const uint32_t at = same(base) + s * STAGE;
+          const uint32_t at = same(base) + s * R::STAGE, da = desc_lo(at, mn), db = desc_lo(at + R::A, B_MN);
 #pragma unroll
           for (int j = 0; j < BK / 16; j++)
-            mma(tm + (i & 1) * 256, desc<A_MN>(at, j), desc<B_MN>(at + HALF, j), id, n > 0 || j > 0, one);
+            mma(tm + (i & 1) * TN, desc_of(da + j * sa), desc_of(db + j * sb), id, n > 0 || j > 0, one);
           commit_both(&sh.empty[s], one);
         }
         if (ok) commit_both(&sh.done[i & 1], one);
       }
     }
   } else {
-    int i = 0;
-    for (int t = first; t < tiles; t += pairs, i++) {
-      if (!all_of(wait_pair(&sh.done[i & 1], (i >> 1) & 1, abort))) break;
+    for (int i = 0;; i++) {
+      const Tile t = tile(i);
+      if (t.steps == 0 || !all_of(wait_pair(&sh.done[i & 1], (i >> 1) & 1, abort))) break;
       fence_after();
       const uint32_t bar = at_leader(smem_addr(&sh.taken[i & 1]));
-      take(t, tmem + ((uint32_t)(warp & 3) << 21) + (i & 1) * 256, [&] {
+      take(t, tmem + ((uint32_t)(warp & 3) << 21) + (i & 1) * TN, base + STAGES * R::STAGE, [&] {
         fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(bar);

@@ -9,18 +9,20 @@
 // M is the rounded c max(x), and whatever its rounding, it is the same in every term and cancels.  M and S go to the gradient,
 // where dx_v = 2^t (A + B t) + [v = target] a / temperature with A and B of the row: one product more than the softmax's own.
 //
-// What bounds it: HBM; x is read once, and once more and dx written in the gradient.  A round of 8 vectors of 16 bytes a
-// thread stays in registers: its maximum, then (the reference moved where that is larger) its terms.
+// What bounds it: HBM; x is read once, and once more and dx written in the gradient.  A step of 4 vectors of 16 bytes a
+// thread stays in registers: its maximum, then (the reference moved where that is larger) its terms, while the next step's
+// loads are under way.
 //
-// Alternatives: the first round's maxima of single threads give a value that at least `top` elements of the row reach (each of the
-// CTA's warps finds its ceil(top / warps)-th largest, the least of them is that value); what reaches it, a few hundred elements
-// of a large row, is collected in shared memory, and one warp takes the largest `top` of that, equal ones by their index.
-// Rows that go on growing fill the list; it is then cut to its `top` largest, which raises the value, and where even a
-// round's own candidates do not fit they are taken again above the `top`-th largest of the threads' best, of which there are
-// at most 64 top.
+// Alternatives: a value that at least `top` elements of the row reach is found from the first step's maxima of single threads (each of
+// the CTA's warps finds its ceil(top / warps)-th largest, the least of them is that value); a warp keeps what reaches it, some
+// tens of elements of a large row, in shared memory, and raises the value now and then by its own and the other warps' ceil(top /
+// warps)-th best so far.  A full list is cut to its `top` largest.  At the end each warp sorts out its `top`, one
+// warp those of all.  Equal values go by their index: a warp meets its elements in order of their indices.  No barrier but the first
+// step's, and which candidates are kept does not change the result.
 //
-// A row is one CTA's; short rows a warp's; where few rows would leave SMs idle, a cluster's, whose parts the first CTA joins through
-// distributed shared memory.  The order of the sums depends on the sizes, the type and what starts on 16 bytes.
+// A row is one CTA's; short rows a warp's; where few rows would leave SMs idle, a cluster's, whose parts hand their sums and
+// lists to the first CTA through distributed shared memory.  The order of the sums depends on the sizes, the type and what
+// starts on 16 bytes.
 #include <algorithm>
 
 #include "../../include/detattn.h"
@@ -34,7 +36,7 @@ namespace {
 using f2::u64;
 using tc5::ex2;
 
-constexpr int NV = 8;                  // vectors of a thread in a round
+constexpr int NV = 4;                  // vectors of a thread in a step
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float FAR = -1000.f;         // t of a probability of zero: 2^t t is 0 there and not NaN
 
@@ -104,18 +106,18 @@ struct Sums {   // reference (log2 units), sum of 2^t, sum of 2^t t
   }
 };
 
+constexpr int CAP = 256;               // candidates that a warp keeps
+
 template <int W>
 struct Shared {
-  static constexpr int CAP = W == 1 ? 2048 : 4096;   // a warp's only round is never more
-  u64 cand[CAP];
-  u64 best[32 * W];
-  u64 list[LP_TOP];
-  uint32_t count, warps[W];
-  u64 above;
-  Sums sums[W];
+  u64 cand[W][CAP];
+  u64 list[W][LP_TOP];
+  u64 best[LP_TOP];
+  u64 join[8][LP_TOP];                 // first CTA of a cluster: the parts' lists
+  uint32_t reached[W];
 };
 
-// The largest n of the first `have` keys of `from`, in order, to `to`; by one whole warp.
+// The largest n of the first `have` keys of `from`, in order, to `to`, zeros behind them; by one whole warp.
 __device__ __forceinline__ void select_largest(u64* from, int have, u64* to, int n) {
   const int lane = threadIdx.x & 31;
   u64 mine = 0;
@@ -129,51 +131,133 @@ __device__ __forceinline__ void select_largest(u64* from, int have, u64* to, int
         at = i;
       }
   };
+  __syncwarp();
   scan();
+  u64 keep = 0;
   for (int j = 0; j < n; j++) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(mine >> 32));
     const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
     const u64 top = (u64)hi << 32 | lo;
-    if (lane == 0) to[j] = top;
-    if (top != 0 && mine == top) {   // keys differ, so one lane
+    if (top == 0) break;
+    if (lane == j) keep = top;
+    if (mine == top) {   // keys differ, so one lane
       from[at] = 0;
       scan();
     }
   }
   __syncwarp();
+  if (lane < LP_TOP) to[lane] = keep;
+  __syncwarp();
 }
 
-__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
+// The candidates of one warp: elements that reach `reach`, a value that at least `top` elements of the row do reach.
+template <int W>
+struct Candidates {
+  Shared<W>& sh;
+  const int top, warp, lane, need;     // need: elements that each of the W warps has to have above a common value
+  float reach = INFINITY;
+  int count = 0, next = 0;
+
+  __device__ __forceinline__ Candidates(Shared<W>& s, int t, int w, int l) : sh(s), top(t), warp(w), lane(l), need((t + W - 1) / W) {}
+  __device__ __forceinline__ void at_least(uint32_t o) { reach = fmaxf(reach, value_of(max(o, 0x00800000u))); }   // above -inf
+
+  // the first step: from the maxima of the CTA's threads
+  __device__ __forceinline__ void begin(float big) {
+    uint32_t o = ordered(big), least = 0;
+    for (int j = 0; j < need; j++) {
+      least = __reduce_max_sync(0xffffffffu, o);
+      const uint32_t who = __ballot_sync(0xffffffffu, o == least);
+      if (lane == __ffs(who) - 1) o = 0;
+    }
+    if (lane == 0) sh.reached[warp] = least;
+    __syncthreads();
+    reach = -INFINITY;
+    common();
+    next = 24;
+  }
+  __device__ __forceinline__ void common() {
+    const volatile uint32_t* const r = sh.reached;
+    at_least(__reduce_min_sync(0xffffffffu, r[lane % W]));
+  }
+  // The value that `need` of this warp's candidates reach, for all warps; and what all of them have found.  Reading older values of
+  // others only keeps more candidates.
+  __device__ __forceinline__ void publish() {
+    u64 last = ~0ull;
+    for (int j = 0; j < need && last; j++) {
+      u64 mine = 0;
+      for (int i = lane; i < count; i += 32) {
+        const u64 k = sh.cand[warp][i];
+        if (k < last && k > mine) mine = k;
+      }
+      const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(mine >> 32));
+      const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
+      last = (u64)hi << 32 | lo;
+    }
+    volatile uint32_t* const mine = &sh.reached[warp];
+    if (lane == 0) *mine = max(*mine, (uint32_t)(last >> 32));
+    __syncwarp();
+    common();
+    next = count + 24;
+  }
+  __device__ __forceinline__ void cut() {   // to the largest `top`; later ones of equal value have larger indices
+    select_largest(sh.cand[warp], count, sh.list[warp], top);
+    if (lane < top) sh.cand[warp][lane] = sh.list[warp][lane];
+    __syncwarp();
+    count = top;
+    at_least((uint32_t)(sh.list[warp][top - 1] >> 32) + 1);
+    publish();
+  }
+  // the warp's vectors of one load, in order of their indices; big: the lane's largest element
+  template <typename T>
+  __device__ __forceinline__ void add(const Run<T, Elem<T>::VEC>& x, float big, uint32_t first) {
+    constexpr int VEC = Elem<T>::VEC;
+    uint32_t who = __ballot_sync(0xffffffffu, big >= reach);
+    while (who) {
+      const int src = __ffs(who) - 1;
+      who &= who - 1;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) w[i] = __shfl_sync(0xffffffffu, x.w[i], src);
+      const uint32_t from = __shfl_sync(0xffffffffu, first, src);
+      const int e = lane & (VEC - 1), i = VEC == 8 ? e >> 1 : e;
+      const uint32_t word = i & 2 ? i & 1 ? w[3] : w[2] : i & 1 ? w[1] : w[0];
+      float y;
+      if constexpr (VEC == 4) y = __uint_as_float(word);
+      else if constexpr (std::is_same<T, __nv_bfloat16>::value) y = __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
+      else y = __half2float(__ushort_as_half((uint16_t)(e & 1 ? word >> 16 : word)));
+      if (count > CAP - VEC) cut();
+      const bool is = lane < VEC && y >= reach;
+      const uint32_t m = __ballot_sync(0xffffffffu, is);
+      if (is) sh.cand[warp][count + __popc(m & ((1u << lane) - 1))] = key_of(y, from + e);
+      count += __popc(m);
+    }
+    if (count >= next) {
+      __syncwarp();
+      publish();
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t leader(uint32_t addr) {
   uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
-}
-__device__ __forceinline__ u64 peer_u64(uint32_t addr) {
-  u64 v;
-  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float peer_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // W warps a CTA; parts: CTAs (a cluster) of a row
 template <typename T, int W, bool TOP>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __grid_constant__ LpArgs a, int parts) {
   constexpr int VEC = Elem<T>::VEC, G = 32 * W;
-  __shared__ std::conditional_t<TOP, Shared<W>, Sums[W]> sh;
+  __shared__ Sums sums[W], joins[8];     // of the warps; of a cluster's parts
+  __shared__ std::conditional_t<TOP, Shared<W>, int> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t r = blockIdx.x / (uint32_t)parts;
   const uint32_t part = blockIdx.x % (uint32_t)parts;
   const T* const row = static_cast<const T*>(a.x) + r * a.xs;
   const int64_t target = a.targets[r];
-  const float at_target = tid == 0 && target >= 0 && target < a.cols ? Elem<T>::get(row[target]) : 0.f;
+  const float at_target = tid == 0 && target >= 0 && target < (int64_t)a.cols ? Elem<T>::get(row[target]) : 0.f;
   const float c = (float)(1.4426950408889634 / (double)a.temperature);
+  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");   // the first CTA's memory is there (waited for below)
 
   const int off = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
   const uint32_t nv = (a.cols + off + VEC - 1) / VEC, per = (nv + parts - 1) / parts;
@@ -181,26 +265,20 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
 
   float top_x = -INFINITY, M = -INFINITY;   // this thread's largest element, and its reference
   u64 S2 = 0, E2 = 0;
-  float reach = -INFINITY;                  // elements below it are no candidates
-  if constexpr (TOP) {
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
-  }
-  for (uint32_t v = v0; v < v1; v += NV * G) {
-    Run<T, VEC> x[NV];
+  const auto load = [&](Run<T, VEC> (&x)[NV], uint32_t v) {
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const uint32_t at = v + i * G + tid;
-      if (at < v1) load_vector(x[i], row, (int64_t)at * VEC - off, a.cols);
-      else {
+      if (at < v1) {
+        load_vector(x[i], row, (int64_t)at * VEC - off, a.cols);
+      } else {
         x[i].zero();
 #pragma unroll
         for (int e = 0; e < VEC; e++) x[i].put_bits(e, lowest<T>());
       }
     }
-    float big = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NV; i++) big = fmaxf(big, largest(x[i]));
+  };
+  const auto sum = [&](const Run<T, VEC> (&x)[NV], float big) {
     if (big > top_x) {
       top_x = big;
       float s0, s1, e0, e1;
@@ -227,80 +305,41 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
         E2 = f2::fma(p, f2::pack(t0, t1), E2);
       }
     }
-    if constexpr (TOP) {
-      using Sh = Shared<W>;
-      if (v == v0) {   // a value that at least `top` elements reach
-        const int need = (a.top + W - 1) / W;
-        uint32_t o = ordered(big), least = 0;
-        for (int j = 0; j < need; j++) {
-          least = __reduce_max_sync(0xffffffffu, o);
-          const uint32_t who = __ballot_sync(0xffffffffu, o == least);
-          if (lane == __ffs(who) - 1) o = 0;
-        }
-        if (lane == 0) sh.warps[warp] = least;
-        __syncthreads();
-        least = sh.warps[0];
+  };
+  const auto most = [&](const Run<T, VEC> (&x)[NV]) {
+    float big = -INFINITY;
 #pragma unroll
-        for (int w = 1; w < W; w++) least = min(least, sh.warps[w]);
-        reach = least <= ordered(-INFINITY) ? -INFINITY : value_of(least);
-      }
-      const auto each = [&](auto f) {   // this round's elements, those of the row
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-          const uint32_t at = v + i * G + tid;
-          const int64_t first = (int64_t)at * VEC - off;
-          if (at < v1 && largest(x[i]) >= reach)
-#pragma unroll
-            for (int e = 0; e < VEC; e++)
-              if (first + e >= 0 && first + e < a.cols) f(x[i].get(e), (uint32_t)(first + e));
-        }
-      };
-      bool full = false;
-      if (big >= reach)
-        each([&](float y, uint32_t index) {
-          if (y >= reach) {
-            const uint32_t slot = atomicAdd(&sh.count, 1u);
-            if (slot < Sh::CAP) sh.cand[slot] = key_of(y, index);
-            full |= slot >= 2048;
-          }
-        });
-      if (W > 1 && __syncthreads_or(full)) {   // the same in all threads
-        const uint32_t count = sh.count, have = min(count, (uint32_t)Sh::CAP);
-        if (warp == 0) select_largest(sh.cand, have, sh.list, a.top);
-        __syncthreads();
-        if (tid < a.top) sh.cand[tid] = sh.list[tid];
-        if (tid == 0) {
-          sh.count = a.top;
-          sh.above = sh.list[a.top - 1];
-        }
-        __syncthreads();
-        u64 above = sh.above;
-        if (count > Sh::CAP) {
-          u64 best = 0;
-          if (big >= reach) each([&](float y, uint32_t index) { best = max(best, key_of(y, index)); });
-          sh.best[tid] = best;
-          __syncthreads();
-          int rank = 0;
-          for (int j = 0; j < G; j++) rank += sh.best[j] > best || (sh.best[j] == best && j < tid);
-          if (rank == a.top - 1 && best > above) sh.above = best;
-          __syncthreads();
-          above = sh.above;
-          if (best >= above && best != 0)
-            each([&](float y, uint32_t index) {
-              const u64 key = key_of(y, index);
-              bool more = key >= above;
-              for (int j = 0; j < a.top && more; j++) more = sh.list[j] != key;
-              if (more) {
-                const uint32_t slot = atomicAdd(&sh.count, 1u);
-                if (slot < Sh::CAP) sh.cand[slot] = key;   // there are at most `top` and 64 top
-              }
-            });
-          __syncthreads();
-        }
-        reach = value_of((uint32_t)(above >> 32) + 1);   // an equal one of a later round has a larger index
-        if (reach != reach) reach = INFINITY;
-      }
+    for (int i = 0; i < NV; i++) big = fmaxf(big, largest(x[i]));
+    return big;
+  };
+  // the loads of one step are under way while the other's elements are worked on
+  constexpr uint32_t STEP = NV * G;
+  Run<T, VEC> x0[NV], x1[NV];
+  load(x0, v0);
+  const auto steps = [&](auto each) {
+    for (uint32_t v = v0; v < v1; v += 2 * STEP) {
+      load(x1, min(v + STEP, v1));
+      each(x0, v);
+      if (v + STEP >= v1) break;
+      load(x0, min(v + 2 * STEP, v1));
+      each(x1, v + STEP);
     }
+  };
+  int count = 0;
+  if constexpr (TOP) {
+    Candidates<W> cand(sh, a.top, warp, lane);
+    cand.begin(most(x0));
+    steps([&](const Run<T, VEC> (&x)[NV], uint32_t v) {
+      const float big = most(x);
+      sum(x, big);
+      if (__any_sync(0xffffffffu, big >= cand.reach)) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) cand.add(x[i], largest(x[i]), (v + i * G + tid) * VEC - off);
+      }
+    });
+    count = cand.count;
+  } else {
+    steps([&](const Run<T, VEC> (&x)[NV], uint32_t) { sum(x, most(x)); });
   }
 
   float s0, s1, e0, e1;
@@ -317,34 +356,32 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
     }
     m.join(u);
   }
-  Sums* sums;
-  if constexpr (TOP) sums = sh.sums;
-  else sums = sh;
   if (lane == 0) sums[warp] = m;
+  if constexpr (TOP) select_largest(sh.cand[warp], count, sh.list[warp], a.top);
   __syncthreads();
   if (warp == 0) {
     for (int w = 1; w < W; w++) m.join(sums[w]);
-    if constexpr (TOP) select_largest(sh.cand, min(sh.count, (uint32_t)Shared<W>::CAP), sh.list, a.top);
+    if constexpr (TOP) select_largest(sh.list[0], W * LP_TOP, sh.best, a.top);
   }
-  if (parts > 1) {
-    if (tid == 0) sums[0] = m;
-    cluster_sync();
-    if (part == 0 && warp == 0) {
-      const uint32_t mine = tc5::smem_addr(&sums[0]);
-      for (int p = 1; p < parts; p++) {
-        const uint32_t at = peer(mine, p);
-        m.join(Sums{peer_f32(at), peer_f32(at + 4), peer_f32(at + 8)});
-      }
-      if constexpr (TOP) {
-        const uint32_t list = tc5::smem_addr(&sh.list[0]);
-        if (lane < a.top)
-          for (int p = 0; p < parts; p++) sh.cand[p * a.top + lane] = peer_u64(peer(list, p) + 8 * lane);
-        __syncwarp();
-        select_largest(sh.cand, parts * a.top, sh.list, a.top);
-      }
+  if (parts > 1) {   // the parts leave their sums and lists with the first CTA
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+    if (warp == 0) {
+      const uint32_t at = leader(tc5::smem_addr(&joins[part]));
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("st.shared::cluster.f32 [%0], %1;\n\tst.shared::cluster.f32 [%0 + 4], %2;\n\tst.shared::cluster.f32 [%0 + 8], %3;" ::"r"(at),
+                     "f"(m.M), "f"(m.S), "f"(m.E)
+                     : "memory");
+      if constexpr (TOP)
+        asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(leader(tc5::smem_addr(&sh.join[part][lane]))), "l"(sh.best[lane]) : "memory");
     }
-    cluster_sync();   // the parts stay until they are read
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     if (part != 0) return;
+    if (warp == 0) {
+      m = joins[0];
+      for (int p = 1; p < parts; p++) m.join(joins[p]);
+      if constexpr (TOP) select_largest(sh.join[0], parts * LP_TOP, sh.best, a.top);
+    }
   }
   if (warp != 0) return;
   const bool none = m.S == 0.f;                             // every logit is -inf
@@ -368,11 +405,19 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
     if (!isfinite(m.S) && a.status) atomicOr(a.status, DA_STATUS_NONFINITE);
   }
   if constexpr (TOP) {
+    u64 key = sh.best[lane];
+    int have = __popc(__ballot_sync(0xffffffffu, key != 0));
+    for (uint32_t i = 0; have < a.top && i < a.cols; i += 32) {   // few are above -inf: the first of the others
+      const bool is = i + lane < a.cols && Elem<T>::get(row[i + lane]) == -INFINITY;
+      const uint32_t who = __ballot_sync(0xffffffffu, is);
+      const int place = lane - have;                              // this lane takes the place-th of them
+      if (place >= 0 && place < __popc(who)) key = key_of(-INFINITY, i + __fns(who, 0, place + 1));
+      have += __popc(who);
+    }
     if (lane < a.top) {
-      const u64 key = sh.list[lane];
-      const float y = value_of((uint32_t)(key >> 32));
+      const float y = key ? value_of((uint32_t)(key >> 32)) : __uint_as_float(0x7fffffffu);
       a.top_lp[r * a.top + lane] = none || y == -INFINITY ? -INFINITY : (__fmaf_rn(y, c, -m.M) - log_s) * LN2;
-      a.top_index[r * a.top + lane] = (int64_t)(uint32_t)~(uint32_t)key;
+      a.top_index[r * a.top + lane] = min((uint32_t)~(uint32_t)key, a.cols - 1);
     }
   }
 }
@@ -454,10 +499,10 @@ cudaError_t forward(const LpArgs& a, int parts, cudaStream_t st) {
 template <typename T>
 cudaError_t forward(const LpArgs& a, cudaStream_t st) {
   const int64_t vectors = (a.cols + Elem<T>::VEC - 1) / Elem<T>::VEC;
-  if (vectors + 1 <= 32 * NV) return forward<T, 1>(a, 1, st);   // one round of a warp, wherever the row starts
-  // parts of a row: as many as keep at most two CTAs an SM, and a round's vectors in each
+  if (vectors <= 64 * NV) return forward<T, 1>(a, 1, st);
+  // parts of a row: as many as keep at most two CTAs an SM, and a step's vectors in each
   int parts = 1;
-  while (parts < 8 && a.rows * parts * 2 <= 304 && vectors >= (int64_t)parts * 2 * 256 * NV / 2) parts *= 2;
+  while (parts < 8 && a.rows * parts * 2 <= 304 && vectors >= (int64_t)parts * 2 * 256 * NV) parts *= 2;
   return forward<T, 8>(a, parts, st);
 }
 template <typename T>
