@@ -86,7 +86,7 @@ int check_rows(const da_matrix* x) {
 int check_logits(const da_matrix* x, float temperature) {
   const int e = check_rows(x);
   if (e) return e;
-  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature)) return DA_EINVAL;
+  if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f)) return DA_EINVAL;
   return x->rows * (x->cols / 4096 + 8) >= (int64_t)1 << 31 ? DA_ESHAPE : DA_OK;   // CTAs of a launch
 }
 int check_ids(const void* ids, int bits, int64_t n, const da_matrix* like) {

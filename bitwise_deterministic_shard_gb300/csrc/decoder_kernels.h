@@ -61,7 +61,7 @@ struct LpArgs {
   const int64_t* targets;        // [rows]
   float* lp;                     // [rows]
   float* entropy;                // [rows]
-  float* stats;                  // [rows][3] or null: reference and sum (log2 units, see log_prob_kernels.cu), entropy
+  float* stats;                  // [rows][3] or null: largest logit, sum of exponentials, entropy
   float* top_lp;                 // [rows, top]
   int64_t* top_index;
   int64_t rows, xs;

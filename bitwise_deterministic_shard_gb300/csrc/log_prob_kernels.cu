@@ -4,13 +4,14 @@
 //   z = x / temperature;  lse = log sum exp z;  lp = z_target - lse;  H = lse - sum p z,  p = exp(z - lse)
 //   dx_v = (a (1[v = target] - p_v) - b p_v (log p_v + H)) / temperature,  a = dL/dlp, b = dL/dH
 //
-// In log2 units with c = log2(e) / temperature, a reference M and t_v = fma(x_v, c, -M), one pass gives
-//   S = sum 2^t,  E = sum 2^t t,  lp = (t_target - log2 S) ln 2,  H = ln S - ln 2 E / S;
-// M is the rounded c max(x), and whatever its rounding, it is the same in every term and cancels.  M and S go to the gradient,
-// where dx_v = 2^t (A + B t) + [v = target] a / temperature with A and B of the row: one product more than the softmax's own.
+// With c = log2(e) / temperature, m = max x and t_v = (x_v - m) c (the difference first: x may be as large, or as low, as its
+// type allows), one pass gives
+//   S = sum 2^t,  E = sum 2^t t,  lp = (x_target - m) / temperature - ln S,  H = ln S - ln 2 E / S.
+// m, S and H go to the gradient, where dx_v = 2^t (A + B t) + [v = target] a / temperature with A and B of the row: one
+// product more than the softmax's own.
 //
 // What bounds it: HBM; x is read once, and once more and dx written in the gradient.  A step of 4 vectors of 16 bytes a
-// thread stays in registers: its maximum, then (the reference moved where that is larger) its terms, while the next step's
+// thread stays in registers: its maximum, then (the sums moved where that is larger) its terms, while the next step's
 // loads are under way.
 //
 // Alternatives: each warp keeps the largest few of its lanes' maxima, step by step; the `top`-th of all warps' is a value that at
@@ -89,19 +90,19 @@ __device__ __forceinline__ void load_vector(Run<T, Elem<T>::VEC>& r, const T* ro
   }
 }
 
-struct Sums {   // reference (log2 units), sum of 2^t, sum of 2^t t
-  float M, S, E;
-  __device__ __forceinline__ void to(float m) {   // m >= M
-    if (m == M) return;
-    const float d = M - m, k = M == -INFINITY ? 0.f : ex2(d);
-    E = M == -INFINITY ? E : k * __fmaf_rn(d, S, E);   // a NaN stays
-    S = M == -INFINITY ? S : k * S;
-    M = m;
+struct Sums {   // the largest element, sum of 2^t, sum of 2^t t
+  float m, S, E;
+  __device__ __forceinline__ void to(float top, float c) {   // top >= m
+    if (top == m) return;
+    const float d = m == -INFINITY ? 0.f : fmaxf((m - top) * c, FAR), k = ex2(d);
+    E = k * __fmaf_rn(d, S, E);   // all are 0 (or NaN, which stays) where no element was above -inf
+    S = k * S;
+    m = top;
   }
-  __device__ __forceinline__ void join(Sums o) {
-    const float m = fmaxf(M, o.M);
-    to(m);
-    o.to(m);
+  __device__ __forceinline__ void join(Sums o, float c) {
+    const float top = fmaxf(m, o.m);
+    to(top, c);
+    o.to(top, c);
     S += o.S;
     E += o.E;
   }
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
   const uint32_t nv = (a.cols + off + VEC - 1) / VEC, per = (nv + parts - 1) / parts;
   const uint32_t v0 = min(nv, part * per), v1 = min(nv, v0 + per);
 
-  float top_x = -INFINITY, M = -INFINITY;   // this thread's largest element, and its reference
+  float top_x = -INFINITY;                  // this thread's largest element
   u64 S2 = 0, E2 = 0;
   const auto load = [&](Run<T, VEC> (&x)[NV], uint32_t v) {
 #pragma unroll
@@ -317,24 +318,23 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
   };
   const auto sum = [&](const Run<T, VEC> (&x)[NV], float big) {
     if (big > top_x) {
-      top_x = big;
       float s0, s1, e0, e1;
       f2::unpack(S2, s0, s1);
       f2::unpack(E2, e0, e1);
-      Sums lo = {M, s0, e0}, hi = {M, s1, e1};
-      M = big * c;
-      lo.to(M);
-      hi.to(M);
+      Sums lo = {top_x, s0, e0}, hi = {top_x, s1, e1};
+      top_x = big;
+      lo.to(big, c);
+      hi.to(big, c);
       S2 = f2::pack(lo.S, hi.S);
       E2 = f2::pack(lo.E, hi.E);
     }
-    const u64 cc = f2::splat(c), mm = f2::splat(M == -INFINITY ? 0.f : -M);
+    const u64 cc = f2::splat(c), mm = f2::splat(top_x == -INFINITY ? 0.f : -top_x);
 #pragma unroll
     for (int i = 0; i < NV; i++) {
 #pragma unroll
       for (int e = 0; e < VEC / 2; e++) {
         float t0, t1;
-        f2::unpack(f2::fma(x[i].get2(e), cc, mm), t0, t1);
+        f2::unpack(f2::mul(f2::add(x[i].get2(e), mm), cc), t0, t1);
         t0 = max_nan(t0, FAR);
         t1 = max_nan(t1, FAR);
         const u64 p = f2::pack(ex2(t0), ex2(t1));
@@ -385,21 +385,21 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
   float s0, s1, e0, e1;
   f2::unpack(S2, s0, s1);
   f2::unpack(E2, e0, e1);
-  Sums m = {M, s0 + s1, e0 + e1};
+  Sums m = {top_x, s0 + s1, e0 + e1};
 #pragma unroll
   for (int o = 16; o; o >>= 1) {   // the lower lane's sums first, so that both get the same bits
-    Sums u = {__shfl_xor_sync(0xffffffffu, m.M, o), __shfl_xor_sync(0xffffffffu, m.S, o), __shfl_xor_sync(0xffffffffu, m.E, o)};
+    Sums u = {__shfl_xor_sync(0xffffffffu, m.m, o), __shfl_xor_sync(0xffffffffu, m.S, o), __shfl_xor_sync(0xffffffffu, m.E, o)};
     if (lane & o) {
       const Sums t = m;
       m = u;
       u = t;
     }
-    m.join(u);
+    m.join(u, c);
   }
   if (lane == 0) sums[warp] = m;
   __syncthreads();
   if (warp == 0)
-    for (int w = 1; w < W; w++) m.join(sums[w]);
+    for (int w = 1; w < W; w++) m.join(sums[w], c);
   if (parts > 1) {   // the parts leave their sums and lists with the first CTA
     asm volatile("barrier.cluster.wait;" ::: "memory");
     if (warp == 0) {
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
       __syncwarp();
       if (lane == 0)
         asm volatile("st.shared::cluster.f32 [%0], %1;\n\tst.shared::cluster.f32 [%0 + 4], %2;\n\tst.shared::cluster.f32 [%0 + 8], %3;" ::"r"(at),
-                     "f"(m.M), "f"(m.S), "f"(m.E)
+                     "f"(m.m), "f"(m.S), "f"(m.E)
                      : "memory");
       if constexpr (TOP)
         asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(leader(tc5::smem_addr(&sh.join[part][lane]))), "l"(sh.best[lane]) : "memory");
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
     if (part != 0) return;
     if (warp == 0) {
       m = joins[0];
-      for (int p = 1; p < parts; p++) m.join(joins[p]);
+      for (int p = 1; p < parts; p++) m.join(joins[p], c);
     }
     if constexpr (TOP) {
       const u64* const all = sh.join[0];
@@ -431,20 +431,21 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
   }
   if (warp != 0) return;
   const bool none = m.S == 0.f;                             // every logit is -inf
-  const float log_s = none ? 0.f : log2f(m.S);
+  const float log_s = none ? 0.f : logf(m.S);
+  const auto log_prob = [&](float y) { return none || (y == -INFINITY && m.S == m.S) ? -INFINITY : __fdiv_rn(y - m.m, a.temperature) - log_s; };
   if (lane == 0) {
     float lp = 0.f;
     if (target >= (int64_t)a.cols) {
       lp = __uint_as_float(0x7fffffffu);
       if (a.status) atomicOr(a.status, DA_STATUS_BAD_TARGET);
     } else if (target >= 0) {
-      lp = none ? -INFINITY : (__fmaf_rn(at_target, c, -m.M) - log_s) * LN2;
+      lp = log_prob(at_target);
     }
     a.lp[r] = lp;
-    const float entropy = none ? 0.f : (log_s - m.E / m.S) * LN2;
+    const float entropy = none ? 0.f : __fmaf_rn(-LN2, m.E / m.S, log_s);
     a.entropy[r] = entropy;
     if (a.stats) {
-      a.stats[3 * r] = m.M;
+      a.stats[3 * r] = m.m;
       a.stats[3 * r + 1] = m.S;
       a.stats[3 * r + 2] = entropy;
     }
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
     }
     if (lane < a.top) {
       const float y = key ? value_of((uint32_t)(key >> 32)) : __uint_as_float(0x7fffffffu);
-      a.top_lp[r * a.top + lane] = none || y == -INFINITY ? -INFINITY : (__fmaf_rn(y, c, -m.M) - log_s) * LN2;
+      a.top_lp[r * a.top + lane] = log_prob(y);
       a.top_index[r * a.top + lane] = min((uint32_t)~(uint32_t)key, a.cols - 1);
     }
   }
@@ -479,14 +480,14 @@ __global__ void __launch_bounds__(256) lp_grad_kernel(const __grid_constant__ Lp
   const T* const row = static_cast<const T*>(a.x) + r * a.xs;
   T* const out = static_cast<T*>(a.dx) + r * a.ds;
   const float c = (float)(1.4426950408889634 / (double)a.temperature), back = 1.f / a.temperature;
-  const float M = a.stats[3 * r], S = a.stats[3 * r + 1], H = a.stats[3 * r + 2];
+  const float m = a.stats[3 * r], S = a.stats[3 * r + 1], H = a.stats[3 * r + 2];
   const int64_t target = a.targets[r];
   const float g = a.grad && target >= 0 && target < (int64_t)a.cols ? a.grad[r] : 0.f, h = a.grad_entropy ? a.grad_entropy[r] : 0.f;
   const bool none = S == 0.f;
   const float inv = none ? 0.f : back / S, log_s = none ? 0.f : log2f(S);
   const float A = -(g + h * __fmaf_rn(-LN2, log_s, H)) * inv, B = -h * LN2 * inv;
   const float hit = none ? 0.f : g * back;
-  const u64 cc = f2::splat(c), mm = f2::splat(none ? 0.f : -M), aa = f2::splat(A), bb = f2::splat(B);
+  const u64 cc = f2::splat(c), mm = f2::splat(none ? 0.f : -m), aa = f2::splat(A), bb = f2::splat(B);
 
   const int off = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
   const bool along = off == (int)((reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T));   // both start alike
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(256) lp_grad_kernel(const __grid_constant__ Lp
 #pragma unroll
     for (int e = 0; e < VEC / 2; e++) {
       float t0, t1;
-      f2::unpack(f2::fma(x[i].get2(e), cc, mm), t0, t1);
+      f2::unpack(f2::mul(f2::add(x[i].get2(e), mm), cc), t0, t1);
       t0 = max_nan(t0, FAR);
       t1 = max_nan(t1, FAR);
       f2::unpack(f2::mul(f2::pack(ex2(t0), ex2(t1)), f2::fma(bb, f2::pack(t0, t1), aa)), v[2 * e], v[2 * e + 1]);

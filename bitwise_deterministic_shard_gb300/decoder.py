@@ -208,15 +208,15 @@ def _logits(logits, targets, temperature):
         if targets.dtype.is_floating_point or targets.dtype.is_complex or targets.dtype == torch.bool:
             raise DetAttnError("targets must be integers")
         targets = targets.to(torch.int64)
-    if not 0.0 < temperature < float("inf"):
-        raise DetAttnError("temperature must be above 0 and finite")
+    if not 2.0 ** -60 <= temperature <= 2.0 ** 60:
+        raise DetAttnError("temperature must be from 2^-60 to 2^60")
     return code, index, targets if targets.is_contiguous() else targets.contiguous()
 
 
 def log_probs_forward(logits, targets, temperature=1.0, top=0, need_saved=True, status=None):
     """Log probabilities of given tokens, entropies and alternatives: (LogProbs, saved).
 
-    logits [..., V] f32, bf16 or f16; targets [...] integers.  With z = logits / temperature and lse = log sum exp z:
+    logits [..., V] f32, bf16 or f16; targets [...] integers; temperature from 2^-60 to 2^60.  With z = logits / temperature and lse = log sum exp z:
       log_probs = z[target] - lse (a negative target: no token, 0);  entropy = lse - sum p z
       top_indices, top_log_probs [..., top]: the top largest logits (up to 32) in order, equal ones by their index; None for 0
     Results are f32 (indices int64).  A logit of -inf is a token of probability 0; a row of nothing else has entropy 0 and log

@@ -437,7 +437,7 @@ int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_matrix* wg, c
                  da_stream_t stream);
 
 /* Log probabilities of given tokens, entropies and the most likely alternatives of rows of logits (f32, bf16, f16; any stride and
- * start).  With z = logits / temperature (above 0) and lse = log sum exp z, all f32:
+ * start).  With z = logits / temperature (2^-60 to 2^60) and lse = log sum exp z, all f32:
  *   log_probs[i] = z[i][targets[i]] - lse_i  (targets: device int64 [rows]; negative: no token, 0)
  *   entropy[i] = lse_i - sum_v p_iv z_iv,  p = exp(z - lse)
  *   top_log_probs, top_indices [rows, top], top up to 32 and cols: the largest logits in order, equal ones by their index
