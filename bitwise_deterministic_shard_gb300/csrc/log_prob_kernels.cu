@@ -218,34 +218,23 @@ struct Candidates {
     raise(least);
     passed = max(passed, least);
   }
-  // a step's elements; big: the lane's largest; first: index of the warp's first vector
-  template <typename T>
-  __device__ __forceinline__ void add(const Run<T, Elem<T>::VEC> (&x)[NV], float big, uint32_t first) {
-    constexpr int VEC = Elem<T>::VEC;
+  // What reaches the value in a step; big: the lane's largest; at(j): the j-th of a lane's elements, as (whether the row has it, its
+  // index).  They are read again, a lane's by the whole warp: the step's registers may hold the next one's.
+  template <int L, typename T, typename At>
+  __device__ __forceinline__ void add(const T* row, float big, At at) {
     uint32_t who = __ballot_sync(0xffffffffu, big >= reach);
     passed = 0;
 #pragma unroll 1
-    while (who) {   // a lane's elements are looked at by as many lanes
-      const int src = __ffs(who) - 1, e = lane % VEC, mine = lane / VEC;
+    while (who) {
+      const int src = __ffs(who) - 1;
       who &= who - 1;
-      uint32_t word = 0;
-#pragma unroll
-      for (int i = 0; i < NV; i++) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) w[j] = __shfl_sync(0xffffffffu, x[i].w[j], src);
-        const int j = VEC == 8 ? e >> 1 : e;
-        const uint32_t at = j & 2 ? j & 1 ? w[3] : w[2] : j & 1 ? w[1] : w[0];
-        if (mine == i) word = at;
-      }
-      float y;
-      if constexpr (VEC == 4) y = __uint_as_float(word);
-      else if constexpr (std::is_same<T, __nv_bfloat16>::value) y = __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
-      else y = __half2float(__ushort_as_half((uint16_t)(e & 1 ? word >> 16 : word)));
+      uint32_t index = 0;
+      float y = -INFINITY;
+      if (lane < L && at(src, lane, index)) y = Elem<T>::get(row[index]);
       if (count > CAP - 32) cut();
-      const bool is = mine < NV && y >= reach;
+      const bool is = y >= reach;                          // above -inf
       const uint32_t m = __ballot_sync(0xffffffffu, is);
-      if (is) sh.cand[warp][count + __popc(m & ((1u << lane) - 1))] = key_of(y, first + (mine * 32 * W + src) * VEC + e);
+      if (is) sh.cand[warp][count + __popc(m & ((1u << lane) - 1))] = key_of(y, index);
       count += __popc(m);
     }
     // elements of later steps have larger indices than the `top` that reach what the list was cut to
@@ -284,7 +273,7 @@ __device__ __forceinline__ uint32_t leader(uint32_t addr) {
 
 // W warps a CTA; parts: CTAs (a cluster) of a row
 template <typename T, int W, bool TOP>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __grid_constant__ LpArgs a, int parts) {
+__global__ void __launch_bounds__(32 * W, W == 1 ? 16 : 4) lp_kernel(const __grid_constant__ LpArgs a, int parts) {
   constexpr int VEC = Elem<T>::VEC, G = 32 * W;
   __shared__ Sums sums[W], joins[8];     // of the warps; of a cluster's parts
   __shared__ std::conditional_t<TOP, Shared<W>, int> sh;
@@ -353,33 +342,44 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 16) lp_kernel(const __gri
   constexpr uint32_t STEP = NV * G;
   Run<T, VEC> x0[NV], x1[NV];
   load(x0, v0);
-  const auto steps = [&](auto each) {
+  const auto steps = [&](auto begin, auto after) {
+    float big[2] = {most(x0), -INFINITY};
+    begin(big[0]);
     for (uint32_t v = v0; v < v1; v += 2 * STEP) {
       load(x1, min(v + STEP, v1));
-      each(x0, v);
-      if (v + STEP >= v1) break;
+      big[0] = most(x0);
+      sum(x0, big[0]);
       load(x0, min(v + 2 * STEP, v1));
-      each(x1, v + STEP);
+      big[1] = most(x1);
+      if (v + STEP < v1) sum(x1, big[1]);
+      after(v, big);
     }
   };
   if constexpr (TOP) {
     Candidates<W> cand(sh, a.top, warp, lane);
-    cand.begin(most(x0));
-    steps([&](const Run<T, VEC> (&x)[NV], uint32_t v) {
-      const float big = most(x);
-      sum(x, big);
-      cand.refresh();
-      if (__any_sync(0xffffffffu, big >= cand.reach)) {
-        if (v > v0) {
-          cand.see(big);
-          cand.common();
-        }
-        cand.template add<T>(x, big, (v + warp * 32) * VEC - off);
-      }
-    });
+    steps([&](float big) { cand.begin(big); },
+          [&](uint32_t v, const float (&big)[2]) {
+#pragma unroll 1
+            for (int s = 0; s < 2; s++) {
+              const float most = s ? big[1] : big[0];
+              cand.refresh();
+              if (!__any_sync(0xffffffffu, most >= cand.reach)) continue;
+              const uint32_t first = v + s * STEP;
+              if (first > v0) {
+                cand.see(most);
+                cand.common();
+              }
+              cand.template add<NV * VEC>(row, most, [&](int src, int j, uint32_t& index) {
+                const uint32_t at = first + (j / VEC) * G + warp * 32 + src;
+                const int64_t i = (int64_t)at * VEC - off + j % VEC;
+                index = (uint32_t)i;
+                return at < v1 && i >= 0 && i < a.cols;
+              });
+            }
+          });
     cand.finish();
   } else {
-    steps([&](const Run<T, VEC> (&x)[NV], uint32_t) { sum(x, most(x)); });
+    steps([](float) {}, [](uint32_t, const float (&)[2]) {});
   }
 
   float s0, s1, e0, e1;
