@@ -156,7 +156,7 @@ DA_EXPORT int dgl_forward(const da_matrix* x, const da_matrix* wg, const da_matr
 }
 
 DA_EXPORT size_t dgl_workspace_bytes(int64_t tokens, int64_t hidden) {
-  return tokens < 0 || hidden < 0 || tokens > kMaxRows || hidden > kMaxRows ? 0 : round_up((size_t)4 * tokens * hidden);
+  return tokens < 0 || hidden < 0 || tokens > kMaxRows || hidden > kMaxRows ? 0 : round_up((size_t)4 * tokens * gl_grad_row(hidden));
 }
 
 DA_EXPORT int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_matrix* wg, const da_matrix* wu, const void* saved,
@@ -187,8 +187,9 @@ DA_EXPORT int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_mat
   std::memset(&a, 0, sizeof(a));
   a.T = (int)T; a.D = (int)D; a.F = (int)F;
   a.status = dev_status;
+  const int64_t row = gl_grad_row(F);
   if (!tensor_map(&a.x, *x) || !tensor_map(&a.wg, *wg) || !tensor_map(&a.wu, *wu) ||
-      !tensor_map(&a.dg, dg, x->dtype, T, F, F) || !tensor_map(&a.du, dg + T * F, x->dtype, T, F, F))
+      !tensor_map(&a.dg, dg, x->dtype, T, F, row) || !tensor_map(&a.du, dg + T * row, x->dtype, T, F, row))
     return DA_ECUDA;
   if (dx) a.dx = const_cast<void*>(dx->ptr), a.dxs = stride(*dx);
   if (dwg) {

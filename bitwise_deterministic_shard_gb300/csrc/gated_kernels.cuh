@@ -32,6 +32,24 @@ constexpr float LOG2E = 1.4426950408889634f;
 // act(g) and act'(g), ACT a DGL_* code.  With s the logistic function: silu g s(g); gelu g Phi(g); its tanh form g s(2 y),
 // y = sqrt(2 / pi) (g + 0.044715 g^3), as (1 + tanh y) / 2 = s(2 y) has no cancellation.
 __device__ __forceinline__ float logistic(float x) { return rcp(1.f + ex2(-LOG2E * x)); }
+// Phi(g) = erfc(-g / sqrt 2) / 2, by erfc(z) = t 2^(P(t) - z^2 log2 e) for z >= 0, t = 2 / (2 + z): P of degree 9, fitted to log2(erfc(z)
+// e^(z^2) / t) for the least greatest error (7.5e-8 of the value, so the tail keeps its digits; least squares with weights moved
+// toward the largest errors).  CUDA's normcdff has branches and made the kernel wait for its results: 8192 hidden units, width
+// 2048, 4096 tokens 190 us, the products alone 144.
+__device__ __forceinline__ float normal_cdf(float g) {
+  const float t = rcp(__fmaf_rn(0.35355339059f, fabsf(g), 1.f));
+  float p = __fmaf_rn(0x1.0202b8p-2f, t, -0x1.363d26p+0f);
+  p = __fmaf_rn(p, t, 0x1.19707ep+1f);
+  p = __fmaf_rn(p, t, -0x1.b18d14p+0f);
+  p = __fmaf_rn(p, t, 0x1.c0f0d6p-2f);
+  p = __fmaf_rn(p, t, -0x1.21a9b2p-2f);
+  p = __fmaf_rn(p, t, 0x1.249cb4p-3f);
+  p = __fmaf_rn(p, t, 0x1.141e74p-1f);
+  p = __fmaf_rn(p, t, 0x1.71583ap+0f);
+  p = __fmaf_rn(p, t, -0x1.d36442p+0f);
+  const float e = 0.5f * t * ex2(__fmaf_rn(-0.5f * LOG2E * g, g, p));
+  return g < 0.f ? e : 1.f - e;
+}
 template <int ACT>
 __device__ __forceinline__ void activate(float g, float& a, float& d) {
   if constexpr (ACT == DGL_SILU) {
@@ -39,7 +57,7 @@ __device__ __forceinline__ void activate(float g, float& a, float& d) {
     a = g * s;
     d = s * __fmaf_rn(g, 1.f - s, 1.f);
   } else if constexpr (ACT == DGL_GELU) {
-    const float s = normcdff(g);
+    const float s = normal_cdf(g);
     a = g * s;
     d = __fmaf_rn(g * 0.3989422804014327f, ex2(-0.5f * LOG2E * g * g), s);
   } else if constexpr (ACT == DGL_GELU_TANH) {
@@ -56,19 +74,19 @@ __device__ __forceinline__ void activate(float g, float& a, float& d) {
 
 // copies of N boxes of 64 rows from row r on, contracted elements [k, k + 64): K-major
 template <int N>
-__device__ __forceinline__ void copy_k(uint32_t to, const CUtensorMap* m, int k, int r, uint32_t bar) {
+__device__ __forceinline__ void copy_k(uint32_t to, const CUtensorMap* m, int k, int r, uint32_t bar, uint32_t one) {
 #pragma unroll
-  for (int i = 0; i < N; i++) pair::load2(to + i * pair::BOX, m, k, r + 64 * i, bar);
+  for (int i = 0; i < N; i++) pair::load2(to + i * pair::BOX, m, k, r + 64 * i, bar, one);
 }
 // and of N panels of 64 columns from c on: MN-major
 template <int N>
-__device__ __forceinline__ void copy_mn(uint32_t to, const CUtensorMap* m, int k, int c, uint32_t bar) {
+__device__ __forceinline__ void copy_mn(uint32_t to, const CUtensorMap* m, int k, int c, uint32_t bar, uint32_t one) {
 #pragma unroll
-  for (int i = 0; i < N; i++) pair::load2(to + i * pair::BOX, m, c + 64 * i, k, bar);
+  for (int i = 0; i < N; i++) pair::load2(to + i * pair::BOX, m, c + 64 * i, k, bar, one);
 }
 
 // ---- forward ----
-// The factors' rows are staged in shared memory, 32 columns at a time, and written 64 bytes a row by neighbouring lanes: a
+// Results are staged in shared memory, here 32 columns of h and the factors at a time, and written 64 bytes a row by neighbouring lanes: a
 // lane that wrote its own row's pieces would touch 32 lines an instruction (8192 tokens, width 2048, 8192 hidden units: 555 us; the
 // products alone take 300).
 template <bool SAVE>
@@ -107,7 +125,7 @@ __global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl
   __shared__ pair::Shared sh;
   constexpr int HALF = TN / 2;
   const int mt = (a.T + 255) / 256, nt = (a.F + HALF - 1) / HALF, steps = (a.D + pair::BK - 1) / pair::BK;
-  const uint32_t rank = pair::cta_rank();
+  const uint32_t rank = tc5::same(pair::cta_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CUtensorMap* const w = rank ? &a.wu : &a.wg;
   pair::run<BF, TN, STAGED<SAVE>, false>(
@@ -117,9 +135,9 @@ __global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl
         return t < mt * nt ? pair::tile_of(t, mt, nt, 0, steps) : pair::Tile{0, 0, 0, 0};
       },
       [](int) { return false; },
-      [&](const pair::Tile& t, int k, uint32_t A, uint32_t B, uint32_t bar) {
-        copy_k<2>(A, &a.x, k * pair::BK, t.m * 256 + rank * 128, bar);
-        copy_k<HALF / 64>(B, w, k * pair::BK, t.n * HALF, bar);
+      [&](const pair::Tile& t, int k, uint32_t A, uint32_t B, uint32_t bar, uint32_t one) {
+        copy_k<2>(A, &a.x, k * pair::BK, t.m * 256 + rank * 128, bar, one);
+        copy_k<HALF / 64>(B, w, k * pair::BK, t.n * HALF, bar, one);
       },
       [&](const pair::Tile& t, uint32_t tm, uint32_t extra, auto release) {
         const int row0 = t.m * 256 + rank * 128 + (warp & 3) * 32, row = row0 + lane;
@@ -224,9 +242,9 @@ __global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl
   const int nx = a.dx ? tt * nt : 0, nw = a.dwg ? 2 * ft * nt : 0, sx = 2 * half, sw = (a.T + pair::BK - 1) / pair::BK;
   const bool x_first = sx >= sw;
   const Shares shares = x_first ? Shares{nx, nw, sx / sw} : Shares{nw, nx, sw / sx};
-  const uint32_t rank = pair::cta_rank();
+  const uint32_t rank = tc5::same(pair::cta_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pair::run<BF, TN, 0, true>(
+  pair::run<BF, TN, STAGED<true>, true>(
       sh, raw, a.status,
       [&](int j) {
         const int t = share(shares, j, blockIdx.x >> 1, gridDim.x >> 1);
@@ -236,39 +254,48 @@ __global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl
         return first == x_first ? pair::tile_of(i, tt, nt, DX, sx) : pair::tile_of(i, 2 * ft, nt, DW, sw);
       },
       [](int kind) { return kind == DW; },
-      [&](const pair::Tile& t, int k, uint32_t A, uint32_t B, uint32_t bar) {
+      [&](const pair::Tile& t, int k, uint32_t A, uint32_t B, uint32_t bar, uint32_t one) {
         const int c = t.n * TN + rank * (TN / 2);
         if (t.kind == DX) {
           const bool u = k >= half;
           const int k0 = (u ? k - half : k) * pair::BK;
-          copy_k<2>(A, u ? &a.du : &a.dg, k0, t.m * 256 + rank * 128, bar);
-          copy_mn<TN / 128>(B, u ? &a.wu : &a.wg, k0, c, bar);
+          copy_k<2>(A, u ? &a.du : &a.dg, k0, t.m * 256 + rank * 128, bar, one);
+          copy_mn<TN / 128>(B, u ? &a.wu : &a.wg, k0, c, bar, one);
         } else {
           const bool u = t.m >= ft;
-          copy_mn<2>(A, u ? &a.du : &a.dg, k * pair::BK, (u ? t.m - ft : t.m) * 256 + rank * 128, bar);
-          copy_mn<TN / 128>(B, &a.x, k * pair::BK, c, bar);
+          copy_mn<2>(A, u ? &a.du : &a.dg, k * pair::BK, (u ? t.m - ft : t.m) * 256 + rank * 128, bar, one);
+          copy_mn<TN / 128>(B, &a.x, k * pair::BK, c, bar, one);
         }
       },
-      [&](const pair::Tile& t, uint32_t tm, uint32_t, auto release) {
+      [&](const pair::Tile& t, uint32_t tm, uint32_t extra, auto release) {
         const bool u = t.kind == DW && t.m >= ft;
-        const int row = (u ? t.m - ft : t.m) * 256 + rank * 128 + (warp & 3) * 32 + lane;
-        const bool live = row < (t.kind == DX ? a.T : a.F);
-        uint16_t* const out = static_cast<uint16_t*>(t.kind == DX ? a.dx : u ? a.dwu : a.dwg) +
-                              row * (t.kind == DX ? a.dxs : u ? a.dwus : a.dwgs);
+        const int row0 = (u ? t.m - ft : t.m) * 256 + rank * 128 + (warp & 3) * 32, rows = t.kind == DX ? a.T : a.F;
+        uint16_t* const out = static_cast<uint16_t*>(t.kind == DX ? a.dx : u ? a.dwu : a.dwg);
+        const int64_t stride = t.kind == DX ? a.dxs : u ? a.dwus : a.dwgs;
+        const uint32_t stage = extra + warp * 4096;
+        const int un = lane & 7;
 #pragma unroll
-        for (int c = 0; c < TN / 2; c += 32) {
+        for (int c = 0; c < TN / 2; c += 64) {
           const int cc = (warp >> 2) * (TN / 2) + c, col = t.n * TN + cc;
-          float v[32];
           __syncwarp();   // the loads are the whole warp's
-          ld_x32(tm + cc, v);
-          ld_wait();
-          if (c == TN / 2 - 32) release();
-          if (live) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              if (col + e < a.D)
-                *reinterpret_cast<uint4*>(out + col + e) = make_uint4(pack16<BF>(v[e], v[e + 1]), pack16<BF>(v[e + 2], v[e + 3]),
-                                                                      pack16<BF>(v[e + 4], v[e + 5]), pack16<BF>(v[e + 6], v[e + 7]));
+          for (int h = 0; h < 64; h += 32) {
+            float v[32];
+            ld_x32(tm + cc + h, v);
+            ld_wait();
+            if (c + h == TN / 2 - 32) release();
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              stage_put(stage, lane, h / 8 + j,
+                        make_uint4(pack16<BF>(v[8 * j], v[8 * j + 1]), pack16<BF>(v[8 * j + 2], v[8 * j + 3]),
+                                   pack16<BF>(v[8 * j + 4], v[8 * j + 5]), pack16<BF>(v[8 * j + 6], v[8 * j + 7])));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int it = 0; it < 8; it++) {
+            const int r = it * 4 + (lane >> 3);
+            const uint4 v = stage_get(stage, r, un);
+            if (row0 + r < rows && col + un * 8 < a.D) *reinterpret_cast<uint4*>(out + (row0 + r) * stride + col + un * 8) = v;
           }
         }
       });
@@ -333,7 +360,7 @@ __global__ void __launch_bounds__(256) gl_few_kernel(const GlFewArgs a) {
 template <bool BF>
 __global__ void __launch_bounds__(256) gl_scale_kernel(const GlScaleArgs a) {
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-  const int64_t fp = gl_saved_row(a.F), n = a.T * fp, per = a.F / 8, all = a.T * per;
+  const int64_t fp = gl_saved_row(a.F), n = a.T * fp, per = a.F / 8, all = a.T * per, dp = gl_grad_row(a.F);
   T* const dg = static_cast<T*>(a.dg);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / per, col = (i - row * per) * 8, at = row * fp + col;
@@ -350,7 +377,7 @@ __global__ void __launch_bounds__(256) gl_scale_kernel(const GlScaleArgs a) {
         v[e] = r.get(e) * __uint_as_float((h[e >> 1] >> (16 * (e & 1)) << 16) | ((e < 4 ? lo.x : lo.y) >> (8 * (e & 3)) & 255) << 8);
       Run<T, 8> o;
       o.set(v);
-      o.store(dg + w * a.T * a.F + 8 * i);
+      o.store(dg + (w * a.T + row) * dp + col);
     }
   }
 }
@@ -371,17 +398,19 @@ cudaError_t forward_as(const GlArgs& a, int64_t tiles, cudaStream_t st) {
   static DeviceOnce once;
   return launch_pairs(once, gl_fwd_kernel<BF, ACT, SAVE, TN>, pair::Ring<TN, STAGED<SAVE>>::SMEM, tiles, PAIRS, a, st);
 }
-// The tile: rounds of pairs times a tile's time, a narrow one 0.6 of a wide one (its products take half, its copies 0.75).
+// The tile: rounds of pairs times a tile's time.  A narrow one's is 0.7 of a wide one's (its products take half, its copies 0.75); where
+// there is one row of tiles, and each weight comes from HBM for one pair, 0.55 (128 tokens, width 4096, 12288 hidden units: three
+// rounds of narrow tiles 41 us, two of wide ones 50).
 template <bool BF, int ACT, bool SAVE>
 cudaError_t forward_of(const GlArgs& a, cudaStream_t st) {
   const int64_t mt = ceil_div(a.T, 256), wide = mt * ceil_div(a.F, 128), narrow = mt * ceil_div(a.F, 64);
-  if (5 * ceil_div(wide, PAIRS) > 3 * ceil_div(narrow, PAIRS)) return forward_as<BF, ACT, SAVE, 128>(a, narrow, st);
+  if (100 * ceil_div(wide, PAIRS) > (mt == 1 ? 55 : 70) * ceil_div(narrow, PAIRS)) return forward_as<BF, ACT, SAVE, 128>(a, narrow, st);
   return forward_as<BF, ACT, SAVE, 256>(a, wide, st);
 }
 template <bool BF, int TN>
 cudaError_t backward_as(const GlArgs& a, int64_t tiles, cudaStream_t st) {
   static DeviceOnce once;
-  return launch_pairs(once, gl_bwd_kernel<BF, TN>, pair::Ring<TN, 0>::SMEM, tiles, PAIRS, a, st);
+  return launch_pairs(once, gl_bwd_kernel<BF, TN>, pair::Ring<TN, STAGED<true>>::SMEM, tiles, PAIRS, a, st);
 }
 template <bool BF, int ACT>
 cudaError_t few_of(const GlFewArgs& a, cudaStream_t st) {
@@ -436,7 +465,7 @@ cudaError_t gl_backward(const GlArgs& a, cudaStream_t st) {
     const int64_t even = ceil_div(nx * sx + nw * sw, PAIRS), first = x ? ceil_div(nx, PAIRS) * sx : ceil_div(nw, PAIRS) * sw;
     most[i] = even > first ? even : first;
   }
-  return 5 * most[0] > 3 * most[1] ? backward_as<BF, 128>(a, tiles[1], st) : backward_as<BF, 256>(a, tiles[0], st);
+  return 10 * most[0] > 7 * most[1] ? backward_as<BF, 128>(a, tiles[1], st) : backward_as<BF, 256>(a, tiles[0], st);
 }
 template <bool BF>
 cudaError_t gl_scale(const GlScaleArgs& a, cudaStream_t st) {

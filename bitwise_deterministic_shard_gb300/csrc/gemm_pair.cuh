@@ -51,20 +51,15 @@ __device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// A bounded wait whose arrivals may come from the other CTA.
+// A bounded wait.  Arrivals may come from the other CTA; what they stand for (copies, products, sums taken from TMEM) is not plain
+// memory, so the wait takes no scope beyond the CTA.
+// A whole warp calls it; the answer is the same in all lanes.
 __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint32_t at = tc5::smem_addr(bar);
-  uint64_t t0 = 0;
-  for (uint32_t it = 0; it < (1u << 30); it++) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (it == 0) t0 = tc5::globaltimer();
-    if ((it & 15) == 15 && (*abort || tc5::globaltimer() - t0 > tc5::WAIT_NS)) break;
+  if (tc5::all_of(tc5::mbar_try(bar, parity))) return true;
+  const uint64_t t0 = tc5::globaltimer();
+  for (uint32_t it = 1; it < (1u << 30); it++) {
+    if (tc5::all_of(tc5::mbar_try(bar, parity))) return true;
+    if ((it & 15) == 0 && tc5::all_of(*abort || tc5::globaltimer() - t0 > tc5::WAIT_NS)) break;
   }
   *abort = 1;
   return false;
@@ -77,11 +72,20 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {   //
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols));
 }
-// box of a rank-2 tensor map -> this CTA's shared memory, completion counted on a barrier of the leader
-__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t leader_bar) {
+// box of a rank-2 tensor map -> this CTA's shared memory, completion counted on a barrier of the leader; by the one lane of a warp
+// that runs it together (tc5_tile.cuh: operands in uniform registers)
+__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t leader_bar, uint32_t one) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(leader_bar)
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(leader_bar), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void expect_one(uint64_t* bar, uint32_t bytes, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(tc5::smem_addr(bar)),
+      "r"(bytes), "r"(one)
       : "memory");
 }
 // D[tmem of both] (+)= A[both CTAs' smem] * B[both CTAs' smem]; issued by one lane of the leader
@@ -131,7 +135,8 @@ __device__ __forceinline__ Tile tile_of(int t, int mt, int nt, int kind, int ste
 
 // The products of this pair's tiles.
 //   tile(j): the pair's j-th Tile
-//   load(tile, step, a, b, leader_bar): copies this CTA's halves of a step (2 and TN / 128 boxes) to the addresses a and b
+//   load(tile, step, a, b, leader_bar, one): copies this CTA's halves of a step (2 and TN / 128 boxes) to the addresses a and b; a
+//     whole warp calls it, `one` in the lane that is to issue them
 //   take(tile, columns, extra, release): takes a tile's sums; columns: TMEM address of this warp's lanes; extra: address of the
 //     shared memory beside the ring; calls release() when it has read them
 // a_mn(kind): whether A is MN-major; B is with B_MN.
@@ -166,47 +171,57 @@ __device__ __forceinline__ void run(Shared& sh, unsigned char* raw, int32_t* sta
   const uint32_t tmem = sh.tmem;
 
   if (warp == TAKERS) {
-    if (lane == 0) {
-      int k = 0;
-      bool ok = true;
-      for (int j = 0; ok; j++) {
-        const Tile t = tile(j);
-        if (t.steps == 0) break;
-        for (int n = 0; n < t.steps; n++, k++) {
-          const int s = k % STAGES;
-          if (k >= STAGES && !(ok = wait_pair(&sh.empty[s], (k / STAGES - 1) & 1, abort))) break;
-          const uint32_t at = base + s * R::STAGE;
-          if (rank == 0) mbar_expect_tx(&sh.full[s], 2 * R::STAGE);
-          load(t, n, at, at + R::A, at_leader(smem_addr(&sh.full[s])));
+    const uint32_t one = elect(), first = one && rank == 0, ring = same(base), bars = same(at_leader(smem_addr(&sh.full[0])));
+    int s = 0, used = 0;       // the stage and how many are in use; round: the fills of the present stage before
+    uint32_t round = 0;
+    bool ok = true;
+    for (int j = 0; ok; j++) {
+      const Tile t = tile(j);
+      const int steps = same(t.steps);
+      if (steps == 0) break;
+      for (int n = 0; n < steps; n++) {
+        if (round > 0 && !(ok = wait_pair(&sh.empty[s], (round - 1) & 1, abort))) break;
+        const uint32_t at = ring + s * R::STAGE;
+        expect_one(&sh.full[s], 2 * R::STAGE, first);
+        load(t, n, at, at + R::A, bars + s * 8, one);
+        if (++s == STAGES) {
+          s = 0;
+          round++;
         }
+        used = round > 0 ? STAGES : s;
       }
-      // every step's products are done, so nothing is in flight when the CTA ends
-      for (int j = max(0, k - STAGES); j < k && ok; j++) ok = wait_pair(&sh.empty[j % STAGES], (j / STAGES) & 1, abort);
-      if (!ok)   // given up: what was copied arrives at the leader
-        for (int j = max(0, k - STAGES); j < k && rank == 0; j++) mbar_drain(&sh.full[j % STAGES], (j / STAGES) & 1);
+    }
+    // every step's products are done, so nothing is in flight when the CTA ends; given up: what was copied arrives at the leader
+    for (int j = 0; j < used; j++) {
+      const uint32_t last = (round - (j >= s)) & 1;   // of the stage's last fill
+      if (ok) ok = wait_pair(&sh.empty[j], last, abort);
+      if (!ok && rank == 0) mbar_drain(&sh.full[j], last);
     }
   } else if (warp == TAKERS + 1) {
     if (rank == 0) {
-      const uint32_t one = elect(), tm = same(tmem);
-      int k = 0;
+      const uint32_t one = elect(), tm = same(tmem), ring = same(base);
+      int s = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int i = 0; ok; i++) {
         const Tile t = tile(i);
         const int steps = same(t.steps);
         if (steps == 0) break;
         const bool mn = a_mn(same(t.kind));
-        const uint32_t id = idesc<BF, TN>(mn, B_MN), sa = desc_step(mn), sb = desc_step(B_MN);
-        if (i >= 2 && !(ok = all_of(wait_pair(&sh.taken[i & 1], ((i >> 1) - 1) & 1, abort)))) break;
+        const uint32_t id = idesc<BF, TN>(mn, B_MN), sa = desc_step(mn), sb = desc_step(B_MN), d = tm + (i & 1) * TN;
+        if (i >= 2 && !(ok = wait_pair(&sh.taken[i & 1], ((i >> 1) - 1) & 1, abort))) break;
         fence_after();
-        for (int n = 0; n < steps; n++, k++) {
-          const int s = same(k % STAGES);
-          if (!(ok = all_of(wait_pair(&sh.full[s], (k / STAGES) & 1, abort)))) break;
+        for (int n = 0; n < steps; n++) {
+          if (!(ok = wait_pair(&sh.full[s], phase, abort))) break;
           fence_after();
-          const uint32_t at = same(base) + s * R::STAGE, da = desc_lo(at, mn), db = desc_lo(at + R::A, B_MN);
+          const uint32_t at = ring + s * R::STAGE, da = desc_lo(at, mn), db = desc_lo(at + R::A, B_MN);
 #pragma unroll
-          for (int j = 0; j < BK / 16; j++)
-            mma(tm + (i & 1) * TN, desc_of(da + j * sa), desc_of(db + j * sb), id, n > 0 || j > 0, one);
+          for (int j = 0; j < BK / 16; j++) mma(d, desc_of(da + j * sa), desc_of(db + j * sb), id, n > 0 || j > 0, one);
           commit_both(&sh.empty[s], one);
+          if (++s == STAGES) {
+            s = 0;
+            phase ^= 1;
+          }
         }
         if (ok) commit_both(&sh.done[i & 1], one);
       }
@@ -214,7 +229,7 @@ __device__ __forceinline__ void run(Shared& sh, unsigned char* raw, int32_t* sta
   } else {
     for (int i = 0;; i++) {
       const Tile t = tile(i);
-      if (t.steps == 0 || !all_of(wait_pair(&sh.done[i & 1], (i >> 1) & 1, abort))) break;
+      if (t.steps == 0 || !wait_pair(&sh.done[i & 1], (i >> 1) & 1, abort)) break;
       fence_after();
       const uint32_t bar = at_leader(smem_addr(&sh.taken[i & 1]));
       take(t, tmem + ((uint32_t)(warp & 3) << 21) + (i & 1) * TN, base + STAGES * R::STAGE, [&] {
