@@ -178,6 +178,7 @@ __device__ __forceinline__ void find_chunk(const EmArgs& a, const uint32_t* key,
 }
 
 __global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_constant__ EmArgs a, int passes, int bits) {
+  next_may_start();
   if (blockIdx.x > 0) {
     fill_zeros<SORT_THREADS>(a, blockIdx.x - 1, gridDim.x - 1);
     return;
@@ -352,6 +353,7 @@ __global__ void __launch_bounds__(RADIX_THREADS) em_scatter_kernel(const __grid_
 
 // ---- chunks of longer ones ----
 __global__ void __launch_bounds__(256) em_chunk_kernel(const __grid_constant__ EmArgs a, int from) {
+  next_may_start();
   find_chunk(a, a.key[from], (int64_t)blockIdx.x * 256 + threadIdx.x, a.n, a.found);
 }
 // Where a chunk of several leaves its sum: full ones start at least a chunk apart, and so do the last ones of their rows.
@@ -446,10 +448,12 @@ __device__ __forceinline__ void sum_chunk(const EmArgs& a, uint4 unit, int64_t c
     }
   }
 }
-constexpr int SUM_CTAS = 152 * 4;
+constexpr int SUM_CTAS = 152 * 3;   // as many as fit
 template <typename T, bool AL>
 __global__ void __launch_bounds__(256, 3) em_sum_kernel(const __grid_constant__ EmArgs a, int from) {
   constexpr int RUN = 32 * (AL ? Elem<T>::VEC : 4), WIDE = 4;
+  after_previous();
+  next_may_start();
   const EmUnits found = *a.found;
   const int64_t narrow = (a.cols + RUN - 1) / RUN, wide = (a.cols + WIDE * RUN - 1) / (WIDE * RUN);
   const int64_t many = found.many * narrow, all = many + found.few * wide, warps = (int64_t)gridDim.x * 8;
@@ -464,6 +468,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ EmArgs a) {
   __shared__ float sums[8][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  after_previous();
   const int64_t pieces = (a.cols + 127) / 128, all = a.found->rows * pieces;
   for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
     const uint4 row = a.row[w / pieces];
@@ -514,10 +519,9 @@ template <typename T, bool AL>
 cudaError_t sums(const EmArgs& a, int from, cudaStream_t st) {
   constexpr int RUN = 32 * (AL ? Elem<T>::VEC : 4);
   const int64_t most = a.n * ((a.cols + RUN - 1) / RUN);   // warps' items
-  em_sum_kernel<T, AL><<<(unsigned)std::min<int64_t>(SUM_CTAS, (most + 7) / 8), 256, 0, st>>>(a, from);
-  if (a.n > EM_CHUNK)
-    em_join_kernel<T><<<(unsigned)std::min<int64_t>(152 * 2, a.n / EM_CHUNK * ((a.cols + 127) / 128)), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e = launch_early(em_sum_kernel<T, AL>, dim3((unsigned)std::min<int64_t>(SUM_CTAS, (most + 7) / 8)), 256, 0, st, a, from);
+  if (e != cudaSuccess || a.n <= EM_CHUNK) return e;
+  return launch_early(em_join_kernel<T>, dim3((unsigned)std::min<int64_t>(152 * 2, a.n / EM_CHUNK * ((a.cols + 127) / 128))), 256, 0, st, a);
 }
 template <typename T>
 cudaError_t gradient(const EmArgs& a, int from, cudaStream_t st) {

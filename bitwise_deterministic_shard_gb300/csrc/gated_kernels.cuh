@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(256) gl_scale_kernel(const GlScaleArgs a) {
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
   const int64_t fp = gl_saved_row(a.F), n = a.T * fp, per = a.F / 8, all = a.T * per, dp = gl_grad_row(a.F);
   T* const dg = static_cast<T*>(a.dg);
+  next_may_start();
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / per, col = (i - row * per) * 8, at = row * fp + col;
     Run<T, 8> r;
@@ -382,13 +383,6 @@ __global__ void __launch_bounds__(256) gl_scale_kernel(const GlScaleArgs a) {
   }
 }
 
-template <typename K>
-cudaError_t launch_pairs(DeviceOnce& once, K kernel, int smem, int64_t tiles, int pairs, const GlArgs& a, cudaStream_t st) {
-  const cudaError_t e = allow_smem(once, kernel, smem);
-  if (e != cudaSuccess) return e;
-  kernel<<<2 * (int)(tiles < pairs ? tiles : pairs), pair::THREADS, smem, st>>>(a);
-  return cudaGetLastError();
-}
 constexpr int PAIRS = 152 / 2;   // of the GPU this is written for: the choice of the tile, and with it no bit, depends on it
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -396,7 +390,11 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 template <bool BF, int ACT, bool SAVE, int TN>
 cudaError_t forward_as(const GlArgs& a, int64_t tiles, cudaStream_t st) {
   static DeviceOnce once;
-  return launch_pairs(once, gl_fwd_kernel<BF, ACT, SAVE, TN>, pair::Ring<TN, STAGED<SAVE>>::SMEM, tiles, PAIRS, a, st);
+  constexpr int smem = pair::Ring<TN, STAGED<SAVE>>::SMEM;
+  const cudaError_t e = allow_smem(once, gl_fwd_kernel<BF, ACT, SAVE, TN>, smem);
+  if (e != cudaSuccess) return e;
+  gl_fwd_kernel<BF, ACT, SAVE, TN><<<2 * (unsigned)(tiles < PAIRS ? tiles : PAIRS), pair::THREADS, smem, st>>>(a);
+  return cudaGetLastError();
 }
 // The tile: rounds of pairs times a tile's time.  A narrow one's is 0.7 of a wide one's (its products take half, its copies 0.75); where
 // there is one row of tiles, and each weight comes from HBM for one pair, 0.55 (128 tokens, width 4096, 12288 hidden units: three
@@ -410,7 +408,10 @@ cudaError_t forward_of(const GlArgs& a, cudaStream_t st) {
 template <bool BF, int TN>
 cudaError_t backward_as(const GlArgs& a, int64_t tiles, cudaStream_t st) {
   static DeviceOnce once;
-  return launch_pairs(once, gl_bwd_kernel<BF, TN>, pair::Ring<TN, STAGED<true>>::SMEM, tiles, PAIRS, a, st);
+  constexpr int smem = pair::Ring<TN, STAGED<true>>::SMEM;
+  const cudaError_t e = allow_smem(once, gl_bwd_kernel<BF, TN>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_early(gl_bwd_kernel<BF, TN>, dim3(2 * (unsigned)(tiles < PAIRS ? tiles : PAIRS)), pair::THREADS, smem, st, a);
 }
 template <bool BF, int ACT>
 cudaError_t few_of(const GlFewArgs& a, cudaStream_t st) {

@@ -16,6 +16,7 @@
 // 64 elements) or over the rows (MN-major: panels of 64 rows of 64 elements), so no operand is ever transposed.  All copies are boxes
 // of 64 x 64 elements: 8 KB, a panel, or 64 rows of a K-major operand.
 #pragma once
+#include "device_once.h"
 #include "tc5_tile.cuh"
 
 namespace detattn {
@@ -169,6 +170,7 @@ __device__ __forceinline__ void run(Shared& sh, unsigned char* raw, int32_t* sta
   cluster_sync();
   fence_after();
   const uint32_t tmem = sh.tmem;
+  after_previous();
 
   if (warp == TAKERS) {
     const uint32_t one = elect(), first = one && rank == 0, ring = same(base), bars = same(at_leader(smem_addr(&sh.full[0])));
