@@ -22,7 +22,7 @@
 // result.  (A value from each warp's ceil(top / warps)-th largest instead let ten times as many through: 4096 x 128256 f32, 5
 // alternatives, 604 us against 312 without alternatives.)
 //
-// A row is one CTA's; short rows a warp's; where few rows would leave SMs idle, a cluster's, whose parts hand their sums and
+// A row is one CTA's of one to eight warps; where few rows would leave SMs idle, a cluster's, whose parts hand their sums and
 // lists to the first CTA through distributed shared memory.  The order of the sums depends on the sizes, the type and what
 // starts on 16 bytes.
 #include <algorithm>
@@ -271,9 +271,9 @@ __device__ __forceinline__ uint32_t leader(uint32_t addr) {
   return r;
 }
 
-// W warps a CTA; parts: CTAs (a cluster) of a row
+// W warps a CTA; parts: CTAs (a cluster, with 8 warps) of a row
 template <typename T, int W, bool TOP>
-__global__ void __launch_bounds__(32 * W, W == 1 ? 16 : 4) lp_kernel(const __grid_constant__ LpArgs a, int parts) {
+__global__ void __launch_bounds__(32 * W, W == 1 ? 24 : 32 / W) lp_kernel(const __grid_constant__ LpArgs a, int parts) {
   constexpr int VEC = Elem<T>::VEC, G = 32 * W;
   __shared__ Sums sums[W], joins[8];     // of the warps; of a cluster's parts
   __shared__ std::conditional_t<TOP, Shared<W>, int> sh;
@@ -546,11 +546,21 @@ cudaError_t forward(const LpArgs& a, int parts, cudaStream_t st) {
 template <typename T>
 cudaError_t forward(const LpArgs& a, cudaStream_t st) {
   const int64_t vectors = (a.cols + Elem<T>::VEC - 1) / Elem<T>::VEC;
-  if (vectors <= 64 * NV) return forward<T, 1>(a, 1, st);
-  // parts of a row: as many as keep at most two CTAs an SM, and a step's vectors in each
+  // Few rows: parts of a row, as many as keep at most two CTAs an SM and a step's vectors in each (8 x 128256 f32: 6.3 us in 8 parts).
   int parts = 1;
   while (parts < 8 && a.rows * parts * 2 <= 304 && vectors >= (int64_t)parts * 2 * 256 * NV) parts *= 2;
-  return forward<T, 8>(a, parts, st);
+  if (parts > 1) return forward<T, 8>(a, parts, st);
+  // Warps of a row: by its length 1 up to 256 vectors, 2 up to 3000, else 4 (fewer leave a warp more steps to one start and end; us of
+  // 8192 bf16 rows with 1, 2, 4 and 8 warps, no and 5 alternatives: 2000 columns 14 19 31 59 and 36 40 59 102, 10000 columns
+  // 40 39 50 76 and 86 89 105 131); more where there are fewer than 16 warps an SM (300 x 50000: 11 with 4, 10 with 8).
+  int warps = vectors <= 256 ? 1 : vectors <= 3000 ? 2 : 4;
+  while (warps < 8 && a.rows * warps < 152 * 16 && vectors >= 128 * warps) warps *= 2;
+  switch (warps) {
+    case 1: return forward<T, 1>(a, 1, st);
+    case 2: return forward<T, 2>(a, 1, st);
+    case 4: return forward<T, 4>(a, 1, st);
+    default: return forward<T, 8>(a, 1, st);
+  }
 }
 template <typename T>
 cudaError_t backward(const LpGradArgs& a, cudaStream_t st) {
