@@ -139,7 +139,7 @@ DA_EXPORT int dgl_forward(const da_matrix* x, const da_matrix* wg, const da_matr
   if (x->rows == 0) return DA_OK;
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf = x->dtype == DA_BF16;
-  if (x->rows <= GL_FEW && !saved) {
+  if (!saved && x->rows <= GL_FEW) {
     const GlFewArgs f = {x->ptr, wg->ptr, wu->ptr, const_cast<void*>(h->ptr), stride(*x), stride(*wg), stride(*wu), stride(*h),
                          (int)x->rows, (int)x->cols, (int)wg->rows, activation};
     return launched(bf ? gl_few<true>(f, st) : gl_few<false>(f, st));

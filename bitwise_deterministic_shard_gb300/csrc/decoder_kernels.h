@@ -9,7 +9,7 @@
 namespace detattn {
 
 // ---- gated feed-forward ----
-constexpr int GL_FEW = 8;        // tokens up to which the weights are read once by plain loads
+constexpr int GL_FEW = 16;       // tokens up to which the weights are read once by plain loads
 
 struct GlArgs {
   CUtensorMap x, wg, wu;         // boxes of 64 x 64

@@ -13,7 +13,7 @@
 // kernel of pair products: dx contracts over both halves of [dg | du] in one chain, dW has the tiles of both weights; the
 // longer tiles come first and the shorter ones fill the pairs up.
 //
-// Up to 8 tokens the forward pass reads the weights once with plain loads instead: a warp a hidden unit.
+// Up to 16 tokens the forward pass (without factors) reads the weights once with plain loads instead.
 #pragma once
 #include "../../include/detattn.h"
 #include "decoder_kernels.h"
@@ -301,59 +301,94 @@ __global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl
       });
 }
 
-// ---- few tokens: a warp a hidden unit, 16 bytes of each weight row a lane ----
-template <bool BF, int NT, int ACT>
-__global__ void __launch_bounds__(256) gl_few_kernel(const GlFewArgs a) {
+// ---- few tokens: 1 to 8 warps for 8 hidden units ----
+// Weights go from memory to registers once: a warp's products are of 16 rows (8 of Wg and the same 8 of Wu) by 8 tokens by 16, each
+// lane holding 8 neighbouring elements of a row of each, and the same 8 of a token's x; which 16 of them one product
+// contracts is free, as long as both operands agree.  A lane then has g and u of a unit for two tokens.  (Warp-wide products: at
+// this size the reading of the weights bounds it, not the matrix rate.  Multiplying by single tokens on the FP32 pipe took 55 us for
+// 4 and 98 for 8, width 4096, 12288 hidden units; the tiles of the other kernel 74 for 5 to 15 tokens, which all SMs read from the few
+// slices of the L2 that hold so small an x.)
+// As many warps as leave each up to eight runs of 32 elements a row.  One token, us (TB/s): width 1024, 4096 hidden units 5.1
+// (3.3); 2048, 8192 14.4 (4.7); 4096, 12288 35.6 (5.7); 8192, 28672 140 (6.7): start and end of a launch, some 4 us, and the rest
+// at the copy bandwidth.
+template <typename R, typename T>
+__device__ __forceinline__ void load_once(R& r, const T* p) {   // of a weight that no other warp reads
+  asm("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "l"(p));
+}
+template <bool BF>
+__device__ __forceinline__ void product(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (BF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <bool BF, int NT, int ACT>   // up to 8 NT tokens
+__global__ void __launch_bounds__(256, 4) gl_few_kernel(const __grid_constant__ GlFewArgs a, int warps) {
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-  using f2::u64;
-  const int lane = threadIdx.x & 31, f = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (f >= a.F) return;
-  const T* const wg = static_cast<const T*>(a.wg) + f * a.gs;
-  const T* const wu = static_cast<const T*>(a.wu) + f * a.us;
-  const T* const x = static_cast<const T*>(a.x);
-  u64 g[NT], u[NT];
+  __shared__ float sums[8][NT][4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % warps, g = lane >> 2, t = lane & 3;
+  const int f0 = (blockIdx.x * (8 / warps) + warp / warps) * 8;
+  const bool live = f0 < a.F;
+  const T* const wg = static_cast<const T*>(a.wg) + (live ? f0 + g : 0) * a.gs;
+  const T* const wu = static_cast<const T*>(a.wu) + (live ? f0 + g : 0) * a.us;
+  const T* x[NT];
+  float c[NT][4];
 #pragma unroll
-  for (int t = 0; t < NT; t++) g[t] = u[t] = 0;
-  constexpr int U = NT > 4 ? 2 : 4;   // runs of 256 elements at once
-  for (int k0 = lane * 8; k0 < a.D; k0 += 256 * U) {
+  for (int n = 0; n < NT; n++) {
+    x[n] = static_cast<const T*>(a.x) + min(8 * n + g, a.T - 1) * a.xs;   // tokens past the last: a copy of it, whose sums are not used
+#pragma unroll
+    for (int i = 0; i < 4; i++) c[n][i] = 0.f;
+  }
+  constexpr int U = 4;                                     // runs at once
+  const int per = ((a.D + 32 * warps - 1) / (32 * warps)) * 32, k1 = min(a.D, (part + 1) * per);
+  for (int k0 = part * per + t * 8; k0 < k1 + t * 8; k0 += 32 * U) {   // the same number of rounds in all lanes
     Run<T, 8> rg[U], ru[U];
 #pragma unroll
     for (int i = 0; i < U; i++) {
       rg[i].zero();
       ru[i].zero();
-      if (k0 + 256 * i < a.D) {
-        rg[i].load(wg + k0 + 256 * i);
-        ru[i].load(wu + k0 + 256 * i);
+      if (k0 + 32 * i < k1) {
+        load_once(rg[i], wg + k0 + 32 * i);
+        load_once(ru[i], wu + k0 + 32 * i);
       }
     }
 #pragma unroll
     for (int i = 0; i < U; i++) {
-      if (k0 + 256 * i >= a.D) break;
 #pragma unroll
-      for (int t = 0; t < NT; t++) {
-        if (t >= a.T) break;
+      for (int n = 0; n < NT; n++) {
         Run<T, 8> rx;
-        rx.load(x + t * a.xs + k0 + 256 * i);
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const u64 v = rx.get2(e);
-          g[t] = f2::fma(rg[i].get2(e), v, g[t]);
-          u[t] = f2::fma(ru[i].get2(e), v, u[t]);
-        }
+        rx.zero();
+        if (k0 + 32 * i < k1) rx.load(x[n] + k0 + 32 * i);
+        __syncwarp();
+        product<BF>(c[n], rg[i].w[0], ru[i].w[0], rg[i].w[1], ru[i].w[1], rx.w[0], rx.w[1]);
+        product<BF>(c[n], rg[i].w[2], ru[i].w[2], rg[i].w[3], ru[i].w[3], rx.w[2], rx.w[3]);
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < NT; t++) {
-    if (t >= a.T) break;
-    float a0, a1, b0, b1;
-    f2::unpack(g[t], a0, a1);
-    f2::unpack(u[t], b0, b1);
-    const float gs = warp_sum(a0 + a1), us = warp_sum(b0 + b1);
-    float q, d;
-    activate<ACT>(gs, q, d);
-    if (lane == 0) static_cast<T*>(a.h)[t * a.hs + f] = Elem<T>::put(q * us);
-  }
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) sums[warp][n][i][lane] = c[n][i];
+  __syncthreads();
+  if (part != 0 || !live) return;
+#pragma unroll
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int token = 8 * n + 2 * t + i;
+      float gs = 0.f, us = 0.f;
+      for (int w = 0; w < warps; w++) {                    // in order
+        gs += sums[warp + w][n][i][lane];
+        us += sums[warp + w][n][2 + i][lane];
+      }
+      float q, d;
+      activate<ACT>(gs, q, d);
+      if (token < a.T) static_cast<T*>(a.h)[token * a.hs + f0 + g] = Elem<T>::put(q * us);
+    }
 }
 
 // ---- dg = dh p, du = dh q: 8 elements a thread ----
@@ -415,11 +450,11 @@ cudaError_t backward_as(const GlArgs& a, int64_t tiles, cudaStream_t st) {
 }
 template <bool BF, int ACT>
 cudaError_t few_of(const GlFewArgs& a, cudaStream_t st) {
-  const int grid = (a.F + 7) / 8;
-  if (a.T <= 1) gl_few_kernel<BF, 1, ACT><<<grid, 256, 0, st>>>(a);
-  else if (a.T <= 2) gl_few_kernel<BF, 2, ACT><<<grid, 256, 0, st>>>(a);
-  else if (a.T <= 4) gl_few_kernel<BF, 4, ACT><<<grid, 256, 0, st>>>(a);
-  else gl_few_kernel<BF, 8, ACT><<<grid, 256, 0, st>>>(a);
+  int warps = 1;
+  while (warps < 8 && a.D > 256 * warps) warps *= 2;
+  const int grid = (a.F / 8 + 8 / warps - 1) / (8 / warps);
+  if (a.T <= 8) gl_few_kernel<BF, 1, ACT><<<grid, 256, 0, st>>>(a, warps);
+  else gl_few_kernel<BF, 2, ACT><<<grid, 256, 0, st>>>(a, warps);
   return cudaGetLastError();
 }
 
