@@ -66,8 +66,9 @@ int check(const da_matrix* x, const da_matrix* wg, const da_matrix* wu) {
   if (e || (e = check(wg)) || (e = check(wu, wg->dtype, wg->rows, wg->cols))) return e;
   if (wg->dtype != x->dtype) return DA_EDTYPE;
   if (wg->cols != x->cols || wg->rows < 8 || wg->rows % 8) return DA_ESHAPE;
-  // tiles of a launch
-  if (((x->rows >> 8) + 1) * ((wg->rows >> 7) + 1) > (int64_t)1 << 30 || ((wg->rows >> 7) + 2) * ((wg->cols >> 8) + 1) > (int64_t)1 << 30)
+  // tiles of a launch, the narrow ones
+  if (((x->rows >> 8) + 1) * ((wg->rows >> 6) + 1) > (int64_t)1 << 28 || ((wg->rows >> 7) + 2) * ((wg->cols >> 7) + 1) > (int64_t)1 << 28 ||
+      ((x->rows >> 8) + 1) * ((wg->cols >> 7) + 1) > (int64_t)1 << 28)
     return DA_ESHAPE;
   return DA_OK;
 }

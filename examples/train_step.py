@@ -1,4 +1,4 @@
-"""A small decoder trained reproducibly: layer norm, attention over packed documents with capped scores and
+"""A small decoder trained reproducibly: embedding lookup, layer norm, attention over packed documents with capped scores and
 shared key heads, the exact cross-entropy, and AdamW with 8-bit states, as one training program.
 
     python examples/train_step.py [--steps 20] [--state-bits 8]
@@ -50,7 +50,7 @@ class Decoder:
     def loss(self, tokens, targets, docs):
         """Mean loss of [B, S] targets; docs: document of each token (attention stays within one)."""
         B, S = tokens.shape
-        x = self.embedding[tokens]
+        x = da.embedding(tokens, self.embedding)
         for p in self.layers:
             q, k, v = (da.layer_norm(x, *p["norm1"]) @ p["qkv"].mT).split(
                 [self.heads * self.head, self.kv_heads * self.head, self.kv_heads * self.head], -1)
