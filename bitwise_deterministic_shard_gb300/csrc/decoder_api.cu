@@ -115,7 +115,7 @@ EmWs em_layout(int64_t n, int64_t cols) {
   w.found = take(sizeof(EmUnits));
   w.unit = take((size_t)n * 16);
   w.row = take(n <= EM_CHUNK ? 0 : (size_t)(n / EM_CHUNK + 1) * 16);
-  w.count = take(small ? 0 : (size_t)((n + EM_BLOCK - 1) / EM_BLOCK) * EM_BINS * 4);
+  w.count = take(small ? 0 : (size_t)((n + em_block(n) - 1) / em_block(n)) * EM_BINS * 4);
   w.part = take(n <= EM_CHUNK ? 0 : (size_t)2 * (n / EM_CHUNK + 1) * cols * 4);
   w.total = at;
   return w;

@@ -6,9 +6,9 @@
 // row of dw, most of them zeros for a large vocabulary.
 //
 // Gradient: the tokens are sorted by id, stably, by counting digits of up to 9 bits from the lowest on (two passes up to 2^18
-// rows).  Up to 16384 tokens one CTA does that in shared memory while the others fill dw with zeros; longer ones take three
-// launches a pass, the zeros beside the first.  Each warp's rank of a token among those of its digit comes from a match over the
-// warp and its counters, so the order never depends on which thread came first.  Then a chunk of up to 64 tokens of a row is one
+// rows).  Up to 4096 tokens one CTA does that in shared memory; longer ones take three launches a pass, each of which starts as the one
+// before it ends.  dw's zeros wait for nothing and are written beside all of these.  A token's place among those of its digit comes
+// from ballots over the warp and the warp's counters, so the order never depends on which thread came first.  Then a chunk of up to 32 tokens of a row is one
 // chain of binary32 additions for each column, in order of the tokens; rows of more leave their chunks' sums in the
 // workspace, and a last kernel adds these, eight runs of chunks in order and then the eight.  So a row's bits depend on its own
 // tokens alone, and no atomics add values (the lists of chunks are filled by atomics: their order is that of the work, not
@@ -86,39 +86,58 @@ __device__ __forceinline__ uint32_t key_at(const EmArgs& a, int64_t i) {   // ro
   }
   return id == a.padding ? (uint32_t)a.rows : (uint32_t)id;
 }
-// zeros over this CTA's share (of `share` CTAs) of a contiguous dw
-template <int THREADS>
-__device__ __forceinline__ void fill_zeros(const EmArgs& a, uint32_t cta, uint32_t share) {
+// Zeros over a contiguous dw, which wait for nothing: they run beside the sort.  Part `part` of `parts` of it, by CTAs of a launch.
+struct Fill {
+  uint32_t part, parts;
+};
+__device__ __forceinline__ void fill_zeros(const EmArgs& a, uint32_t cta, uint32_t ctas, Fill f) {
   const int64_t bytes = a.rows * a.cols * (a.dtype == DA_F32 ? 4 : 2);
   unsigned char* const p = static_cast<unsigned char*>(a.dw);
   const int64_t head = min(bytes, (int64_t)(-reinterpret_cast<intptr_t>(p) & 15)), body = (bytes - head) / 16;
-  for (int64_t i = (int64_t)cta * THREADS + threadIdx.x; i < body; i += (int64_t)share * THREADS)
+  const int64_t end = body / f.parts * (f.part + 1) + (f.part + 1 == f.parts ? body % f.parts : 0);
+  for (int64_t i = body / f.parts * f.part + (int64_t)cta * blockDim.x + threadIdx.x; i < end; i += (int64_t)ctas * blockDim.x)
     reinterpret_cast<uint4*>(p + head)[i] = make_uint4(0, 0, 0, 0);
-  if (cta == 0 && threadIdx.x < 32) {
+  if (f.part == 0 && cta == 0 && threadIdx.x < 32) {
     if (threadIdx.x < head) p[threadIdx.x] = 0;
     const int64_t tail = head + body * 16 + threadIdx.x;
     if (tail < bytes) p[tail] = 0;
   }
 }
-
-// A warp's tokens of one digit each: this lane's rank among equal digits of lower lanes, and whether it is their last.
-__device__ __forceinline__ uint32_t rank_of(uint32_t digit, bool& last) {
-  const uint32_t same = __match_any_sync(0xffffffffu, digit), lane = threadIdx.x & 31;
-  last = same >> lane == 1;
-  return __popc(same & ((1u << lane) - 1));
+// Beside the kernel before it, which it does not depend on; it ends after that one, so what follows may take both as done.
+__global__ void __launch_bounds__(256) em_fill_kernel(const __grid_constant__ EmArgs a) {
+  next_may_start();
+  fill_zeros(a, blockIdx.x, gridDim.x, Fill{0, 1});
+  after_previous();
 }
 
-// One CTA (the first) sorts up to EM_SMALL tokens; the others fill zeros.
-constexpr int SORT_THREADS = 1024, SORT_WARPS = 32;
+// Places of a warp's tokens among those of the same digit, in their order: what the counters held and, of this step's, how many lower
+// lanes have it.  A lane without a token has a digit of its own, EM_BINS.  By ballots over the digit's bits.
+__device__ __forceinline__ uint32_t count_digit(uint32_t digit, int bits, uint32_t* hist) {
+  const uint32_t lane = threadIdx.x & 31;
+  const bool live = digit < EM_BINS;
+  uint32_t same = __ballot_sync(0xffffffffu, live);
+  for (int b = 0; b < bits; b++) {
+    const bool bit = digit >> b & 1;
+    const uint32_t who = __ballot_sync(0xffffffffu, bit);
+    same &= bit ? who : ~who;
+  }
+  const uint32_t before = live ? hist[digit] : 0, rank = __popc(same & ((1u << lane) - 1));
+  __syncwarp();
+  if (live && same >> lane == 1) hist[digit] = before + rank + 1;   // the last of them
+  __syncwarp();
+  return before + rank;
+}
+
+// One CTA sorts up to EM_SMALL tokens.
+constexpr int SORT_THREADS = 1024, SORT_WARPS = 32, SORT_RUN = EM_SMALL / SORT_WARPS;
 struct SortSmall {
   uint32_t key[EM_SMALL];
-  uint16_t pos0[EM_SMALL];
-  uint16_t hist[SORT_WARPS][EM_BINS];
-  uint16_t pos1[EM_SMALL];          // in the end the sorted keys lie over the counters and the places no longer used
+  uint16_t pos[2][EM_SMALL];
+  uint32_t hist[SORT_WARPS][EM_BINS];   // in the end the sorted keys lie here
   uint32_t base[EM_BINS], warps[32];
   EmUnits found;
 };
-static_assert(sizeof(uint16_t) * (EM_SMALL + SORT_WARPS * EM_BINS) == sizeof(uint32_t) * EM_SMALL, "room for the sorted keys");
+static_assert(SORT_WARPS * EM_BINS >= EM_SMALL, "room for the sorted keys");
 
 // What starts at place i of the sorted keys: a chunk of a row's tokens, or nothing.  Called by whole warps; the counters are atomics.
 __device__ __forceinline__ void find_chunk(const EmArgs& a, const uint32_t* key, int64_t i, int64_t n, EmUnits* found) {
@@ -179,39 +198,36 @@ __device__ __forceinline__ void find_chunk(const EmArgs& a, const uint32_t* key,
 
 __global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_constant__ EmArgs a, int passes, int bits) {
   next_may_start();
-  if (blockIdx.x > 0) {
-    fill_zeros<SORT_THREADS>(a, blockIdx.x - 1, gridDim.x - 1);
-    return;
-  }
   extern __shared__ unsigned char raw[];
   SortSmall& s = *reinterpret_cast<SortSmall*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = (int)a.n;
-  const int per = ((n + SORT_THREADS - 1) / SORT_THREADS) * 32, i0 = warp * per, i1 = min(n, i0 + per);   // a warp's run of places
+  constexpr int K = SORT_RUN / 32;
+  const int i0 = warp * SORT_RUN + lane, used = (n + SORT_RUN - 1) / SORT_RUN;   // a warp's run of places; warps that have one
   for (int i = tid; i < n; i += SORT_THREADS) s.key[i] = key_at(a, i);
   __syncthreads();
   for (int p = 0; p < passes; p++) {
     const int shift = p * bits;
     const uint32_t mask = (1u << bits) - 1;
-    const uint16_t* const from = p & 1 ? s.pos0 : s.pos1;
-    uint16_t* const to = p & 1 ? s.pos1 : s.pos0;
+    const uint16_t* const from = s.pos[(p + 1) & 1];
+    uint16_t* const to = s.pos[p & 1];
+    int token[K];
+    uint32_t digit[K], place[K];
+#pragma unroll
+    for (int k = 0; k < K; k++) token[k] = i0 + 32 * k < n ? p ? from[i0 + 32 * k] : i0 + 32 * k : -1;
+#pragma unroll
+    for (int k = 0; k < K; k++) digit[k] = token[k] < 0 ? EM_BINS : s.key[token[k]] >> shift & mask;
     for (int b = lane; b <= (int)mask; b += 32) s.hist[warp][b] = 0;
     __syncwarp();
-    for (int i = i0; i < i1; i += 32) {
-      const int at = i + lane;
-      const bool live = at < i1;
-      const uint32_t d = live ? s.key[p ? from[at] : at] >> shift & mask : EM_BINS;
-      bool last;
-      const uint32_t rank = rank_of(d, last);
-      if (live && last) s.hist[warp][d] += rank + 1;
-      __syncwarp();
-    }
+#pragma unroll
+    for (int k = 0; k < K; k++) place[k] = count_digit(digit[k], bits, s.hist[warp]);
     __syncthreads();
     // places before each digit, and within it before each warp
     uint32_t total = 0;
     if (tid <= (int)mask)
-      for (int w = 0; w < SORT_WARPS; w++) {
+#pragma unroll 8
+      for (int w = 0; w < used; w++) {
         const uint32_t c = s.hist[w][tid];
-        s.hist[w][tid] = (uint16_t)total;
+        s.hist[w][tid] = total;
         total += c;
       }
     uint32_t sum = total;
@@ -228,26 +244,13 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_c
       s.base[tid] = before;
     }
     __syncthreads();
-    for (int i = i0; i < i1; i += 32) {
-      const int at = i + lane;
-      const bool live = at < i1;
-      const int place = live ? p ? from[at] : at : 0;
-      const uint32_t d = live ? s.key[place] >> shift & mask : EM_BINS;
-      bool last;
-      const uint32_t rank = rank_of(d, last);
-      uint32_t mine = 0;
-      if (live) {
-        mine = s.hist[warp][d];
-        to[s.base[d] + mine + rank] = (uint16_t)place;
-      }
-      __syncwarp();
-      if (live && last) s.hist[warp][d] = (uint16_t)(mine + rank + 1);
-      __syncwarp();
-    }
+#pragma unroll
+    for (int k = 0; k < K; k++)
+      if (token[k] >= 0) to[s.base[digit[k]] + s.hist[warp][digit[k]] + place[k]] = (uint16_t)token[k];
     __syncthreads();
   }
-  const uint16_t* const done = passes & 1 ? s.pos0 : s.pos1;
-  uint32_t* const sorted = reinterpret_cast<uint32_t*>(passes & 1 ? &s.hist[0][0] : s.pos0);
+  const uint16_t* const done = s.pos[(passes - 1) & 1];
+  uint32_t* const sorted = &s.hist[0][0];
   if (tid == 0) s.found = {0, 0, 0};
   for (int i = tid; i < n; i += SORT_THREADS) {
     a.pos[0][i] = done[i];
@@ -259,31 +262,47 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_c
   if (tid == 0) *a.found = s.found;
 }
 
-// A pass over longer ones.  Counts of a block's digits (the first pass: from the ids; blocks past the tokens' fill zeros).
-constexpr int RADIX_THREADS = 256, RADIX_WARPS = 8, RADIX_RUN = EM_BLOCK / RADIX_WARPS;
-__global__ void __launch_bounds__(RADIX_THREADS) em_count_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int from, int shift, int bits) {
+// ---- a pass over longer ones; CTAs past a kernel's own fill their part of the zeros ----
+constexpr int RADIX_THREADS = 256, RADIX_WARPS = 8;
+// counts of a block's digits (the first pass: from the ids)
+__global__ void __launch_bounds__(RADIX_THREADS) em_count_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int block, int from, int shift, int bits,
+                                                                 Fill fill) {
+  next_may_start();
   if (blockIdx.x >= blocks) {
-    fill_zeros<RADIX_THREADS>(a, blockIdx.x - blocks, gridDim.x - blocks);
+    fill_zeros(a, blockIdx.x - blocks, gridDim.x - blocks, fill);
     return;
   }
   __shared__ uint32_t hist[EM_BINS];
   const uint32_t mask = (1u << bits) - 1;
   for (int b = threadIdx.x; b < EM_BINS; b += RADIX_THREADS) hist[b] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * EM_BLOCK, i1 = min(a.n, i0 + EM_BLOCK);
+  after_previous();
+  const int64_t i0 = (int64_t)blockIdx.x * block, i1 = min(a.n, i0 + block);
   for (int64_t i = i0 + threadIdx.x; i < i1; i += RADIX_THREADS)
     atomicAdd(&hist[(from < 0 ? key_at(a, i) : a.key[from][i]) >> shift & mask], 1u);
   __syncthreads();
   for (uint32_t b = threadIdx.x; b <= mask; b += RADIX_THREADS) a.count[(size_t)b * blocks + blockIdx.x] = hist[b];
 }
-// Places before each (digit, block): one CTA, a run of counts a thread.
-__global__ void __launch_bounds__(1024) em_scan_kernel(uint32_t* count, int64_t n, EmUnits* found) {
-  if (threadIdx.x == 0) *found = {0, 0, 0};
+// places before each (digit, block): one CTA, a run of counts a thread
+__global__ void __launch_bounds__(1024) em_scan_kernel(const __grid_constant__ EmArgs a, int64_t n, Fill fill) {
+  next_may_start();
+  if (blockIdx.x > 0) {
+    fill_zeros(a, blockIdx.x - 1, gridDim.x - 1, fill);
+    return;
+  }
   __shared__ uint32_t warps[32];
+  after_previous();
+  if (threadIdx.x == 0) *a.found = {0, 0, 0};
+  uint32_t* const count = a.count;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t per = (n + 1023) / 1024, i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  const int64_t per = (n + 4095) / 4096, i0 = min(n / 4, tid * per), i1 = min(n / 4, i0 + per);   // n is a multiple of 4: so are the bins
+  uint4* const four = reinterpret_cast<uint4*>(count);
   uint32_t total = 0;
-  for (int64_t i = i0; i < i1; i++) total += count[i];
+#pragma unroll 4
+  for (int64_t i = i0; i < i1; i++) {
+    const uint4 c = four[i];
+    total += c.x + c.y + c.z + c.w;
+  }
   uint32_t sum = total;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -294,37 +313,41 @@ __global__ void __launch_bounds__(1024) em_scan_kernel(uint32_t* count, int64_t 
   __syncthreads();
   uint32_t before = sum - total;
   for (int w = 0; w < warp; w++) before += warps[w];
+#pragma unroll 4
   for (int64_t i = i0; i < i1; i++) {
-    const uint32_t c = count[i];
-    count[i] = before;
-    before += c;
+    const uint4 c = four[i];
+    four[i] = make_uint4(before, before + c.x, before + c.x + c.y, before + c.x + c.y + c.z);
+    before += c.x + c.y + c.z + c.w;
   }
 }
-__global__ void __launch_bounds__(RADIX_THREADS) em_scatter_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int from, int to, int shift, int bits) {
+template <int K>   // steps of a warp: blocks of 256 K tokens
+__global__ void __launch_bounds__(RADIX_THREADS) em_scatter_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int from, int to, int shift, int bits,
+                                                                   Fill fill) {
+  next_may_start();
+  if (blockIdx.x >= blocks) {
+    fill_zeros(a, blockIdx.x - blocks, gridDim.x - blocks, fill);
+    return;
+  }
   __shared__ uint32_t hist[RADIX_WARPS][EM_BINS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t mask = (1u << bits) - 1;
-  const int64_t i0 = (int64_t)blockIdx.x * EM_BLOCK + warp * RADIX_RUN, i1 = min(a.n, i0 + RADIX_RUN);
-  uint32_t key[RADIX_RUN / 32];
+  const int64_t i0 = ((int64_t)blockIdx.x * RADIX_WARPS + warp) * 32 * K + lane;
+  uint32_t key[K], pos[K], place[K];
   for (int b = lane; b < EM_BINS; b += 32) hist[warp][b] = 0;
+  after_previous();
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+    const int64_t i = i0 + k * 32;
+    key[k] = i < a.n ? from < 0 ? key_at(a, i) : a.key[from][i] : 0;
+    pos[k] = i < a.n && from >= 0 ? a.pos[from][i] : (uint32_t)i;
+  }
   __syncwarp();
 #pragma unroll
-  for (int k = 0; k < RADIX_RUN / 32; k++) {
-    const int64_t i = i0 + k * 32 + lane;
-    key[k] = i < i1 ? from < 0 ? key_at(a, i) : a.key[from][i] : 0;
-  }
-#pragma unroll
-  for (int k = 0; k < RADIX_RUN / 32; k++) {
-    const bool live = i0 + k * 32 + lane < i1;
-    const uint32_t d = live ? key[k] >> shift & mask : EM_BINS;
-    bool last;
-    const uint32_t rank = rank_of(d, last);
-    if (live && last) hist[warp][d] += rank + 1;
-    __syncwarp();
-  }
+  for (int k = 0; k < K; k++) place[k] = count_digit(i0 + k * 32 < a.n ? key[k] >> shift & mask : EM_BINS, bits, hist[warp]);
   __syncthreads();
   for (uint32_t b = tid; b <= mask; b += RADIX_THREADS) {
     uint32_t before = a.count[(size_t)b * blocks + blockIdx.x];
+#pragma unroll
     for (int w = 0; w < RADIX_WARPS; w++) {
       const uint32_t c = hist[w][b];
       hist[w][b] = before;
@@ -333,27 +356,20 @@ __global__ void __launch_bounds__(RADIX_THREADS) em_scatter_kernel(const __grid_
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < RADIX_RUN / 32; k++) {
-    const int64_t i = i0 + k * 32 + lane;
-    const bool live = i < i1;
-    const uint32_t d = live ? key[k] >> shift & mask : EM_BINS;
-    bool last;
-    const uint32_t rank = rank_of(d, last);
-    uint32_t mine = 0;
-    if (live) {
-      mine = hist[warp][d];
-      a.key[to][mine + rank] = key[k];
-      a.pos[to][mine + rank] = from < 0 ? (uint32_t)i : a.pos[from][i];
+  for (int k = 0; k < K; k++)
+    if (i0 + k * 32 < a.n) {
+      const uint32_t at = hist[warp][key[k] >> shift & mask] + place[k];
+      a.key[to][at] = key[k];
+      a.pos[to][at] = pos[k];
     }
-    __syncwarp();
-    if (live && last) hist[warp][d] = mine + rank + 1;
-    __syncwarp();
-  }
 }
-
-// ---- chunks of longer ones ----
-__global__ void __launch_bounds__(256) em_chunk_kernel(const __grid_constant__ EmArgs a, int from) {
+__global__ void __launch_bounds__(256) em_chunk_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int from, Fill fill) {
   next_may_start();
+  if (blockIdx.x >= blocks) {
+    fill_zeros(a, blockIdx.x - blocks, gridDim.x - blocks, fill);
+    return;
+  }
+  after_previous();
   find_chunk(a, a.key[from], (int64_t)blockIdx.x * 256 + threadIdx.x, a.n, a.found);
 }
 // Where a chunk of several leaves its sum: full ones start at least a chunk apart, and so do the last ones of their rows.
@@ -386,7 +402,7 @@ __device__ __forceinline__ void sum_chunk(const EmArgs& a, uint4 unit, int64_t c
 #pragma unroll
     for (int u = 0; u < R; u++) {
       const uint32_t t = j + u;
-      at[u] = dy + (int64_t)__shfl_sync(0xffffffffu, t < 32 ? token[0] : token[1], t & 31) * a.ys;
+      at[u] = dy + (int64_t)__shfl_sync(0xffffffffu, EM_CHUNK == 32 || t < 32 ? token[0] : token[EM_CHUNK / 32 - 1], t & 31) * a.ys;
     }
     if constexpr (AL) {
       Run<T, VEC> r[R][C];
@@ -422,7 +438,7 @@ __device__ __forceinline__ void sum_chunk(const EmArgs& a, uint4 unit, int64_t c
         }
     }
   }
-  static_assert(EM_CHUNK == 64, "two words of tokens a lane");
+  static_assert(EM_CHUNK == 32 || EM_CHUNK == 64, "one or two words of tokens a lane");
   if (unit.y & EM_MORE) {
     float* const to = a.part + slot_of(a, unit.x, len) * a.cols + c0;
 #pragma unroll
@@ -545,27 +561,41 @@ cudaError_t launch_embedding_grad(const EmArgs& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (!flat || a.n == 0) e = cudaMemset2DAsync(a.dw, (size_t)a.ws * es, 0, (size_t)a.cols * es, (size_t)a.rows, st);
   if (e != cudaSuccess || a.n == 0) return e;
-  // CTAs that fill zeros: at least 64 KB each, beside the one that sorts one an SM (it takes most of the shared memory)
-  const unsigned fill = flat ? (unsigned)std::min<int64_t>(a.n <= EM_SMALL ? 151 : 152 * 4, a.rows * a.cols * es / 65536 + 1) : 0;
   int need = 1, from = 0;
   while (need < 32 && ((uint64_t)1 << need) <= (uint64_t)a.rows) need++;   // bits of the keys 0 .. rows
-  const int passes = (need + 8) / 9, bits = (need + passes - 1) / passes;
+  const int passes = (need + 8) / 9, bits = std::max(2, (need + passes - 1) / passes);
+  const int64_t bytes = flat ? a.rows * a.cols * es : 0;
+  const auto fillers = [&](int64_t part, int threads) {   // CTAs for so many bytes of zeros
+    return (unsigned)std::min<int64_t>(152 * 1024 / threads, (part + 128 * threads - 1) / (128 * threads));
+  };
   if (a.n <= EM_SMALL) {
     static DeviceOnce once;
     if ((e = allow_smem(once, em_sort_kernel, (int)sizeof(SortSmall))) != cudaSuccess) return e;
-    em_sort_kernel<<<1 + fill, SORT_THREADS, sizeof(SortSmall), st>>>(a, passes, bits);
+    em_sort_kernel<<<1, SORT_THREADS, sizeof(SortSmall), st>>>(a, passes, bits);
+    if ((e = cudaGetLastError()) == cudaSuccess && flat) e = launch_early(em_fill_kernel, dim3(fillers(bytes, 256)), 256, 0, st, a);
   } else {
-    const uint32_t blocks = (uint32_t)((a.n + EM_BLOCK - 1) / EM_BLOCK);
-    for (int p = 0; p < passes; p++) {
+    const int block = em_block(a.n);
+    const uint32_t blocks = (uint32_t)((a.n + block - 1) / block), chunks = (uint32_t)((a.n + 255) / 256);
+    const uint32_t parts = 3 * passes + 1;
+    const unsigned f = fillers(bytes / parts, 256), g = fillers(bytes / parts, 1024);
+    for (int p = 0; p < passes && e == cudaSuccess; p++) {
       const int src = p ? (p + 1) & 1 : -1, dst = p & 1, shift = p * bits;
-      em_count_kernel<<<blocks + (p ? 0 : fill), RADIX_THREADS, 0, st>>>(a, blocks, src, shift, bits);
-      em_scan_kernel<<<1, 1024, 0, st>>>(a.count, (int64_t)blocks << bits, a.found);
-      em_scatter_kernel<<<blocks, RADIX_THREADS, 0, st>>>(a, blocks, src, dst, shift, bits);
+      const auto fill = [&](uint32_t k) { return Fill{3 * p + k, parts}; };
+      if (p == 0) {   // after everything before it; the others only wait for each other
+        em_count_kernel<<<blocks + f, RADIX_THREADS, 0, st>>>(a, blocks, block, src, shift, bits, fill(0));
+        e = cudaGetLastError();
+      } else {
+        e = launch_early(em_count_kernel, dim3(blocks + f), RADIX_THREADS, 0, st, a, blocks, block, src, shift, bits, fill(0));
+      }
+      if (e == cudaSuccess) e = launch_early(em_scan_kernel, dim3(1 + g), 1024, 0, st, a, (int64_t)blocks << bits, fill(1));
+      if (e == cudaSuccess)
+        e = launch_early(block == 1024 ? em_scatter_kernel<4> : em_scatter_kernel<8>, dim3(blocks + f), RADIX_THREADS, 0, st, a, blocks, src, dst, shift,
+                         bits, fill(2));
       from = dst;
     }
-    em_chunk_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, st>>>(a, from);
+    if (e == cudaSuccess) e = launch_early(em_chunk_kernel, dim3(chunks + f), 256, 0, st, a, chunks, from, Fill{parts - 1, parts});
   }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (e != cudaSuccess) return e;
   if (a.dtype == DA_F32) return gradient<float>(a, from, st);
   return a.dtype == DA_BF16 ? gradient<__nv_bfloat16>(a, from, st) : gradient<__half>(a, from, st);
 }

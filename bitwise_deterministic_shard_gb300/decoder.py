@@ -332,7 +332,7 @@ def embedding_forward(ids, weight, scale=1.0, out=None, status=None):
 
 def embedding_backward(grad, ids, rows, scale=1.0, padding_idx=None, workspace=None, status=None):
     """The gradient [rows, cols] of sum(embedding * grad) for the weight, of grad's dtype: each row the binary32 sum over its own
-    tokens, in order and 64 at a time, rounded once; a row's bits depend on its own tokens alone.  Tokens of id padding_idx
+    tokens, in order and 32 at a time, rounded once; a row's bits depend on its own tokens alone.  Tokens of id padding_idx
     give nothing, nor do those outside [0, rows), which set STATUS_BAD_TARGET."""
     _da._cuda(grad, "grad")
     if grad.dim() < 1 or grad.shape[:-1] != ids.shape or grad.shape[-1] < 1:

@@ -461,7 +461,7 @@ int dte_forward(const void* ids, int id_bits, const da_matrix* w, float scale, c
                 da_stream_t stream);
 
 /* Its gradient, every row of dw [rows, cols] written: dw[v] = scale (sum over i with ids[i] == v of dy[i]), a binary32 sum in order of
- * the tokens, 64 at a time, rounded once; the tokens of id `padding` (-1: none) and those outside [0, rows), which set
+ * the tokens, 32 at a time, rounded once; the tokens of id `padding` (-1: none) and those outside [0, rows), which set
  * DA_STATUS_BAD_TARGET, give nothing.  A row's bits depend on its own tokens alone.  ws: dte_workspace_bytes(n, cols),
  * 256-byte aligned. */
 size_t dte_workspace_bytes(int64_t n, int64_t cols);

@@ -36,11 +36,11 @@ def embedding(ids, weight, dy, scale=1.0, padding_idx=None):
 
 def embedding_tolerance(r, dtype, scale):
     """The lookup: the product in binary32 and the type's rounding (none of them for a scale of 1).  The gradient: a chain of up to
-    64 tokens, an eighth of the chunks, eight sums of those and the scale."""
+    32 tokens, an eighth of the chunks, eight sums of those and the scale."""
     u = half_step(dtype)
     f = 2.0 ** -24 if scale != 1.0 else 0.0        # a scale that is not a binary32 number
     ty = 0.0 * r["y"].abs() if scale == 1.0 else (u + e + f) * r["y"].abs() + least(dtype)
-    chain = 64 + torch.ceil(r["count"] / 512.0) + 8 + 2
+    chain = 32 + torch.ceil(r["count"] / 256.0) + 8 + 2
     rounded = 0.0 if dtype == torch.float32 else u
     tw = chain[:, None] * e * r["size"] + (rounded + f) * r["dw"].abs() + (least(dtype) if rounded else 0.0)
     return {"y": 1.02 * ty, "dw": 1.02 * tw + 1e-300}

@@ -117,11 +117,11 @@ def test_embedding_is_refused(L):
 
 def test_workspaces_hold_every_list(L):
     """The sorted places, a chunk each token at most, the sums of chunks."""
-    for n in (1, 64, 65, 16384, 16385, 1 << 20):
+    for n in (1, 32, 33, 4096, 4097, 32768, 32769, 1 << 20):
         for cols in (1, 1000):
             b = L.dte_workspace_bytes(n, cols)
-            sums = 8 * (n // 64 + 1) * cols if n > 64 else 0
-            assert sums + 20 * n <= b <= sums + 20 * n + (20 * n + 2048 * (n // 4096 + 1) if n > 16384 else 0) + n + 4096
+            sums = 8 * (n // 32 + 1) * cols if n > 32 else 0
+            assert sums + 20 * n <= b <= sums + 20 * n + (12 * n + 2048 * (n // 1024 + 1) if n > 4096 else 0) + n + 4096
 
 
 # ---------------------------------------------------------------- binding

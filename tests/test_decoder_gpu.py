@@ -40,10 +40,11 @@ def _words(n, v, g):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("n, v, w", [(0, 5, 8), (1, 1, 1), (5, 20, 16), (64, 1, 8), (65, 1, 33), (129, 3, 264), (3001, 2001, 1003), (16384, 5000, 72),
-                                     (16385, 70001, 40), (40000, 513, 136), (9000, 2, 24), (20000, 262145, 8)])
+@pytest.mark.parametrize("n, v, w", [(0, 5, 8), (1, 1, 1), (5, 20, 16), (32, 1, 8), (33, 1, 33), (64, 1, 8), (65, 1, 33), (129, 3, 264), (3001, 2001, 1003),
+                                     (4096, 5000, 72), (4097, 5000, 72), (16385, 70001, 40), (40000, 513, 136), (9000, 2, 24), (20000, 262145, 8),
+                                     (33000, 1, 8), (5000, 1, 40)])
 def test_embedding(n, v, w, dtype):
-    """Rows of no, one, 64, 65 and thousands of tokens; one CTA's sort and the longer one; one to three digits."""
+    """Rows of no, one, 32, 33 and thousands of tokens; one CTA's sort and the longer one; one to three digits."""
     g = _gen(n + v)
     ids, weight, dy = _words(n, v, g), _randn(v, w, g=g, to=dtype), _randn(n, w, g=g, to=dtype)
     st = da.new_status()
