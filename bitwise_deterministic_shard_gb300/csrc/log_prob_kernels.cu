@@ -419,10 +419,10 @@ __global__ void __launch_bounds__(32 * W, W == 1 ? 24 : 32 / W) lp_kernel(const 
       for (int p = 1; p < parts; p++) m.join(joins[p], c);
     }
     if constexpr (TOP) {
-      const u64* const all = sh.join[0];
-      const u64 key = tid < parts * LP_TOP ? all[tid] : 0;
+      const u64 key = warp < parts ? sh.join[warp % 8][lane] : 0;   // a warp a part's list
       int rank = 0;
-      for (int j = 0; j < parts * LP_TOP; j++) rank += all[j] > key;
+      for (int p = 0; p < parts; p++)
+        for (int j = 0; j < a.top; j++) rank += sh.join[p][j] > key;
       if (warp == 0) sh.best[lane] = 0;
       __syncthreads();
       if (key != 0 && rank < a.top) sh.best[rank] = key;
