@@ -236,6 +236,21 @@ def test_gated_parts_alone_and_none():
     assert da.gated_linear(x[0], wg, wu).shape == (136,)
 
 
+@pytest.mark.parametrize("D, F", [(264, 1032), (2048, 10008)])
+def test_gated_rows_do_not_depend_on_the_batch(D, F):
+    """A token's h and dx have the same bits with any other tokens, in wide tiles and narrow ones; up to 16 tokens without saved
+    factors among themselves."""
+    x, wg, wu, dh = _gated_inputs(4000, D, F, torch.bfloat16, 9)
+    h, saved = da.gated_linear_forward(x, wg, wu)
+    dx = da.gated_linear_backward(dh, x, wg, wu, saved, need_weights=False)[0]
+    for n in (1, 5, 17, 300, 2100):
+        some, part = da.gated_linear_forward(x[:n], wg, wu)
+        assert torch.equal(some, h[:n])
+        assert torch.equal(da.gated_linear_backward(dh[:n], x[:n], wg, wu, part, need_weights=False)[0], dx[:n])
+        alone = da.gated_linear(x[:n], wg, wu)
+        assert torch.equal(alone, h[:n] if n > 16 else da.gated_linear(x[:16], wg, wu)[:n])
+
+
 def test_gated_special_values_stay_in_their_rows():
     """A row of NaN or infinities gives what the formula gives there, and nothing elsewhere."""
     for T in (6, 300):
