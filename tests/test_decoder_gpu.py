@@ -1,4 +1,5 @@
 """The decoder's operators on the GPU against plain 64-bit forms, at the sizes, masks, strides and types where they can go wrong."""
+import ctypes
 import math
 import os
 import sys
@@ -511,6 +512,57 @@ def test_log_probs_offsets_past_32_bits():
     assert r.top_indices[-1].tolist() == [77777, 0] and r.top_indices[0].tolist() == [0, 1]
     dx = da.log_probs_backward(x, t, saved, torch.ones(rows, device="cuda"))
     _close(dx[-2:], w["dx"], tol["dx"], "dlogits")
+
+
+# ---------------------------------------------------------------- C ABI
+
+def _matrix(t):
+    m = da._Matrix()
+    m.ptr, m.rows, m.cols, m.row_stride = t.data_ptr(), t.shape[0], t.shape[1], t.stride(0)
+    m.dtype = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[t.dtype]
+    return ctypes.byref(m)
+
+
+def test_outputs_in_wider_buffers():
+    """Row strides of the outputs, and what lies between the rows stays as it was."""
+    L, t = da.lib(), torch.bfloat16
+    x, wg, wu, dh = _gated_inputs(300, 72, 136, t, 10)
+    h, saved = da.gated_linear_forward(x, wg, wu)
+    want = da.gated_linear_backward(dh, x, wg, wu, saved)
+    g = _gen(10)
+    ids, dy, w, logits = _words(300, 40, g), _randn(300, 24, g=g), _randn(40, 24, g=g), _randn(300, 40, g=g)
+    wide = lambda n, c, to=t: torch.full((n, c + 16), 7.0, device="cuda", dtype=to)  # noqa: E731
+    s = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+
+    def check(buffers, wants):
+        torch.cuda.synchronize()
+        for b, v in zip(buffers, wants):
+            c = v.shape[1]
+            assert torch.equal(b[:, :c], v) and (b[:, c:] == 7).all()
+    for n in (300, 5):
+        b = wide(n, 136)
+        assert L.dgl_forward(_matrix(x[:n]), _matrix(wg), _matrix(wu), 0, _matrix(b[:, :136]), saved.data_ptr() if n > 5 else None, None, s) == 0
+        check([b], [h if n > 5 else da.gated_linear(x[:n], wg, wu)])
+    bs = [wide(300, 72), wide(136, 72), wide(136, 72)]
+    m = [_matrix(b[:, :72]) for b in bs]
+    assert L.dgl_backward(_matrix(dh), _matrix(x), _matrix(wg), _matrix(wu), saved.data_ptr(), *m, ws.data_ptr(), ws.numel(), None, s) == 0
+    check(bs, want)
+    assert L.dgl_backward(_matrix(dh[:0]), _matrix(x[:0]), _matrix(wg), _matrix(wu), None, None, *m[1:], ws.data_ptr(), ws.numel(), None, s) == 0
+    check(bs[1:], [torch.zeros_like(want[1])] * 2)
+    f = torch.float32
+    bs = [wide(300, 24, f), wide(40, 24, f)]
+    assert L.dte_forward(ids.data_ptr(), 64, _matrix(w), 2.0, _matrix(bs[0][:, :24]), None, s) == 0
+    assert L.dte_backward(ids.data_ptr(), 64, _matrix(dy), 2.0, -1, _matrix(bs[1][:, :24]), ws.data_ptr(), ws.numel(), None, s) == 0
+    check(bs, [da.embedding_forward(ids, w, 2.0), da.embedding_backward(dy, ids, 40, 2.0)])
+    for n in (0, 5000):                                    # no tokens; the longer sort
+        many, dm, b = _words(n, 40, g), _randn(n, 24, g=g), wide(40, 24, f)
+        assert L.dte_backward(many.data_ptr(), 64, _matrix(dm), 1.0, 3, _matrix(b[:, :24]), ws.data_ptr(), ws.numel(), None, s) == 0
+        check([b], [da.embedding_backward(dm, many, 40, 1.0, 3)])
+    targets, up, b = ids % 40, _randn(300, g=g), wide(300, 40, f)
+    _, kept = da.log_probs_forward(logits, targets)
+    assert L.dlp_backward(_matrix(logits), targets.data_ptr(), kept.data_ptr(), up.data_ptr(), None, 1.0, _matrix(b[:, :40]), s) == 0
+    check([b], [da.log_probs_backward(logits, targets, kept, up)])
 
 
 # ---------------------------------------------------------------- together
