@@ -15,7 +15,8 @@
 // of a sum).
 //
 // A warp takes a short chunk's 1024 16-bit columns at once (its loads are independent), a long one's 256 with eight tokens'
-// loads under way: with one column width for all, 16384 tokens of width 2048 took 64 us instead of ~20.
+// loads under way: with one column width for all, 16384 tokens of width 2048 took 64 us instead of 22.  16384 tokens, 128256 rows of
+// 2048 bf16: lookup 12 us, gradient 109, of which 78 are the zeros (6.7 TB/s); 3001 tokens, 20011 rows of 1003 f32: 5 and 24.
 #include <algorithm>
 
 #include "../../include/detattn.h"

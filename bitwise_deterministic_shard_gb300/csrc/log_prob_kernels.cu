@@ -12,7 +12,8 @@
 //
 // What bounds it: HBM; x is read once, and once more and dx written in the gradient.  A step of 4 vectors of 16 bytes a
 // thread stays in registers: its maximum, then (the sums moved where that is larger) its terms, while the next step's
-// loads are under way.
+// loads are under way.  128256 columns: 4096 f32 rows 302 us (6.96 TB/s), with 5 alternatives 342; 8192 bf16 rows 343 us (6.13 TB/s;
+// issue slots 62 %), with 5 alternatives 462; the gradient of these 629 us (6.68 TB/s).
 //
 // Alternatives: each warp keeps the largest few of its lanes' maxima, step by step; the `top`-th of all warps' is a value that at
 // least `top` elements of the row reach.  What reaches it is kept in shared memory, some tens of elements of a large row; whenever
@@ -218,8 +219,8 @@ struct Candidates {
     raise(least);
     passed = max(passed, least);
   }
-  // What reaches the value in a step; big: the lane's largest; at(j): the j-th of a lane's elements, as (whether the row has it, its
-  // index).  They are read again, a lane's by the whole warp: the step's registers may hold the next one's.
+  // What reaches the value in a step; big: the lane's largest; at(src, j, index): whether the row has the j-th of lane src's
+  // elements, and its index.  They are read again, a lane's by the whole warp: the step's registers may hold the next one's.
   template <int L, typename T, typename At>
   __device__ __forceinline__ void add(const T* row, float big, At at) {
     uint32_t who = __ballot_sync(0xffffffffu, big >= reach);
