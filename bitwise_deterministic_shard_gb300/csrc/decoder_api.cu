@@ -5,30 +5,11 @@
 
 #include "../../include/detattn.h"
 #include "decoder_kernels.h"
+#include "host_util.h"
 
 using namespace detattn;
 
 namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
-int launched(cudaError_t e) { return e == cudaSuccess ? DA_OK : DA_ECUDA; }
-
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encoder() {
-  static const EncodeFn fn = []() -> EncodeFn {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
 
 // boxes of 64 x 64 of a matrix of 16-bit elements
 bool tensor_map(CUtensorMap* m, const void* at, int dtype, int64_t rows, int64_t cols, int64_t stride) {

@@ -6,6 +6,7 @@
 
 #include "../../include/detattn.h"
 #include "attn_train.h"
+#include "host_util.h"
 #include "train_kernels.h"
 
 using namespace detattn;
@@ -13,10 +14,6 @@ using namespace detattn;
 namespace {
 
 constexpr int64_t kMaxS = (int64_t)1 << 24;   // positions are exact in binary32
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
-int launched(cudaError_t e) { return e == cudaSuccess ? DA_OK : DA_ECUDA; }
 
 int check(const da_tensor& t) {
   if (t.dtype != DA_BF16 && t.dtype != DA_F16) return DA_EDTYPE;
@@ -60,22 +57,6 @@ int check_like(const da_tensor* t, const da_tensor& like) {
   if (e) return e;
   if (t->dtype != like.dtype) return DA_EDTYPE;
   return same_shape(*t, like) ? DA_OK : DA_ESHAPE;
-}
-
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encoder() {
-  static const EncodeFn fn = []() -> EncodeFn {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
 }
 
 // {D, pack heads, S, H / pack, B}; boxes of 64 columns x (pack heads x rows) of one group of heads

@@ -69,7 +69,7 @@ typedef struct CUstream_st* da_stream_t; /* a cudaStream_t */
 /* element types */
 #define DA_F32 0
 #define DA_BF16 1
-#define DA_F16 2   /* training operators (dta_*, dln_*, dow_*) only */
+#define DA_F16 2   /* training operators (dta_*, dln_*, dow_*) and a decoder's (dgl_*, dlp_*, dte_*) only */
 
 #define DA_NUM_NDIG 15
 #define DA_DEN_NDIG 6
