@@ -133,7 +133,7 @@ def gated_linear_backward(grad, x, w_gate, w_up, saved, need_x=True, need_weight
     if grad.get_device() != index or grad.dtype != x.dtype or grad.shape != (*x.shape[:-1], F):
         raise DetAttnError(f"grad must be {x.dtype} {(*x.shape[:-1], F)} on x's device")
     n, L, dev, dt = x.numel() // D, _da.lib(), x.device, x.dtype
-    if saved.get_device() != index or saved.dtype != torch.uint8 or saved.numel() != L.dgl_saved_bytes(n, F) or not saved.is_contiguous():
+    if saved is None or saved.get_device() != index or saved.dtype != torch.uint8 or saved.numel() != L.dgl_saved_bytes(n, F) or not saved.is_contiguous():
         raise DetAttnError("saved must be what gated_linear_forward gave for these sizes")
     status = _status(status, index)
     if not need_x and not need_weights:
@@ -244,7 +244,7 @@ def log_probs_backward(logits, targets, saved, grad, grad_entropy=None, temperat
     are as far apart as the logits' are, up to 16 bytes."""
     code, index, targets = _logits(logits, targets, temperature)
     shape, V, n = logits.shape[:-1], logits.shape[-1], targets.numel()
-    if saved.get_device() != index or saved.dtype != torch.float32 or saved.numel() != 3 * n or not saved.is_contiguous():
+    if saved is None or saved.get_device() != index or saved.dtype != torch.float32 or saved.numel() != 3 * n or not saved.is_contiguous():
         raise DetAttnError("saved must be what log_probs_forward gave for these logits")
     grads = []
     for t, name in ((grad, "grad"), (grad_entropy, "grad_entropy")):

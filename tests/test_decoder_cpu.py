@@ -199,6 +199,16 @@ def test_binding_refuses_embedding_tensors(stub):
         da.embedding_forward(ids, w, out=torch.zeros(5, 9))
 
 
+def test_binding_refuses_a_missing_saved_tensor(stub):
+    x, w, t = torch.zeros(4, 16, dtype=B16), torch.zeros(24, 16, dtype=B16), torch.zeros(4, dtype=torch.int64)
+    h, saved = da.gated_linear_forward(x, w, w, need_saved=False)
+    with pytest.raises(da.DetAttnError):
+        da.gated_linear_backward(h, x, w, w, saved)
+    _, saved = da.log_probs_forward(x, t, need_saved=False)
+    with pytest.raises(da.DetAttnError):
+        da.log_probs_backward(x, t, saved, torch.zeros(4))
+
+
 def test_layouts_that_are_passed_on_and_copied(stub):
     """One run of rows goes to the kernels as it is, 16-byte rows apart where they are needed; others are copied."""
     big = torch.zeros(6, 5, 32, dtype=B16)
