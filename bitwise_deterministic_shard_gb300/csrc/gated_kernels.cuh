@@ -68,7 +68,8 @@ __device__ __forceinline__ void activate(float g, float& a, float& d) {
     const float g2 = g * g;
     const float s = logistic(2.f * c * g * __fmaf_rn(k, g2, 1.f));
     a = g * s;
-    d = s * __fmaf_rn(2.f * c * g * __fmaf_rn(3.f * k, g2, 1.f), 1.f - s, 1.f);
+    const float b = fminf(fmaxf(g, -16.f), 16.f);   // past these s is 0 or 1, and y' may be infinite
+    d = s * __fmaf_rn(2.f * c * b * __fmaf_rn(3.f * k, b * b, 1.f), 1.f - s, 1.f);
   } else {
     a = g > 0.f ? g : g != g ? g : 0.f;
     d = g > 0.f ? 1.f : g != g ? g : 0.f;

@@ -265,6 +265,27 @@ def test_gated_special_values_stay_in_their_rows():
         assert torch.equal(got[keep], want[keep])
 
 
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("power", [7, 50, 62])
+def test_gated_far_activations(power, kind):
+    """Where act' is 0 or 1 and the cubic, the square or the exponential overflow: powers of two, so every result is exact."""
+    far = 2.0 ** power
+    x = torch.zeros(3, 8, dtype=torch.bfloat16, device="cuda")
+    x[0, 0], x[0, 1], x[2, 0], x[2, 1] = far, 1.0, -far, 1.0
+    wg, wu = torch.zeros(2, 16, 8, dtype=torch.bfloat16, device="cuda").unbind(0)
+    wg[:, 0], wu[:, 1] = 1.0, 2.0
+    dh = torch.full((3, 16), 0.5, dtype=torch.bfloat16, device="cuda")
+    h, saved = da.gated_linear_forward(x, wg, wu, kind)
+    dx, dwg, dwu = da.gated_linear_backward(dh, x, wg, wu, saved)
+    for got in (h, da.gated_linear(x, wg, wu, kind)):
+        assert (got[0] == 2 * far).all() and (got[1:] == 0).all()
+    want = torch.zeros(3, 8, device="cuda")
+    want[0, 0], want[0, 1] = 16.0, 16 * far                # sums over the 16 hidden units of dh u and 2 dh act(g)
+    assert torch.equal(dx.float(), want)
+    assert (dwg[:, 0] == far).all() and (dwg[:, 1] == 1).all() and (dwg[:, 2:] == 0).all()
+    assert (dwu[:, 0] == far * far / 2).all() and (dwu[:, 1] == far / 2).all() and (dwu[:, 2:] == 0).all()
+
+
 def test_gated_same_bytes_on_another_stream_and_in_a_graph():
     x, wg, wu, dh = _gated_inputs(700, 520, 1000, torch.bfloat16, 7)
 
