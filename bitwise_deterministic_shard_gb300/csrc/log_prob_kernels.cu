@@ -556,6 +556,16 @@ cudaError_t forward(const LpArgs& a, cudaStream_t st) {
   // 40 39 50 76 and 86 89 105 131); more where there are fewer than 16 warps an SM (300 x 50000: 11 with 4, 10 with 8).
   int warps = vectors <= 256 ? 1 : vectors <= 3000 ? 2 : 4;
   while (warps < 8 && a.rows * warps < 152 * 16 && vectors >= 128 * warps) warps *= 2;
+  // More rows than the 1216 CTAs of four warps that fit, and a last round of less than half of them: eight warps, whose rounds are
+  // shorter, where a row is long enough for them, up to three rounds (binary32, which waits for memory alone, four); else two
+  // warps, which need one round up to 2432 rows.  us with 2, 4 and 8 warps: 1300 x 128256 f32 112 129 117, with 5 alternatives
+  // 144 154 136; 1300 x 50000 f32 50 58 56; 2432 x 50000 bf16 48 51 59; 2700 x 262144 f32 509 437 406.
+  constexpr int64_t round = 152 * 8;
+  if (warps == 4 && a.rows > round) {
+    const bool little = (a.rows - 1) % round < round / 2;
+    if (little && vectors >= 16000 && a.rows <= (sizeof(T) == 4 ? 4 : 3) * round) warps = 8;
+    else if (a.rows <= 2 * round) warps = 2;
+  }
   switch (warps) {
     case 1: return forward<T, 1>(a, 1, st);
     case 2: return forward<T, 2>(a, 1, st);

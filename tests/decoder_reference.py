@@ -135,11 +135,11 @@ def log_probs(x, targets, temperature=1.0, top=0, a=None, b=None):
 
 def log_probs_tolerance(r, dtype, temperature):
     """A sum over V: a thread's terms one after the other in two lanes, then up to 24 joins of two roundings.  A row is read by one warp
-    (up to 2048 columns: 64 lanes, 32 terms in each), two (up to 24008: 128 lanes, at most 188), four (256 lanes: V / 256) or
+    (up to 2048 columns: 64 lanes, 32 terms in each), two (up to 24008: 128 lanes, at most 188; from 1217 to 2432 rows also longer ones, V / 128), four (256 lanes: V / 256) or
     more; vectors that start before the row add 8.  Each term's exponent has three roundings (2^-24 of |ln p| each) and ex2 2^-22.
     So the sum is off by K of it and by 3 e of the mean |ln p|, and the entropy's sum by the same of its own."""
-    V = r["z"].shape[1]
-    K = (max(V / 256, 188) + 8 + 48) * e + 2.0 ** -21
+    rows, V = r["z"].shape
+    K = (max(V / 128 if 1216 < rows <= 2432 else V / 256, 188) + 8 + 48) * e + 2.0 ** -21
     of_sum = K + 3 * e * r["far"]
     tl = of_sum[:, None] + 4 * e * (r["lp_all"].abs() + 1)
     tH = 2 * of_sum * (1 + r["H"]) + 4 * e * r["far"] + 8 * e * (1 + r["H"])

@@ -370,6 +370,14 @@ def test_log_probs(rows, V, top, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows, V, top", [(1217, 64003, 5), (1300, 128256, 1), (1900, 30001, 7), (2432, 25000, 0), (2500, 64008, 3)])
+def test_log_probs_of_more_rows_than_one_round(rows, V, top, dtype):
+    """Long rows of which more than one round of CTAs, with two, four and eight warps each."""
+    x, t, a, b = _logits(rows, V, dtype)
+    _probs_check(x, t, 1.3, top, a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("V", [40, 3001, 40001])
 @pytest.mark.parametrize("gap, shift", [(3, 1), (8, 0), (13, 5), (1, 0)])
 def test_log_probs_rows_of_wider_buffers(V, gap, shift, dtype):
