@@ -118,7 +118,7 @@ struct EmArgs {
   // workspace of the gradient
   uint32_t* key[2];              // longer sorts: [n] ids in sorted order (rows: no gradient), and of the pass before
   uint32_t* pos[2];              // [n] their tokens
-  uint32_t* count;               // longer sorts: [EM_BINS][blocks]
+  uint32_t* count;               // longer sorts: [blocks][EM_BINS] or [bins][blocks]
   EmUnits* found;
   uint4* unit;                   // [n]: chunks (first place, tokens and EM_MORE, row): short ones from the front, long ones from the back
   uint4* row;                    // [n / EM_CHUNK + 1]: rows of several chunks (first place, end, row)

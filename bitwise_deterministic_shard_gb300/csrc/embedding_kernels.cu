@@ -6,8 +6,8 @@
 // row of dw, most of them zeros for a large vocabulary.
 //
 // Gradient: the tokens are sorted by id, stably, by counting digits of up to 9 bits from the lowest on (two passes up to 2^18
-// rows).  Up to 4096 tokens one CTA does that in shared memory; longer ones take three launches a pass, each of which starts as the one
-// before it ends.  dw's zeros wait for nothing and are written beside all of these.  A token's place among those of its digit comes
+// rows).  Up to 4096 tokens one CTA does that in shared memory; longer ones take two launches a pass (three past 32768), each of
+// which starts as the one before it ends.  dw's zeros wait for nothing and are written beside all of these.  A token's place among those of its digit comes
 // from ballots over the warp and the warp's counters, so the order never depends on which thread came first.  Then a chunk of up to 32 tokens of a row is one
 // chain of binary32 additions for each column, in order of the tokens; rows of more leave their chunks' sums in the
 // workspace, and a last kernel adds these, eight runs of chunks in order and then the eight.  So a row's bits depend on its own
@@ -265,9 +265,10 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) em_sort_kernel(const __grid_c
 
 // ---- a pass over longer ones; CTAs past a kernel's own fill their part of the zeros ----
 constexpr int RADIX_THREADS = 256, RADIX_WARPS = 8;
-// counts of a block's digits (the first pass: from the ids)
-__global__ void __launch_bounds__(RADIX_THREADS) em_count_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int block, int from, int shift, int bits,
-                                                                 Fill fill) {
+// counts of a block's digits (the first pass: from the ids), as [blocks][EM_BINS] where the next kernel adds them up itself, else as
+// [bins][blocks]
+__global__ void __launch_bounds__(RADIX_THREADS) em_count_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int block, bool by_block, int from, int shift,
+                                                                 int bits, Fill fill) {
   next_may_start();
   if (blockIdx.x >= blocks) {
     fill_zeros(a, blockIdx.x - blocks, gridDim.x - blocks, fill);
@@ -278,11 +279,15 @@ __global__ void __launch_bounds__(RADIX_THREADS) em_count_kernel(const __grid_co
   for (int b = threadIdx.x; b < EM_BINS; b += RADIX_THREADS) hist[b] = 0;
   __syncthreads();
   after_previous();
+  if (from < 0 && blockIdx.x == 0 && threadIdx.x == 0) *a.found = {0, 0, 0};
   const int64_t i0 = (int64_t)blockIdx.x * block, i1 = min(a.n, i0 + block);
   for (int64_t i = i0 + threadIdx.x; i < i1; i += RADIX_THREADS)
     atomicAdd(&hist[(from < 0 ? key_at(a, i) : a.key[from][i]) >> shift & mask], 1u);
   __syncthreads();
-  for (uint32_t b = threadIdx.x; b <= mask; b += RADIX_THREADS) a.count[(size_t)b * blocks + blockIdx.x] = hist[b];
+  if (by_block)
+    for (int b = threadIdx.x; b < EM_BINS; b += RADIX_THREADS) a.count[(size_t)blockIdx.x * EM_BINS + b] = hist[b];
+  else
+    for (uint32_t b = threadIdx.x; b <= mask; b += RADIX_THREADS) a.count[(size_t)b * blocks + blockIdx.x] = hist[b];
 }
 // places before each (digit, block): one CTA, a run of counts a thread
 __global__ void __launch_bounds__(1024) em_scan_kernel(const __grid_constant__ EmArgs a, int64_t n, Fill fill) {
@@ -293,7 +298,6 @@ __global__ void __launch_bounds__(1024) em_scan_kernel(const __grid_constant__ E
   }
   __shared__ uint32_t warps[32];
   after_previous();
-  if (threadIdx.x == 0) *a.found = {0, 0, 0};
   uint32_t* const count = a.count;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t per = (n + 4095) / 4096, i0 = min(n / 4, tid * per), i1 = min(n / 4, i0 + per);   // n is a multiple of 4: so are the bins
@@ -321,7 +325,11 @@ __global__ void __launch_bounds__(1024) em_scan_kernel(const __grid_constant__ E
     before += c.x + c.y + c.z + c.w;
   }
 }
-template <int K>   // steps of a warp: blocks of 256 K tokens
+// K: steps of a warp, blocks of 256 K tokens.  ADD: this kernel adds up the blocks' counts (a thread two neighbouring digits), else
+// em_scan_kernel has: a launch less, as long as there are few blocks to read (5000 tokens, 1000 rows of 64: 29 us instead of 35; 32768,
+// 50000 rows of 512, 32 blocks of 1024: 47.6 and 48.4; but 65536, 30000 rows of 64, 32 blocks of 2048: 52 and 46).
+static_assert(EM_BINS == 2 * RADIX_THREADS, "two digits a thread");
+template <int K, bool ADD>
 __global__ void __launch_bounds__(RADIX_THREADS) em_scatter_kernel(const __grid_constant__ EmArgs a, uint32_t blocks, int from, int to, int shift, int bits,
                                                                    Fill fill) {
   next_may_start();
@@ -342,12 +350,36 @@ __global__ void __launch_bounds__(RADIX_THREADS) em_scatter_kernel(const __grid_
     key[k] = i < a.n ? from < 0 ? key_at(a, i) : a.key[from][i] : 0;
     pos[k] = i < a.n && from >= 0 ? a.pos[from][i] : (uint32_t)i;
   }
+  __shared__ uint32_t base[ADD ? EM_BINS : 1], warps[RADIX_WARPS];
+  if constexpr (ADD) {
+    uint2 all = make_uint2(0, 0), earlier = make_uint2(0, 0);
+    const uint2* const count = reinterpret_cast<const uint2*>(a.count) + tid;
+#pragma unroll 8
+    for (uint32_t b = 0; b < blocks; b++) {
+      const uint2 c = count[(size_t)b * RADIX_THREADS];
+      if (b == blockIdx.x) earlier = all;
+      all.x += c.x;
+      all.y += c.y;
+    }
+    uint32_t sum = all.x + all.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    if (lane == 31) warps[warp] = sum;
+    __syncthreads();
+    uint32_t before = sum - all.x - all.y;
+    for (int w = 0; w < warp; w++) before += warps[w];
+    base[2 * tid] = before + earlier.x;
+    base[2 * tid + 1] = before + all.x + earlier.y;
+  }
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < K; k++) place[k] = count_digit(i0 + k * 32 < a.n ? key[k] >> shift & mask : EM_BINS, bits, hist[warp]);
   __syncthreads();
   for (uint32_t b = tid; b <= mask; b += RADIX_THREADS) {
-    uint32_t before = a.count[(size_t)b * blocks + blockIdx.x];
+    uint32_t before = ADD ? base[ADD ? b : 0] : a.count[(size_t)b * blocks + blockIdx.x];
 #pragma unroll
     for (int w = 0; w < RADIX_WARPS; w++) {
       const uint32_t c = hist[w][b];
@@ -577,21 +609,22 @@ cudaError_t launch_embedding_grad(const EmArgs& a, cudaStream_t st) {
   } else {
     const int block = em_block(a.n);
     const uint32_t blocks = (uint32_t)((a.n + block - 1) / block), chunks = (uint32_t)((a.n + 255) / 256);
-    const uint32_t parts = 3 * passes + 1;
+    const bool add = block == 1024;   // 32 blocks at most
+    const uint32_t each = add ? 2 : 3, parts = each * passes + 1;   // launches of a pass
     const unsigned f = fillers(bytes / parts, 256), g = fillers(bytes / parts, 1024);
     for (int p = 0; p < passes && e == cudaSuccess; p++) {
       const int src = p ? (p + 1) & 1 : -1, dst = p & 1, shift = p * bits;
-      const auto fill = [&](uint32_t k) { return Fill{3 * p + k, parts}; };
+      const auto fill = [&](uint32_t k) { return Fill{each * p + k, parts}; };
       if (p == 0) {   // after everything before it; the others only wait for each other
-        em_count_kernel<<<blocks + f, RADIX_THREADS, 0, st>>>(a, blocks, block, src, shift, bits, fill(0));
+        em_count_kernel<<<blocks + f, RADIX_THREADS, 0, st>>>(a, blocks, block, add, src, shift, bits, fill(0));
         e = cudaGetLastError();
       } else {
-        e = launch_early(em_count_kernel, dim3(blocks + f), RADIX_THREADS, 0, st, a, blocks, block, src, shift, bits, fill(0));
+        e = launch_early(em_count_kernel, dim3(blocks + f), RADIX_THREADS, 0, st, a, blocks, block, add, src, shift, bits, fill(0));
       }
-      if (e == cudaSuccess) e = launch_early(em_scan_kernel, dim3(1 + g), 1024, 0, st, a, (int64_t)blocks << bits, fill(1));
+      if (e == cudaSuccess && !add) e = launch_early(em_scan_kernel, dim3(1 + g), 1024, 0, st, a, (int64_t)blocks << bits, fill(1));
+      const auto scatter = add ? em_scatter_kernel<4, true> : em_scatter_kernel<8, false>;
       if (e == cudaSuccess)
-        e = launch_early(block == 1024 ? em_scatter_kernel<4> : em_scatter_kernel<8>, dim3(blocks + f), RADIX_THREADS, 0, st, a, blocks, src, dst, shift,
-                         bits, fill(2));
+        e = launch_early(scatter, dim3(blocks + f), RADIX_THREADS, 0, st, a, blocks, src, dst, shift, bits, fill(each - 1));
       from = dst;
     }
     if (e == cudaSuccess) e = launch_early(em_chunk_kernel, dim3(chunks + f), 256, 0, st, a, chunks, from, Fill{parts - 1, parts});

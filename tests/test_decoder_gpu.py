@@ -62,6 +62,17 @@ def test_embedding(n, v, w, dtype):
     assert da.read_status(st) == 0
 
 
+@pytest.mark.parametrize("n, v", [(32768, 600), (32769, 300000), (131072, 5), (131073, 5), (150001, 70000), (200000, 1)])
+def test_embedding_of_many_tokens(n, v):
+    """The longer sort's blocks of both sizes, up to 32 of them and more."""
+    g = _gen(n)
+    ids, dy = _words(n, v, g), _randn(n, 12, g=g)
+    dw = da.embedding_backward(dy, ids, v)
+    r = R.embedding(ids, torch.zeros(v, 12, device="cuda"), dy)
+    _close(dw, r["dw"], R.embedding_tolerance(r, torch.float32, 1.0)["dw"], "dw")
+    assert torch.equal(dw, da.embedding_backward(dy, ids.int(), v))
+
+
 @pytest.mark.parametrize("n", [50, 20000])
 def test_embedding_unknown_ids(n):
     g = _gen(1)
