@@ -125,6 +125,7 @@ struct Shared {
 // The value of rank k (from 0) of one value a lane, largest first.
 __device__ __forceinline__ uint32_t of_rank(uint32_t v, int k) {
   const int lane = threadIdx.x & 31;
+  if (k == 0) return __reduce_max_sync(0xffffffffu, v);
 #pragma unroll
   for (int size = 2; size <= 32; size *= 2)
 #pragma unroll
