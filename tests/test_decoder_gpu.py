@@ -136,6 +136,39 @@ def test_embedding_row_depends_on_its_own_tokens():
         assert torch.equal(first[17], da.embedding_backward(dy, other, 4000)[17])
 
 
+@pytest.mark.parametrize("n, v, w", [(20, 300, 16), (3000, 20000, 264), (20000, 70000, 136), (40000, 900, 33)])
+def test_embedding_in_graphs_and_on_two_streams(n, v, w):
+    """Replayed with other ids and gradients, and two calls at once: equal bytes to a call alone."""
+    g = _gen(n + w)
+    sets = [(_words(n, v, g), _randn(n, w, g=g, to=torch.bfloat16)) for _ in range(4)]
+    weight = _randn(v, w, g=g, to=torch.bfloat16)
+    want = [(da.embedding_forward(ids, weight, 2.0), da.embedding_backward(dy, ids, v, 2.0, 0)) for ids, dy in sets]
+    held = [[t.clone() for t in sets[i]] for i in range(2)]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for ids, dy in held:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append((da.embedding_forward(ids, weight, 2.0), da.embedding_backward(dy, ids, v, 2.0, 0)))
+    for turn in range(3):
+        for k in range(2):
+            for to, new in zip(held[k], sets[(turn + k) % 4]):
+                to.copy_(new)
+        torch.cuda.synchronize()
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                graphs[k].replay()
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert all(torch.equal(p, q) for p, q in zip(outs[k], want[(turn + k) % 4]))
+    got = [[], []]
+    for i in range(4):
+        with torch.cuda.stream(streams[i % 2]):
+            got[i % 2].append(da.embedding_backward(sets[i][1], sets[i][0], v, 2.0, 0))
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[i % 2][i // 2], want[i][1]) for i in range(4))
+
+
 def test_embedding_offsets_past_32_bits():
     v, w = 530000, 4104                                   # 2.17e9 elements
     weight = torch.zeros(v, w, device="cuda", dtype=torch.bfloat16)
