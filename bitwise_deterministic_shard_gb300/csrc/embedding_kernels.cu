@@ -611,7 +611,8 @@ cudaError_t launch_embedding_grad(const EmArgs& a, cudaStream_t st) {
     const uint32_t blocks = (uint32_t)((a.n + block - 1) / block), chunks = (uint32_t)((a.n + 255) / 256);
     const bool add = block == 1024;   // 32 blocks at most
     const uint32_t each = add ? 2 : 3, parts = each * passes + 1;   // launches of a pass
-    const unsigned f = fillers(bytes / parts, 256), g = fillers(bytes / parts, 1024);
+    const int64_t part = (bytes + parts - 1) / parts;   // rounded up: where there are fewer bytes than parts, one CTA still writes the ends
+    const unsigned f = fillers(part, 256), g = fillers(part, 1024);
     for (int p = 0; p < passes && e == cudaSuccess; p++) {
       const int src = p ? (p + 1) & 1 : -1, dst = p & 1, shift = p * bits;
       const auto fill = [&](uint32_t k) { return Fill{each * p + k, parts}; };
