@@ -434,7 +434,13 @@ __global__ void __launch_bounds__(32 * W, W == 1 ? 24 : 32 / W) lp_kernel(const 
   if (warp != 0) return;
   const bool none = m.S == 0.f;                             // every logit is -inf
   const float log_s = none ? 0.f : logf(m.S);
-  const auto log_prob = [&](float y) { return none || (y == -INFINITY && m.S == m.S) ? -INFINITY : __fdiv_rn(y - m.m, a.temperature) - log_s; };
+  // The difference first, which keeps small ones of large logits exact; where it passes the largest finite number its quotient
+  // may still be one, and is the difference of the quotients.
+  const auto log_prob = [&](float y) {
+    if (none || (y == -INFINITY && m.S == m.S)) return -INFINITY;
+    const float d = y - m.m;
+    return (isfinite(d) ? __fdiv_rn(d, a.temperature) : __fdiv_rn(y, a.temperature) - __fdiv_rn(m.m, a.temperature)) - log_s;
+  };
   if (lane == 0) {
     float lp = 0.f;
     if (target >= (int64_t)a.cols) {

@@ -10,6 +10,7 @@ import torch
 import bitwise_deterministic_shard_gb300 as da
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import decoder_reference as R  # noqa: E402
 import test_decoder_gpu as T  # noqa: E402
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -47,3 +48,33 @@ def test_every_row_of_a_small_gradient_is_written(n, dtype):
                     want[-1] = torch.tensor(float(n)).to(dtype)       # ones: every sum is exact
                 assert torch.equal(dw.view(rows, cols), want), (rows, cols, id_, padding, start)
                 assert (buffer[:start] == 7).all() and (buffer[start + rows * cols:] == 7).all()
+
+
+# ---------------------------------------------------------------- log probabilities
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows, V, top", [(3, 2, 2), (5, 50, 32), (300, 3001, 20), (4, 40001, 32), (1300, 20000, 5)])
+@pytest.mark.parametrize("temperature", [4.0, 1.0e3, 2.0 ** 60])
+def test_log_probs_of_logits_farther_apart_than_the_type_reaches(temperature, rows, V, top, dtype):
+    """Differences past the largest finite number whose quotients by the temperature are finite: the lowest logits as targets and among
+    the alternatives."""
+    x, t, a, b = T._logits(rows, V, dtype, 11)
+    x[:, 0], x[:, V // 2], x[:, V - 1] = 3e38, -3e38, torch.finfo(dtype).min
+    t[0::3], t[1::3], t[2::3] = V // 2, V - 1, 0
+    x[1::2, 1:] = torch.where(torch.rand(x[1::2, 1:].shape, device="cuda", generator=T._gen(V)) < 0.5, -3e38, -1.5e38).to(dtype)
+    r, _ = T._probs_check(x, t, temperature, top, a, b)
+    assert torch.isfinite(r.log_probs).all() and torch.isfinite(r.top_log_probs).all()
+    assert (r.log_probs[0] < -5e38 / temperature) and (r.log_probs[1] < -4e38 / temperature)
+
+
+def test_log_probs_past_the_results_range_are_infinite():
+    """Quotients that binary32 does not hold, and those it just holds."""
+    x = torch.tensor([[3e38, -3e38, 1.0, -INF]] * 3, device="cuda")
+    t = torch.tensor([1, 2, 3], device="cuda")
+    for temperature in (0.5, 1.0, 1.7, 1.8, 2.0):
+        r = da.log_probs_forward(x, t, temperature, 4)[0]
+        want = R.log_probs(x, t, torch.tensor(temperature).item(), 4)
+        for got, w in ((r.log_probs, want["lp"]), (r.top_log_probs, want["top_lp"])):
+            T._close(got, w.float().double(), 1.02 * 5 * R.e * w.abs() + 1e-30, temperature)
+        assert torch.equal(r.top_indices, want["top"]) and (r.entropy == 0).all()
+        assert r.log_probs[0].isinf() == (temperature < 1.75) and r.log_probs[1].isinf() == (temperature < 0.8) and r.log_probs[2] == -INF
