@@ -39,8 +39,8 @@ struct GlScaleArgs {             // dg = dh p, du = dh q
   void* dg;                      // [T, F] in rows of gl_grad_row(F), du behind it
   int64_t T, F;
 };
-// The saved factors p and q of [T, F], in planes of rows of F rounded up to 16: the high 16 bits of each binary32 value of p,
-// those of q, then the next 8 bits of p, those of q.
+// The saved factors p and q of [T, F], rounded to 24 bits, in planes of rows of F rounded up to 16: the high 16 bits of each binary32
+// value of p, those of q, then the next 8 bits of p, those of q.
 __host__ __device__ inline int64_t gl_saved_row(int64_t F) { return (F + 15) / 16 * 16; }
 __host__ __device__ inline size_t gl_saved_bytes(int64_t T, int64_t F) { return (size_t)6 * T * gl_saved_row(F); }
 

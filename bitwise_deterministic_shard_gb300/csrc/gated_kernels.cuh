@@ -7,7 +7,7 @@
 // Forward: one kernel of pair products (gemm_pair.cuh).  Half the rows of its second operand are rows of Wg (one CTA's half)
 // and the other half the same rows of Wu, so g and u of a token and hidden unit lie in one TMEM lane, half a tile apart,
 // and a thread forms h from them.  For the backward pass it also writes p and q, the only values of the activation that the
-// gradient needs: 24 bits of each (2^-15 of the value left out), as 16 would add a rounding of the size of the result's own to dg
+// gradient needs: each rounded to 24 bits (2^-16 of the value at most), as 16 would add a rounding of the size of the result's own to dg
 // and du (dx then 2.9e-3 off in bf16 instead of 2.35e-3; 1.66e-3 is a result only rounded).
 // Backward: dg and du as one pass over dh, p and q, rounded to 16 bits (the tensor cores take operands of one 16-bit type), then one
 // kernel of pair products: dx contracts over both halves of [dg | du] in one chain, dW has the tiles of both weights; the
@@ -109,6 +109,12 @@ __device__ __forceinline__ uint4 stage_get(uint32_t stage, int r, int u) {
                : "memory");
   return v;
 }
+// v rounded to the nearest 24-bit value, but for its low byte, which is left out later; ties away from zero.  (Cut off instead, all
+// factors would be too small, by up to 2^-15.)  What would become an infinity, infinities and NaN stay as they are.
+__device__ __forceinline__ float nearest_24(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return __uint_as_float((b & 0x7fffffffu) < 0x7f7fff80u ? b + 0x80u : b);
+}
 // the high halves of 8 binary32 values; the bytes below them of 16
 __device__ __forceinline__ uint4 high_halves(const float* v) {
   const auto two = [&](int i) { return __byte_perm(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), 0x7632); };
@@ -165,6 +171,10 @@ __global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl
             activate<ACT>(g[e], q[e], d);
             g[e] = q[e] * u[e];
             u[e] *= d;
+            if constexpr (SAVE) {
+              q[e] = nearest_24(q[e]);
+              u[e] = nearest_24(u[e]);
+            }
           }
           const auto units = [&](int j) {
             return make_uint4(pack16<BF>(g[8 * j], g[8 * j + 1]), pack16<BF>(g[8 * j + 2], g[8 * j + 3]),

@@ -98,7 +98,7 @@ def gated_linear_forward(x, w_gate, w_up, activation="silu", need_saved=True, ou
     x [..., width], w_gate and w_up [hidden, width], all bf16 or all f16, width and hidden multiples of 8; h [..., hidden].
     activation: "silu", "gelu" (with the error function), "gelu_tanh" or "relu" (whose derivative follows the sign of the
     binary32 sum: of a g that is within that sum's rounding of 0, either one).  Both products are binary32 sums, h is
-    rounded once.  saved, which the backward pass takes, holds act(g) and act'(g) u with 24 bits each (6 bytes a hidden
+    rounded once.  saved, which the backward pass takes, holds act(g) and act'(g) u rounded to 24 bits each (6 bytes a hidden
     value); None without need_saved.  Up to 16 tokens without it the weights are read once by another kernel, whose sums are in
     another order.  Tensors that the kernels cannot address (columns not contiguous, starts or row strides off 16 bytes) are
     copied."""

@@ -422,7 +422,7 @@ int dow_adamw(const dow_tensor* tensors, int n, int dtype, int state_bits, void*
 /* h = act(x wg^T) (x wu^T): x [tokens, width], wg and wu [hidden, width], h [tokens, hidden], all bf16 or all f16.  width and
  * hidden are multiples of 8, pointers 16-byte aligned, row strides multiples of 8 elements.  The products are binary32 sums; h is
  * rounded once.  saved: optional device memory of dgl_saved_bytes(tokens, hidden), 16-byte aligned, which the backward
- * pass takes (act(g) and act'(g) u, 24 bits of each binary32 value).  Up to 16 tokens without saved, the sums are in another
+ * pass takes (act(g) and act'(g) u, each rounded to 24 bits).  Up to 16 tokens without saved, the sums are in another
  * order than with more tokens or with saved. */
 size_t dgl_saved_bytes(int64_t tokens, int64_t hidden);
 int dgl_forward(const da_matrix* x, const da_matrix* wg, const da_matrix* wu, int activation, const da_matrix* h, void* saved,

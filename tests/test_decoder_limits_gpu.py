@@ -78,3 +78,51 @@ def test_log_probs_past_the_results_range_are_infinite():
             T._close(got, w.float().double(), 1.02 * 5 * R.e * w.abs() + 1e-30, temperature)
         assert torch.equal(r.top_indices, want["top"]) and (r.entropy == 0).all()
         assert r.log_probs[0].isinf() == (temperature < 1.75) and r.log_probs[1].isinf() == (temperature < 0.8) and r.log_probs[2] == -INF
+
+
+# ---------------------------------------------------------------- gated feed-forward
+
+@pytest.mark.parametrize("dtype, bits", [(torch.bfloat16, 8), (torch.float16, 11)])
+@pytest.mark.parametrize("tokens", [1, 300])
+def test_gated_factors_are_rounded_to_nearest(tokens, dtype, bits):
+    """A factor v is kept with 16 significant bits and rounded to the operands' type in the backward pass.  Here v is half a step of that type above 1,
+    and three quarters of a step of 2^-15 more: to nearest this stays above the half step and the gradient is rounded up;
+    cut off toward zero it falls back onto the half step, which goes to the even neighbour, 1."""
+    x = torch.zeros(tokens, 16, device="cuda", dtype=dtype)
+    half, step = 2.0 ** -bits, 2.0 ** (1 - bits)
+    x[0, 0], x[0, 1], x[0, 2], x[0, 3] = 1.0, half, 2.0 ** -9, 2.0 ** -9
+    wg, wu = (torch.zeros(24, 16, device="cuda", dtype=dtype) for _ in range(2))
+    sign = torch.where(torch.arange(24, device="cuda") % 3 == 0, -1.0, 1.0).to(dtype)
+    for w, s in ((wg, torch.ones_like(sign)), (wu, sign)):            # relu: q = g, p = u
+        w[:, 0], w[:, 1], w[:, 2], w[:, 3] = s, s, s * 2.0 ** -7, s * 2.0 ** -8
+    h, saved = da.gated_linear_forward(x, wg, wu, "relu")
+    dh = torch.zeros(tokens, 24, device="cuda", dtype=dtype)
+    dh[0] = 1.0
+    _, dwg, dwu = da.gated_linear_backward(dh, x, wg, wu, saved)      # one token: dwu[:, 0] = du x[0, 0] = q
+    v = 1.0 + half + 2.0 ** -16 + 2.0 ** -17
+    assert torch.tensor(v, dtype=torch.float64).to(dtype) == 1 + step
+    assert (dwu[:, 0] == 1 + step).all() and torch.equal(dwg[:, 0], (1 + step) * sign)
+
+
+def test_gated_factors_at_the_ends_of_binary32():
+    """The largest finite factor stays finite, infinities and NaN stay what they are."""
+    t, top, far = torch.bfloat16, 2.0 - 2.0 ** -7, 2.0 ** 120
+    x = torch.zeros(4, 16, device="cuda", dtype=t)
+    x[:, :4] = 1.0
+    x[2, 5], x[3, 5] = INF, float("nan")
+    wg, wu = (torch.zeros(24, 16, device="cuda", dtype=t) for _ in range(2))
+    wg[:, 3], wg[:, 5] = 1.0, 1.0
+    wu[:, 0], wu[:, 1], wu[:, 2] = top * 2.0 ** 127, top * 2.0 ** 119, top * 2.0 ** 111      # their sum is 2^128 - 2^104
+    wu[1::2] = -wu[1::2]
+    h, saved = da.gated_linear_forward(x, wg, wu, "relu")
+    dh = torch.zeros(4, 24, device="cuda", dtype=t)
+    for row, want in ((0, far), (1, far), (2, INF), (3, float("nan"))):
+        dh.zero_()
+        dh[row] = 2.0 ** -8
+        _, dwg, dwu = da.gated_linear_backward(dh[row:row + 1], x[row:row + 1], wg, wu, da.gated_linear_forward(x[row:row + 1], wg, wu, "relu")[1])
+        if row < 2:
+            assert (dwg[0::2, 3] == want).all() and (dwg[1::2, 3] == -want).all() and (dwu[:, 3] == 2.0 ** -8).all()
+        elif row == 2:
+            assert (dwu[:, 3] == INF).all()
+        else:
+            assert dwu[:, 3].isnan().all()
