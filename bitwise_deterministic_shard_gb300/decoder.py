@@ -2,8 +2,9 @@
 log probabilities of given tokens with entropy and alternatives, each with its gradient.
 
 Argument marshalling only, as in train.py: the computation runs in the CUDA kernels behind include/detattn.h on the current stream
-of the tensors' device, and there is no CPU path.  Every kernel adds in an order that depends on the sizes and types alone,
-so equal calls give equal bytes on every run.
+of the tensors' device, and there is no CPU path.  Every kernel adds in an order that depends on the sizes and types and, for log
+probabilities, on where the rows of logits start within 16 bytes, so equal calls (for log probabilities: on equally aligned rows) give
+equal bytes on every run.
 """
 from __future__ import annotations
 
@@ -221,7 +222,9 @@ def log_probs_forward(logits, targets, temperature=1.0, top=0, need_saved=True, 
       log_probs = z[target] - lse (a negative target: no token, 0);  entropy = lse - sum p z
       top_indices, top_log_probs [..., top]: the top largest logits (up to 32) in order, equal ones by their index; None for 0
     Results are f32 (indices int64).  A logit of -inf is a token of probability 0; a row of nothing else has entropy 0 and log
-    probabilities of -inf.  saved, which the backward pass takes, is None without need_saved."""
+    probabilities of -inf.  saved, which the backward pass takes, is None without need_saved.  How a row's sums are shared out depends on
+    the number of rows and on where the row starts within 16 bytes: the same row among others, or in a shifted view, can differ in low
+    bits (top_indices do not)."""
     code, index, targets = _logits(logits, targets, temperature)
     shape, V, dev = logits.shape[:-1], logits.shape[-1], logits.device
     if not 0 <= top <= min(TOP_MOST, V):

@@ -410,8 +410,9 @@ int dow_adamw(const dow_tensor* tensors, int n, int dtype, int state_bits, void*
 /* ---- Operators at the ends and in the middle of a decoder ----------------------------------
  * Gated feed-forward projections, embedding lookup and log probabilities, each with its gradient.  As the training operators
  * above they compute in binary32 in a fixed order: no atomics add values, and the order depends on the sizes and types
- * given (an embedding row's gradient: on the places of its own tokens alone), so equal calls give equal bytes on every run.  The
- * conventions above hold. */
+ * given (an embedding row's gradient: on the places of its own tokens alone) and, for log probabilities, on where the rows of logits start
+ * within 16 bytes.  So equal calls give equal bytes on every run; for log probabilities that is equal values in equally aligned places.
+ * The conventions above hold. */
 
 /* activations */
 #define DGL_SILU 0        /* g / (1 + exp(-g)) */
@@ -443,7 +444,11 @@ int dgl_backward(const da_matrix* dh, const da_matrix* x, const da_matrix* wg, c
  *   top_log_probs, top_indices [rows, top], top up to 32 and cols: the largest logits in order, equal ones by their index
  * A logit of -inf is a token of probability 0; a row of nothing else has an entropy of 0 and log probabilities of -inf.  A target past
  * the last column gives NaN and DA_STATUS_BAD_TARGET.  Other logits must be finite: NaN or +inf makes its row's results NaN (its
- * alternatives unspecified) and sets DA_STATUS_NONFINITE.  saved: optional device f32 [rows, 3] for the backward pass. */
+ * alternatives unspecified, a log probability of no token still 0) and sets DA_STATUS_NONFINITE.  saved: optional device f32 [rows, 3] for
+ * the backward pass.
+ * How many threads share a row depends on the number of rows, and which elements a thread adds on the row's start modulo 16 bytes: a
+ * row among other rows, or at another start (in a slice, in rows of an odd number of columns), can differ in low bits.  top_indices do
+ * not depend on either. */
 int dlp_forward(const da_matrix* logits, const int64_t* targets, float temperature, int top, float* log_probs, float* entropy,
                 float* saved, float* top_log_probs, int64_t* top_indices, int32_t* dev_status, da_stream_t stream);
 

@@ -80,6 +80,28 @@ def test_log_probs_past_the_results_range_are_infinite():
         assert r.log_probs[0].isinf() == (temperature < 1.75) and r.log_probs[1].isinf() == (temperature < 0.8) and r.log_probs[2] == -INF
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows, V", [(5, 40001), (300, 3001), (1300, 20003)])
+def test_log_probs_have_equal_bytes_in_equally_aligned_places(rows, V, dtype):
+    """The order of a row's sums depends on the number of rows and on where the rows start within 16 bytes: on nothing else of
+    their place.  Other starts and other numbers of rows stay within the tolerance of the sums."""
+    per = 16 // dtype.itemsize
+    x, t, a, b = T._logits(rows, V, dtype, 12)
+    want, dx = T._probs_check(x, t, 0.9, 7, a, b)
+    buffer = torch.empty(rows * V + 3 * per, device="cuda", dtype=dtype)
+    same = buffer[2 * per:2 * per + rows * V].view(rows, V)
+    wide = torch.empty(rows, V + 5 * per, device="cuda", dtype=dtype)[:, :V]      # rows that start as x's do
+    other = torch.empty(rows, V + 5 * per + 3, device="cuda", dtype=dtype)[:, 1:V + 1]
+    for y, equal in ((same, True), (wide, True), (other, False)):
+        y.copy_(x)
+        got, grad = T._probs_check(y, t, 0.9, 7, a, b)
+        assert torch.equal(got.top_indices, want.top_indices)
+        if equal:
+            assert all(torch.equal(p, q) for p, q in zip(got, want)) and torch.equal(grad, dx)
+    first, _ = T._probs_check(x[:1], t[:1], 0.9, 7, a[:1], b[:1])      # a row by itself
+    assert torch.equal(first.top_indices, want.top_indices[:1])
+
+
 # ---------------------------------------------------------------- gated feed-forward
 
 @pytest.mark.parametrize("dtype, bits", [(torch.bfloat16, 8), (torch.float16, 11)])
