@@ -102,6 +102,36 @@ def test_log_probs_have_equal_bytes_in_equally_aligned_places(rows, V, dtype):
     assert torch.equal(first.top_indices, want.top_indices[:1])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [70, 3000, 40001, 128256])
+def test_alternatives_of_rows_of_which_little_is_finite(V, dtype):
+    """Finite logits at every other place; fewer than the alternatives, spread over the row, at its ends, side by side; among the type's
+    lowest; none: the finite ones come first in order, then the first of the others."""
+    g, places = T._gen(V), torch.arange(V, device="cuda")
+    up = (places.float() / V * 8).to(dtype)
+    nothing = torch.full_like(up, -INF)
+    x = [torch.where(places % 2 == 1, up, nothing), torch.where(places % 2 == 0, -up, nothing)]
+    for k in (1, 2, 5, 31, 32, 33):
+        row = nothing.clone()
+        row[torch.randperm(V, device="cuda", generator=g)[:k]] = T._randn(k, g=g, to=dtype)
+        x.append(row)
+    for at in ([0], [V - 1], [0, V - 1], list(range(V - 9, V)), list(range(20))):
+        row = nothing.clone()
+        row[at] = 1.5
+        x.append(row)
+    low = torch.where(places % 3 == 0, torch.full_like(up, torch.finfo(dtype).min), nothing)
+    x.append(low.clone())
+    low[V // 2] = 3.0
+    x += [low, nothing]
+    x = torch.stack(x)
+    t = torch.zeros(len(x), dtype=torch.int64, device="cuda")
+    for top in (1, 3, 8, 20, 32):
+        r = da.log_probs_forward(x, t, 1.0, top)[0]
+        want = torch.sort(x, dim=1, descending=True, stable=True)
+        assert torch.equal(r.top_indices, want.indices[:, :top]), top
+        assert torch.equal(r.top_log_probs == -INF, want.values[:, :top] == -INF), top
+
+
 # ---------------------------------------------------------------- gated feed-forward
 
 @pytest.mark.parametrize("dtype, bits", [(torch.bfloat16, 8), (torch.float16, 11)])
