@@ -178,3 +178,58 @@ def test_gated_factors_at_the_ends_of_binary32():
             assert (dwu[:, 3] == INF).all()
         else:
             assert dwu[:, 3].isnan().all()
+
+
+# ---------------------------------------------------------------- graphs and streams
+
+def _replayed_and_at_once(sets, step):
+    """step(*set) captured twice, both graphs replayed on two streams with other inputs each time, and called on two streams
+    at once: equal bytes to a call alone."""
+    want = [[v.clone() for v in step(*s)] for s in sets]
+    held = [[v.clone() for v in sets[i]] for i in range(2)]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for h in held:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(*h))
+    for turn in range(3):
+        for k in range(2):
+            for to, new in zip(held[k], sets[(turn + k) % len(sets)]):
+                to.copy_(new)
+        torch.cuda.synchronize()
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                graphs[k].replay()
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert all(torch.equal(p, q) for p, q in zip(outs[k], want[(turn + k) % len(sets)]))
+    got = []
+    for i, s in enumerate(sets):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(step(*s))
+    torch.cuda.synchronize()
+    for p, q in zip(got, want):
+        assert all(torch.equal(v, w) for v, w in zip(p, q))
+
+
+@pytest.mark.parametrize("tokens, D, F, dtype", [(1, 520, 1000, torch.bfloat16), (13, 2048, 4104, torch.float16), (48, 264, 1032, torch.float16),
+                                                 (700, 520, 1000, torch.bfloat16), (2049, 1000, 2744, torch.float16)])
+def test_gated_in_graphs_and_on_two_streams(tokens, D, F, dtype):
+    sets = [T._gated_inputs(tokens, D, F, dtype, seed) for seed in range(20, 24)]
+
+    def step(x, wg, wu, dh):
+        h, saved = da.gated_linear_forward(x, wg, wu, "gelu")
+        return (h, *da.gated_linear_backward(dh, x, wg, wu, saved), da.gated_linear(x, wg, wu))
+    _replayed_and_at_once(sets, step)
+
+
+@pytest.mark.parametrize("rows, V, top, dtype", [(1, 128256, 32, torch.float32), (8, 70001, 20, torch.bfloat16), (100, 16385, 5, torch.float16),
+                                                 (300, 3001, 7, torch.float32), (1300, 20000, 3, torch.bfloat16), (3000, 200, 0, torch.float16)])
+def test_log_probs_in_graphs_and_on_two_streams(rows, V, top, dtype):
+    sets = [T._logits(rows, V, dtype, seed) for seed in range(30, 34)]
+
+    def step(x, t, a, b):
+        r, saved = da.log_probs_forward(x, t, 1.1, top)
+        return (*(v for v in r if v is not None), da.log_probs_backward(x, t, saved, a, b, 1.1))
+    _replayed_and_at_once(sets, step)
