@@ -5,7 +5,7 @@
 // What bounds both: HBM.  The lookup reads the named rows and writes one a token; the gradient reads dy once and writes every
 // row of dw, most of them zeros for a large vocabulary.
 //
-// Gradient: the tokens are sorted by id, stably, by counting digits of up to 9 bits from the lowest on (two passes up to 2^18
+// Gradient: the tokens are sorted by id, stably, by counting digits of up to 9 bits from the lowest on (two passes below 2^18
 // rows).  Up to 4096 tokens one CTA does that in shared memory; longer ones take two launches a pass (three past 32768), each of
 // which starts as the one before it ends.  dw's zeros wait for nothing and are written beside all of these.  A token's place among those of its digit comes
 // from ballots over the warp and the warp's counters, so the order never depends on which thread came first.  Then a chunk of up to 32 tokens of a row is one
@@ -31,10 +31,11 @@ __device__ __forceinline__ int64_t id_at(const EmArgs& a, int64_t i) {
   return a.wide ? static_cast<const int64_t*>(a.ids)[i] : (int64_t) static_cast<const int32_t*>(a.ids)[i];
 }
 
-// ---- lookup: a warp 8 runs (of 16 bytes or one element a lane) of a token ----
+// ---- lookup: a warp LOOKUP_RUNS runs (of 16 bytes or one element a lane) of a token ----
+constexpr int LOOKUP_RUNS = 4;
 template <typename T, bool AL>
 __global__ void __launch_bounds__(256) em_lookup_kernel(const __grid_constant__ EmArgs a, uint32_t pieces) {
-  constexpr int VEC = AL ? Elem<T>::VEC : 1, U = 4;
+  constexpr int VEC = AL ? Elem<T>::VEC : 1, U = LOOKUP_RUNS;
   const int lane = threadIdx.x & 31;
   const uint64_t w = ((uint64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
   const int64_t i = w / pieces, c0 = (int64_t)(w % pieces) * 32 * VEC * U;
@@ -560,7 +561,7 @@ bool rows_aligned(const void* p, int64_t stride, int64_t cols, int es) {
 
 template <typename T, bool AL>
 cudaError_t lookup(const EmArgs& a, cudaStream_t st) {
-  const int64_t run = 32 * 4 * (AL ? Elem<T>::VEC : 1), pieces = (a.cols + run - 1) / run;
+  const int64_t run = 32 * LOOKUP_RUNS * (AL ? Elem<T>::VEC : 1), pieces = (a.cols + run - 1) / run;
   em_lookup_kernel<T, AL><<<(unsigned)((a.n * pieces + 7) / 8), 256, 0, st>>>(a, (uint32_t)pieces);
   return cudaGetLastError();
 }

@@ -37,7 +37,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 __device__ __forceinline__ float logistic(float x) { return rcp(1.f + ex2(-LOG2E * x)); }
 // Phi(g) = erfc(-g / sqrt 2) / 2, by erfc(z) = t 2^(P(t) - z^2 log2 e) for z >= 0, t = 2 / (2 + z): P of degree 9, fitted to log2(erfc(z)
 // e^(z^2) / t) for the least greatest error (7.5e-8 of the value, so the tail keeps its digits; least squares with weights moved
-// toward the largest errors).  CUDA's normcdff has branches and made the kernel wait for its results: 8192 hidden units, width
+// toward the largest errors).  The form t e^(polynomial in t - z^2) is published in Press, Teukolsky, Vetterling and Flannery, Numerical
+// Recipes, section 6.2; the coefficients here are the fit's own.  CUDA's normcdff has branches and made the kernel wait for its results: 8192 hidden units, width
 // 2048, 4096 tokens 190 us, the products alone 144.
 __device__ __forceinline__ float normal_cdf(float g) {
   const float t = rcp(__fmaf_rn(0.35355339059f, fabsf(g), 1.f));
@@ -322,9 +323,9 @@ __global__ void __launch_bounds__(pair::THREADS, 1) __cluster_dims__(2, 1, 1) gl
 // this size the reading of the weights bounds it, not the matrix rate.  Multiplying by single tokens on the FP32 pipe took 55 us for
 // 4 and 98 for 8, width 4096, 12288 hidden units; the tiles of the other kernel 74 for 5 to 15 tokens, which all SMs read from the few
 // slices of the L2 that hold so small an x.)
-// As many warps as leave each up to eight runs of 32 elements a row.  One token, us (TB/s): width 1024, 4096 hidden units 5.1
-// (3.3); 2048, 8192 14.4 (4.7); 4096, 12288 35.6 (5.7); 8192, 28672 140 (6.7): start and end of a launch, some 4 us, and the rest
-// at the copy bandwidth.
+// As many warps as leave each up to eight runs of 32 elements a row.  One token, us (TB/s), one call after another with weights that the
+// L2 does not hold: width 1024, 4096 hidden units 5.7 (2.9); 2048, 8192 13.5 (5.0); 4096, 12288 32.2 (6.3); 8192, 28672 136 (6.9): start
+// and end of a launch, some 3 us, and the rest at the copy bandwidth.
 template <typename R, typename T>
 __device__ __forceinline__ void load_once(R& r, const T* p) {   // of a weight that no other warp reads
   asm("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "l"(p));
