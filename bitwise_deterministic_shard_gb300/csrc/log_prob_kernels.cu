@@ -12,8 +12,8 @@
 //
 // What bounds it: HBM; x is read once, and once more and dx written in the gradient.  A step of 4 vectors of 16 bytes a
 // thread stays in registers: its maximum, then (the sums moved where that is larger) its terms, while the next step's
-// loads are under way.  128256 columns: 4096 f32 rows 302 us (6.96 TB/s), with 5 alternatives 342; 8192 bf16 rows 343 us (6.13 TB/s;
-// issue slots 62 %), with 5 alternatives 462; the gradient of these 629 us (6.68 TB/s).
+// loads are under way.  128256 columns: 4096 f32 rows 302 us (6.96 TB/s), with 5 alternatives 342; 8192 bf16 rows 327 to 343 us (6.13 to 6.43 TB/s;
+// issue slots 62 %), with 5 alternatives 440 to 462; the gradient of these 629 us (6.68 TB/s).
 //
 // Alternatives: each warp keeps the largest few of its lanes' maxima, step by step; the `top`-th of all warps' is a value that at
 // least `top` elements of the row reach.  What reaches it is kept in shared memory, some tens of elements of a large row; whenever
