@@ -62,6 +62,18 @@ def _run_of_rows(t, cols):
     return cols if run is None else run if run >= cols else None
 
 
+def _apart(out, *inputs):
+    """Refuses a contiguous out that shares memory with an input, given as the bytes of a matrix: other threads may still read what
+    one has overwritten."""
+    a0, size = out.data_ptr(), out.element_size()
+    a1 = a0 + out.numel() * size
+    for m in inputs:
+        at, _, rows, cols, run = _MATRIX.unpack(m)
+        i = max(0, (a0 - at - cols * size) // (run * size) + 1)     # the first row that ends past out's start
+        if i < rows and at + i * run * size < a1:
+            raise DetAttnError("out must not share memory with the inputs")
+
+
 # ---------------------------------------------------------------- gated feed-forward
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
@@ -102,7 +114,7 @@ def gated_linear_forward(x, w_gate, w_up, activation="silu", need_saved=True, ou
     rounded once.  saved, which the backward pass takes, holds act(g) and act'(g) u rounded to 24 bits each (6 bytes a hidden
     value); None without need_saved.  Up to 16 tokens without it the weights are read once by another kernel, whose sums are in
     another order.  Tensors that the kernels cannot address (columns not contiguous, starts or row strides off 16 bytes) are
-    copied."""
+    copied.  out must not share memory with the inputs."""
     index, code, D, F = _gated_args(x, w_gate, w_up)
     act = ACTIVATIONS.get(activation)
     if act is None:
@@ -119,6 +131,7 @@ def gated_linear_forward(x, w_gate, w_up, activation="silu", need_saved=True, ou
         _on(index, "out", out)
         if out.dtype != x.dtype or out.shape != shape or not out.is_contiguous() or out.data_ptr() % 16:
             raise DetAttnError(f"out must be contiguous {x.dtype} {shape} that starts on 16 bytes")
+        _apart(out, X, G, U)
     L = _da.lib()
     saved = torch.empty(L.dgl_saved_bytes(n, F), dtype=torch.uint8, device=x.device) if need_saved else None
     _run("gated_linear_forward", index, L.dgl_forward, X, G, U, act, _MATRIX.pack(out.data_ptr(), code, n, F, F), _addr(saved),
@@ -244,7 +257,7 @@ def log_probs_forward(logits, targets, temperature=1.0, top=0, need_saved=True, 
 
 def log_probs_backward(logits, targets, saved, grad, grad_entropy=None, temperature=1.0, out=None):
     """Gradient of sum(grad * log_probs) + sum(grad_entropy * entropy) (f32 [...], either None: zeros) for the logits, rounded once
-    to their dtype.  out: contiguous memory for it, such as the logits themselves; without it the rows of the result
+    to their dtype.  out: contiguous memory for it, the logits themselves or none of theirs; without it the rows of the result
     are as far apart as the logits' are, up to 16 bytes."""
     code, index, targets = _logits(logits, targets, temperature)
     shape, V, n = logits.shape[:-1], logits.shape[-1], targets.numel()
@@ -266,6 +279,8 @@ def log_probs_backward(logits, targets, saved, grad, grad_entropy=None, temperat
         _on(index, "out", out)
         if out.dtype != logits.dtype or out.shape != logits.shape or not out.is_contiguous():
             raise DetAttnError(f"out must be contiguous {logits.dtype} {list(logits.shape)}")
+        if out.data_ptr() != x.data_ptr() or (run != V and n > 1):
+            _apart(out, X)
         given, step = out, V
     _run("log_probs_backward", index, _da.lib().dlp_backward, X, targets.data_ptr(), saved.data_ptr(), _addr(grads[0]),
          _addr(grads[1]), temperature, _MATRIX.pack(out.data_ptr(), code, n, V, step))
@@ -312,7 +327,7 @@ def _ids(ids, index):
 def embedding_forward(ids, weight, scale=1.0, out=None, status=None):
     """Embedding lookup: scale * weight[ids], rounded once (scale 1: the same bits).  ids [...] int32 or int64, weight [rows, cols]
     f32, bf16 or f16; the result is [..., cols] of weight's dtype.  An id outside [0, rows) gives zeros and sets
-    STATUS_BAD_TARGET."""
+    STATUS_BAD_TARGET.  out must not share memory with weight."""
     _da._cuda(weight, "weight")
     if weight.dim() != 2 or weight.shape[0] < 1 or weight.shape[1] < 1:
         raise DetAttnError("weight must be [rows, cols] with at least one row and column")
@@ -327,6 +342,7 @@ def embedding_forward(ids, weight, scale=1.0, out=None, status=None):
         _on(index, "out", out)
         if out.dtype != weight.dtype or out.shape != shape or not out.is_contiguous():
             raise DetAttnError(f"out must be contiguous {weight.dtype} {list(shape)}")
+        _apart(out, W)
     _run("embedding_forward", index, _da.lib().dte_forward, ids.data_ptr(), bits, W, scale,
          _MATRIX.pack(out.data_ptr(), code, ids.numel(), cols, cols), status)
     if given is not None:

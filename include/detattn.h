@@ -412,7 +412,7 @@ int dow_adamw(const dow_tensor* tensors, int n, int dtype, int state_bits, void*
  * above they compute in binary32 in a fixed order: no atomics add values, and the order depends on the sizes and types
  * given (an embedding row's gradient: on the places of its own tokens alone) and, for log probabilities, on where the rows of logits start
  * within 16 bytes.  So equal calls give equal bytes on every run; for log probabilities that is equal values in equally aligned places.
- * The conventions above hold. */
+ * The conventions above hold.  Outputs and workspaces share no memory with each other or with inputs, but where said. */
 
 /* activations */
 #define DGL_SILU 0        /* g / (1 + exp(-g)) */
@@ -456,7 +456,7 @@ int dlp_forward(const da_matrix* logits, const int64_t* targets, float temperatu
  * logits' type:
  *   dlogits[i][v] = (grad_i ([v == targets[i]] - p_iv) - grad_entropy_i p_iv (log p_iv + entropy_i)) / temperature
  * zeros for a row of nothing but -inf; a row whose target is outside [0, cols) has the second term alone.  dlogits may be the logits'
- * own memory. */
+ * own memory, with their row stride. */
 int dlp_backward(const da_matrix* logits, const int64_t* targets, const float* saved, const float* grad, const float* grad_entropy,
                  float temperature, const da_matrix* dlogits, da_stream_t stream);
 
